@@ -531,6 +531,219 @@ plm_status plm_subdots_q4K(const void* w, const void* xq, int32_t* out,
 plm_status plm_subdots_q6K(const void* w, const void* xq, int32_t* out,
                            int64_t m, int64_t n, int64_t k, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * What stands between the q/k/v products and the output product of an
+ * attention block: rotary positions, the pages of a key/value cache, and the
+ * attention that reads them.  The PocketLLM pages name the attention and the
+ * K/V cache as parts of the engine around the packed matmul and give no
+ * layouts for them; the layouts here are this library's own.  The general
+ * rules above hold (device pointers, one stream, host checks before anything
+ * is enqueued, nothing allocated).
+ *
+ * A CACHE is a pool of pages, each of page_tokens token rows per key/value
+ * head.  Element (page, head, token in page, i) of the keys lies at
+ *   page * page_stride + head * head_stride + token * token_stride + i
+ * (elements), the same for the values from their own base.  Any order of the
+ * middle axes is possible, and one page may hold several layers.  A SLOT is
+ * page * page_tokens + token in page.  A page TABLE has one row of page
+ * indices per sequence: token j of sequence s lies in page
+ * table[s][j / page_tokens].
+ * ---------------------------------------------------------------------------
+ */
+#define PLM_F32 0
+#define PLM_F16 1
+#define PLM_BF16 2
+
+/*
+ * Rotary positions.  A position p turns pair i of a head by the angle
+ * p * w_i.  freqs holds w_i / (2 pi) as 64-bit fractions of a turn, so that
+ * p * freqs[i] wraps at whole turns exactly and every position is as exact
+ * as the first (f32 angles lose a bit with every doubling of p).
+ */
+#define PLM_ROPE_HALF 0           /* pair i of R/2: values i and i + R/2 */
+#define PLM_ROPE_INTERLEAVED 1    /* pair i: values 2i and 2i + 1 */
+
+#define PLM_ROPE_SCALING_NONE 0
+#define PLM_ROPE_SCALING_LINEAR 1   /* w_i / factor */
+#define PLM_ROPE_SCALING_BASE 2     /* base * factor^(R / (R - 2)): the slowest pair slows by factor */
+#define PLM_ROPE_SCALING_BANDS 3    /* by the turns n_i = trained * w_i / (2 pi) a pair makes over the
+                                       trained length: w_i * (r + (1 - r) / factor),
+                                       r = clamp((n_i - low) / (high - low), 0, 1) */
+#define PLM_ROPE_SCALING_RAMP 4     /* the same blend with r falling linearly in the pair's index i, from 1 at
+                                       the pair of `high` turns (rounded down) to 0 at that of `low`
+                                       (rounded up); *scale = 0.1 ln(factor) + 1 */
+typedef struct {
+    int32_t kind;       /* PLM_ROPE_SCALING_* */
+    double factor;      /* >= 1 */
+    double trained;     /* positions the model was trained on (BANDS, RAMP) */
+    double low, high;   /* turns, 0 < low < high (BANDS, RAMP) */
+} plm_rope_scaling;
+
+/*
+ * Fills freqs (HOST memory, rotary_dim / 2 values) for w_i = base^(-2i/R),
+ * scaled as `scaling` says (null: not at all), and *scale (may be null) with
+ * the factor of cos and sin that belongs to it.  Host arithmetic in f64.
+ * PLM_ERR_INVALID_ARG: null freqs, rotary_dim odd or < 2 or > 65536,
+ * base <= 1, a scaling field out of range, BASE with rotary_dim = 2.
+ */
+plm_status plm_rope_freqs(uint64_t* freqs, int64_t rotary_dim, double base, const plm_rope_scaling* scaling,
+                          float* scale);
+
+/*
+ * Turns (or only moves) the heads of up to PLM_ROPE_MAX_TENSORS tensors in one
+ * launch: typically q to rows, k and v of the same product into the cache.
+ * For each token t, head h, the first rotary_dim values by pairs (a, b):
+ *   y = (a c - b s, b c + a s), c = scale cos(angle), s = scale sin(angle);
+ * the others, and every value where rotate = 0, are copied.  inverse != 0
+ * turns the other way: with the same scale it is the gradient of the forward
+ * call, with scale 1 it takes a position back.  f32 arithmetic, one rounding
+ * to y_type.
+ *   x  [tokens][heads][head_dim] with strides in elements, the last axis dense.
+ *   y  the same shape with its own strides; may be x itself (same pointer,
+ *      strides and type).  With slots: into pages (see above); a token whose
+ *      slot is negative or >= pages * page_tokens is not written.
+ *   positions int32 [tokens], freqs uint64 [rotary_dim / 2]: device memory.
+ * Pointers are aligned to their elements.  PLM_ERR_INVALID_ARG: null
+ * pointers, count outside 1..8, sizes < 1 (tokens = 0 is allowed: nothing is
+ * done), tokens or heads past int32, head_dim > 1024, rotary_dim odd, < 2 or
+ * > head_dim, unknown layout or type, page sizes < 1 with slots, y = x with
+ * another stride or type.  Distinct tensors must not overlap otherwise.
+ */
+#define PLM_ROPE_MAX_TENSORS 8
+typedef struct {
+    const void* x;
+    void* y;
+    const int64_t* slots;                      /* [tokens], or null: y is rows */
+    int64_t heads;
+    int64_t x_token_stride, x_head_stride;
+    int64_t y_token_stride, y_head_stride;     /* with slots: inside a page */
+    int64_t page_tokens, page_stride, pages;   /* with slots */
+    int32_t x_type, y_type;                    /* PLM_F32, PLM_F16, PLM_BF16 */
+    int32_t rotate;
+} plm_rope_tensor;
+
+plm_status plm_rope(const plm_rope_tensor* tensors, int64_t count, const int32_t* positions, const uint64_t* freqs,
+                    int64_t tokens, int64_t head_dim, int64_t rotary_dim, int layout, float scale, int inverse,
+                    cudaStream_t stream);
+
+/*
+ * Pages of a cache, kept on the device: no call reads them back or waits.
+ * The state is the caller's:
+ *   table  int32 [max_seqs][max_pages]  row s: the pages of sequence s, then -1;
+ *   lens   int32 [max_seqs]             tokens of sequence s (0: not in use);
+ *   refs   int32 [pages]                table rows that hold the page; 0: free;
+ *   pool   pages * page_bytes bytes, opaque here (all layers, keys and values);
+ *   status int32 [1], may be null       flags that calls add (bitwise or).
+ * A page that is held more than once is full and never written; a sequence's
+ * partly filled last page is its own.  New pages are the free ones of lowest
+ * index, in the order of the call's items, so results do not depend on
+ * timing.  An item that cannot be done (a sequence out of range, a row too
+ * short, a child in use) is left out and flagged; if the free pages do not
+ * suffice for all the others, none is done.
+ * Sequences (for fork: children) are distinct within a call, and a fork's
+ * parents are not its children; the state is undefined otherwise, but no
+ * memory outside it is touched.
+ */
+#define PLM_KV_OUT_OF_PAGES 1
+#define PLM_KV_BAD_ITEM 2
+typedef struct {
+    void* pool;            /* 16-byte aligned */
+    int64_t page_bytes;    /* a multiple of 16 */
+    int64_t pages;
+    int32_t* table;
+    int32_t* lens;
+    int32_t* refs;
+    int32_t* status;
+    int64_t max_seqs, max_pages;
+    int64_t page_tokens;
+} plm_kv_state;
+
+/* Workspace bytes of the calls below for n items (0: invalid arguments);
+ * 256-byte aligned, free for other use when the call's kernels are done. */
+size_t plm_kv_workspace_size(int64_t pages, int64_t n);
+
+/* Sequence seqs[i] grows by add[i] >= 0 tokens.  slots int64 [n][slots_stride]
+ * (null: not wanted): slots[i][j] = the slot of its j-th new token, -1 for
+ * j >= add[i] and where nothing was done. */
+plm_status plm_kv_reserve(const plm_kv_state* kv, const int32_t* seqs, const int32_t* add, int64_t n, int64_t* slots,
+                          int64_t slots_stride, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Unused sequence children[i] becomes a copy of the first keep[i] tokens of
+ * parents[i] (keep null: of all; keep is cut to the parent's length): full
+ * pages are shared, a partly filled last one is copied into a new page. */
+plm_status plm_kv_fork(const plm_kv_state* kv, const int32_t* parents, const int32_t* children, const int32_t* keep,
+                       int64_t n, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The sequences give their pages back; their rows become -1, their lengths 0. */
+plm_status plm_kv_free(const plm_kv_state* kv, const int32_t* seqs, int64_t n, cudaStream_t stream);
+
+/* Moves pages so that the L pages in use are pages 0 .. L-1: the k-th free
+ * page below L takes the k-th used page from L on, and the table follows.
+ * live int32 [1] (may be null) = L. */
+plm_status plm_kv_compact(const plm_kv_state* kv, int32_t* live, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Page dst[i] = page src[i], i < n (device int32 lists; a pair with an index
+ * out of range is left out).  No dst is twice in the list or also a src. */
+plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const int32_t* dst, int64_t n,
+                             cudaStream_t stream);
+
+/*
+ * Attention over a paged cache for a batch whose sequences share their first
+ * prefix_len tokens (the same pages in every row): those are read once for
+ * all the batch.  prefix_len = 0 is plain paged attention; what is computed
+ * does not depend on it.
+ * Query t of sequence b (row b * tokens + t of q) stands at position
+ * len_b - tokens + t, where len_b counts all its tokens, the new ones
+ * included, and sees the keys j <= that position:
+ *   o = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j).
+ * A query that sees no key (or only scores of -inf) has o = 0, lse = -inf.
+ * Query head h reads key/value head h / (heads / kv_heads).
+ * Scores, maxima, sums and the output are held in f32; the probabilities are
+ * rounded to the cache's type for the second product (their sum is not).
+ *   q [batch*tokens][heads][head_dim] of `type`, strides in elements;
+ *   o the same shape of o_type (type or PLM_F32) with its own strides;
+ *   lse f32 [batch*tokens][heads], or null;
+ *   k, v pages of `type` as above; a table entry outside 0 .. pages-1 reads
+ *   as zeros; what lies past a sequence's end is never used, whatever its bits;
+ *   table int32 [rows][table_stride], lens int32 [rows]; sequence b is row
+ *   seqs[b] (null: row b), a row out of range has no keys; a length is cut to
+ *   max_len and to the row;
+ *   prefix_len a multiple of page_tokens, <= max_len; max_len bounds the
+ *   lengths (it sets the grid: a tight bound is faster).
+ * The prefix pages are read from the row of the first sequence that is at
+ * least prefix_len long (the longest if there is none).
+ * PLM_ERR_UNSUPPORTED: head_dim other than 64 or 128, page_tokens not a
+ * power of two from 16 on.  PLM_ERR_MISALIGNED: q, k, v below 16 bytes (o
+ * too), a stride of q, o, k, v not a multiple of 16 bytes, the workspace
+ * below 256.  PLM_ERR_INVALID_ARG: null pointers, sizes < 1, heads not a
+ * multiple of kv_heads, unknown types, a workspace below
+ * plm_attn_workspace_size bytes.  batch = 0 does nothing.
+ */
+typedef struct {
+    const void* q;
+    void* o;
+    float* lse;
+    const void* k;
+    const void* v;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* seqs;
+    int64_t batch, tokens, heads, kv_heads, head_dim;
+    int64_t q_token_stride, q_head_stride, o_token_stride, o_head_stride;
+    int64_t page_tokens, pages, page_stride, kv_head_stride, kv_token_stride;
+    int64_t table_stride, rows;
+    int64_t prefix_len, max_len;
+    float scale;
+    int32_t type, o_type;
+} plm_attn_problem;
+
+size_t plm_attn_workspace_size(int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                               int64_t prefix_len, int64_t max_len);
+plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 // The C ABI of libplm: argument checks on the host, then one or more kernel
 // launches on the caller's stream.  Nothing is allocated and nothing waits.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/plm.h"
@@ -482,6 +483,219 @@ plm_status plm_subdots_q4K(const void* w, const void* xq, int32_t* out, int64_t 
 plm_status plm_subdots_q6K(const void* w, const void* xq, int32_t* out, int64_t m, int64_t n,
                            int64_t k, cudaStream_t stream) {
     return subdots_common(6, w, xq, out, m, n, k, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Rotary positions, cache pages, attention
+// ---------------------------------------------------------------------------
+int64_t type_size(int type) { return type == PLM_F32 ? 4 : type == PLM_F16 || type == PLM_BF16 ? 2 : 0; }
+
+bool in_range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+
+plm_status check_kv(const plm_kv_state* kv) {
+    if (!kv || !kv->table || !kv->lens || !kv->refs) return PLM_ERR_INVALID_ARG;
+    if (!in_range(kv->pages, 1, kMaxIndex) || !in_range(kv->max_seqs, 1, kMaxIndex) ||
+        !in_range(kv->max_pages, 1, kMaxIndex) || !in_range(kv->page_tokens, 1, kMaxIndex))
+        return PLM_ERR_INVALID_ARG;
+    if (kv->max_seqs > (INT64_MAX >> 8) / kv->max_pages) return PLM_ERR_INVALID_ARG;
+    if (!aligned(kv->table, 4) || !aligned(kv->lens, 4) || !aligned(kv->refs, 4) || !aligned(kv->status, 4))
+        return PLM_ERR_MISALIGNED;
+    return PLM_OK;
+}
+
+// The pool, for the calls that move pages.
+plm_status check_pool(const plm_kv_state* kv) {
+    if (!kv->pool || kv->page_bytes < 16 || kv->page_bytes % 16 != 0) return PLM_ERR_INVALID_ARG;
+    if (kv->page_bytes > (INT64_MAX >> 8) / kv->pages) return PLM_ERR_INVALID_ARG;
+    return aligned(kv->pool, 16) ? PLM_OK : PLM_ERR_MISALIGNED;
+}
+
+plm_status check_kv_workspace(const plm_kv_state* kv, int64_t n, const void* ws, size_t bytes) {
+    if (!ws || bytes < plm::kv_workspace_bytes(kv->pages, n)) return PLM_ERR_INVALID_ARG;
+    return aligned(ws, 256) ? PLM_OK : PLM_ERR_MISALIGNED;
+}
+
+}  // namespace
+
+extern "C" {
+
+plm_status plm_rope_freqs(uint64_t* freqs, int64_t rotary_dim, double base, const plm_rope_scaling* scaling,
+                          float* scale) {
+    if (!freqs || !in_range(rotary_dim, 2, 65536) || rotary_dim % 2 || !(base > 1.0) || !std::isfinite(base))
+        return PLM_ERR_INVALID_ARG;
+    const int kind = scaling ? scaling->kind : PLM_ROPE_SCALING_NONE;
+    if (!in_range(kind, PLM_ROPE_SCALING_NONE, PLM_ROPE_SCALING_RAMP)) return PLM_ERR_INVALID_ARG;
+    const bool blend = kind == PLM_ROPE_SCALING_BANDS || kind == PLM_ROPE_SCALING_RAMP;
+    const double factor = kind == PLM_ROPE_SCALING_NONE ? 1.0 : scaling->factor;
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return PLM_ERR_INVALID_ARG;
+    if (blend && !(scaling->trained >= 1.0 && scaling->low > 0.0 && scaling->high > scaling->low &&
+                   std::isfinite(scaling->trained) && std::isfinite(scaling->high)))
+        return PLM_ERR_INVALID_ARG;
+    if (kind == PLM_ROPE_SCALING_BASE && rotary_dim == 2) return PLM_ERR_INVALID_ARG;
+    const double kTwoPi = 6.283185307179586476925286766559;
+    const double R = (double)rotary_dim;
+    const double b = kind == PLM_ROPE_SCALING_BASE ? base * std::pow(factor, R / (R - 2.0)) : base;
+    double first = 0.0, last = 0.0;   // RAMP: the pairs between which r falls from 1 to 0
+    if (kind == PLM_ROPE_SCALING_RAMP) {
+        // pair i makes trained / (2 pi) base^(-2i/R) turns
+        auto pair_of = [&](double turns) { return R * std::log(scaling->trained / (turns * kTwoPi)) / (2.0 * std::log(base)); };
+        first = std::fmax(std::floor(pair_of(scaling->high)), 0.0);
+        last = std::fmin(std::ceil(pair_of(scaling->low)), R - 1.0);
+        if (last <= first) last = first + 0.001;
+    }
+    for (int64_t i = 0; i < rotary_dim / 2; ++i) {
+        double w = std::pow(b, -2.0 * (double)i / R);
+        if (kind == PLM_ROPE_SCALING_LINEAR) w /= factor;
+        if (blend) {
+            const double r = kind == PLM_ROPE_SCALING_BANDS
+                                 ? (scaling->trained * w / kTwoPi - scaling->low) / (scaling->high - scaling->low)
+                                 : 1.0 - ((double)i - first) / (last - first);
+            const double keep = std::fmin(1.0, std::fmax(0.0, r));
+            w = w * (keep + (1.0 - keep) / factor);
+        }
+        // w <= 1 radian: below a sixth of a turn, so the product is below 2^62
+        freqs[i] = (uint64_t)std::llround(w / kTwoPi * 18446744073709551616.0);
+    }
+    if (scale) *scale = kind == PLM_ROPE_SCALING_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return PLM_OK;
+}
+
+plm_status plm_rope(const plm_rope_tensor* tensors, int64_t count, const int32_t* positions, const uint64_t* freqs,
+                    int64_t tokens, int64_t head_dim, int64_t rotary_dim, int layout, float scale, int inverse,
+                    cudaStream_t stream) {
+    if (!tensors || !in_range(count, 1, PLM_ROPE_MAX_TENSORS) || !positions || !freqs) return PLM_ERR_INVALID_ARG;
+    if (!in_range(tokens, 0, kMaxIndex) || !in_range(head_dim, 2, 1024) || head_dim % 2) return PLM_ERR_INVALID_ARG;
+    if (!in_range(rotary_dim, 2, head_dim) || rotary_dim % 2) return PLM_ERR_INVALID_ARG;
+    if (layout != PLM_ROPE_HALF && layout != PLM_ROPE_INTERLEAVED) return PLM_ERR_INVALID_ARG;
+    int64_t heads = 0;
+    for (int64_t j = 0; j < count; ++j) {
+        const plm_rope_tensor& t = tensors[j];
+        if (!t.x || !t.y || !type_size(t.x_type) || !type_size(t.y_type) || !in_range(t.heads, 1, 65536))
+            return PLM_ERR_INVALID_ARG;
+        if (t.slots && (!in_range(t.page_tokens, 1, kMaxIndex) || !in_range(t.pages, 1, kMaxIndex)))
+            return PLM_ERR_INVALID_ARG;
+        if (t.x == t.y && (t.slots || t.x_type != t.y_type || t.x_token_stride != t.y_token_stride ||
+                           t.x_head_stride != t.y_head_stride))
+            return PLM_ERR_INVALID_ARG;
+        heads += t.heads;
+    }
+    if (heads > 65536) return PLM_ERR_INVALID_ARG;
+    if (!aligned(positions, 4) || !aligned(freqs, 8)) return PLM_ERR_MISALIGNED;
+    for (int64_t j = 0; j < count; ++j) {
+        const plm_rope_tensor& t = tensors[j];
+        if (!aligned(t.x, type_size(t.x_type)) || !aligned(t.y, type_size(t.y_type)) || !aligned(t.slots, 8))
+            return PLM_ERR_MISALIGNED;
+    }
+    if (tokens == 0) return PLM_OK;
+    return cuda_status(plm::launch_rope(tensors, (int)count, positions, freqs, tokens, (int)head_dim, (int)rotary_dim,
+                                        layout, scale, inverse != 0, stream));
+}
+
+size_t plm_kv_workspace_size(int64_t pages, int64_t n) {
+    if (!in_range(pages, 1, kMaxIndex) || !in_range(n, 0, kMaxIndex)) return 0;
+    return plm::kv_workspace_bytes(pages, n);
+}
+
+plm_status plm_kv_reserve(const plm_kv_state* kv, const int32_t* seqs, const int32_t* add, int64_t n, int64_t* slots,
+                          int64_t slots_stride, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    plm_status s = check_kv(kv);
+    if (s != PLM_OK) return s;
+    if (!seqs || !add || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if (slots && !in_range(slots_stride, 1, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    s = check_kv_workspace(kv, n, workspace, workspace_bytes);
+    if (s != PLM_OK) return s;
+    if (!aligned(seqs, 4) || !aligned(add, 4) || !aligned(slots, 8)) return PLM_ERR_MISALIGNED;
+    if (n == 0) return PLM_OK;
+    return cuda_status(plm::launch_kv_reserve(*kv, seqs, add, n, reinterpret_cast<long long*>(slots),
+                                              slots ? slots_stride : 0, workspace, stream));
+}
+
+plm_status plm_kv_fork(const plm_kv_state* kv, const int32_t* parents, const int32_t* children, const int32_t* keep,
+                       int64_t n, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    plm_status s = check_kv(kv);
+    if (s == PLM_OK) s = check_pool(kv);
+    if (s != PLM_OK) return s;
+    if (!parents || !children || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    s = check_kv_workspace(kv, n, workspace, workspace_bytes);
+    if (s != PLM_OK) return s;
+    if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(keep, 4)) return PLM_ERR_MISALIGNED;
+    if (n == 0) return PLM_OK;
+    return cuda_status(plm::launch_kv_fork(*kv, parents, children, keep, n, workspace, stream));
+}
+
+plm_status plm_kv_free(const plm_kv_state* kv, const int32_t* seqs, int64_t n, cudaStream_t stream) {
+    plm_status s = check_kv(kv);
+    if (s != PLM_OK) return s;
+    if (!seqs || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if (!aligned(seqs, 4)) return PLM_ERR_MISALIGNED;
+    if (n == 0) return PLM_OK;
+    return cuda_status(plm::launch_kv_free(*kv, seqs, n, stream));
+}
+
+plm_status plm_kv_compact(const plm_kv_state* kv, int32_t* live, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+    plm_status s = check_kv(kv);
+    if (s == PLM_OK) s = check_pool(kv);
+    if (s == PLM_OK) s = check_kv_workspace(kv, 0, workspace, workspace_bytes);
+    if (s != PLM_OK) return s;
+    if (!aligned(live, 4)) return PLM_ERR_MISALIGNED;
+    return cuda_status(plm::launch_kv_compact(*kv, live, workspace, stream));
+}
+
+plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const int32_t* dst, int64_t n,
+                             cudaStream_t stream) {
+    plm_status s = check_kv(kv);
+    if (s == PLM_OK) s = check_pool(kv);
+    if (s != PLM_OK) return s;
+    if (!src || !dst || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return PLM_ERR_MISALIGNED;
+    if (n == 0) return PLM_OK;
+    return cuda_status(plm::launch_kv_copy_pages(*kv, src, dst, n, stream));
+}
+
+size_t plm_attn_workspace_size(int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                               int64_t prefix_len, int64_t max_len) {
+    if (!in_range(batch, 1, kMaxIndex) || !in_range(tokens, 1, kMaxIndex) || !in_range(heads, 1, kMaxIndex) ||
+        !in_range(kv_heads, 1, heads) || heads % kv_heads || (head_dim != 64 && head_dim != 128) ||
+        !in_range(max_len, 1, kMaxIndex) || !in_range(prefix_len, 0, max_len))
+        return 0;
+    if (batch * tokens > kMaxIndex / heads) return 0;
+    return plm::attn_workspace_bytes(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len);
+}
+
+plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+    if (!p || !p->q || !p->o || !p->k || !p->v || !p->table || !p->lens) return PLM_ERR_INVALID_ARG;
+    if (!in_range(p->batch, 0, kMaxIndex) || !in_range(p->tokens, 1, kMaxIndex) || !in_range(p->heads, 1, kMaxIndex) ||
+        !in_range(p->kv_heads, 1, p->heads) || p->heads % p->kv_heads || p->head_dim < 1)
+        return PLM_ERR_INVALID_ARG;
+    if (p->batch * p->tokens > kMaxIndex / p->heads) return PLM_ERR_INVALID_ARG;
+    if ((p->type != PLM_F16 && p->type != PLM_BF16) || (p->o_type != p->type && p->o_type != PLM_F32))
+        return PLM_ERR_INVALID_ARG;
+    if (!in_range(p->pages, 1, kMaxIndex) || !in_range(p->rows, 1, kMaxIndex) || p->page_tokens < 1 ||
+        !in_range(p->table_stride, 1, kMaxIndex) || !in_range(p->max_len, 1, kMaxIndex) ||
+        !in_range(p->prefix_len, 0, p->max_len) || p->prefix_len % p->page_tokens)
+        return PLM_ERR_INVALID_ARG;
+    if (p->page_stride < 0 || p->kv_head_stride < 0 || p->kv_token_stride < 0) return PLM_ERR_INVALID_ARG;
+    if ((p->head_dim != 64 && p->head_dim != 128) || !in_range(p->page_tokens, 16, 1 << 30) ||
+        (p->page_tokens & (p->page_tokens - 1)))
+        return PLM_ERR_UNSUPPORTED;
+    if (p->batch == 0) return PLM_OK;
+    const size_t need = plm_attn_workspace_size(p->batch, p->tokens, p->heads, p->kv_heads, p->head_dim,
+                                                p->prefix_len, p->max_len);
+    if (need && (!workspace || workspace_bytes < need)) return PLM_ERR_INVALID_ARG;
+    const int64_t oe = p->o_type == PLM_F32 ? 4 : 8;   // elements of 16 bytes
+    if (!aligned(p->q, 16) || !aligned(p->o, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->lse, 4) ||
+        !aligned(p->table, 4) || !aligned(p->lens, 4) || !aligned(p->seqs, 4) || !aligned(workspace, 256))
+        return PLM_ERR_MISALIGNED;
+    if (p->q_token_stride % 8 || p->q_head_stride % 8 || p->o_token_stride % oe || p->o_head_stride % oe ||
+        p->page_stride % 8 || p->kv_head_stride % 8 || p->kv_token_stride % 8)
+        return PLM_ERR_MISALIGNED;
+    return cuda_status(plm::launch_attn(*p, workspace, stream));
 }
 
 }  // extern "C"

@@ -5,6 +5,8 @@
 #include <utility>
 #include <cuda_runtime.h>
 
+#include "../../include/plm.h"
+
 namespace plm {
 
 // Number of SMs of the current device (queried per call; no cached state).
@@ -149,5 +151,26 @@ size_t x16_bytes(int fmt, long long n, int k);   // fmt 4 (q4_K) or 6 (q6_K)
 cudaError_t launch_repack_x16(int fmt, const uint8_t* w, uint8_t* out, int n, int k, cudaStream_t stream);
 cudaError_t launch_gemv_x16(int fmt, const uint8_t* w, const uint8_t* xq, float* y, int m, int n, int k,
                             cudaStream_t stream);
+
+// Rotary positions: up to PLM_ROPE_MAX_TENSORS tensors, checked arguments.
+cudaError_t launch_rope(const plm_rope_tensor* tensors, int count, const int32_t* positions, const uint64_t* freqs,
+                        long long tokens, int head_dim, int rotary_dim, int layout, float scale, int inverse,
+                        cudaStream_t stream);
+
+// Pages of a cache; ws: kv_workspace_bytes(pages, n) bytes, 256-byte aligned.
+size_t kv_workspace_bytes(long long pages, long long n);
+cudaError_t launch_kv_reserve(const plm_kv_state& S, const int* seqs, const int* add, long long n, long long* slots,
+                              long long slots_stride, void* ws, cudaStream_t stream);
+cudaError_t launch_kv_fork(const plm_kv_state& S, const int* parents, const int* children, const int* keep,
+                           long long n, void* ws, cudaStream_t stream);
+cudaError_t launch_kv_free(const plm_kv_state& S, const int* seqs, long long n, cudaStream_t stream);
+cudaError_t launch_kv_compact(const plm_kv_state& S, int* live, void* ws, cudaStream_t stream);
+cudaError_t launch_kv_copy_pages(const plm_kv_state& S, const int* src, const int* dst, long long n,
+                                 cudaStream_t stream);
+
+// Attention over a paged cache, checked arguments.
+size_t attn_workspace_bytes(long long batch, long long tokens, long long heads, long long kv_heads, long long head_dim,
+                            long long prefix_len, long long max_len);
+cudaError_t launch_attn(const plm_attn_problem& p, void* ws, cudaStream_t stream);
 
 }  // namespace plm

@@ -52,6 +52,35 @@ class _QProblem(ctypes.Structure):
                 ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("trained", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("x_type", ctypes.c_int32), ("y_type", ctypes.c_int32), ("rotate", ctypes.c_int32)]
+
+
+class _KvState(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("max_seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int64)]
+
+
+class _AttnProblem(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("q", "o", "lse", "k", "v", "table", "lens", "seqs")] +
+                [(f, ctypes.c_int64) for f in ("batch", "tokens", "heads", "kv_heads", "head_dim", "q_token_stride",
+                                               "q_head_stride", "o_token_stride", "o_head_stride", "page_tokens",
+                                               "pages", "page_stride", "kv_head_stride", "kv_token_stride",
+                                               "table_stride", "rows", "prefix_len", "max_len")] +
+                [("scale", ctypes.c_float), ("type", ctypes.c_int32), ("o_type", ctypes.c_int32)])
+
+
 _lib = None
 
 
@@ -127,6 +156,20 @@ def load(build_if_missing=True):
         fn = getattr(lib, name)
         fn.argtypes = [vp, vp, vp, i64, i64, i64, vp]
         fn.restype = ctypes.c_int
+    dbl, sz, i32, f32 = ctypes.c_double, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+    for name, res, args in (
+            ("plm_rope_freqs", i32, [vp, i64, dbl, ctypes.POINTER(_RopeScaling), ctypes.POINTER(f32)]),
+            ("plm_rope", i32, [ctypes.POINTER(_RopeTensor), i64, vp, vp, i64, i64, i64, i32, f32, i32, vp]),
+            ("plm_kv_workspace_size", sz, [i64, i64]),
+            ("plm_kv_reserve", i32, [ctypes.POINTER(_KvState), vp, vp, i64, vp, i64, vp, sz, vp]),
+            ("plm_kv_fork", i32, [ctypes.POINTER(_KvState), vp, vp, vp, i64, vp, sz, vp]),
+            ("plm_kv_free", i32, [ctypes.POINTER(_KvState), vp, i64, vp]),
+            ("plm_kv_compact", i32, [ctypes.POINTER(_KvState), vp, vp, sz, vp]),
+            ("plm_kv_copy_pages", i32, [ctypes.POINTER(_KvState), vp, vp, i64, vp]),
+            ("plm_attn_workspace_size", sz, [i64] * 7),
+            ("plm_attn_shared_prefix", i32, [ctypes.POINTER(_AttnProblem), vp, sz, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = res
     _lib = lib
     return lib
 
@@ -369,3 +412,194 @@ def raw_status(name, *args):
     """Calls an entry point and returns its status code without raising
     (used by the argument-check tests)."""
     return getattr(load(), name)(*args)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions, cache pages, attention over a shared prefix.  Shapes and
+# strides come from the torch tensors.
+# ---------------------------------------------------------------------------
+PLM_F32, PLM_F16, PLM_BF16 = 0, 1, 2
+PLM_ROPE_HALF, PLM_ROPE_INTERLEAVED = 0, 1
+PLM_KV_OUT_OF_PAGES, PLM_KV_BAD_ITEM = 1, 2
+_LAYOUTS = {"half": PLM_ROPE_HALF, "interleaved": PLM_ROPE_INTERLEAVED}
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def _type(t):
+    import torch
+    code = {torch.float32: PLM_F32, torch.float16: PLM_F16, torch.bfloat16: PLM_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError("expected float32, float16 or bfloat16, got %s" % t.dtype)
+    return code
+
+
+def _ints(t, dtype, name, shape=None):
+    """Address of a contiguous CUDA tensor of the given integer type (None stays None)."""
+    if t is None:
+        return None
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
+    return _addr(t)
+
+
+def _rows(t, name, dims):
+    """Strides of a CUDA tensor whose last axis is dense."""
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor" % name)
+    if t.dim() != dims:
+        raise ValueError("%s: expected %d dimensions, got %d" % (name, dims, t.dim()))
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError("%s: the last dimension has to be dense" % name)
+    return st
+
+
+def plm_rope_freqs(rotary_dim, base, scaling="none", factor=1.0, trained=0.0, low=1.0, high=32.0, device=None):
+    """(freqs, scale): an int64 tensor with the bits of plm_rope's uint64 frequencies (on `device`, the CPU if None)
+    and the factor of cos and sin; scaling: "none", "linear", "base", "bands" or "ramp" (see include/plm.h)."""
+    import torch
+    lib = load()
+    freqs = torch.empty(max(0, rotary_dim // 2), dtype=torch.int64)
+    s = _RopeScaling(_SCALINGS[scaling], factor, trained, low, high)
+    scale = ctypes.c_float(0)
+    _check("plm_rope_freqs", lib.plm_rope_freqs(freqs.data_ptr() or None, rotary_dim, base, ctypes.byref(s),
+                                                ctypes.byref(scale)))
+    return (freqs if device is None else freqs.to(device)), scale.value
+
+
+def plm_rope_tensor(x, y, slots=None, rotate=True):
+    """One tensor of a plm_rope call.  x [tokens][heads][head_dim]; y the same shape, or with slots (int64 [tokens])
+    the pages [pages][heads][page_tokens][head_dim] of a cache, as any strided view."""
+    xs = _rows(x, "x", 3)
+    if slots is None:
+        ys = _rows(y, "y", 3)
+        if y.shape != x.shape:
+            raise ValueError("y: expected shape %s, got %s" % (tuple(x.shape), tuple(y.shape)))
+        page = (0, 0, 0)
+        yt, yh = ys[0], ys[1]
+    else:
+        ys = _rows(y, "y", 4)
+        if y.shape[1] != x.shape[1] or y.shape[3] != x.shape[2]:
+            raise ValueError("y: expected pages [.][%d][.][%d], got %s" % (x.shape[1], x.shape[2], tuple(y.shape)))
+        page = (y.shape[2], ys[0], y.shape[0])
+        yt, yh = ys[2], ys[1]
+    t = _RopeTensor(x.data_ptr() or None, y.data_ptr() or None, _ints(slots, "int64", "slots", (x.shape[0],)),
+                    x.shape[1], xs[0], xs[1], yt, yh, page[0], page[1], page[2], _type(x), _type(y), 1 if rotate else 0)
+    t.shape = (x.shape[0], x.shape[2])
+    return t
+
+
+def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, inverse=False, stream=None):
+    """Turns the heads of the tensors (plm_rope_tensor) by their positions (int32 [tokens]); see include/plm.h."""
+    lib = load()
+    tokens, d = tensors[0].shape if tensors else (positions.numel(), 0)
+    for t in tensors:
+        if t.shape != (tokens, d):
+            raise ValueError("the tensors differ in tokens or head size")
+    if freqs.numel() != rotary_dim // 2:
+        raise ValueError("freqs: expected %d values, got %d" % (rotary_dim // 2, freqs.numel()))
+    if tokens == 0 and tensors:
+        return
+    arr = (_RopeTensor * len(tensors))(*tensors)
+    _check("plm_rope", lib.plm_rope(arr, len(tensors), _ints(positions, "int32", "positions", (tokens,)),
+                                    _ints(freqs, "int64", "freqs"), tokens, d, rotary_dim,
+                                    _LAYOUTS.get(layout, layout), scale, 1 if inverse else 0, _stream(stream)))
+
+
+def plm_kv_state(pool, table, lens, refs, page_tokens, status=None):
+    """Page state over device tensors: pool [pages][...] of any type, table int32 [max_seqs][max_pages], lens int32
+    [max_seqs], refs int32 [pages], status int32 [1] or None.  It holds addresses: keep the tensors."""
+    pages, (seqs, width) = pool.shape[0], table.shape
+    s = _KvState(_addr(pool), pool.numel() // max(1, pages) * pool.element_size(), pages,
+                 _ints(table, "int32", "table"), _ints(lens, "int32", "lens", (seqs,)),
+                 _ints(refs, "int32", "refs", (pages,)), _ints(status, "int32", "status"), seqs, width, page_tokens)
+    return s
+
+
+def plm_kv_workspace_size(pages, n):
+    """Workspace bytes of the page calls for n items (0: invalid arguments)."""
+    return load().plm_kv_workspace_size(pages, n)
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def plm_kv_reserve(kv, seqs, add, slots, workspace, stream=None):
+    """Sequences seqs grow by add tokens (int32 [n]); slots int64 [n][most] or None gets the new tokens' slots."""
+    lib, n = load(), seqs.numel()
+    if slots is not None and (slots.dim() != 2 or slots.shape[0] != n):
+        raise ValueError("slots: expected [%d][.], got %s" % (n, tuple(slots.shape)))
+    _check("plm_kv_reserve", lib.plm_kv_reserve(ctypes.byref(kv), _ints(seqs, "int32", "seqs"),
+                                                _ints(add, "int32", "add", (n,)), n, _ints(slots, "int64", "slots"),
+                                                0 if slots is None else slots.shape[1], _addr(workspace),
+                                                _bytes(workspace), _stream(stream)))
+
+
+def plm_kv_fork(kv, parents, children, workspace, keep=None, stream=None):
+    """Unused sequences children (int32 [n]) become copies of parents, of their first keep tokens if given."""
+    lib, n = load(), parents.numel()
+    _check("plm_kv_fork", lib.plm_kv_fork(ctypes.byref(kv), _ints(parents, "int32", "parents"),
+                                          _ints(children, "int32", "children", (n,)), _ints(keep, "int32", "keep", (n,)),
+                                          n, _addr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def plm_kv_free(kv, seqs, stream=None):
+    """The sequences (int32 [n]) give their pages back."""
+    lib = load()
+    _check("plm_kv_free", lib.plm_kv_free(ctypes.byref(kv), _ints(seqs, "int32", "seqs"), seqs.numel(), _stream(stream)))
+
+
+def plm_kv_compact(kv, live, workspace, stream=None):
+    """Packs the pages in use to the front of the pool; live (int32 [1] or None) gets their number."""
+    lib = load()
+    _check("plm_kv_compact", lib.plm_kv_compact(ctypes.byref(kv), _ints(live, "int32", "live"), _addr(workspace),
+                                                _bytes(workspace), _stream(stream)))
+
+
+def plm_kv_copy_pages(kv, src, dst, stream=None):
+    """Page dst[i] = page src[i] (int32 lists of the same length)."""
+    lib, n = load(), src.numel()
+    _check("plm_kv_copy_pages", lib.plm_kv_copy_pages(ctypes.byref(kv), _ints(src, "int32", "src"),
+                                                      _ints(dst, "int32", "dst", (n,)), n, _stream(stream)))
+
+
+def plm_attn_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len):
+    """Workspace bytes of plm_attn_shared_prefix (0: none needed, or invalid arguments)."""
+    return load().plm_attn_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len)
+
+
+def plm_attn_shared_prefix(q, o, k, v, table, lens, tokens, prefix_len, max_len, scale, workspace, lse=None, seqs=None,
+                           stream=None):
+    """Attention of q [batch*tokens][heads][head_dim] over the pages k, v [pages][kv_heads][page_tokens][head_dim]
+    (strided views of one shape and strides) into o; the batch's first prefix_len tokens are shared (see include/plm.h)."""
+    lib = load()
+    qs, os_, ks = _rows(q, "q", 3), _rows(o, "o", 3), _rows(k, "k", 4)
+    if o.shape != q.shape:
+        raise ValueError("o: expected shape %s, got %s" % (tuple(q.shape), tuple(o.shape)))
+    if v.shape != k.shape or _rows(v, "v", 4) != ks or v.dtype != k.dtype or q.dtype != k.dtype:
+        raise ValueError("k and v have to agree in shape, strides and type, and q in type")
+    if k.shape[3] != q.shape[2]:
+        raise ValueError("k: expected heads of %d, got %d" % (q.shape[2], k.shape[3]))
+    n, heads, d = q.shape
+    if tokens < 1 or n % tokens:
+        raise ValueError("q: %d rows are no multiple of %d tokens" % (n, tokens))
+    rows, width = table.shape
+    batch = n // tokens
+    p = _AttnProblem(q.data_ptr() or None, o.data_ptr() or None, None, k.data_ptr() or None, v.data_ptr() or None,
+                     _ints(table, "int32", "table"), _ints(lens, "int32", "lens", (rows,)),
+                     _ints(seqs, "int32", "seqs", (batch,)), batch, tokens, heads, k.shape[1], d, qs[0], qs[1], os_[0],
+                     os_[1], k.shape[2], k.shape[0], ks[0], ks[1], ks[2], width, rows, prefix_len, max_len, scale,
+                     _type(k), _type(o))
+    if seqs is None and batch > rows:
+        raise ValueError("table: %d rows for a batch of %d" % (rows, batch))
+    if lse is not None:
+        if _type(lse) != PLM_F32 or tuple(lse.shape) != (n, heads):
+            raise ValueError("lse: expected float32 %s" % ((n, heads),))
+        p.lse = _addr(lse)
+    if batch == 0:
+        return
+    _check("plm_attn_shared_prefix", lib.plm_attn_shared_prefix(ctypes.byref(p), _addr(workspace), _bytes(workspace),
+                                                                _stream(stream)))
