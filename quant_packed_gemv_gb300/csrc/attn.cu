@@ -113,6 +113,7 @@ cudaError_t launch_attn(const plm_attn_problem& p, void*, cudaStream_t stream) {
     A.cap = (int)(p.max_len < room ? p.max_len : room);
     A.scale = p.scale;
     A.o_f32 = p.o_type == PLM_F32;
+    if (A.nq * A.group <= 16) return launch_attn_rows(A, p.type, (int)p.head_dim, stream);
     return p.type == PLM_F16 ? attn_type<__half>(A, (int)p.head_dim, stream)
                              : attn_type<__nv_bfloat16>(A, (int)p.head_dim, stream);
 }

@@ -50,4 +50,53 @@ template <> __device__ __forceinline__ float2 pair_to_f32<__nv_bfloat16>(uint32_
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
 
+// Two f32 rounded to the cache's type, the first in the low half.
+template <class E> __device__ __forceinline__ uint32_t pack_pair(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack_pair<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four values of an output row, at element offset off (a multiple of 4).
+template <class E>
+__device__ __forceinline__ void attn_store4(const AttnArgs& A, long long off, float4 v) {
+    if (A.o_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(A.o) + off) = v;
+    else
+        *reinterpret_cast<uint2*>(static_cast<E*>(A.o) + off) = make_uint2(pack_pair<E>(v.x, v.y), pack_pair<E>(v.z, v.w));
+}
+
+// The cluster's CTAs: a barrier over all their threads, and shared memory of
+// the CTA of rank z at the place of `p` here (its own where n = 1).
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int z) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(z));
+    return a;
+}
+__device__ __forceinline__ float peer_f32(const float* p, int z, int n) {
+    if (n == 1) return *p;
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, z)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(const float* p, int z, int n) {
+    if (n == 1) return *reinterpret_cast<const float4*>(p);
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_addr(p, z)) : "memory");
+    return v;
+}
+
+// At most 16 query rows per sequence and key/value head.
+cudaError_t launch_attn_rows(const AttnArgs& A, int type, int d, cudaStream_t stream);
+
 }  // namespace plm
