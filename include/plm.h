@@ -101,7 +101,8 @@ int plm_last_cuda_error(void);
 /*
  * Diagnostic: the device fault word of the current device.  Kernels that
  * stream through asynchronous copies bound every wait; a wait that runs out
- * sets bit 0 here and the kernel stops (its outputs are then incomplete).
+ * sets a bit here (0: GEMV, 1: GEMM, 2: attention) and the kernel stops (its
+ * outputs are then incomplete).
  * *code receives the word; clear != 0 resets it.  Unlike the compute entry
  * points this call synchronizes with the device (it copies one word).
  */
@@ -712,8 +713,11 @@ plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const i
  *   max_len and to the row;
  *   prefix_len a multiple of page_tokens, <= max_len; max_len bounds the
  *   lengths (it sets the grid: a tight bound is faster).
- * The prefix pages are read from the row of the first sequence that is at
- * least prefix_len long (the longest if there is none).
+ * A sequence takes part in the shared prefix when each of its queries sees
+ * all of it; the prefix pages are read from the row of the first one that
+ * does.  The others (shorter, or idle) read their own rows throughout.
+ * Values of a sequence's own tokens that are infinite or NaN may reach the
+ * queries of the same call that stand before them (0 * inf).
  * PLM_ERR_UNSUPPORTED: head_dim other than 64 or 128, page_tokens not a
  * power of two from 16 on.  PLM_ERR_MISALIGNED: q, k, v below 16 bytes (o
  * too), a stride of q, o, k, v not a multiple of 16 bytes, the workspace

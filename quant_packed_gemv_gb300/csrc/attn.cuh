@@ -96,7 +96,4 @@ __device__ __forceinline__ float4 peer_f32x4(const float* p, int z, int n) {
     return v;
 }
 
-// At most 16 query rows per sequence and key/value head.
-cudaError_t launch_attn_rows(const AttnArgs& A, int type, int d, cudaStream_t stream);
-
 }  // namespace plm

@@ -19,7 +19,7 @@
 // row).  A warp keeps the next 16 keys' K and this block's V in flight (8 KB
 // at D = 128); the warps of a CTA and the CTAs of a cluster take the blocks
 // in turn and add their parts through shared memory, in a fixed order.
-#include "attn.cuh"
+#include "attn_tile.cuh"
 
 namespace plm {
 
@@ -66,12 +66,14 @@ template <int D, int NB> struct RowsSmem {
 };
 
 template <class E, int D, int NB>
-__global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A) {
+__global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     using Sm = RowsSmem<D, NB>;
     constexpr int KC = D / 32, VC = D / 64;   // 16-byte chunks per lane of a K row, of a V row
     __shared__ __align__(16) Sm sm;
     grid_launch_dependents();
-    grid_wait_prior();
+    // after the tile kernel there is nothing to wait for yet: it starts this
+    // kernel once the work before it has finished
+    if (P.prefix_tiles == 0) grid_wait_prior();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int b = blockIdx.x / A.kv_heads, h = blockIdx.x - b * A.kv_heads;
     const int rows = A.nq * A.group;
@@ -118,6 +120,8 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const float sl2 = A.scale * LOG2E;
     const int streams = DW * gridDim.z, stream = blockIdx.z * DW + warp;
     const int blocks = (len + 15) >> 4;
+    const bool shares = attn_shares(A, P, len);
+    const int first = shares ? A.prefix >> 4 : 0;   // the prefix is a multiple of 16
 
     const uint4 zero = make_uint4(0, 0, 0, 0);
     auto page_of = [&](int blk) -> int { return blk < blocks ? __ldg(tab + ((blk << 4) >> A.page_shift)) : -1; };
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
                 kf[i][c] = in && j + g + 8 * i < len ? ldg_nc_v4(p + 8 * i * A.kv_ts + 32 * c) : zero;
     };
 
-    int blk = stream, page = page_of(blk), page_n = page_of(blk + streams);
+    int blk = first + stream, page = page_of(blk), page_n = page_of(blk + streams);
     uint4 kf[2][KC];
     if (blk < blocks) load_k(blk, page, kf);
     for (; blk < blocks; blk += streams) {
@@ -237,6 +241,7 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const int cs = gridDim.z;   // the cluster: the CTAs of this pair
     if (cs > 1) cluster_barrier();
     else __syncthreads();
+    if (P.prefix_tiles > 0) grid_wait_prior();   // the tile kernel's results
     // every CTA of the cluster writes its share of the rows' values, four dims a thread
     const int share = blockIdx.z, quads = rows * (D / 4);
     for (int e = share * (DW * 32) + threadIdx.x; e < quads; e += cs * DW * 32) {
@@ -259,43 +264,57 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
             }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // no key: o = 0, lse = -inf
+        RowSum<4> R;
+        R.add(top, sum, {acc.x, acc.y, acc.z, acc.w});
+        if (shares) {   // the pieces of the row's prefix item, in order
+            const long long gr = (long long)b * rows + r, rt = gr / P.tile_rows, item = h * (long long)P.prefix_row_tiles + rt;
+            const long long U = (long long)A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, u0 = item * P.prefix_tiles;
+            const int c1 = unit_cta(u0 + P.prefix_tiles - 1, U, P.ctas);
+            for (int c = unit_cta(u0, U, P.ctas); c <= c1; ++c) {
+                const long long at = piece_slot(P, c, item, false) * P.tile_rows + (gr - rt * P.tile_rows);
+                const float2 ml = P.ml[at];
+                const float4 v = *reinterpret_cast<const float4*>(P.o + at * D + d);
+                R.add(ml.x, ml.y, {v.x, v.y, v.z, v.w});
+            }
+        }
+        const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;   // no key: o = 0, lse = -inf
         const long long tok = (long long)b * A.nq + r / A.group;
         const int qh = h * A.group + r % A.group;
         attn_store4<E>(A, tok * A.o_ts + (long long)qh * A.o_hs + d,
-                       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (A.lse && d == 0) A.lse[tok * A.heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
+                       make_float4(R.o[0] * inv, R.o[1] * inv, R.o[2] * inv, R.o[3] * inv));
+        if (A.lse && d == 0) A.lse[tok * A.heads + qh] = R.l == 0.0f ? -INFINITY : (R.m + log2f(R.l)) * LN2;
     }
     if (cs > 1) cluster_barrier();   // no CTA leaves while its part is read
 }
 
 template <class E, int D, int NB>
-cudaError_t rows_launch(const AttnArgs& A, int cs, cudaStream_t stream) {
+cudaError_t rows_launch(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t stream) {
     const dim3 grid((unsigned)(A.batch * A.kv_heads), 1, (unsigned)cs);
-    if (cs == 1) return launch_kernel(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), 0, stream, A);
-    return launch_kernel_cluster(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), 0, stream, (unsigned)cs, A);
+    if (cs == 1) return launch_kernel(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), 0, stream, A, P);
+    return launch_kernel_cluster(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), 0, stream, (unsigned)cs, A, P);
 }
 
 template <class E, int D>
-cudaError_t rows_nb(const AttnArgs& A, int cs, cudaStream_t stream) {
-    return A.nq * A.group <= 8 ? rows_launch<E, D, 1>(A, cs, stream) : rows_launch<E, D, 2>(A, cs, stream);
+cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t stream) {
+    return A.nq * A.group <= 8 ? rows_launch<E, D, 1>(A, P, cs, stream) : rows_launch<E, D, 2>(A, P, cs, stream);
 }
-
-}  // namespace
 
 // CTAs of a pair: while the pairs alone leave warps idle (12 fit an SM), and
 // every warp still gets two blocks of 16 keys.
-static int rows_cluster(const AttnArgs& A, int keys) {
+int rows_cluster(const AttnArgs& A, int keys) {
     const long long pairs = (long long)A.batch * A.kv_heads, room = 3LL * num_sms();
     int cs = 1;
     while (cs < 8 && pairs * cs * 2 <= room && keys > 2 * 16 * DW * cs) cs *= 2;
     return cs;
 }
 
-cudaError_t launch_attn_rows(const AttnArgs& A, int type, int d, cudaStream_t stream) {
-    const int cs = rows_cluster(A, A.cap);
-    if (type == PLM_F16) return d == 64 ? rows_nb<__half, 64>(A, cs, stream) : rows_nb<__half, 128>(A, cs, stream);
-    return d == 64 ? rows_nb<__nv_bfloat16, 64>(A, cs, stream) : rows_nb<__nv_bfloat16, 128>(A, cs, stream);
+}  // namespace
+
+cudaError_t launch_attn_rows(const AttnArgs& A, const TilePlan* plan, int type, int d, cudaStream_t stream) {
+    const TilePlan P = plan ? *plan : TilePlan{};
+    const int cs = rows_cluster(A, plan ? A.cap - A.prefix : A.cap);
+    if (type == PLM_F16) return d == 64 ? rows_nb<__half, 64>(A, P, cs, stream) : rows_nb<__half, 128>(A, P, cs, stream);
+    return d == 64 ? rows_nb<__nv_bfloat16, 64>(A, P, cs, stream) : rows_nb<__nv_bfloat16, 128>(A, P, cs, stream);
 }
 
 }  // namespace plm

@@ -1,0 +1,722 @@
+// Paged attention on the 5th-generation tensor cores (tcgen05): the shared
+// prefix for all rows of a batch at once, and prompts.
+//
+// Mathematics.  A row tile is 128 query rows of one key/value head (of any
+// sequences for the prefix; of one sequence otherwise).  Per unit of 128 keys
+//   S = Q K^T (f32, tensor memory), P = 2^(scale log2 e S - m), O += P V,
+// with a running reference m per row that is raised (O and l scaled) only
+// when a score exceeds it by more than 2^8.  The sum l is of the unrounded p.
+//
+// Roles.  NT row tiles share the K and V tiles of a CTA (NT = 2 when there are
+// that many rows: half the shared-memory traffic per product).  Per row tile a
+// warpgroup, one thread per row (= TMEM lane): reads S, writes P over it, and
+// at the end of a piece reads O.  One warp brings the pages' rows in by TMA (one
+// box per page and 64 dims; pages out of range read as zeros), one issues the
+// MMAs.  For NT = 2 the products of one tile run while the other tile's
+// softmax does; for NT = 1 two S buffers do the same.
+//   TMEM columns: S 0..255 (two buffers of 128), O 256.. (NT x D).
+//   V is the MN-major operand as it lies in the page ([key][dim]); P is the
+//   A operand in tensor memory.
+//
+// Work: equal shares of units per CTA (attn_tile.cuh), one CTA per SM.
+// Bound: the tensor cores from ~270 rows per head on, HBM below.  Every wait
+// is bounded; one that runs out records a fault and the kernel winds down.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "attn_tile.cuh"
+
+namespace plm {
+
+namespace {
+
+constexpr float RAISE = 8.0f, LOG2E = 1.4426950408889634f;
+constexpr uint32_t TM_S = 0, TM_O = 256;   // TMEM columns
+
+template <int D, int NT> struct TileSmem {
+    static constexpr int HALF = 128 * 128;               // 128 rows x 64 values, 128-byte swizzle
+    static constexpr int QTILE = (D / 64) * HALF, STAGE = (D / 64) * HALF;
+    static constexpr int SLOTS = D == 64 ? 10 : NT == 2 ? 5 : 6;
+    static constexpr int RING = NT * QTILE;
+    static constexpr int BAR = RING + SLOTS * STAGE;
+    // full, empty per slot; S ready, P ready, O done, Q ready per buffer
+    static constexpr int NBAR = 2 * SLOTS + 8;
+    static constexpr int TMEMP = BAR + 8 * NBAR;
+    static constexpr int ALLOC = TMEMP + 16 + 1024;
+    static_assert(ALLOC <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lead) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+template <class E> struct KindOf;
+template <> struct KindOf<__half> { static constexpr uint32_t AB = 0; };
+template <> struct KindOf<__nv_bfloat16> { static constexpr uint32_t AB = (1u << 7) | (1u << 10); };
+template <class E> __host__ __device__ constexpr uint32_t idesc(uint32_t n, bool b_mn) {
+    return (1u << 4) | KindOf<E>::AB | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define PLM_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define PLM_R16(r, i) PLM_R4(r, i), PLM_R4(r, i + 4), PLM_R4(r, i + 8), PLM_R4(r, i + 12)
+#define PLM_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+#define PLM_I16(r, i) PLM_I4(r, i), PLM_I4(r, i + 4), PLM_I4(r, i + 8), PLM_I4(r, i + 12)
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : PLM_R16(r, 0), PLM_R16(r, 16) : "r"(a));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 :: "r"(a), PLM_I16(r, 0), PLM_I16(r, 16) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int token, int head, int page,
+                                        uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A piece: consecutive units of one item.
+struct Piece {
+    bool prefix, begins, whole;
+    int b, rt, h;       // sequence (own), row tile, head
+    int key0, keys;     // first key of the piece; end of the keys to load (own: that its rows see)
+    int tiles;
+    int row;            // table row, or -1
+    long long item;
+    long long unit0;    // the item's first unit
+};
+
+// Walks the CTA's share of the units; every warp for itself, by all its lanes.
+struct Walk {
+    long long U, up, u, end;   // all units, the prefix job's, the next one, the end of the share
+    int prefix_row;            // table row that holds the prefix
+    int pair, T, h;            // own cursor: (sequence, row tile), its units per head, head
+    long long item_u0;         // first unit of the cursor's item
+
+    __device__ void start(const AttnArgs& A, const TilePlan& P, int lane) {
+        up = (long long)A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
+        const int pairs = P.own ? A.batch * P.own_row_tiles : 0;
+        long long sum = 0;
+        for (int p = lane; p < pairs; p += 32) sum += own_tiles(A, P, p);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        U = up + sum * A.kv_heads;
+        const int ctas = unit_ctas(P, U);
+        const bool mine = (int)blockIdx.x < ctas;
+        u = mine ? U * blockIdx.x / ctas : U;
+        end = mine ? U * (blockIdx.x + 1) / ctas : U;
+        pair = -1;
+        T = h = 0;
+        item_u0 = 0;
+        prefix_row = -1;
+        if (u < up)   // the first sequence that takes part
+            for (int b0 = 0; b0 < A.batch && prefix_row < 0; b0 += 32) {
+                const int b = b0 + lane, row = b < A.batch ? attn_row(A, b) : -1;
+                const unsigned hit = __ballot_sync(0xFFFFFFFFu, row >= 0 && attn_shares(A, P, attn_len(A, row)));
+                if (hit) prefix_row = __shfl_sync(0xFFFFFFFFu, row, __ffs(hit) - 1);
+            }
+    }
+
+    // The pair, head and item of own unit u.
+    __device__ void locate(const AttnArgs& A, const TilePlan& P, int lane) {
+        const int pairs = A.batch * P.own_row_tiles;
+        long long acc = up;
+        for (int p0 = 0; p0 < pairs; p0 += 32) {
+            const int p = p0 + lane;
+            const int n = p < pairs ? own_tiles(A, P, p) : 0;
+            long long x = (long long)n * A.kv_heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, acc + x > u);
+            if (hit) {
+                const int w = __ffs(hit) - 1;
+                pair = p0 + w;
+                T = __shfl_sync(0xFFFFFFFFu, n, w);
+                const long long first = acc + __shfl_sync(0xFFFFFFFFu, x, w) - (long long)T * A.kv_heads;
+                h = (int)((u - first) / T);
+                item_u0 = first + (long long)h * T;
+                return;
+            }
+            acc += __shfl_sync(0xFFFFFFFFu, x, 31);
+        }
+    }
+
+    __device__ bool next(const AttnArgs& A, const TilePlan& P, int lane, Piece& S) {
+        if (u >= end) return false;
+        if (u < up) {
+            S.item = u / P.prefix_tiles;
+            const int t0 = (int)(u - S.item * P.prefix_tiles);
+            S.prefix = true;
+            S.b = 0;
+            S.h = (int)(S.item / P.prefix_row_tiles);
+            S.rt = (int)(S.item - (long long)S.h * P.prefix_row_tiles);
+            S.tiles = (int)min((long long)(P.prefix_tiles - t0), end - u);
+            S.unit0 = u - t0;
+            S.begins = t0 == 0;
+            S.whole = S.begins && S.tiles == P.prefix_tiles;
+            S.key0 = t0 * TK;
+            S.keys = A.prefix;
+            S.row = prefix_row;
+        } else {
+            if (pair < 0) locate(A, P, lane);
+            else if (u == item_u0 + T) {   // the next item
+                item_u0 = u;
+                if (++h == A.kv_heads) {
+                    h = 0;
+                    do { T = own_tiles(A, P, ++pair); } while (T == 0);   // u < end <= U: there is one
+                }
+            }
+            const int t0 = (int)(u - item_u0);
+            S.prefix = false;
+            S.b = pair / P.own_row_tiles;
+            S.rt = pair - S.b * P.own_row_tiles;
+            S.h = h;
+            S.row = attn_row(A, S.b);
+            const int len = attn_len(A, S.row);
+            S.tiles = (int)min((long long)(T - t0), end - u);
+            S.unit0 = item_u0;
+            S.begins = t0 == 0;
+            S.whole = S.begins && S.tiles == T;
+            S.key0 = own_begin(A, P, len) + t0 * TK;
+            S.keys = own_end(A, P, len, S.rt);
+            S.item = (long long)A.kv_heads * (P.prefix_row_tiles + pair) + h;
+        }
+        u += S.tiles;
+        return true;
+    }
+};
+
+// Row i of a piece's row tile: the token (row of q) and query head, or false.
+__device__ __forceinline__ bool tile_row(const AttnArgs& A, const TilePlan& P, const Piece& S, int i, long long& tok,
+                                         int& qh) {
+    const long long r = (long long)S.rt * P.tile_rows + i;
+    const long long all = (long long)A.nq * A.group * (S.prefix ? A.batch : 1);
+    if (r >= all) return false;
+    const long long t = r / A.group;
+    tok = (S.prefix ? 0 : (long long)S.b * A.nq) + t;
+    qh = S.h * A.group + (int)(r - t * A.group);
+    return true;
+}
+
+// A bounded wait of a whole warp: all its lanes go on or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+
+template <class E, int D, int NT>
+__global__ void __launch_bounds__(NT * 128 + 64, 1)
+attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, unsigned* fault) {
+    using L = TileSmem<D, NT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR);
+    uint64_t* empty = full + L::SLOTS;
+    uint64_t* s_ready = empty + L::SLOTS;   // [2] per S buffer
+    uint64_t* p_ready = s_ready + 2;        // [2] per S buffer, one arrival per warp
+    uint64_t* o_done = p_ready + 2;         // [2] per row tile: a PV product has finished
+    uint64_t* q_ready = o_done + 2;         // [2] per row tile
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::TMEMP);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int TMA_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * L::SLOTS; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_ready[i], 1);
+            mbar_init(&p_ready[i], 4);
+            mbar_init(&o_done[i], 1);
+            mbar_init(&q_ready[i], 4);
+        }
+        fence_barrier_init();
+    }
+    if (warp == MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    // the kernels before this one have finished; only then may the next one
+    // start, which reads what they wrote before it waits for this one
+    grid_wait_prior();
+    grid_launch_dependents();
+    bool ok = true;
+    Walk W;
+    W.start(A, P, lane);
+    Piece S;
+
+    if (warp == TMA_WARP) {
+        // ---------------------------------------------------- pages -> K, V
+        const int bt = min(1 << A.page_shift, TK), per = TK / bt;   // tokens per box, boxes per 64 dims
+        int n = 0;                                                  // tiles loaded: slot n % SLOTS
+        const int part = lane / per, box = lane - part * per;
+        const bool active = part < D / 64;
+        while (ok && W.next(A, P, lane, S)) {
+            const int* tab = A.table + (long long)max(S.row, 0) * A.table_stride;
+            if (!S.prefix && S.begins && lane == 0) P.item_unit[S.item - (long long)A.kv_heads * P.prefix_row_tiles] = S.unit0;
+            for (int i = 0; ok && i < S.tiles; ++i) {
+                const int j = S.key0 + i * TK + box * bt;
+                int page = A.pages;   // out of range: the box is filled with zeros
+                if (active && S.row >= 0 && j < S.keys) {
+                    const int p = __ldg(tab + (j >> A.page_shift));
+                    if (p >= 0 && p < A.pages) page = p;
+                }
+                const int token = j & ((1 << A.page_shift) - 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int slot = n % L::SLOTS;
+                    if (n >= L::SLOTS) ok = warp_wait(&empty[slot], (n / L::SLOTS - 1) & 1);
+                    if (!ok) break;
+                    uint8_t* dst = sm + L::RING + slot * L::STAGE;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], L::STAGE);
+                    __syncwarp();
+                    if (active)
+                        tma_box(dst + part * L::HALF + box * bt * 128, kv ? &vmap : &kmap, 64 * part, token, S.h, page,
+                                &full[slot]);
+                }
+            }
+        }
+        if (!ok)   // wind down: this CTA's copies have to land before it ends
+            for (int i = max(0, n - L::SLOTS); i < n; ++i) mbar_wait(&full[i % L::SLOTS], (i / L::SLOTS) & 1);
+        if (blockIdx.x == 0 && lane == 0) *P.units = W.U;
+    } else if (warp == MMA_WARP) {
+        // ------------------------------------------------------- the products
+        constexpr uint32_t ID_S = idesc<E>(128, false), ID_O = idesc<E>(D, true);
+        const uint32_t ring = smem_u32(sm + L::RING), qs = smem_u32(sm);
+        int n = 0;            // tiles taken from the ring
+        int step = 0;         // units so far (all pieces)
+        int pieces = 0;
+        // S of row tile t (buffer sb) from the K tile in slot
+        auto product_s = [&](int t, int sb, int slot) {
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * L::HALF + (k & 3) * 32;
+                    mma_ss(tmem + TM_S + 128 * sb, desc_sw128(qs + t * L::QTILE + off, 16),
+                           desc_sw128(ring + slot * L::STAGE + off, 16), ID_S, k > 0);
+                }
+                commit(&s_ready[sb]);
+            }
+            __syncwarp();
+        };
+        auto product_o = [&](int t, int sb, int slot, bool first) {
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < TK / 16; ++k)
+                    mma_ts(tmem + TM_O + D * t, tmem + TM_S + 128 * sb + 8 * k,
+                           desc_sw128(ring + slot * L::STAGE + k * 2048, L::HALF), ID_O, !(first && k == 0));
+                commit(&o_done[t]);
+            }
+            __syncwarp();
+        };
+        auto free_slot = [&](int slot) {
+            if (lane == 0) commit(&empty[slot]);
+            __syncwarp();
+        };
+        while (ok && W.next(A, P, lane, S)) {
+            // unit i of the piece: K is ring tile n0 + 2 i, V the next one
+            const int n0 = n;
+            n += 2 * S.tiles;
+            auto wait_full = [&](int at) { return warp_wait(&full[at % L::SLOTS], (at / L::SLOTS) & 1); };
+            for (int t = 0; ok && t < NT; ++t) ok = warp_wait(&q_ready[t], pieces & 1);
+            if (ok) ok = wait_full(n0);
+            if (!ok) break;
+            tc_after();
+            for (int t = 0; t < NT; ++t) product_s(t, NT == 2 ? t : step & 1, n0 % L::SLOTS);
+            free_slot(n0 % L::SLOTS);
+            for (int i = 0; ok && i < S.tiles; ++i, ++step) {
+                const int vt = n0 + 2 * i + 1, kt = vt + 1;
+                const bool more = i + 1 < S.tiles;
+                if (NT == 1 && more) {   // the next S into the other buffer, before waiting for P
+                    ok = wait_full(kt);
+                    if (!ok) break;
+                    tc_after();
+                    product_s(0, (step + 1) & 1, kt % L::SLOTS);
+                    free_slot(kt % L::SLOTS);
+                }
+                ok = wait_full(vt);
+                if (!ok) break;
+                const int left = S.keys - (S.key0 + i * TK);
+                if (!S.prefix && left < TK) {
+                    // the pages' rows past the end may hold anything, and 0 * NaN is NaN
+                    uint8_t* v = sm + L::RING + (vt % L::SLOTS) * L::STAGE;
+                    for (int e = lane; e < (TK - left) * (D / 8); e += 32) {
+                        const int r = left + e / (D / 8), c = e % (D / 8);
+                        *reinterpret_cast<uint4*>(v + (c >> 3) * L::HALF + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int sb = NT == 2 ? t : step & 1;
+                    ok = warp_wait(&p_ready[sb], NT == 2 ? step & 1 : (step >> 1) & 1);
+                    if (!ok) break;
+                    tc_after();
+                    product_o(t, sb, vt % L::SLOTS, i == 0);
+                    if (t == NT - 1) free_slot(vt % L::SLOTS);
+                    if (NT == 2 && more) {
+                        if (t == 0) {
+                            ok = wait_full(kt);
+                            if (!ok) break;
+                            tc_after();
+                        }
+                        product_s(t, t, kt % L::SLOTS);
+                        if (t == NT - 1) free_slot(kt % L::SLOTS);
+                    }
+                }
+            }
+            ++pieces;
+        }
+    } else {
+        // ------------------------------------- the softmax, a row per thread
+        const int t = warp >> 2, i = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const float sl2 = fabsf(A.scale) * LOG2E, raise_at = RAISE / sl2;
+        int step = 0;   // units so far
+        long long tok;
+        int qh;
+        // Q row i into the operand tile; a negative scale turns its signs
+        auto load_q = [&](const Piece& C) {
+            uint8_t* dst = sm + t * L::QTILE + i * 128;
+            const bool in = tile_row(A, P, C, t * 128 + i, tok, qh);
+            const uint32_t sign = A.scale < 0.0f ? 0x80008000u : 0u;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + (in ? tok * A.q_ts + (long long)qh * A.q_hs : 0));
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * L::HALF + (((c ^ i) & 7) << 4)) = v;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[t]);
+        };
+        bool have = W.next(A, P, lane, S);
+        if (have) load_q(S);
+        while (have && ok) {
+            const bool in = tile_row(A, P, S, t * 128 + i, tok, qh);
+            int seen = S.keys;   // keys that the row sees
+            if (!S.prefix && in) seen = attn_seen(A, attn_len(A, S.row), (int)(tok - (long long)S.b * A.nq));
+            float m = -INFINITY, l = 0.0f;   // m in units of S
+            for (int u = 0; ok && u < S.tiles; ++u, ++step) {
+                const int sb = NT == 2 ? t : step & 1;
+                const uint32_t sa = tmem + lanes + TM_S + 128 * sb;
+                ok = warp_wait(&s_ready[sb], NT == 2 ? step & 1 : (step >> 1) & 1);
+                if (!ok) break;
+                tc_after();
+                float s[128];
+                uint32_t* sr = reinterpret_cast<uint32_t*>(s);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(sa + 32 * c, sr + 32 * c);
+                tmem_ld_wait();
+                const int left = seen - (S.key0 + u * TK);
+                if (__any_sync(0xFFFFFFFFu, left < TK)) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= left) s[c] = -INFINITY;
+                }
+                float mx = fmaxf(s[0], s[1]), my = fmaxf(s[2], s[3]);
+#pragma unroll
+                for (int c = 4; c < 128; c += 4) {
+                    mx = max3(mx, s[c], s[c + 1]);
+                    my = max3(my, s[c + 2], s[c + 3]);
+                }
+                mx = fmaxf(mx, my);
+                const bool raise = mx > m + raise_at || m == -INFINITY;
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+                    const float mn = raise ? fmaxf(m, mx) : m;
+                    const float keep = mn == m ? 1.0f : ex2((m - mn) * sl2);
+                    if (u > 0) {   // O holds the products of the units before
+                        // the (step)-th PV product of this row tile is the last one issued
+                        ok = warp_wait(&o_done[t], (step - 1) & 1);
+                        if (!ok) break;
+                        tc_after();
+                        const uint32_t oa = tmem + lanes + TM_O + D * t;
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t r[32];
+                            tmem_ld32(oa + c, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * keep);
+                            tmem_st32(oa + c, r);
+                        }
+                    }
+                    l *= keep;
+                    m = mn;
+                }
+                const float base = m == -INFINITY ? 0.0f : -m * sl2;
+                uint32_t pk[64];
+                float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 128; c += 2) {
+                    const float p0 = ex2(fmaf(s[c], sl2, base)), p1 = ex2(fmaf(s[c + 1], sl2, base));
+                    l0 += p0;
+                    l1 += p1;
+                    pk[c / 2] = pack_pair<E>(p0, p1);
+                }
+                l += l0 + l1;
+                tmem_st32(sa, pk);
+                tmem_st32(sa + 32, pk + 32);
+                tmem_st_wait();
+                // a wait tells two phases apart, no more: with two S buffers the
+                // product before the last one may still be running here
+                if (NT == 1 && step > 0) ok = warp_wait(&o_done[t], (step - 1) & 1);
+                if (!ok) break;
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[sb]);
+            }
+            if (!ok) break;
+            // the next piece's Q, while the last product runs: S of this piece is done with it
+            const Piece C = S;
+            const long long my_tok = tok;
+            const int my_qh = qh;
+            have = W.next(A, P, lane, S);
+            if (have) load_q(S);
+            ok = warp_wait(&o_done[t], (step - 1) & 1);
+            if (!ok) break;
+            tc_after();
+            const uint32_t oa = tmem + lanes + TM_O + D * t;
+            const float m2 = m * sl2;
+            const bool final = C.whole && P.prefix_tiles == 0;
+            if (final) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const long long off = in ? my_tok * A.o_ts + (long long)my_qh * A.o_hs : 0;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(oa + c, r);
+                    tmem_ld_wait();
+                    if (in)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            attn_store4<E>(A, off + c + k, make_float4(__uint_as_float(r[k]) * inv, __uint_as_float(r[k + 1]) * inv,
+                                                                       __uint_as_float(r[k + 2]) * inv, __uint_as_float(r[k + 3]) * inv));
+                }
+                if (in && A.lse)
+                    A.lse[my_tok * A.heads + my_qh] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
+            } else {
+                const long long slot = piece_slot(P, blockIdx.x, C.item, C.begins);
+                const long long row = slot * P.tile_rows + t * 128 + i;
+                float4* o = reinterpret_cast<float4*>(P.o + row * D);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(oa + c, r);
+                    tmem_ld_wait();
+                    if (in)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            o[(c + k) / 4] = make_float4(__uint_as_float(r[k]), __uint_as_float(r[k + 1]),
+                                                         __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                }
+                if (in) P.ml[row] = make_float2(m2, l);
+            }
+            // O has been read: the next piece's first product (after its P) may overwrite it
+            tc_before();
+        }
+    }
+    if (!ok && lane == 0) atomicOr(fault, 4u);
+    tc_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    }
+}
+
+// Adds the pieces of every row (own jobs in the tile kernel): a warp per row
+// and query head.
+template <class E, int D>
+__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
+    grid_launch_dependents();
+    grid_wait_prior();
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long U = *P.units;
+    const long long all = (long long)A.batch * A.nq * A.heads;
+    for (long long e = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5; e < all; e += (long long)gridDim.x * 8) {
+        const long long tok = e / A.heads;
+        const int qh = (int)(e - tok * A.heads), h = qh / A.group, g = qh - h * A.group;
+        const int b = (int)(tok / A.nq), t = (int)(tok - (long long)b * A.nq);
+        const int len = attn_len(A, attn_row(A, b));
+        RowSum<PER> R;
+        auto add = [&](long long item, long long u0, int tiles, long long row) {
+            const int ctas = unit_ctas(P, U), c1 = unit_cta(u0 + tiles - 1, U, ctas);
+            int c = unit_cta(u0, U, ctas);
+            if (P.prefix_tiles == 0 && c == c1) return false;   // a whole item: already written
+            for (bool begins = true; c <= c1; ++c, begins = false) {
+                const long long at = piece_slot(P, c, item, begins) * P.tile_rows + row;
+                const float2 ml = P.ml[at];
+                float o[PER];
+                const float* src = P.o + at * D + PER * lane;
+                if constexpr (PER == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    o[0] = v.x; o[1] = v.y;
+                }
+                R.add(ml.x, ml.y, o);
+            }
+            return true;
+        };
+        if (attn_shares(A, P, len)) {
+            const long long r = tok * A.group + g, rt = r / P.tile_rows;
+            const long long item = (long long)h * P.prefix_row_tiles + rt;
+            add(item, item * P.prefix_tiles, P.prefix_tiles, r - rt * P.tile_rows);
+        }
+        const long long r = (long long)t * A.group + g;
+        const int rt = (int)(r / P.tile_rows), pair = b * P.own_row_tiles + rt;
+        const int tiles = own_tiles(A, P, pair);
+        if (tiles > 0) {
+            const long long at = (long long)pair * A.kv_heads + h;
+            if (!add((long long)A.kv_heads * P.prefix_row_tiles + at, P.item_unit[at], tiles, r - (long long)rt * P.tile_rows)) continue;
+        }
+        const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
+        const long long off = tok * A.o_ts + (long long)qh * A.o_hs + PER * lane;
+        if constexpr (PER == 4) {
+            attn_store4<E>(A, off, make_float4(R.o[0] * inv, R.o[1] * inv, R.o[2] * inv, R.o[3] * inv));
+        } else if (A.o_f32) {
+            *reinterpret_cast<float2*>(static_cast<float*>(A.o) + off) = make_float2(R.o[0] * inv, R.o[1] * inv);
+        } else {
+            *reinterpret_cast<uint32_t*>(static_cast<E*>(A.o) + off) = pack_pair<E>(R.o[0] * inv, R.o[1] * inv);
+        }
+        if (A.lse && lane == 0)
+            A.lse[tok * A.heads + qh] = R.l == 0.0f ? -INFINITY : (R.m + log2f(R.l)) * 0.6931471805599453f;
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                               cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// Pages as a tensor (dim, token, head, page); a box is 64 dims of the tokens
+// of one page, at most 128.
+bool page_map(CUtensorMap* map, const AttnArgs& A, const void* base, int type, int d) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t tokens = 1ull << A.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, tokens, (cuuint64_t)A.kv_heads, (cuuint64_t)A.pages};
+    // an axis of length one may come with any stride
+    const cuuint64_t strides[3] = {(cuuint64_t)A.kv_ts * 2, (cuuint64_t)(A.kv_heads > 1 ? A.kv_hs : A.kv_ts) * 2,
+                                   (cuuint64_t)(A.pages > 1 ? A.page_stride : A.kv_ts) * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(tokens < TK ? tokens : TK), 1, 1}, one[4] = {1, 1, 1, 1};
+    return enc(map, type == PLM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class E, int D, int NT>
+cudaError_t tile_launch(const AttnArgs& A, const TilePlan& P, const CUtensorMap& km, const CUtensorMap& vm,
+                        cudaStream_t stream) {
+    unsigned* fault = fault_word();
+    if (!fault) return cudaErrorInvalidDevicePointer;
+    constexpr int bytes = TileSmem<D, NT>::ALLOC;
+    cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<E, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(attn_tile_kernel<E, D, NT>, dim3((unsigned)P.ctas), dim3(NT * 128 + 64), bytes, stream, A, P, km, vm, fault);
+    if (e != cudaSuccess || !P.own) return e;
+    const long long rows = (long long)A.batch * A.nq * A.heads, cap = 8LL * num_sms();
+    const long long ctas = (rows + 7) / 8 < cap ? (rows + 7) / 8 : cap;
+    return launch_kernel(attn_merge_kernel<E, D>, dim3((unsigned)ctas), dim3(256), 0, stream, A, P);
+}
+
+template <class E>
+cudaError_t tile_type(const AttnArgs& A, const TilePlan& P, const CUtensorMap& km, const CUtensorMap& vm, int d, cudaStream_t stream) {
+    if (d == 64)
+        return P.tile_rows == 256 ? tile_launch<E, 64, 2>(A, P, km, vm, stream) : tile_launch<E, 64, 1>(A, P, km, vm, stream);
+    return P.tile_rows == 256 ? tile_launch<E, 128, 2>(A, P, km, vm, stream) : tile_launch<E, 128, 1>(A, P, km, vm, stream);
+}
+
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t tile_plan(const AttnArgs& A, int d, bool share, bool own, void* ws, TilePlan* P) {
+    const long long mine = (long long)A.nq * A.group, all = mine * A.batch;
+    TilePlan T = {};
+    T.tile_rows = (share ? all : mine) > 128 ? 256 : 128;
+    T.prefix_tiles = share ? (A.prefix + TK - 1) / TK : 0;
+    T.prefix_row_tiles = share ? (int)((all + T.tile_rows - 1) / T.tile_rows) : 0;
+    T.own = own;
+    T.own_row_tiles = own ? (int)((mine + T.tile_rows - 1) / T.tile_rows) : 0;
+    const long long prefix_items = (long long)A.kv_heads * T.prefix_row_tiles;
+    const long long own_items = own ? (long long)A.batch * T.own_row_tiles * A.kv_heads : 0;
+    const long long most = prefix_items * T.prefix_tiles + own_items * ((A.cap + TK - 1) / TK);
+    const int sms = num_sms();
+    T.ctas = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
+    const size_t slots = share ? (size_t)(T.ctas + prefix_items + own_items) : 2 * (size_t)T.ctas;
+    const size_t units_b = 256, item_b = up256(8 * (size_t)own_items), ml_b = up256(slots * T.tile_rows * sizeof(float2));
+    if (P) {
+        uint8_t* p = static_cast<uint8_t*>(ws);
+        T.units = reinterpret_cast<long long*>(p);
+        T.item_unit = reinterpret_cast<long long*>(p + units_b);
+        T.ml = reinterpret_cast<float2*>(p + units_b + item_b);
+        T.o = reinterpret_cast<float*>(p + units_b + item_b + ml_b);
+        *P = T;
+    }
+    return units_b + item_b + ml_b + up256(slots * T.tile_rows * (size_t)d * sizeof(float));
+}
+
+cudaError_t launch_attn_tile(const AttnArgs& A, const TilePlan& P, int type, int d, cudaStream_t stream) {
+    CUtensorMap km, vm;
+    if (!page_map(&km, A, A.k, type, d) || !page_map(&vm, A, A.v, type, d)) return cudaErrorInvalidValue;
+    return type == PLM_F16 ? tile_type<__half>(A, P, km, vm, d, stream) : tile_type<__nv_bfloat16>(A, P, km, vm, d, stream);
+}
+
+}  // namespace plm
