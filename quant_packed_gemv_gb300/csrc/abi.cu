@@ -664,7 +664,8 @@ size_t plm_attn_workspace_size(int64_t batch, int64_t tokens, int64_t heads, int
         !in_range(max_len, 1, kMaxIndex) || !in_range(prefix_len, 0, max_len))
         return 0;
     if (batch * tokens > kMaxIndex / heads) return 0;
-    return plm::attn_workspace_bytes(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len);
+    const size_t need = plm::attn_workspace_bytes(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len);
+    return need == SIZE_MAX ? 0 : need;
 }
 
 plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, size_t workspace_bytes,
@@ -685,8 +686,9 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
         (p->page_tokens & (p->page_tokens - 1)))
         return PLM_ERR_UNSUPPORTED;
     if (p->batch == 0) return PLM_OK;
-    const size_t need = plm_attn_workspace_size(p->batch, p->tokens, p->heads, p->kv_heads, p->head_dim,
-                                                p->prefix_len, p->max_len);
+    const size_t need = plm::attn_workspace_bytes(p->batch, p->tokens, p->heads, p->kv_heads, p->head_dim,
+                                                  p->prefix_len, p->max_len);
+    if (need == SIZE_MAX) return PLM_ERR_UNSUPPORTED;
     if (need && (!workspace || workspace_bytes < need)) return PLM_ERR_INVALID_ARG;
     const int64_t oe = p->o_type == PLM_F32 ? 4 : 8;   // elements of 16 bytes
     if (!aligned(p->q, 16) || !aligned(p->o, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->lse, 4) ||

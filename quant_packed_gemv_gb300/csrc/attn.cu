@@ -61,6 +61,7 @@ size_t attn_workspace_bytes(long long batch, long long tokens, long long heads, 
     A.prefix = (int)prefix_len;
     A.cap = (int)max_len;
     const Choice c = choose(A);
+    if (c.tile && tile_units(A, c.share, !c.rows) > 0x7FFFFFFFLL) return SIZE_MAX;
     return c.tile ? tile_plan(A, (int)head_dim, c.share, !c.rows, nullptr, nullptr) : 0;
 }
 

@@ -267,8 +267,9 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
         RowSum<4> R;
         R.add(top, sum, {acc.x, acc.y, acc.z, acc.w});
         if (shares) {   // the pieces of the row's prefix item, in order
-            const long long gr = (long long)b * rows + r, rt = gr / P.tile_rows, item = h * (long long)P.prefix_row_tiles + rt;
-            const long long U = (long long)A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, u0 = item * P.prefix_tiles;
+            const long long gr = (long long)b * rows + r, rt = gr / P.tile_rows;
+            const int item = h * P.prefix_row_tiles + (int)rt, u0 = item * P.prefix_tiles;
+            const int U = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
             const int c1 = unit_cta(u0 + P.prefix_tiles - 1, U, P.ctas);
             for (int c = unit_cta(u0, U, P.ctas); c <= c1; ++c) {
                 const long long at = piece_slot(P, c, item, false) * P.tile_rows + (gr - rt * P.tile_rows);

@@ -104,6 +104,25 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two f32 in one 64-bit register.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -117,29 +136,30 @@ struct Piece {
     int key0, keys;     // first key of the piece; end of the keys to load (own: that its rows see)
     int tiles;
     int row;            // table row, or -1
-    long long item;
-    long long unit0;    // the item's first unit
+    int item;
+    int unit0;          // the item's first unit
 };
 
 // Walks the CTA's share of the units; every warp for itself, by all its lanes.
 struct Walk {
-    long long U, up, u, end;   // all units, the prefix job's, the next one, the end of the share
-    int prefix_row;            // table row that holds the prefix
-    int pair, T, h;            // own cursor: (sequence, row tile), its units per head, head
-    long long item_u0;         // first unit of the cursor's item
+    int up, u, end;    // the prefix job's units, the next unit, the end of the share
+    int prefix_row;    // table row that holds the prefix
+    int pair, T, h;    // own cursor: (sequence, row tile), its units per head, head
+    int item_u0;       // first unit of the cursor's item
 
-    __device__ void start(const AttnArgs& A, const TilePlan& P, int lane) {
-        up = (long long)A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
+    // Returns the number of all units.
+    __device__ int start(const AttnArgs& A, const TilePlan& P, int lane) {
+        up = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
         const int pairs = P.own ? A.batch * P.own_row_tiles : 0;
-        long long sum = 0;
+        int sum = 0;
         for (int p = lane; p < pairs; p += 32) sum += own_tiles(A, P, p);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        U = up + sum * A.kv_heads;
+        const int U = up + sum * A.kv_heads;
         const int ctas = unit_ctas(P, U);
         const bool mine = (int)blockIdx.x < ctas;
-        u = mine ? U * blockIdx.x / ctas : U;
-        end = mine ? U * (blockIdx.x + 1) / ctas : U;
+        u = mine ? (int)((long long)U * blockIdx.x / ctas) : U;
+        end = mine ? (int)((long long)U * (blockIdx.x + 1) / ctas) : U;
         pair = -1;
         T = h = 0;
         item_u0 = 0;
@@ -150,19 +170,20 @@ struct Walk {
                 const unsigned hit = __ballot_sync(0xFFFFFFFFu, row >= 0 && attn_shares(A, P, attn_len(A, row)));
                 if (hit) prefix_row = __shfl_sync(0xFFFFFFFFu, row, __ffs(hit) - 1);
             }
+        return U;
     }
 
     // The pair, head and item of own unit u.
     __device__ void locate(const AttnArgs& A, const TilePlan& P, int lane) {
         const int pairs = A.batch * P.own_row_tiles;
-        long long acc = up;
+        int acc = up;
         for (int p0 = 0; p0 < pairs; p0 += 32) {
             const int p = p0 + lane;
             const int n = p < pairs ? own_tiles(A, P, p) : 0;
-            long long x = (long long)n * A.kv_heads;
+            int x = n * A.kv_heads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
                 if (lane >= o) x += y;
             }
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, acc + x > u);
@@ -170,9 +191,9 @@ struct Walk {
                 const int w = __ffs(hit) - 1;
                 pair = p0 + w;
                 T = __shfl_sync(0xFFFFFFFFu, n, w);
-                const long long first = acc + __shfl_sync(0xFFFFFFFFu, x, w) - (long long)T * A.kv_heads;
-                h = (int)((u - first) / T);
-                item_u0 = first + (long long)h * T;
+                const int first = acc + __shfl_sync(0xFFFFFFFFu, x, w) - T * A.kv_heads;
+                h = (u - first) / T;
+                item_u0 = first + h * T;
                 return;
             }
             acc += __shfl_sync(0xFFFFFFFFu, x, 31);
@@ -183,12 +204,12 @@ struct Walk {
         if (u >= end) return false;
         if (u < up) {
             S.item = u / P.prefix_tiles;
-            const int t0 = (int)(u - S.item * P.prefix_tiles);
+            const int t0 = u - S.item * P.prefix_tiles;
             S.prefix = true;
             S.b = 0;
-            S.h = (int)(S.item / P.prefix_row_tiles);
-            S.rt = (int)(S.item - (long long)S.h * P.prefix_row_tiles);
-            S.tiles = (int)min((long long)(P.prefix_tiles - t0), end - u);
+            S.h = S.item / P.prefix_row_tiles;
+            S.rt = S.item - S.h * P.prefix_row_tiles;
+            S.tiles = min(P.prefix_tiles - t0, end - u);
             S.unit0 = u - t0;
             S.begins = t0 == 0;
             S.whole = S.begins && S.tiles == P.prefix_tiles;
@@ -204,20 +225,20 @@ struct Walk {
                     do { T = own_tiles(A, P, ++pair); } while (T == 0);   // u < end <= U: there is one
                 }
             }
-            const int t0 = (int)(u - item_u0);
+            const int t0 = u - item_u0;
             S.prefix = false;
             S.b = pair / P.own_row_tiles;
             S.rt = pair - S.b * P.own_row_tiles;
             S.h = h;
             S.row = attn_row(A, S.b);
             const int len = attn_len(A, S.row);
-            S.tiles = (int)min((long long)(T - t0), end - u);
+            S.tiles = min(T - t0, end - u);
             S.unit0 = item_u0;
             S.begins = t0 == 0;
             S.whole = S.begins && S.tiles == T;
             S.key0 = own_begin(A, P, len) + t0 * TK;
             S.keys = own_end(A, P, len, S.rt);
-            S.item = (long long)A.kv_heads * (P.prefix_row_tiles + pair) + h;
+            S.item = A.kv_heads * (P.prefix_row_tiles + pair) + h;
         }
         u += S.tiles;
         return true;
@@ -282,10 +303,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
     grid_launch_dependents();
     bool ok = true;
     Walk W;
-    W.start(A, P, lane);
     Piece S;
-
     if (warp == TMA_WARP) {
+        const int U = W.start(A, P, lane);
         // ---------------------------------------------------- pages -> K, V
         const int bt = min(1 << A.page_shift, TK), per = TK / bt;   // tokens per box, boxes per 64 dims
         int n = 0;                                                  // tiles loaded: slot n % SLOTS
@@ -293,7 +313,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         const bool active = part < D / 64;
         while (ok && W.next(A, P, lane, S)) {
             const int* tab = A.table + (long long)max(S.row, 0) * A.table_stride;
-            if (!S.prefix && S.begins && lane == 0) P.item_unit[S.item - (long long)A.kv_heads * P.prefix_row_tiles] = S.unit0;
+            if (!S.prefix && S.begins && lane == 0) P.item_unit[S.item - A.kv_heads * P.prefix_row_tiles] = S.unit0;
             for (int i = 0; ok && i < S.tiles; ++i) {
                 const int j = S.key0 + i * TK + box * bt;
                 int page = A.pages;   // out of range: the box is filled with zeros
@@ -318,8 +338,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         }
         if (!ok)   // wind down: this CTA's copies have to land before it ends
             for (int i = max(0, n - L::SLOTS); i < n; ++i) mbar_wait(&full[i % L::SLOTS], (i / L::SLOTS) & 1);
-        if (blockIdx.x == 0 && lane == 0) *P.units = W.U;
+        if (blockIdx.x == 0 && lane == 0) *P.units = U;
     } else if (warp == MMA_WARP) {
+        W.start(A, P, lane);
         // ------------------------------------------------------- the products
         constexpr uint32_t ID_S = idesc<E>(128, false), ID_O = idesc<E>(D, true);
         const uint32_t ring = smem_u32(sm + L::RING), qs = smem_u32(sm);
@@ -409,6 +430,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             ++pieces;
         }
     } else {
+        W.start(A, P, lane);
         // ------------------------------------- the softmax, a row per thread
         const int t = warp >> 2, i = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -445,23 +467,33 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 ok = warp_wait(&s_ready[sb], NT == 2 ? step & 1 : (step >> 1) & 1);
                 if (!ok) break;
                 tc_after();
-                float s[128];
-                uint32_t* sr = reinterpret_cast<uint32_t*>(s);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(sa + 32 * c, sr + 32 * c);
-                tmem_ld_wait();
                 const int left = seen - (S.key0 + u * TK);
-                if (__any_sync(0xFFFFFFFFu, left < TK)) {
+                const bool part = __any_sync(0xFFFFFFFFu, left < TK);
+                // the row's S in halves of 64: the second is read twice, which
+                // saves 64 registers
+                float s[64];
+                auto load_half = [&](int c0) {
+                    uint32_t* r = reinterpret_cast<uint32_t*>(s);
+                    tmem_ld32(sa + c0, r);
+                    tmem_ld32(sa + c0 + 32, r + 32);
+                    tmem_ld_wait();
+                    if (part)
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= left) s[c] = -INFINITY;
-                }
-                float mx = fmaxf(s[0], s[1]), my = fmaxf(s[2], s[3]);
+                        for (int c = 0; c < 64; ++c)
+                            if (c0 + c >= left) s[c] = -INFINITY;
+                };
+                float mx = -INFINITY, my = -INFINITY;
+                auto half_max = [&] {
 #pragma unroll
-                for (int c = 4; c < 128; c += 4) {
-                    mx = max3(mx, s[c], s[c + 1]);
-                    my = max3(my, s[c + 2], s[c + 3]);
-                }
+                    for (int c = 0; c < 64; c += 4) {
+                        mx = max3(mx, s[c], s[c + 1]);
+                        my = max3(my, s[c + 2], s[c + 3]);
+                    }
+                };
+                load_half(64);
+                half_max();
+                load_half(0);
+                half_max();
                 mx = fmaxf(mx, my);
                 const bool raise = mx > m + raise_at || m == -INFINITY;
                 if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -487,18 +519,28 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                     m = mn;
                 }
                 const float base = m == -INFINITY ? 0.0f : -m * sl2;
-                uint32_t pk[64];
-                float l0 = 0.0f, l1 = 0.0f;
+                const uint64_t sl22 = f2(sl2, sl2), base2 = f2(base, base);
+                uint64_t la = f2(0.0f, 0.0f), lb = la;
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) {
-                    const float p0 = ex2(fmaf(s[c], sl2, base)), p1 = ex2(fmaf(s[c + 1], sl2, base));
-                    l0 += p0;
-                    l1 += p1;
-                    pk[c / 2] = pack_pair<E>(p0, p1);
+                for (int c = 0; c < 128; c += 64) {   // P of a half lies where S has been read
+                    if (c) load_half(c);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 64; k += 4) {
+                        float p0, p1, p2, p3;
+                        f2_split(f2_fma(f2(s[k], s[k + 1]), sl22, base2), p0, p1);
+                        f2_split(f2_fma(f2(s[k + 2], s[k + 3]), sl22, base2), p2, p3);
+                        p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
+                        la = f2_add(la, f2(p0, p1));
+                        lb = f2_add(lb, f2(p2, p3));
+                        pk[k / 2] = pack_pair<E>(p0, p1);
+                        pk[k / 2 + 1] = pack_pair<E>(p2, p3);
+                    }
+                    tmem_st32(sa + c / 2, pk);
                 }
+                float l0, l1;
+                f2_split(f2_add(la, lb), l0, l1);
                 l += l0 + l1;
-                tmem_st32(sa, pk);
-                tmem_st32(sa + 32, pk + 32);
                 tmem_st_wait();
                 // a wait tells two phases apart, no more: with two S buffers the
                 // product before the last one may still be running here
@@ -575,7 +617,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
     grid_wait_prior();
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
-    const long long U = *P.units;
+    const int U = *P.units;
     const long long all = (long long)A.batch * A.nq * A.heads;
     for (long long e = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5; e < all; e += (long long)gridDim.x * 8) {
         const long long tok = e / A.heads;
@@ -583,7 +625,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         const int b = (int)(tok / A.nq), t = (int)(tok - (long long)b * A.nq);
         const int len = attn_len(A, attn_row(A, b));
         RowSum<PER> R;
-        auto add = [&](long long item, long long u0, int tiles, long long row) {
+        auto add = [&](int item, int u0, int tiles, long long row) {
             const int ctas = unit_ctas(P, U), c1 = unit_cta(u0 + tiles - 1, U, ctas);
             int c = unit_cta(u0, U, ctas);
             if (P.prefix_tiles == 0 && c == c1) return false;   // a whole item: already written
@@ -605,15 +647,15 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         };
         if (attn_shares(A, P, len)) {
             const long long r = tok * A.group + g, rt = r / P.tile_rows;
-            const long long item = (long long)h * P.prefix_row_tiles + rt;
+            const int item = h * P.prefix_row_tiles + (int)rt;
             add(item, item * P.prefix_tiles, P.prefix_tiles, r - rt * P.tile_rows);
         }
         const long long r = (long long)t * A.group + g;
         const int rt = (int)(r / P.tile_rows), pair = b * P.own_row_tiles + rt;
         const int tiles = own_tiles(A, P, pair);
         if (tiles > 0) {
-            const long long at = (long long)pair * A.kv_heads + h;
-            if (!add((long long)A.kv_heads * P.prefix_row_tiles + at, P.item_unit[at], tiles, r - (long long)rt * P.tile_rows)) continue;
+            const int at = pair * A.kv_heads + h;
+            if (!add(A.kv_heads * P.prefix_row_tiles + at, P.item_unit[at], tiles, r - (long long)rt * P.tile_rows)) continue;
         }
         const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
         const long long off = tok * A.o_ts + (long long)qh * A.o_hs + PER * lane;
@@ -687,6 +729,12 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 }  // namespace
 
+long long tile_units(const AttnArgs& A, bool share, bool own) {
+    const long long mine = (long long)A.nq * A.group, all = mine * A.batch, per = 128;
+    return (share ? A.kv_heads * ((all + per - 1) / per) * ((A.prefix + TK - 1) / TK) : 0) +
+           (own ? A.batch * A.kv_heads * ((mine + per - 1) / per) * ((A.cap + TK - 1) / TK) : 0);
+}
+
 size_t tile_plan(const AttnArgs& A, int d, bool share, bool own, void* ws, TilePlan* P) {
     const long long mine = (long long)A.nq * A.group, all = mine * A.batch;
     TilePlan T = {};
@@ -701,11 +749,11 @@ size_t tile_plan(const AttnArgs& A, int d, bool share, bool own, void* ws, TileP
     const int sms = num_sms();
     T.ctas = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
     const size_t slots = share ? (size_t)(T.ctas + prefix_items + own_items) : 2 * (size_t)T.ctas;
-    const size_t units_b = 256, item_b = up256(8 * (size_t)own_items), ml_b = up256(slots * T.tile_rows * sizeof(float2));
+    const size_t units_b = 256, item_b = up256(4 * (size_t)own_items), ml_b = up256(slots * T.tile_rows * sizeof(float2));
     if (P) {
         uint8_t* p = static_cast<uint8_t*>(ws);
-        T.units = reinterpret_cast<long long*>(p);
-        T.item_unit = reinterpret_cast<long long*>(p + units_b);
+        T.units = reinterpret_cast<int*>(p);
+        T.item_unit = reinterpret_cast<int*>(p + units_b);
         T.ml = reinterpret_cast<float2*>(p + units_b + item_b);
         T.o = reinterpret_cast<float*>(p + units_b + item_b + ml_b);
         *P = T;

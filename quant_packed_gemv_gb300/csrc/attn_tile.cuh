@@ -22,8 +22,8 @@ struct TilePlan {
     int own;               // own jobs in the tile kernel
     int own_row_tiles;     // row tiles of a sequence's rows (per head)
     // workspace
-    long long* units;      // [1] all units (own: known on the device only)
-    long long* item_unit;  // [own items] first unit of the item (own jobs)
+    int* units;            // [1] all units (own: known on the device only)
+    int* item_unit;        // [own items] first unit of the item (own jobs)
     float* o;              // [slots][tile_rows][D], not divided by the sum
     float2* ml;            // [slots][tile_rows]: m (log2), l
 };
@@ -53,12 +53,12 @@ __device__ __forceinline__ int own_tiles(const AttnArgs& A, const TilePlan& P, i
 
 // CTAs that get units: with fewer units than CTAs the others stay idle, so that
 // no share between two others is empty.
-__device__ __forceinline__ int unit_ctas(const TilePlan& P, long long U) { return (int)min((long long)P.ctas, U); }
+__device__ __forceinline__ int unit_ctas(const TilePlan& P, int U) { return min(P.ctas, U); }
 
 // The CTA (of ctas) that holds unit u of U.
-__device__ __forceinline__ int unit_cta(long long u, long long U, int ctas) {
-    int c = (int)(u * ctas / U);
-    while (U * (c + 1) / ctas <= u) ++c;
+__device__ __forceinline__ int unit_cta(int u, int U, int ctas) {
+    int c = (int)((long long)u * ctas / U);
+    while ((long long)U * (c + 1) / ctas <= u) ++c;
     return c;
 }
 
@@ -66,8 +66,8 @@ __device__ __forceinline__ int unit_cta(long long u, long long U, int ctas) {
 // piece of every item is kept: items and CTAs both follow the units' order,
 // so c + item is free.  Otherwise only cut items are: a CTA has at most one
 // piece that does not begin its item and one cut piece that does.
-__host__ __device__ __forceinline__ long long piece_slot(const TilePlan& P, int c, long long item, bool begins) {
-    return P.prefix_tiles > 0 ? c + item : 2LL * c + begins;
+__host__ __device__ __forceinline__ long long piece_slot(const TilePlan& P, int c, int item, bool begins) {
+    return P.prefix_tiles > 0 ? (long long)c + item : 2LL * c + begins;
 }
 
 // One row's sums over partial results.
@@ -83,6 +83,9 @@ template <int PER> struct RowSum {
         m = mn;
     }
 };
+
+// Units at most (the kernel counts them in an int).
+long long tile_units(const AttnArgs& A, bool share, bool own);
 
 // TilePlan of a problem; its workspace pointers are set from ws (may be null).
 size_t tile_plan(const AttnArgs& A, int d, bool share, bool own, void* ws, TilePlan* P);

@@ -174,6 +174,19 @@ def load(build_if_missing=True):
     return lib
 
 
+def _current_stream():
+    """Address of torch's current stream (by the call that gives it without a Stream object, where torch has it)."""
+    global _current_stream
+    import torch
+    get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if get is None or dev is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        torch.cuda.current_stream()   # initializes CUDA
+        _current_stream = lambda: get(dev())  # noqa: E731
+    return _current_stream()
+
+
 def _addr(t):
     if t is None:
         return None
@@ -188,8 +201,7 @@ def _addr(t):
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -425,32 +437,44 @@ _LAYOUTS = {"half": PLM_ROPE_HALF, "interleaved": PLM_ROPE_INTERLEAVED}
 _SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 
+_types = {}    # torch type -> PLM_F32 .., filled on first use (torch is imported where it is needed)
+
+
 def _type(t):
-    import torch
-    code = {torch.float32: PLM_F32, torch.float16: PLM_F16, torch.bfloat16: PLM_BF16}.get(t.dtype)
+    code = _types.get(t.dtype)
     if code is None:
+        if not _types:
+            import torch
+            _types.update({torch.float32: PLM_F32, torch.float16: PLM_F16, torch.bfloat16: PLM_BF16,
+                           torch.int32: -32, torch.int64: -64})
+            return _type(t)
+        code = -1
+    if code < 0:
         raise ValueError("expected float32, float16 or bfloat16, got %s" % t.dtype)
     return code
 
 
-def _ints(t, dtype, name, shape=None):
-    """Address of a contiguous CUDA tensor of the given integer type (None stays None)."""
+def _ints(t, bits, name, shape=None):
+    """Address of a contiguous CUDA tensor of 32- or 64-bit integers (None stays None)."""
     if t is None:
         return None
-    if str(t.dtype) != "torch." + dtype:
-        raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != shape:
+    if not _types:
+        import torch
+        _type(torch.empty(0))
+    if _types.get(t.dtype) != -bits:
+        raise ValueError("%s: expected int%d, got %s" % (name, bits, t.dtype))
+    if shape is not None and t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
     return _addr(t)
 
 
 def _rows(t, name, dims):
     """Strides of a CUDA tensor whose last axis is dense."""
+    st = t.stride()
+    if len(st) != dims:
+        raise ValueError("%s: expected %d dimensions, got %d" % (name, dims, len(st)))
     if not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor" % name)
-    if t.dim() != dims:
-        raise ValueError("%s: expected %d dimensions, got %d" % (name, dims, t.dim()))
-    st = t.stride()
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError("%s: the last dimension has to be dense" % name)
     return st
@@ -485,7 +509,7 @@ def plm_rope_tensor(x, y, slots=None, rotate=True):
             raise ValueError("y: expected pages [.][%d][.][%d], got %s" % (x.shape[1], x.shape[2], tuple(y.shape)))
         page = (y.shape[2], ys[0], y.shape[0])
         yt, yh = ys[2], ys[1]
-    t = _RopeTensor(x.data_ptr() or None, y.data_ptr() or None, _ints(slots, "int64", "slots", (x.shape[0],)),
+    t = _RopeTensor(x.data_ptr() or None, y.data_ptr() or None, _ints(slots, 64, "slots", (x.shape[0],)),
                     x.shape[1], xs[0], xs[1], yt, yh, page[0], page[1], page[2], _type(x), _type(y), 1 if rotate else 0)
     t.shape = (x.shape[0], x.shape[2])
     return t
@@ -503,8 +527,8 @@ def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, in
     if tokens == 0 and tensors:
         return
     arr = (_RopeTensor * len(tensors))(*tensors)
-    _check("plm_rope", lib.plm_rope(arr, len(tensors), _ints(positions, "int32", "positions", (tokens,)),
-                                    _ints(freqs, "int64", "freqs"), tokens, d, rotary_dim,
+    _check("plm_rope", lib.plm_rope(arr, len(tensors), _ints(positions, 32, "positions", (tokens,)),
+                                    _ints(freqs, 64, "freqs"), tokens, d, rotary_dim,
                                     _LAYOUTS.get(layout, layout), scale, 1 if inverse else 0, _stream(stream)))
 
 
@@ -513,8 +537,8 @@ def plm_kv_state(pool, table, lens, refs, page_tokens, status=None):
     [max_seqs], refs int32 [pages], status int32 [1] or None.  It holds addresses: keep the tensors."""
     pages, (seqs, width) = pool.shape[0], table.shape
     s = _KvState(_addr(pool), pool.numel() // max(1, pages) * pool.element_size(), pages,
-                 _ints(table, "int32", "table"), _ints(lens, "int32", "lens", (seqs,)),
-                 _ints(refs, "int32", "refs", (pages,)), _ints(status, "int32", "status"), seqs, width, page_tokens)
+                 _ints(table, 32, "table"), _ints(lens, 32, "lens", (seqs,)),
+                 _ints(refs, 32, "refs", (pages,)), _ints(status, 32, "status"), seqs, width, page_tokens)
     return s
 
 
@@ -532,8 +556,8 @@ def plm_kv_reserve(kv, seqs, add, slots, workspace, stream=None):
     lib, n = load(), seqs.numel()
     if slots is not None and (slots.dim() != 2 or slots.shape[0] != n):
         raise ValueError("slots: expected [%d][.], got %s" % (n, tuple(slots.shape)))
-    _check("plm_kv_reserve", lib.plm_kv_reserve(ctypes.byref(kv), _ints(seqs, "int32", "seqs"),
-                                                _ints(add, "int32", "add", (n,)), n, _ints(slots, "int64", "slots"),
+    _check("plm_kv_reserve", lib.plm_kv_reserve(ctypes.byref(kv), _ints(seqs, 32, "seqs"),
+                                                _ints(add, 32, "add", (n,)), n, _ints(slots, 64, "slots"),
                                                 0 if slots is None else slots.shape[1], _addr(workspace),
                                                 _bytes(workspace), _stream(stream)))
 
@@ -541,29 +565,29 @@ def plm_kv_reserve(kv, seqs, add, slots, workspace, stream=None):
 def plm_kv_fork(kv, parents, children, workspace, keep=None, stream=None):
     """Unused sequences children (int32 [n]) become copies of parents, of their first keep tokens if given."""
     lib, n = load(), parents.numel()
-    _check("plm_kv_fork", lib.plm_kv_fork(ctypes.byref(kv), _ints(parents, "int32", "parents"),
-                                          _ints(children, "int32", "children", (n,)), _ints(keep, "int32", "keep", (n,)),
+    _check("plm_kv_fork", lib.plm_kv_fork(ctypes.byref(kv), _ints(parents, 32, "parents"),
+                                          _ints(children, 32, "children", (n,)), _ints(keep, 32, "keep", (n,)),
                                           n, _addr(workspace), _bytes(workspace), _stream(stream)))
 
 
 def plm_kv_free(kv, seqs, stream=None):
     """The sequences (int32 [n]) give their pages back."""
     lib = load()
-    _check("plm_kv_free", lib.plm_kv_free(ctypes.byref(kv), _ints(seqs, "int32", "seqs"), seqs.numel(), _stream(stream)))
+    _check("plm_kv_free", lib.plm_kv_free(ctypes.byref(kv), _ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)))
 
 
 def plm_kv_compact(kv, live, workspace, stream=None):
     """Packs the pages in use to the front of the pool; live (int32 [1] or None) gets their number."""
     lib = load()
-    _check("plm_kv_compact", lib.plm_kv_compact(ctypes.byref(kv), _ints(live, "int32", "live"), _addr(workspace),
+    _check("plm_kv_compact", lib.plm_kv_compact(ctypes.byref(kv), _ints(live, 32, "live"), _addr(workspace),
                                                 _bytes(workspace), _stream(stream)))
 
 
 def plm_kv_copy_pages(kv, src, dst, stream=None):
     """Page dst[i] = page src[i] (int32 lists of the same length)."""
     lib, n = load(), src.numel()
-    _check("plm_kv_copy_pages", lib.plm_kv_copy_pages(ctypes.byref(kv), _ints(src, "int32", "src"),
-                                                      _ints(dst, "int32", "dst", (n,)), n, _stream(stream)))
+    _check("plm_kv_copy_pages", lib.plm_kv_copy_pages(ctypes.byref(kv), _ints(src, 32, "src"),
+                                                      _ints(dst, 32, "dst", (n,)), n, _stream(stream)))
 
 
 def plm_attn_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len):
@@ -589,8 +613,8 @@ def plm_attn_shared_prefix(q, o, k, v, table, lens, tokens, prefix_len, max_len,
     rows, width = table.shape
     batch = n // tokens
     p = _AttnProblem(q.data_ptr() or None, o.data_ptr() or None, None, k.data_ptr() or None, v.data_ptr() or None,
-                     _ints(table, "int32", "table"), _ints(lens, "int32", "lens", (rows,)),
-                     _ints(seqs, "int32", "seqs", (batch,)), batch, tokens, heads, k.shape[1], d, qs[0], qs[1], os_[0],
+                     _ints(table, 32, "table"), _ints(lens, 32, "lens", (rows,)),
+                     _ints(seqs, 32, "seqs", (batch,)), batch, tokens, heads, k.shape[1], d, qs[0], qs[1], os_[0],
                      os_[1], k.shape[2], k.shape[0], ks[0], ks[1], ks[2], width, rows, prefix_len, max_len, scale,
                      _type(k), _type(o))
     if seqs is None and batch > rows:
