@@ -1,10 +1,11 @@
 // Attention over a paged cache (plm_attn_shared_prefix): which kernels a call
 // runs.
 //
-// Decode (at most 16 rows per sequence and head): attn_rows.cu, a cluster per
+// Decode (at most 32 rows per sequence and head): attn_rows.cu, a cluster per
 // (sequence, head); a shared prefix is first done for the whole batch by the
 // tile kernel (attn_tile.cu), and the rows kernel adds its results at the end.
-// More rows: the tile kernel does both, and a last kernel adds the pieces.
+// More rows: the tile kernel does the own keys too, and a last kernel adds what
+// was cut.
 #include "attn_tile.cuh"
 
 namespace plm {
@@ -30,16 +31,18 @@ AttnArgs attn_args(const plm_attn_problem& p) {
     return A;
 }
 
+// A call's kernels and their plans.
 struct Choice {
-    bool rows;    // the rows kernel (own keys)
-    bool share;   // the prefix apart, for the whole batch
-    bool tile;    // the tile kernel
+    bool rows;     // own keys in the rows kernel, else in the tile kernel
+    bool share;    // the prefix apart, for the whole batch
+    TilePlan prefix, own;
+    size_t bytes;  // workspace, SIZE_MAX: too many units
 };
 
-Choice choose(const AttnArgs& A) {
+Choice choose(const AttnArgs& A, int d, void* ws) {
     const long long mine = (long long)A.nq * A.group;
-    Choice c;
-    c.rows = mine <= 16;
+    Choice c = {};
+    c.rows = mine <= 32;
     c.share = A.prefix > 0 && A.batch > 1;
     if (!c.rows && c.share) {
         // a sequence's rows fill their own tiles well: its prefix keys are then
@@ -47,7 +50,11 @@ Choice choose(const AttnArgs& A) {
         const long long tile = mine > 128 ? 256 : 128, full = (mine + tile - 1) / tile * tile;
         if (5 * mine >= 4 * full) c.share = false;
     }
-    c.tile = c.share || !c.rows;
+    size_t a = 0, b = 0;
+    if (c.share) c.prefix = tile_plan(A, d, 0, true, ws, &a);
+    if (a == SIZE_MAX) { c.bytes = a; return c; }
+    if (!c.rows) c.own = tile_plan(A, d, 1, c.share, ws ? static_cast<uint8_t*>(ws) + a : nullptr, &b);
+    c.bytes = b == SIZE_MAX ? b : a + b;
     return c;
 }
 
@@ -60,22 +67,20 @@ size_t attn_workspace_bytes(long long batch, long long tokens, long long heads, 
     A.group = A.heads / A.kv_heads;
     A.prefix = (int)prefix_len;
     A.cap = (int)max_len;
-    const Choice c = choose(A);
-    if (c.tile && tile_units(A, c.share, !c.rows) > 0x7FFFFFFFLL) return SIZE_MAX;
-    return c.tile ? tile_plan(A, (int)head_dim, c.share, !c.rows, nullptr, nullptr) : 0;
+    return choose(A, (int)head_dim, nullptr).bytes;
 }
 
 cudaError_t launch_attn(const plm_attn_problem& p, void* ws, cudaStream_t stream) {
     const AttnArgs A = attn_args(p);
     const int d = (int)p.head_dim;
-    const Choice c = choose(A);
-    TilePlan P = {};
-    if (c.tile) {
-        tile_plan(A, d, c.share, !c.rows, ws, &P);
-        const cudaError_t e = launch_attn_tile(A, P, p.type, d, stream);
+    const Choice c = choose(A, d, ws);
+    if (c.share) {
+        const cudaError_t e = launch_attn_tile(A, c.prefix, p.type, d, stream);
         if (e != cudaSuccess) return e;
     }
-    return c.rows ? launch_attn_rows(A, c.share ? &P : nullptr, p.type, d, stream) : cudaSuccess;
+    if (c.rows) return launch_attn_rows(A, c.share ? &c.prefix : nullptr, p.type, d, stream);
+    const cudaError_t e = launch_attn_tile(A, c.own, p.type, d, stream);
+    return e == cudaSuccess && c.share ? launch_attn_merge(A, c.prefix, c.own, p.type, d, stream) : e;
 }
 
 }  // namespace plm

@@ -1,4 +1,4 @@
-// Paged attention for up to 16 query rows per (sequence, key/value head):
+// Paged attention for up to 32 query rows per (sequence, key/value head):
 // decode, and a few drafted tokens (plm_attn_shared_prefix).
 //
 // Mathematics.  With R = tokens * group rows, each block of 16 keys is two
@@ -14,6 +14,8 @@
 // g + 8 (dims 32 c + 8 t ..) and of V rows 2t, 2t + 1, 2t + 8, 2t + 9 (dims
 // 64 c + 8 g ..) and uses them as fragments where they are: no shared memory.
 // Rows of Q follow K's order of d; P^T needs one movmatrix per 8 x 8 block.
+// Up to 16 rows Q stays in registers; beyond, the warps share it in shared
+// memory, so that O (32 registers per 8 rows at D = 128) has room.
 //
 // Bound: HBM (4 D bytes per key and head pair, ~2 operations per byte and
 // row).  A warp keeps the next 16 keys' K and this block's V in flight (8 KB
@@ -27,7 +29,7 @@ namespace {
 
 constexpr int DW = 4;               // warps per CTA
 constexpr float RAISE = 8.0f;       // log2 by which a score may exceed the reference
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.4426950408889634f;
 
 template <class E> __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                             uint32_t a3, uint32_t b0, uint32_t b1);
@@ -50,17 +52,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t words(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
-// The parts of a pair's warps, in shared memory: per warp the references m
-// and sums l of its rows, then O [rows][D + 4] (padded against conflicts).
+// Shared memory: Q fragments (NB > 2), then the parts of a pair's warps: per
+// warp the references m and sums l of its rows, then O [rows][D + 4] (padded
+// against conflicts).
 template <int D, int NB> struct RowsSmem {
     static constexpr int ROWS = 8 * NB, PITCH = D + 4;
+    uint4 q[NB > 2 ? NB * (D / 32) * 32 : 1];
     float m[DW][ROWS], l[DW][ROWS];
     float o[DW][ROWS][PITCH];
 };
@@ -69,7 +68,9 @@ template <class E, int D, int NB>
 __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     using Sm = RowsSmem<D, NB>;
     constexpr int KC = D / 32, VC = D / 64;   // 16-byte chunks per lane of a K row, of a V row
-    __shared__ __align__(16) Sm sm;
+    constexpr bool QS = NB > 2;
+    extern __shared__ __align__(16) uint8_t rows_raw[];
+    Sm& sm = *reinterpret_cast<Sm*>(rows_raw);
     grid_launch_dependents();
     // after the tile kernel there is nothing to wait for yet: it starts this
     // kernel once the work before it has finished
@@ -85,27 +86,31 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const int mask = (1 << A.page_shift) - 1;
 
     // Q as the B operand: row 8 nb + g, dims 32 c + 8 t ..; zeros past the rows
-    uint4 qf[NB][KC];
-    int seen[NB][2];   // keys that rows 8 nb + 2t, + 1 see
-    int all = len;     // keys that every row sees
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    uint4 qf[QS ? 1 : NB][QS ? 1 : KC];
+    auto q_part = [&](int nb, int c) {
         const int r = 8 * nb + g;
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        return *reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + r / A.group) * A.q_ts +
+                                               (long long)(h * A.group + r % A.group) * A.q_hs + 8 * t + 32 * c);
+    };
+    if constexpr (QS) {
+        for (int i = warp; i < NB * KC; i += DW) sm.q[i * 32 + lane] = q_part(i / KC, i % KC);
+        __syncthreads();
+    } else {
 #pragma unroll
-        for (int c = 0; c < KC; ++c) qf[nb][c] = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-            const E* q = static_cast<const E*>(A.q) + ((long long)b * A.nq + r / A.group) * A.q_ts +
-                         (long long)(h * A.group + r % A.group) * A.q_hs + 8 * t;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) qf[nb][c] = *reinterpret_cast<const uint4*>(q + 32 * c);
-        }
+            for (int c = 0; c < KC; ++c) qf[nb][c] = q_part(nb, c);
+    }
+    int seen[NB][2];   // keys that rows 8 nb + 2t, + 1 see
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int rr = 8 * nb + 2 * t + i;
             seen[nb][i] = rr < rows ? attn_seen(A, len, rr / A.group) : 0;
         }
-    }
-    all = attn_seen(A, len, 0);
+    const int all = attn_seen(A, len, 0);   // keys that every row sees
 
     float m[NB][2], l[NB][2], o[NB][2 * VC * 2][4];   // o: D / 16 tiles of 16 dims x 8 rows
 #pragma unroll
@@ -160,8 +165,9 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
             s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                mma16816<E>(s[nb], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qf[nb][c].x, qf[nb][c].y);
-                mma16816<E>(s[nb], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qf[nb][c].z, qf[nb][c].w);
+                const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
+                mma16816<E>(s[nb], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qv.x, qv.y);
+                mma16816<E>(s[nb], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qv.z, qv.w);
             }
         }
         if (blk + streams < blocks) load_k(blk + streams, page_n, kf);
@@ -242,48 +248,35 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     if (cs > 1) cluster_barrier();
     else __syncthreads();
     if (P.prefix_tiles > 0) grid_wait_prior();   // the tile kernel's results
-    // every CTA of the cluster writes its share of the rows' values, four dims a thread
-    const int share = blockIdx.z, quads = rows * (D / 4);
-    for (int e = share * (DW * 32) + threadIdx.x; e < quads; e += cs * DW * 32) {
-        const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
-        float top = -INFINITY;
-        for (int z = 0; z < cs; ++z)
+    // A warp adds up a row at a time, 4 (2 at D = 64) dims a lane: the parts of
+    // the cluster's warps (at most 32, a lane each for their weights), then the
+    // pieces of the row's prefix item, both in order.
+    constexpr int PER = D / 32;
+    for (int r = blockIdx.z + cs * warp; r < rows; r += cs * DW) {
+        const bool part = lane < cs * DW;
+        const int pz = lane / DW, pw = lane % DW;
+        float pm = part ? peer_f32(&sm.m[pw][r], pz, cs) : -INFINITY;
+        const float pl = part ? peer_f32(&sm.l[pw][r], pz, cs) : 0.0f;
+        if (pl == 0.0f) pm = -INFINITY;   // no key
+        RowSum<PER> R;
+        R.m = warp_max(pm);
+        const float wgt = pm == -INFINITY ? 0.0f : ex2(pm - R.m);
+        R.l = warp_sum(wgt * pl);
+        for (int p = 0; p < cs * DW; ++p) {
+            const float f = __shfl_sync(0xFFFFFFFFu, wgt, p);
+            float v[PER];
+            peer_dims<PER>(&sm.o[p % DW][r][PER * lane], p / DW, cs, v);
+            if (f != 0.0f)
 #pragma unroll
-            for (int w = 0; w < DW; ++w) top = fmaxf(top, peer_f32(&sm.m[w][r], z, cs));
-        const float base = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int z = 0; z < cs; ++z)
-#pragma unroll
-            for (int w = 0; w < DW; ++w) {
-                const float f = ex2(peer_f32(&sm.m[w][r], z, cs) - base);
-                const float4 v = peer_f32x4(&sm.o[w][r][d], z, cs);
-                sum = fmaf(f, peer_f32(&sm.l[w][r], z, cs), sum);
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            }
-        RowSum<4> R;
-        R.add(top, sum, {acc.x, acc.y, acc.z, acc.w});
-        if (shares) {   // the pieces of the row's prefix item, in order
+                for (int i = 0; i < PER; ++i) R.o[i] = fmaf(f, v[i], R.o[i]);
+        }
+        if (shares) {
             const long long gr = (long long)b * rows + r, rt = gr / P.tile_rows;
             const int item = h * P.prefix_row_tiles + (int)rt, u0 = item * P.prefix_tiles;
-            const int U = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
-            const int c1 = unit_cta(u0 + P.prefix_tiles - 1, U, P.ctas);
-            for (int c = unit_cta(u0, U, P.ctas); c <= c1; ++c) {
-                const long long at = piece_slot(P, c, item, false) * P.tile_rows + (gr - rt * P.tile_rows);
-                const float2 ml = P.ml[at];
-                const float4 v = *reinterpret_cast<const float4*>(P.o + at * D + d);
-                R.add(ml.x, ml.y, {v.x, v.y, v.z, v.w});
-            }
+            R.pieces(P, u0, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, item,
+                     (int)(gr - rt * P.tile_rows), lane);
         }
-        const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;   // no key: o = 0, lse = -inf
-        const long long tok = (long long)b * A.nq + r / A.group;
-        const int qh = h * A.group + r % A.group;
-        attn_store4<E>(A, tok * A.o_ts + (long long)qh * A.o_hs + d,
-                       make_float4(R.o[0] * inv, R.o[1] * inv, R.o[2] * inv, R.o[3] * inv));
-        if (A.lse && d == 0) A.lse[tok * A.heads + qh] = R.l == 0.0f ? -INFINITY : (R.m + log2f(R.l)) * LN2;
+        R.template store<E>(A, (long long)b * A.nq + r / A.group, h * A.group + r % A.group, lane);
     }
     if (cs > 1) cluster_barrier();   // no CTA leaves while its part is read
 }
@@ -291,16 +284,24 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
 template <class E, int D, int NB>
 cudaError_t rows_launch(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t stream) {
     const dim3 grid((unsigned)(A.batch * A.kv_heads), 1, (unsigned)cs);
-    if (cs == 1) return launch_kernel(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), 0, stream, A, P);
-    return launch_kernel_cluster(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), 0, stream, (unsigned)cs, A, P);
+    constexpr int bytes = sizeof(RowsSmem<D, NB>);
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<E, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    if (cs == 1) return launch_kernel(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), bytes, stream, A, P);
+    return launch_kernel_cluster(attn_rows_kernel<E, D, NB>, grid, dim3(DW * 32), bytes, stream, (unsigned)cs, A, P);
 }
 
 template <class E, int D>
 cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t stream) {
-    return A.nq * A.group <= 8 ? rows_launch<E, D, 1>(A, P, cs, stream) : rows_launch<E, D, 2>(A, P, cs, stream);
+    const int rows = A.nq * A.group;
+    if (rows <= 8) return rows_launch<E, D, 1>(A, P, cs, stream);
+    if (rows <= 16) return rows_launch<E, D, 2>(A, P, cs, stream);
+    return rows <= 24 ? rows_launch<E, D, 3>(A, P, cs, stream) : rows_launch<E, D, 4>(A, P, cs, stream);
 }
 
-// CTAs of a pair: while the pairs alone leave warps idle (12 fit an SM), and
+// CTAs of a pair (at most 8: 32 warps): while the pairs alone leave warps idle (12 fit an SM), and
 // every warp still gets two blocks of 16 keys.
 int rows_cluster(const AttnArgs& A, int keys) {
     const long long pairs = (long long)A.batch * A.kv_heads, room = 3LL * num_sms();

@@ -99,11 +99,6 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x
                  :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Two f32 in one 64-bit register.
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
     uint64_t r;
@@ -131,7 +126,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // A piece: consecutive units of one item.
 struct Piece {
-    bool prefix, begins, whole;
+    bool begins, whole;
     int b, rt, h;       // sequence (own), row tile, head
     int key0, keys;     // first key of the piece; end of the keys to load (own: that its rows see)
     int tiles;
@@ -142,29 +137,31 @@ struct Piece {
 
 // Walks the CTA's share of the units; every warp for itself, by all its lanes.
 struct Walk {
-    int up, u, end;    // the prefix job's units, the next unit, the end of the share
-    int prefix_row;    // table row that holds the prefix
-    int pair, T, h;    // own cursor: (sequence, row tile), its units per head, head
-    int item_u0;       // first unit of the cursor's item
+    int u, end;        // the next unit, the end of the share
+    int prefix_row;    // prefix: table row that holds it
+    int pair, T, h;    // own: (sequence, row tile), its units per head, head
+    int item_u0;       // own: first unit of the item
 
     // Returns the number of all units.
     __device__ int start(const AttnArgs& A, const TilePlan& P, int lane) {
-        up = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
-        const int pairs = P.own ? A.batch * P.own_row_tiles : 0;
-        int sum = 0;
-        for (int p = lane; p < pairs; p += 32) sum += own_tiles(A, P, p);
+        int U;
+        if (P.job == 0) {
+            U = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
+        } else {
+            const int pairs = A.batch * P.own_row_tiles;
+            int sum = 0;
+            for (int p = lane; p < pairs; p += 32) sum += own_tiles(A, P, p);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const int U = up + sum * A.kv_heads;
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            U = sum * A.kv_heads;
+        }
         const int ctas = unit_ctas(P, U);
         const bool mine = (int)blockIdx.x < ctas;
         u = mine ? (int)((long long)U * blockIdx.x / ctas) : U;
         end = mine ? (int)((long long)U * (blockIdx.x + 1) / ctas) : U;
-        pair = -1;
-        T = h = 0;
-        item_u0 = 0;
-        prefix_row = -1;
-        if (u < up)   // the first sequence that takes part
+        pair = prefix_row = -1;
+        T = h = item_u0 = 0;
+        if (P.job == 0)   // the first sequence that takes part
             for (int b0 = 0; b0 < A.batch && prefix_row < 0; b0 += 32) {
                 const int b = b0 + lane, row = b < A.batch ? attn_row(A, b) : -1;
                 const unsigned hit = __ballot_sync(0xFFFFFFFFu, row >= 0 && attn_shares(A, P, attn_len(A, row)));
@@ -176,7 +173,7 @@ struct Walk {
     // The pair, head and item of own unit u.
     __device__ void locate(const AttnArgs& A, const TilePlan& P, int lane) {
         const int pairs = A.batch * P.own_row_tiles;
-        int acc = up;
+        int acc = 0;
         for (int p0 = 0; p0 < pairs; p0 += 32) {
             const int p = p0 + lane;
             const int n = p < pairs ? own_tiles(A, P, p) : 0;
@@ -202,10 +199,9 @@ struct Walk {
 
     __device__ bool next(const AttnArgs& A, const TilePlan& P, int lane, Piece& S) {
         if (u >= end) return false;
-        if (u < up) {
+        if (P.job == 0) {
             S.item = u / P.prefix_tiles;
             const int t0 = u - S.item * P.prefix_tiles;
-            S.prefix = true;
             S.b = 0;
             S.h = S.item / P.prefix_row_tiles;
             S.rt = S.item - S.h * P.prefix_row_tiles;
@@ -226,7 +222,6 @@ struct Walk {
                 }
             }
             const int t0 = u - item_u0;
-            S.prefix = false;
             S.b = pair / P.own_row_tiles;
             S.rt = pair - S.b * P.own_row_tiles;
             S.h = h;
@@ -238,7 +233,7 @@ struct Walk {
             S.whole = S.begins && S.tiles == T;
             S.key0 = own_begin(A, P, len) + t0 * TK;
             S.keys = own_end(A, P, len, S.rt);
-            S.item = A.kv_heads * (P.prefix_row_tiles + pair) + h;
+            S.item = A.kv_heads * pair + h;
         }
         u += S.tiles;
         return true;
@@ -249,10 +244,10 @@ struct Walk {
 __device__ __forceinline__ bool tile_row(const AttnArgs& A, const TilePlan& P, const Piece& S, int i, long long& tok,
                                          int& qh) {
     const long long r = (long long)S.rt * P.tile_rows + i;
-    const long long all = (long long)A.nq * A.group * (S.prefix ? A.batch : 1);
+    const long long all = (long long)A.nq * A.group * (P.job == 0 ? A.batch : 1);
     if (r >= all) return false;
     const long long t = r / A.group;
-    tok = (S.prefix ? 0 : (long long)S.b * A.nq) + t;
+    tok = (long long)S.b * A.nq + t;
     qh = S.h * A.group + (int)(r - t * A.group);
     return true;
 }
@@ -306,6 +301,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
     Piece S;
     if (warp == TMA_WARP) {
         const int U = W.start(A, P, lane);
+        bool first = true;
         // ---------------------------------------------------- pages -> K, V
         const int bt = min(1 << A.page_shift, TK), per = TK / bt;   // tokens per box, boxes per 64 dims
         int n = 0;                                                  // tiles loaded: slot n % SLOTS
@@ -313,7 +309,14 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         const bool active = part < D / 64;
         while (ok && W.next(A, P, lane, S)) {
             const int* tab = A.table + (long long)max(S.row, 0) * A.table_stride;
-            if (!S.prefix && S.begins && lane == 0) P.item_unit[S.item - A.kv_heads * P.prefix_row_tiles] = S.unit0;
+            if (P.job == 1 && lane == 0) {
+                if (P.keep) {
+                    if (S.begins) P.item_unit[S.item] = S.unit0;
+                } else if (first) {
+                    P.cut[blockIdx.x] = make_int4(S.begins ? -1 : W.pair, S.h, S.unit0, W.T);
+                }
+            }
+            first = false;
             for (int i = 0; ok && i < S.tiles; ++i) {
                 const int j = S.key0 + i * TK + box * bt;
                 int page = A.pages;   // out of range: the box is filled with zeros
@@ -338,7 +341,10 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         }
         if (!ok)   // wind down: this CTA's copies have to land before it ends
             for (int i = max(0, n - L::SLOTS); i < n; ++i) mbar_wait(&full[i % L::SLOTS], (i / L::SLOTS) & 1);
-        if (blockIdx.x == 0 && lane == 0) *P.units = U;
+        if (P.job == 1 && lane == 0) {
+            if (blockIdx.x == 0) *P.units = U;
+            if (first && !P.keep) P.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);   // no units
+        }
     } else if (warp == MMA_WARP) {
         W.start(A, P, lane);
         // ------------------------------------------------------- the products
@@ -398,7 +404,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 ok = wait_full(vt);
                 if (!ok) break;
                 const int left = S.keys - (S.key0 + i * TK);
-                if (!S.prefix && left < TK) {
+                if (P.job == 1 && left < TK) {
                     // the pages' rows past the end may hold anything, and 0 * NaN is NaN
                     uint8_t* v = sm + L::RING + (vt % L::SLOTS) * L::STAGE;
                     for (int e = lane; e < (TK - left) * (D / 8); e += 32) {
@@ -459,7 +465,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         while (have && ok) {
             const bool in = tile_row(A, P, S, t * 128 + i, tok, qh);
             int seen = S.keys;   // keys that the row sees
-            if (!S.prefix && in) seen = attn_seen(A, attn_len(A, S.row), (int)(tok - (long long)S.b * A.nq));
+            if (P.job == 1 && in) seen = attn_seen(A, attn_len(A, S.row), (int)(tok - (long long)S.b * A.nq));
             float m = -INFINITY, l = 0.0f;   // m in units of S
             for (int u = 0; ok && u < S.tiles; ++u, ++step) {
                 const int sb = NT == 2 ? t : step & 1;
@@ -562,7 +568,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             tc_after();
             const uint32_t oa = tmem + lanes + TM_O + D * t;
             const float m2 = m * sl2;
-            const bool final = C.whole && P.prefix_tiles == 0;
+            const bool final = C.whole && !P.keep;
             if (final) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const long long off = in ? my_tok * A.o_ts + (long long)my_qh * A.o_hs : 0;
@@ -609,65 +615,69 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
     }
 }
 
-// Adds the pieces of every row (own jobs in the tile kernel): a warp per row
-// and query head.
+// The items that are cut between CTAs (own keys alone): block (c, y) adds the
+// rows of the item that CTA c goes on with, if c - 1 began it.  The blocks
+// from P.ctas on write the rows of sequences without keys.
+constexpr int JOIN_Y = 8;
 template <class E, int D>
-__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     grid_launch_dependents();
     grid_wait_prior();
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int U = *P.units;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int pair, h0, h1;
+    if ((int)blockIdx.x >= P.ctas) {
+        pair = blockIdx.x - P.ctas;
+        if (own_tiles(A, P, pair) > 0) return;
+        h0 = 0;
+        h1 = A.kv_heads;
+    } else {
+        const int c = blockIdx.x, U = *P.units;
+        const int4 cut = P.cut[c];
+        if (cut.x < 0 || unit_cta(cut.z, U, unit_ctas(P, U)) != c - 1) return;
+        pair = cut.x;
+        h0 = cut.y;
+        h1 = h0 + 1;
+    }
+    const int b = pair / P.own_row_tiles, rt = pair - b * P.own_row_tiles;
+    const int rows = (int)min((long long)P.tile_rows, (long long)A.nq * A.group - (long long)rt * P.tile_rows);
+    for (int h = h0; h < h1; ++h)
+        for (int i = blockIdx.y * 8 + warp; i < rows; i += JOIN_Y * 8) {
+            RowSum<D / 32> R;
+            if ((int)blockIdx.x < P.ctas) {
+                const int4 cut = P.cut[blockIdx.x];
+                R.pieces(P, cut.z, cut.w, *P.units, 0, i, lane);
+            }
+            const long long r = (long long)rt * P.tile_rows + i, t = r / A.group;
+            R.template store<E>(A, (long long)b * A.nq + t, h * A.group + (int)(r - t * A.group), lane);
+        }
+}
+
+// All rows: the pieces of their prefix item and of their own item.
+template <class E, int D>
+__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P,
+                                                         const __grid_constant__ TilePlan W) {
+    grid_launch_dependents();
+    grid_wait_prior();
+    const int lane = threadIdx.x & 31, U = *W.units;
     const long long all = (long long)A.batch * A.nq * A.heads;
     for (long long e = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5; e < all; e += (long long)gridDim.x * 8) {
         const long long tok = e / A.heads;
         const int qh = (int)(e - tok * A.heads), h = qh / A.group, g = qh - h * A.group;
         const int b = (int)(tok / A.nq), t = (int)(tok - (long long)b * A.nq);
-        const int len = attn_len(A, attn_row(A, b));
-        RowSum<PER> R;
-        auto add = [&](int item, int u0, int tiles, long long row) {
-            const int ctas = unit_ctas(P, U), c1 = unit_cta(u0 + tiles - 1, U, ctas);
-            int c = unit_cta(u0, U, ctas);
-            if (P.prefix_tiles == 0 && c == c1) return false;   // a whole item: already written
-            for (bool begins = true; c <= c1; ++c, begins = false) {
-                const long long at = piece_slot(P, c, item, begins) * P.tile_rows + row;
-                const float2 ml = P.ml[at];
-                float o[PER];
-                const float* src = P.o + at * D + PER * lane;
-                if constexpr (PER == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(src);
-                    o[0] = v.x; o[1] = v.y;
-                }
-                R.add(ml.x, ml.y, o);
-            }
-            return true;
-        };
-        if (attn_shares(A, P, len)) {
+        RowSum<D / 32> R;
+        if (attn_shares(A, P, attn_len(A, attn_row(A, b)))) {
             const long long r = tok * A.group + g, rt = r / P.tile_rows;
             const int item = h * P.prefix_row_tiles + (int)rt;
-            add(item, item * P.prefix_tiles, P.prefix_tiles, r - rt * P.tile_rows);
+            R.pieces(P, item * P.prefix_tiles, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, item,
+                     (int)(r - rt * P.tile_rows), lane);
         }
-        const long long r = (long long)t * A.group + g;
-        const int rt = (int)(r / P.tile_rows), pair = b * P.own_row_tiles + rt;
-        const int tiles = own_tiles(A, P, pair);
+        const int r = t * A.group + g, rt = r / W.tile_rows, pair = b * W.own_row_tiles + rt;
+        const int tiles = own_tiles(A, W, pair);
         if (tiles > 0) {
-            const int at = pair * A.kv_heads + h;
-            if (!add(A.kv_heads * P.prefix_row_tiles + at, P.item_unit[at], tiles, r - (long long)rt * P.tile_rows)) continue;
+            const int item = pair * A.kv_heads + h;
+            R.pieces(W, W.item_unit[item], tiles, U, item, r - rt * W.tile_rows, lane);
         }
-        const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
-        const long long off = tok * A.o_ts + (long long)qh * A.o_hs + PER * lane;
-        if constexpr (PER == 4) {
-            attn_store4<E>(A, off, make_float4(R.o[0] * inv, R.o[1] * inv, R.o[2] * inv, R.o[3] * inv));
-        } else if (A.o_f32) {
-            *reinterpret_cast<float2*>(static_cast<float*>(A.o) + off) = make_float2(R.o[0] * inv, R.o[1] * inv);
-        } else {
-            *reinterpret_cast<uint32_t*>(static_cast<E*>(A.o) + off) = pack_pair<E>(R.o[0] * inv, R.o[1] * inv);
-        }
-        if (A.lse && lane == 0)
-            A.lse[tok * A.heads + qh] = R.l == 0.0f ? -INFINITY : (R.m + log2f(R.l)) * 0.6931471805599453f;
+        R.template store<E>(A, tok, qh, lane);
     }
 }
 
@@ -712,10 +722,15 @@ cudaError_t tile_launch(const AttnArgs& A, const TilePlan& P, const CUtensorMap&
     cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<E, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     e = launch_kernel(attn_tile_kernel<E, D, NT>, dim3((unsigned)P.ctas), dim3(NT * 128 + 64), bytes, stream, A, P, km, vm, fault);
-    if (e != cudaSuccess || !P.own) return e;
+    if (e != cudaSuccess || P.job == 0 || P.keep) return e;
+    return launch_kernel(attn_join_kernel<E, D>, dim3((unsigned)(P.ctas + A.batch * P.own_row_tiles), JOIN_Y), dim3(256), 0, stream, A, P);
+}
+
+template <class E, int D>
+cudaError_t merge_launch(const AttnArgs& A, const TilePlan& P, const TilePlan& W, cudaStream_t stream) {
     const long long rows = (long long)A.batch * A.nq * A.heads, cap = 8LL * num_sms();
     const long long ctas = (rows + 7) / 8 < cap ? (rows + 7) / 8 : cap;
-    return launch_kernel(attn_merge_kernel<E, D>, dim3((unsigned)ctas), dim3(256), 0, stream, A, P);
+    return launch_kernel(attn_merge_kernel<E, D>, dim3((unsigned)ctas), dim3(256), 0, stream, A, P, W);
 }
 
 template <class E>
@@ -729,36 +744,43 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 }  // namespace
 
-long long tile_units(const AttnArgs& A, bool share, bool own) {
-    const long long mine = (long long)A.nq * A.group, all = mine * A.batch, per = 128;
-    return (share ? A.kv_heads * ((all + per - 1) / per) * ((A.prefix + TK - 1) / TK) : 0) +
-           (own ? A.batch * A.kv_heads * ((mine + per - 1) / per) * ((A.cap + TK - 1) / TK) : 0);
-}
-
-size_t tile_plan(const AttnArgs& A, int d, bool share, bool own, void* ws, TilePlan* P) {
-    const long long mine = (long long)A.nq * A.group, all = mine * A.batch;
+TilePlan tile_plan(const AttnArgs& A, int d, int job, bool share, void* ws, size_t* bytes) {
+    const long long mine = (long long)A.nq * A.group, all = job == 0 ? mine * A.batch : mine;
     TilePlan T = {};
-    T.tile_rows = (share ? all : mine) > 128 ? 256 : 128;
+    T.job = job;
+    T.keep = share;
+    T.tile_rows = all > 128 ? 256 : 128;
+    const long long row_tiles = (all + T.tile_rows - 1) / T.tile_rows;
     T.prefix_tiles = share ? (A.prefix + TK - 1) / TK : 0;
-    T.prefix_row_tiles = share ? (int)((all + T.tile_rows - 1) / T.tile_rows) : 0;
-    T.own = own;
-    T.own_row_tiles = own ? (int)((mine + T.tile_rows - 1) / T.tile_rows) : 0;
-    const long long prefix_items = (long long)A.kv_heads * T.prefix_row_tiles;
-    const long long own_items = own ? (long long)A.batch * T.own_row_tiles * A.kv_heads : 0;
-    const long long most = prefix_items * T.prefix_tiles + own_items * ((A.cap + TK - 1) / TK);
+    const long long items = (long long)A.kv_heads * row_tiles * (job == 0 ? 1 : A.batch);
+    const long long most = items * (job == 0 ? T.prefix_tiles : (A.cap + TK - 1) / TK);
+    if (most > 0x7FFFFFFFLL) {
+        *bytes = SIZE_MAX;
+        return T;
+    }
+    (job == 0 ? T.prefix_row_tiles : T.own_row_tiles) = (int)row_tiles;
     const int sms = num_sms();
     T.ctas = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
-    const size_t slots = share ? (size_t)(T.ctas + prefix_items + own_items) : 2 * (size_t)T.ctas;
-    const size_t units_b = 256, item_b = up256(4 * (size_t)own_items), ml_b = up256(slots * T.tile_rows * sizeof(float2));
-    if (P) {
-        uint8_t* p = static_cast<uint8_t*>(ws);
-        T.units = reinterpret_cast<int*>(p);
-        T.item_unit = reinterpret_cast<int*>(p + units_b);
-        T.ml = reinterpret_cast<float2*>(p + units_b + item_b);
-        T.o = reinterpret_cast<float*>(p + units_b + item_b + ml_b);
-        *P = T;
-    }
-    return units_b + item_b + ml_b + up256(slots * T.tile_rows * (size_t)d * sizeof(float));
+    const size_t slots = T.keep ? (size_t)(T.ctas + items) : 2 * (size_t)T.ctas;
+    const size_t item_b = job == 1 && T.keep ? up256(4 * (size_t)items) : 0, cut_b = up256(sizeof(int4) * (size_t)T.ctas);
+    const size_t ml_b = up256(slots * T.tile_rows * sizeof(float2));
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    auto take = [&](size_t b) { uint8_t* r = p; p += ws ? b : 0; return r; };
+    T.units = reinterpret_cast<int*>(take(256));
+    T.item_unit = reinterpret_cast<int*>(take(item_b));
+    T.cut = reinterpret_cast<int4*>(take(cut_b));
+    T.ml = reinterpret_cast<float2*>(take(ml_b));
+    T.o = reinterpret_cast<float*>(p);
+    *bytes = 256 + item_b + cut_b + ml_b + up256(slots * T.tile_rows * (size_t)d * sizeof(float));
+    return T;
+}
+
+cudaError_t launch_attn_merge(const AttnArgs& A, const TilePlan& prefix, const TilePlan& own, int type, int d,
+                              cudaStream_t stream) {
+    if (type == PLM_F16)
+        return d == 64 ? merge_launch<__half, 64>(A, prefix, own, stream) : merge_launch<__half, 128>(A, prefix, own, stream);
+    return d == 64 ? merge_launch<__nv_bfloat16, 64>(A, prefix, own, stream)
+                   : merge_launch<__nv_bfloat16, 128>(A, prefix, own, stream);
 }
 
 cudaError_t launch_attn_tile(const AttnArgs& A, const TilePlan& P, int type, int d, cudaStream_t stream) {

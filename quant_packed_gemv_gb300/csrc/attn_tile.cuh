@@ -2,10 +2,10 @@
 // partial results.
 //
 // A UNIT is 128 keys for one row tile and key/value head.  An ITEM is a row
-// tile of a job with all its keys: job one is the shared prefix, whose row
-// tiles run over the rows of the whole batch; the others are the sequences'
-// own keys.  The units of all items in order are cut evenly over the CTAs, so
-// an item may be cut too; each piece leaves (m, l, O) in a slot.
+// tile with all its keys: of the shared prefix, whose row tiles run over the
+// rows of the whole batch, or of a sequence's own keys (two launches, where a
+// call has both).  The units of all items in order are cut evenly over the
+// CTAs, so an item may be cut too; its pieces leave (m, l, O) in slots.
 #pragma once
 
 #include "attn.cuh"
@@ -19,11 +19,14 @@ struct TilePlan {
     int ctas;
     int prefix_tiles;      // units per prefix item; 0: no prefix job
     int prefix_row_tiles;  // row tiles of the prefix job (per head)
-    int own;               // own jobs in the tile kernel
     int own_row_tiles;     // row tiles of a sequence's rows (per head)
+    int job;               // what a launch does: 0 the prefix, 1 the own keys
+    int keep;              // every piece is kept, to be added to others
     // workspace
     int* units;            // [1] all units (own: known on the device only)
-    int* item_unit;        // [own items] first unit of the item (own jobs)
+    int* item_unit;        // [own items] first unit of the item (own, kept pieces)
+    int4* cut;             // [ctas] the item that a CTA goes on with, if it does not begin with one
+                           // (own, else): (sequence, row tile) or -1, head, first unit, units
     float* o;              // [slots][tile_rows][D], not divided by the sum
     float2* ml;            // [slots][tile_rows]: m (log2), l
 };
@@ -62,37 +65,87 @@ __device__ __forceinline__ int unit_cta(int u, int U, int ctas) {
     return c;
 }
 
-// Slot of the piece of an item that CTA c holds.  With a prefix job every
-// piece of every item is kept: items and CTAs both follow the units' order,
-// so c + item is free.  Otherwise only cut items are: a CTA has at most one
-// piece that does not begin its item and one cut piece that does.
+// Slot of the piece of an item that CTA c holds.  Where every piece is kept:
+// items and CTAs both follow the units' order, so c + item is free.  Otherwise
+// only cut items are: a CTA has at most one piece that does not begin its item
+// and one cut piece that does.
 __host__ __device__ __forceinline__ long long piece_slot(const TilePlan& P, int c, int item, bool begins) {
-    return P.prefix_tiles > 0 ? (long long)c + item : 2LL * c + begins;
+    return P.keep ? (long long)c + item : 2LL * c + begins;
 }
 
-// One row's sums over partial results.
+// One row's sums, by a warp: PER dims a lane.
 template <int PER> struct RowSum {
     float m = -INFINITY, l = 0.0f, o[PER] = {};
-    __device__ __forceinline__ void add(float m2, float l2, const float (&o2)[PER]) {
-        if (l2 == 0.0f) return;   // a piece without keys
-        const float mn = fmaxf(m, m2);
-        const float a = exp2f(m - mn), b = exp2f(m2 - mn);
-        l = l * a + l2 * b;
+
+    // Adds the pieces of an item (first unit u0, `tiles` of U units), row i of
+    // its tile: a lane each for their weights, then their dims four pieces at a
+    // time, all in the order of the units.
+    __device__ void pieces(const TilePlan& P, int u0, int tiles, int U, int item, int i, int lane) {
+        const int ctas = unit_ctas(P, U), c0 = unit_cta(u0, U, ctas), n = unit_cta(u0 + tiles - 1, U, ctas) - c0 + 1;
+        for (int p0 = 0; p0 < n; p0 += 32) {
+            const int some = min(32, n - p0);
+            const long long at = piece_slot(P, c0 + p0 + min(lane, some - 1), item, p0 + lane == 0) * P.tile_rows + i;
+            float2 ml = P.ml[at];
+            if (lane >= some || ml.y == 0.0f) ml = make_float2(-INFINITY, 0.0f);   // a piece without keys
+            const float mn = fmaxf(m, warp_max(ml.x));
+            const float old = m == -INFINITY ? 0.0f : ex2(m - mn), w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mn);
+            m = mn;
+            l = l * old + warp_sum(w * ml.y);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) o[i] = o[i] * a + o2[i] * b;
-        m = mn;
+            for (int k = 0; k < PER; ++k) o[k] *= old;
+            for (int p = 0; p < some; p += 4) {
+                float v[4][PER];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const long long row = __shfl_sync(0xFFFFFFFFu, at, min(p + q, some - 1));
+                    const float* src = P.o + row * (32 * PER) + PER * lane;
+                    if constexpr (PER == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
+                        v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        v[q][0] = x.x; v[q][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float f = __shfl_sync(0xFFFFFFFFu, w, min(p + q, 31));
+                    if (p + q < some && f != 0.0f)
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) o[k] = fmaf(f, v[q][k], o[k]);
+                }
+            }
+        }
+    }
+
+    // Row of the output: o / l, or zeros and lse = -inf where there was no key.
+    template <class E>
+    __device__ void store(const AttnArgs& A, long long tok, int qh, int lane) const {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const long long off = tok * A.o_ts + (long long)qh * A.o_hs + PER * lane;
+        if constexpr (PER == 4) {
+            attn_store4<E>(A, off, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+        } else if (A.o_f32) {
+            *reinterpret_cast<float2*>(static_cast<float*>(A.o) + off) = make_float2(o[0] * inv, o[1] * inv);
+        } else {
+            *reinterpret_cast<uint32_t*>(static_cast<E*>(A.o) + off) = pack_pair<E>(o[0] * inv, o[1] * inv);
+        }
+        if (A.lse && lane == 0) A.lse[tok * A.heads + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 };
 
-// Units at most (the kernel counts them in an int).
-long long tile_units(const AttnArgs& A, bool share, bool own);
-
-// TilePlan of a problem; its workspace pointers are set from ws (may be null).
-size_t tile_plan(const AttnArgs& A, int d, bool share, bool own, void* ws, TilePlan* P);
+// Plan of a launch of the tile kernel: of the prefix (job 0), or of the own
+// keys (job 1; share: the prefix is done apart).  Its workspace starts at ws
+// (may be null); *bytes is its size, or SIZE_MAX if there are too many units.
+TilePlan tile_plan(const AttnArgs& A, int d, int job, bool share, void* ws, size_t* bytes);
 
 cudaError_t launch_attn_tile(const AttnArgs& A, const TilePlan& P, int type, int d, cudaStream_t stream);
 
-// At most 16 query rows per sequence and key/value head; P: prefix results to
+// Adds the pieces of both launches for every row.
+cudaError_t launch_attn_merge(const AttnArgs& A, const TilePlan& prefix, const TilePlan& own, int type, int d,
+                              cudaStream_t stream);
+
+// At most 32 query rows per sequence and key/value head; P: prefix results to
 // add, or null.
 cudaError_t launch_attn_rows(const AttnArgs& A, const TilePlan* P, int type, int d, cudaStream_t stream);
 
