@@ -89,7 +89,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
                  "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
                  :: "r"(a), PLM_I16(r, 0), PLM_I16(r, 16) : "memory");
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads before it; names the registers of one so that nothing
+// uses them earlier.
+#define PLM_W4(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+#define PLM_W16(r, i) PLM_W4(r, i), PLM_W4(r, i + 4), PLM_W4(r, i + 8), PLM_W4(r, i + 12)
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PLM_W16(r, 0), PLM_W16(r, 16) :: "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int token, int head, int page,
@@ -349,30 +355,33 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         W.start(A, P, lane);
         // ------------------------------------------------------- the products
         constexpr uint32_t ID_S = idesc<E>(128, false), ID_O = idesc<E>(D, true);
-        const uint32_t ring = smem_u32(sm + L::RING), qs = smem_u32(sm);
+        // the operands' descriptors; a place in shared memory adds bytes / 16
+        const uint64_t qd = desc_sw128(smem_u32(sm), 16), kd = desc_sw128(smem_u32(sm + L::RING), 16),
+                       vd = desc_sw128(smem_u32(sm + L::RING), L::HALF);
         int n = 0;            // tiles taken from the ring
         int step = 0;         // units so far (all pieces)
         int pieces = 0;
         // S of row tile t (buffer sb) from the K tile in slot
         auto product_s = [&](int t, int sb, int slot) {
             if (lane == 0) {
+                const uint64_t a = qd + t * (L::QTILE / 16), b = kd + (uint32_t)slot * (L::STAGE / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * L::HALF + (k & 3) * 32;
-                    mma_ss(tmem + TM_S + 128 * sb, desc_sw128(qs + t * L::QTILE + off, 16),
-                           desc_sw128(ring + slot * L::STAGE + off, 16), ID_S, k > 0);
+                    const uint32_t off = ((k >> 2) * L::HALF + (k & 3) * 32) / 16;
+                    mma_ss(tmem + TM_S + 128 * sb, a + off, b + off, ID_S, k > 0);
                 }
                 commit(&s_ready[sb]);
             }
             __syncwarp();
         };
-        auto product_o = [&](int t, int sb, int slot, bool first) {
+        auto product_o = [&](int t, int sb, int slot, bool first, bool last) {
             if (lane == 0) {
+                const uint64_t b = vd + (uint32_t)slot * (L::STAGE / 16);
+                const uint32_t p = tmem + TM_S + 128 * sb, o = tmem + TM_O + D * t;
+                mma_ts(o, p, b, ID_O, !first);
 #pragma unroll
-                for (int k = 0; k < TK / 16; ++k)
-                    mma_ts(tmem + TM_O + D * t, tmem + TM_S + 128 * sb + 8 * k,
-                           desc_sw128(ring + slot * L::STAGE + k * 2048, L::HALF), ID_O, !(first && k == 0));
-                commit(&o_done[t]);
+                for (int k = 1; k < TK / 16; ++k) mma_ts(o, p + 8 * k, b + k * (2048 / 16), ID_O, 1);
+                if (NT == 1 || last) commit(&o_done[t]);
             }
             __syncwarp();
         };
@@ -401,33 +410,29 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                     product_s(0, (step + 1) & 1, kt % L::SLOTS);
                     free_slot(kt % L::SLOTS);
                 }
-                ok = wait_full(vt);
+                if (NT == 1) ok = wait_full(vt);
                 if (!ok) break;
                 const int left = S.keys - (S.key0 + i * TK);
-                if (P.job == 1 && left < TK) {
-                    // the pages' rows past the end may hold anything, and 0 * NaN is NaN
-                    uint8_t* v = sm + L::RING + (vt % L::SLOTS) * L::STAGE;
-                    for (int e = lane; e < (TK - left) * (D / 8); e += 32) {
-                        const int r = left + e / (D / 8), c = e % (D / 8);
-                        *reinterpret_cast<uint4*>(v + (c >> 3) * L::HALF + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int sb = NT == 2 ? t : step & 1;
+                    // P of this unit; for NT = 2 its arrivals also say that V and the next K have landed
                     ok = warp_wait(&p_ready[sb], NT == 2 ? step & 1 : (step >> 1) & 1);
                     if (!ok) break;
                     tc_after();
-                    product_o(t, sb, vt % L::SLOTS, i == 0);
+                    if (t == 0 && P.job == 1 && left < TK) {
+                        // the pages' rows past the end may hold anything, and 0 * NaN is NaN
+                        uint8_t* v = sm + L::RING + (vt % L::SLOTS) * L::STAGE;
+                        for (int e = lane; e < (TK - left) * (D / 8); e += 32) {
+                            const int r = left + e / (D / 8), c = e % (D / 8);
+                            *reinterpret_cast<uint4*>(v + (c >> 3) * L::HALF + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    product_o(t, sb, vt % L::SLOTS, i == 0, !more);
                     if (t == NT - 1) free_slot(vt % L::SLOTS);
                     if (NT == 2 && more) {
-                        if (t == 0) {
-                            ok = wait_full(kt);
-                            if (!ok) break;
-                            tc_after();
-                        }
                         product_s(t, t, kt % L::SLOTS);
                         if (t == NT - 1) free_slot(kt % L::SLOTS);
                     }
@@ -442,6 +447,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const float sl2 = fabsf(A.scale) * LOG2E, raise_at = RAISE / sl2;
         int step = 0;   // units so far
+        int pieces = 0;
         long long tok;
         int qh;
         // Q row i into the operand tile; a negative scale turns its signs
@@ -469,6 +475,14 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             float m = -INFINITY, l = 0.0f;   // m in units of S
             for (int u = 0; ok && u < S.tiles; ++u, ++step) {
                 const int sb = NT == 2 ? t : step & 1;
+                if (NT == 2 && (warp & 3) == 0) {
+                    // while S is on its way: V of this unit and the next K of the piece (a wait of
+                    // the MMA warp leaves the tensor cores idle, one here does not)
+                    const int vt = 2 * step + 1;
+                    ok = warp_wait(&full[vt % L::SLOTS], (vt / L::SLOTS) & 1);
+                    if (ok && u + 1 < S.tiles) ok = warp_wait(&full[(vt + 1) % L::SLOTS], ((vt + 1) / L::SLOTS) & 1);
+                    if (!ok) break;
+                }
                 const uint32_t sa = tmem + lanes + TM_S + 128 * sb;
                 ok = warp_wait(&s_ready[sb], NT == 2 ? step & 1 : (step >> 1) & 1);
                 if (!ok) break;
@@ -482,7 +496,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                     uint32_t* r = reinterpret_cast<uint32_t*>(s);
                     tmem_ld32(sa + c0, r);
                     tmem_ld32(sa + c0 + 32, r + 32);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
+                    tmem_ld_wait(r + 32);
                     if (part)
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
@@ -506,8 +521,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                     const float mn = raise ? fmaxf(m, mx) : m;
                     const float keep = mn == m ? 1.0f : ex2((m - mn) * sl2);
                     if (u > 0) {   // O holds the products of the units before
-                        // the (step)-th PV product of this row tile is the last one issued
-                        ok = warp_wait(&o_done[t], (step - 1) & 1);
+                        // (NT = 2: S of this unit was issued after them and is there)
+                        if (NT == 1) ok = warp_wait(&o_done[t], (step - 1) & 1);
                         if (!ok) break;
                         tc_after();
                         const uint32_t oa = tmem + lanes + TM_O + D * t;
@@ -515,7 +530,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                         for (int c = 0; c < D; c += 32) {
                             uint32_t r[32];
                             tmem_ld32(oa + c, r);
-                            tmem_ld_wait();
+                            tmem_ld_wait(r);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * keep);
                             tmem_st32(oa + c, r);
@@ -563,7 +578,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             const int my_qh = qh;
             have = W.next(A, P, lane, S);
             if (have) load_q(S);
-            ok = warp_wait(&o_done[t], (step - 1) & 1);
+            ok = warp_wait(&o_done[t], (NT == 1 ? step - 1 : pieces) & 1);
+            ++pieces;
             if (!ok) break;
             tc_after();
             const uint32_t oa = tmem + lanes + TM_O + D * t;
@@ -576,7 +592,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 for (int c = 0; c < D; c += 32) {
                     uint32_t r[32];
                     tmem_ld32(oa + c, r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
                     if (in)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
@@ -593,7 +609,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 for (int c = 0; c < D; c += 32) {
                     uint32_t r[32];
                     tmem_ld32(oa + c, r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
                     if (in)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
