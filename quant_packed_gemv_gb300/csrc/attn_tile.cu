@@ -47,9 +47,10 @@ template <int D, int NT> struct TileSmem {
     static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lead) {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Low word of a shared-memory operand's descriptor: address and leading offset
+// in units of 16 bytes.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
+    return ((saddr >> 4) & 0x3FFF) | ((lead >> 4) << 16);
 }
 template <class E> struct KindOf;
 template <> struct KindOf<__half> { static constexpr uint32_t AB = 0; };
@@ -58,15 +59,24 @@ template <class E> __host__ __device__ constexpr uint32_t idesc(uint32_t n, bool
     return (1u << 4) | KindOf<E>::AB | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+// The MMAs.  All lanes of the warp execute the code around them, so that the
+// operands stay in uniform registers, and one lane (`lead`) issues: in a
+// branch of one lane every operand is moved over, and an MMA took ~95 cycles
+// to issue instead of the 64 it takes to run (prompts 456 -> 395 us).
+// Operands in shared memory are given by the low words of their descriptors;
+// the high word is the same for all.
+#define PLM_DESC_HI "0x40004040"
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "mov.b64 da, {%1, " PLM_DESC_HI "};\n\tmov.b64 db, {%2, " PLM_DESC_HI "};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "mov.b64 db, {%2, " PLM_DESC_HI "};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(lead) : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
@@ -356,37 +366,35 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         // ------------------------------------------------------- the products
         constexpr uint32_t ID_S = idesc<E>(128, false), ID_O = idesc<E>(D, true);
         // the operands' descriptors; a place in shared memory adds bytes / 16
-        const uint64_t qd = desc_sw128(smem_u32(sm), 16), kd = desc_sw128(smem_u32(sm + L::RING), 16),
-                       vd = desc_sw128(smem_u32(sm + L::RING), L::HALF);
+        const uint32_t qd = desc_lo(smem_u32(sm), 16), kd = desc_lo(smem_u32(sm + L::RING), 16),
+                       vd = desc_lo(smem_u32(sm + L::RING), L::HALF);
+        uint32_t leader;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
         int n = 0;            // tiles taken from the ring
         int step = 0;         // units so far (all pieces)
         int pieces = 0;
         // S of row tile t (buffer sb) from the K tile in slot
         auto product_s = [&](int t, int sb, int slot) {
-            if (lane == 0) {
-                const uint64_t a = qd + t * (L::QTILE / 16), b = kd + (uint32_t)slot * (L::STAGE / 16);
+            const uint32_t a = qd + t * (L::QTILE / 16), b = kd + (uint32_t)slot * (L::STAGE / 16);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * L::HALF + (k & 3) * 32) / 16;
-                    mma_ss(tmem + TM_S + 128 * sb, a + off, b + off, ID_S, k > 0);
-                }
-                commit(&s_ready[sb]);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * L::HALF + (k & 3) * 32) / 16;
+                mma_ss(tmem + TM_S + 128 * sb, a + off, b + off, ID_S, k > 0, leader);
             }
+            if (leader) commit(&s_ready[sb]);
             __syncwarp();
         };
         auto product_o = [&](int t, int sb, int slot, bool first, bool last) {
-            if (lane == 0) {
-                const uint64_t b = vd + (uint32_t)slot * (L::STAGE / 16);
-                const uint32_t p = tmem + TM_S + 128 * sb, o = tmem + TM_O + D * t;
-                mma_ts(o, p, b, ID_O, !first);
+            const uint32_t b = vd + (uint32_t)slot * (L::STAGE / 16);
+            const uint32_t p = tmem + TM_S + 128 * sb, o = tmem + TM_O + D * t;
+            mma_ts(o, p, b, ID_O, !first, leader);
 #pragma unroll
-                for (int k = 1; k < TK / 16; ++k) mma_ts(o, p + 8 * k, b + k * (2048 / 16), ID_O, 1);
-                if (NT == 1 || last) commit(&o_done[t]);
-            }
+            for (int k = 1; k < TK / 16; ++k) mma_ts(o, p + 8 * k, b + k * (2048 / 16), ID_O, 1, leader);
+            if (leader && (NT == 1 || last)) commit(&o_done[t]);
             __syncwarp();
         };
         auto free_slot = [&](int slot) {
-            if (lane == 0) commit(&empty[slot]);
+            if (leader) commit(&empty[slot]);
             __syncwarp();
         };
         while (ok && W.next(A, P, lane, S)) {
