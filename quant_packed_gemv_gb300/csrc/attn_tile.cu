@@ -40,8 +40,8 @@ template <int D, int NT> struct TileSmem {
     static constexpr int SLOTS = D == 64 ? 10 : NT == 2 ? 5 : 6;
     static constexpr int RING = NT * QTILE;
     static constexpr int BAR = RING + SLOTS * STAGE;
-    // full, empty per slot; S ready, P ready, O done, Q ready per buffer
-    static constexpr int NBAR = 2 * SLOTS + 8;
+    // full, empty per slot; S ready, P ready, O done, Q ready, warps together per buffer
+    static constexpr int NBAR = 2 * SLOTS + 10;
     static constexpr int TMEMP = BAR + 8 * NBAR;
     static constexpr int ALLOC = TMEMP + 16 + 1024;
     static_assert(ALLOC <= 227 * 1024, "shared memory");
@@ -286,6 +286,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
     uint64_t* p_ready = s_ready + 2;        // [2] per S buffer, one arrival per warp
     uint64_t* o_done = p_ready + 2;         // [2] per row tile: a PV product has finished
     uint64_t* q_ready = o_done + 2;         // [2] per row tile
+    uint64_t* together = q_ready + 2;       // [2] per row tile: its four warps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::TMEMP);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int TMA_WARP = 4 * NT, MMA_WARP = 4 * NT + 1;
@@ -296,6 +297,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             mbar_init(&p_ready[i], 4);
             mbar_init(&o_done[i], 1);
             mbar_init(&q_ready[i], 4);
+            mbar_init(&together[i], 4);
         }
         fence_barrier_init();
     }
@@ -458,17 +460,24 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         int pieces = 0;
         long long tok;
         int qh;
-        // Q row i into the operand tile; a negative scale turns its signs
+        // This warp's 32 rows of Q into the operand tile, whole rows at a time (a
+        // row per thread instead costs 7 k cycles a piece, four times as much); a
+        // negative scale turns its signs
         auto load_q = [&](const Piece& C) {
-            uint8_t* dst = sm + t * L::QTILE + i * 128;
             const bool in = tile_row(A, P, C, t * 128 + i, tok, qh);
+            const long long mine = in ? tok * A.q_ts + (long long)qh * A.q_hs : -1;
             const uint32_t sign = A.scale < 0.0f ? 0x80008000u : 0u;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + (in ? tok * A.q_ts + (long long)qh * A.q_hs : 0));
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            constexpr int CH = D / 8, AT = 32 / CH;   // 16-byte chunks of a row, rows at a time
+            const int c = lane % CH;
+            uint8_t* dst = sm + t * L::QTILE + (c >> 3) * L::HALF;
+#pragma unroll 8
+            for (int k = 0; k < 32 / AT; ++k) {
+                const int r = k * AT + lane / CH;
+                const long long off = __shfl_sync(0xFFFFFFFFu, mine, r);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (off >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + off) + c);
                 v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
-                *reinterpret_cast<uint4*>(dst + (c >> 3) * L::HALF + (((c ^ i) & 7) << 4)) = v;
+                *reinterpret_cast<uint4*>(dst + (32 * (warp & 3) + r) * 128 + (((c ^ r) & 7) << 4)) = v;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -580,52 +589,61 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 if (lane == 0) mbar_arrive(&p_ready[sb]);
             }
             if (!ok) break;
-            // the next piece's Q, while the last product runs: S of this piece is done with it
-            const Piece C = S;
-            const long long my_tok = tok;
-            const int my_qh = qh;
-            have = W.next(A, P, lane, S);
-            if (have) load_q(S);
             ok = warp_wait(&o_done[t], (NT == 1 ? step - 1 : pieces) & 1);
             ++pieces;
             if (!ok) break;
             tc_after();
+            // O by way of the Q tile (its products are done), half of the dims at
+            // a time: rows go out whole, 16-byte chunks XORed with the row against
+            // bank conflicts
             const uint32_t oa = tmem + lanes + TM_O + D * t;
+            const bool final = S.whole && !P.keep;
+            const float f = !final ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;   // no key: zeros
             const float m2 = m * sl2;
-            const bool final = C.whole && !P.keep;
-            if (final) {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                const long long off = in ? my_tok * A.o_ts + (long long)my_qh * A.o_hs : 0;
+            const long long slot_row = piece_slot(P, blockIdx.x, S.item, S.begins) * P.tile_rows + t * 128 + i;
+            const long long mine = final ? (in ? tok * A.o_ts + (long long)qh * A.o_hs : -1) : slot_row * D;
+            constexpr int CW = D / 2, CH = CW / 4, AT = 32 / CH;   // dims and chunks of a half, rows at a time
+            // (a bounded wait, as every other: a barrier of the warps would hang if
+            // one of them gave up)
+            auto all_warps = [&](int nth) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&together[t]);
+                return warp_wait(&together[t], nth);
+            };
+            ok = all_warps(0);   // they have seen the piece's last S
+            if (!ok) break;
+            float4* stage = reinterpret_cast<float4*>(sm + t * L::QTILE + (warp & 3) * (32 * CW * 4));
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < CW; c += 32) {
                     uint32_t r[32];
-                    tmem_ld32(oa + c, r);
+                    tmem_ld32(oa + h * CW + c, r);
                     tmem_ld_wait(r);
-                    if (in)
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            attn_store4<E>(A, off + c + k, make_float4(__uint_as_float(r[k]) * inv, __uint_as_float(r[k + 1]) * inv,
-                                                                       __uint_as_float(r[k + 2]) * inv, __uint_as_float(r[k + 3]) * inv));
+                    for (int k = 0; k < 32; k += 4)
+                        stage[lane * CH + (((c + k) / 4) ^ (lane & (CH - 1)))] =
+                            make_float4(__uint_as_float(r[k]) * f, __uint_as_float(r[k + 1]) * f,
+                                        __uint_as_float(r[k + 2]) * f, __uint_as_float(r[k + 3]) * f);
                 }
-                if (in && A.lse)
-                    A.lse[my_tok * A.heads + my_qh] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
-            } else {
-                const long long slot = piece_slot(P, blockIdx.x, C.item, C.begins);
-                const long long row = slot * P.tile_rows + t * 128 + i;
-                float4* o = reinterpret_cast<float4*>(P.o + row * D);
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(oa + c, r);
-                    tmem_ld_wait(r);
-                    if (in)
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            o[(c + k) / 4] = make_float4(__uint_as_float(r[k]), __uint_as_float(r[k + 1]),
-                                                         __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                __syncwarp();
+                const int c = lane % CH;
+#pragma unroll 4
+                for (int k = 0; k < 32 / AT; ++k) {
+                    const int r = k * AT + lane / CH;
+                    const long long off = __shfl_sync(0xFFFFFFFFu, mine, r);
+                    const float4 v = stage[r * CH + (c ^ (r & (CH - 1)))];
+                    if (!final) *reinterpret_cast<float4*>(P.o + off + h * CW + 4 * c) = v;
+                    else if (off >= 0) attn_store4<E>(A, off + h * CW + 4 * c, v);
                 }
-                if (in) P.ml[row] = make_float2(m2, l);
+                __syncwarp();
             }
+            if (!final) P.ml[slot_row] = make_float2(m2, l);
+            else if (in && A.lse) A.lse[tok * A.heads + qh] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
+            ok = all_warps(1);   // the tile is free
+            if (!ok) break;
+            have = W.next(A, P, lane, S);
+            if (have) load_q(S);
             // O has been read: the next piece's first product (after its P) may overwrite it
             tc_before();
         }
@@ -642,7 +660,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
 // The items that are cut between CTAs (own keys alone): block (c, y) adds the
 // rows of the item that CTA c goes on with, if c - 1 began it.  The blocks
 // from P.ctas on write the rows of sequences without keys.
-constexpr int JOIN_Y = 8;
+constexpr int JOIN_Y = 32;   // a row per warp
 template <class E, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     grid_launch_dependents();
