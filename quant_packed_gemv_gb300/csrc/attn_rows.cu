@@ -10,17 +10,19 @@
 //
 // Layout.  The keys are the M side of mma.sync m16n8k16, so 8 rows cost no
 // padding, and the sums over d and over keys may run in any order.  Lane
-// (g, t) = (lane / 4, lane % 4) therefore loads 16 bytes of K rows g and
-// g + 8 (dims 32 c + 8 t ..) and of V rows 2t, 2t + 1, 2t + 8, 2t + 9 (dims
-// 64 c + 8 g ..) and uses them as fragments where they are: no shared memory.
-// Rows of Q follow K's order of d; P^T needs one movmatrix per 8 x 8 block.
-// Up to 16 rows Q stays in registers; beyond, the warps share it in shared
-// memory, so that O (32 registers per 8 rows at D = 128) has room.
+// (g, t) = (lane / 4, lane % 4) therefore takes 16 bytes of K rows g and g + 8
+// (dims 32 c + 8 t ..) and of V rows 2t, 2t + 1, 2t + 8, 2t + 9 (dims 64 c + 8 g
+// ..) as they lie and uses them as fragments.  Rows of Q follow K's order of d;
+// P^T needs one movmatrix per 8 x 8 block.  Up to 16 rows Q stays in registers;
+// beyond, the warps share it in shared memory, so that O (32 registers per 8
+// rows at D = 128) has room.
 //
 // Bound: HBM (4 D bytes per key and head pair, ~2 operations per byte and
-// row).  A warp keeps the next 16 keys' K and this block's V in flight (8 KB
-// at D = 128); the warps of a CTA and the CTAs of a cluster take the blocks
-// in turn and add their parts through shared memory, in a fixed order.
+// row).  Each warp brings its blocks (8 KB of K and V at D = 128) into a ring of
+// its own by cp.async, 16-byte chunks XORed so that the fragment loads are free
+// of bank conflicts; keys past the end are filled with zeros and not read.  The
+// warps of a CTA and the CTAs of a cluster take the blocks in turn and add
+// their parts through shared memory, in a fixed order.
 #include "attn_tile.cuh"
 
 namespace plm {
@@ -54,18 +56,31 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t words(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
-// Shared memory: Q fragments (NB > 2), then the parts of a pair's warps: per
-// warp the references m and sums l of its rows, then O [rows][D + 4] (padded
-// against conflicts).
+// Shared memory: Q fragments (NB > 2), then the warps' rings, in whose place
+// the parts of the warps go at the end: references m and sums l of the rows,
+// O [rows][D + 4] (padded against conflicts).
 template <int D, int NB> struct RowsSmem {
     static constexpr int ROWS = 8 * NB, PITCH = D + 4;
+    static constexpr int STAGES = D == 64 ? 4 : 2, STAGE = 16 * D * 2;   // bytes of 16 keys' K, or V
+    struct Parts {
+        float m[DW][ROWS], l[DW][ROWS];
+        float o[DW][ROWS][PITCH];
+    };
     uint4 q[NB > 2 ? NB * (D / 32) * 32 : 1];
-    float m[DW][ROWS], l[DW][ROWS];
-    float o[DW][ROWS][PITCH];
+    union {
+        uint8_t ring[DW][STAGES][2][STAGE];
+        Parts part;
+    };
 };
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
 template <class E, int D, int NB>
-__global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
+__global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     using Sm = RowsSmem<D, NB>;
     constexpr int KC = D / 32, VC = D / 64;   // 16-byte chunks per lane of a K row, of a V row
     constexpr bool QS = NB > 2;
@@ -81,8 +96,8 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const int row = attn_row(A, b), len = attn_len(A, row);
     const int* tab = A.table + (long long)max(row, 0) * A.table_stride;
     const long long head = (long long)h * A.kv_hs;
-    const E* kbase = static_cast<const E*>(A.k) + head + 8 * t;
-    const E* vbase = static_cast<const E*>(A.v) + head + 8 * g;
+    const E* kbase = static_cast<const E*>(A.k) + head;
+    const E* vbase = static_cast<const E*>(A.v) + head;
     const int mask = (1 << A.page_shift) - 1;
 
     // Q as the B operand: row 8 nb + g, dims 32 c + 8 t ..; zeros past the rows
@@ -128,49 +143,60 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const bool shares = attn_shares(A, P, len);
     const int first = shares ? A.prefix >> 4 : 0;   // the prefix is a multiple of 16
 
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // Block i of this warp's turn into its ring; K and V rows are whole, 16 bytes
+    // (8 dims) a lane, chunk c of row r at c ^ 4 (r % 2) for K, c ^ (r & 6) for V
+    constexpr int CH = D / 8;
+    const int cc = lane % CH, cr = lane / CH;
+    const uint32_t ring = smem_u32(&sm.ring[warp][0][0][0]);
     auto page_of = [&](int blk) -> int { return blk < blocks ? __ldg(tab + ((blk << 4) >> A.page_shift)) : -1; };
-    auto load_k = [&](int blk, int page, uint4 (&kf)[2][KC]) {
-        const int j = blk << 4;
-        const bool in = page >= 0 && page < A.pages;
-        const E* p = kbase + (long long)page * A.page_stride + (long long)((j & mask) + g) * A.kv_ts;
+    auto fetch = [&](int blk, int page, int slot) {
+        if (blk < blocks) {
+            const int j = blk << 4;
+            const bool there = page >= 0 && page < A.pages;
+            const long long off = there ? (long long)page * A.page_stride + (long long)((j & mask) + cr) * A.kv_ts + 8 * cc : 0;
+            const uint32_t dst = ring + slot * (2 * Sm::STAGE);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-                kf[i][c] = in && j + g + 8 * i < len ? ldg_nc_v4(p + 8 * i * A.kv_ts + 32 * c) : zero;
+            for (int r = 0; r < 16; r += 32 / CH) {
+                const int row_ = r + cr;
+                const bool in = there && j + row_ < len;
+                const long long o_ = in ? off + (long long)r * A.kv_ts : 0;
+                cp16(dst + row_ * (2 * D) + ((cc ^ ((row_ & 1) << 2)) << 4), kbase + o_, in);
+                cp16(dst + Sm::STAGE + row_ * (2 * D) + ((cc ^ (row_ & 6)) << 4), vbase + o_, in);
+            }
+        }
+        cp_commit();
     };
 
-    int blk = first + stream, page = page_of(blk), page_n = page_of(blk + streams);
-    uint4 kf[2][KC];
-    if (blk < blocks) load_k(blk, page, kf);
-    for (; blk < blocks; blk += streams) {
-        const int j = blk << 4;
-        uint4 vf[4][VC];   // rows 2t, 2t + 1, 2t + 8, 2t + 9
-        {
-            const bool in = page >= 0 && page < A.pages;
-            const E* p = vbase + (long long)page * A.page_stride + (long long)((j & mask) + 2 * t) * A.kv_ts;
+    int blk = first + stream, page = page_of(blk);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = (i & 1) + 8 * (i >> 1);
-#pragma unroll
-                for (int c = 0; c < VC; ++c)
-                    vf[i][c] = in && j + 2 * t + k < len ? ldg_nc_v4(p + k * A.kv_ts + 64 * c) : zero;
-            }
-        }
-        const int page_nn = page_of(blk + 2 * streams);
+    for (int i = 0; i < Sm::STAGES - 1; ++i) {
+        const int next = page_of(blk + (i + 1) * streams);
+        fetch(blk + i * streams, page, i);
+        page = next;
+    }
+    for (int n = 0; blk < blocks; blk += streams, ++n) {
+        const int j = blk << 4, ahead = blk + (Sm::STAGES - 1) * streams;
+        const int next = page_of(ahead + streams);
+        cp_wait<Sm::STAGES - 2>();
+        __syncwarp();   // the block is there, and the slot of the one before has been read
+        fetch(ahead, page, (n + Sm::STAGES - 1) % Sm::STAGES);
+        page = next;
+        const uint8_t* ks = &sm.ring[warp][n % Sm::STAGES][0][0];
+        const uint8_t* vs = ks + Sm::STAGE;
         float s[NB][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
+        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
+        for (int c = 0; c < KC; ++c) {
+            const int at = g * (2 * D) + (((4 * c + t) ^ ((g & 1) << 2)) << 4);
+            const uint4 k0 = *reinterpret_cast<const uint4*>(ks + at), k1 = *reinterpret_cast<const uint4*>(ks + at + 16 * D);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
                 const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
-                mma16816<E>(s[nb], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qv.x, qv.y);
-                mma16816<E>(s[nb], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qv.z, qv.w);
+                mma16816<E>(s[nb], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
+                mma16816<E>(s[nb], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
             }
         }
-        if (blk + streams < blocks) load_k(blk + streams, page_n, kf);
         const bool part = j + 16 > all;
         bool raise = false;
 #pragma unroll
@@ -213,19 +239,23 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
             pb[nb][1] = transpose8x8(pack_pair<E>(p[2], p[3]));
         }
 #pragma unroll
-        for (int c = 0; c < VC; ++c)
+        for (int c = 0; c < VC; ++c) {
+            const uint8_t* at = vs + 2 * t * (2 * D) + (((8 * c + g) ^ (2 * t)) << 4);
+            uint4 vf[4];   // rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vf[i] = *reinterpret_cast<const uint4*>(at + ((i & 1) + 8 * (i >> 1)) * (2 * D));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {   // dims 64 c + 8 g + 2 i, + 1
-                const uint32_t w0 = words(vf[0][c], i), w1 = words(vf[1][c], i), w2 = words(vf[2][c], i),
-                               w3 = words(vf[3][c], i);
+                const uint32_t w0 = words(vf[0], i), w1 = words(vf[1], i), w2 = words(vf[2], i), w3 = words(vf[3], i);
                 const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
                 const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) mma16816<E>(o[nb][4 * c + i], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
             }
-        page = page_n;
-        page_n = page_nn;
+        }
     }
+    cp_wait<0>();
+    __syncthreads();   // the rings make room for the parts
 
     // this warp's part
 #pragma unroll
@@ -235,12 +265,12 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
 #pragma unroll
             for (int of = 4; of < 32; of <<= 1) l[nb][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][i], of);
             if (g == 0) {
-                sm.m[warp][8 * nb + 2 * t + i] = m[nb][i];
-                sm.l[warp][8 * nb + 2 * t + i] = l[nb][i];
+                sm.part.m[warp][8 * nb + 2 * t + i] = m[nb][i];
+                sm.part.l[warp][8 * nb + 2 * t + i] = l[nb][i];
             }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                *reinterpret_cast<float2*>(&sm.o[warp][8 * nb + 2 * t + i][64 * (k >> 2) + 8 * g + 2 * (k & 3)]) =
+                *reinterpret_cast<float2*>(&sm.part.o[warp][8 * nb + 2 * t + i][64 * (k >> 2) + 8 * g + 2 * (k & 3)]) =
                     make_float2(o[nb][k][i], o[nb][k][i + 2]);
         }
     }
@@ -248,35 +278,49 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     if (cs > 1) cluster_barrier();
     else __syncthreads();
     if (P.prefix_tiles > 0) grid_wait_prior();   // the tile kernel's results
-    // A warp adds up a row at a time, 4 (2 at D = 64) dims a lane: the parts of
+    // A warp adds up N rows at a time, 4 (2 at D = 64) dims a lane: the parts of
     // the cluster's warps (at most 32, a lane each for their weights), then the
-    // pieces of the row's prefix item, both in order.
-    constexpr int PER = D / 32;
-    for (int r = blockIdx.z + cs * warp; r < rows; r += cs * DW) {
-        const bool part = lane < cs * DW;
+    // pieces of the rows' prefix items, both in order.
+    constexpr int PER = D / 32, N = NB == 1 ? 2 : 4;
+    const int step = cs * DW;
+    for (int r0 = blockIdx.z + cs * warp; r0 < rows; r0 += N * step) {
+        RowSum<PER, N> R;
         const int pz = lane / DW, pw = lane % DW;
-        float pm = part ? peer_f32(&sm.m[pw][r], pz, cs) : -INFINITY;
-        const float pl = part ? peer_f32(&sm.l[pw][r], pz, cs) : 0.0f;
-        if (pl == 0.0f) pm = -INFINITY;   // no key
-        RowSum<PER> R;
-        R.m = warp_max(pm);
-        const float wgt = pm == -INFINITY ? 0.0f : ex2(pm - R.m);
-        R.l = warp_sum(wgt * pl);
-        for (int p = 0; p < cs * DW; ++p) {
-            const float f = __shfl_sync(0xFFFFFFFFu, wgt, p);
-            float v[PER];
-            peer_dims<PER>(&sm.o[p % DW][r][PER * lane], p / DW, cs, v);
-            if (f != 0.0f)
 #pragma unroll
-                for (int i = 0; i < PER; ++i) R.o[i] = fmaf(f, v[i], R.o[i]);
+        for (int j = 0; j < N; ++j) {
+            const int r = min(r0 + j * step, rows - 1);
+            const bool part = lane < cs * DW;
+            float pm = part ? peer_f32(&sm.part.m[pw][r], pz, cs) : -INFINITY;
+            const float pl = part ? peer_f32(&sm.part.l[pw][r], pz, cs) : 0.0f;
+            if (pl == 0.0f) pm = -INFINITY;   // no key
+            R.m[j] = warp_max(pm);
+            const float wgt = pm == -INFINITY ? 0.0f : ex2(pm - R.m[j]);
+            R.l[j] = warp_sum(wgt * pl);
+            for (int p = 0; p < cs * DW; ++p) {
+                const float f = __shfl_sync(0xFFFFFFFFu, wgt, p);
+                float v[PER];
+                peer_dims<PER>(&sm.part.o[p % DW][r][PER * lane], p / DW, cs, v);
+                if (f != 0.0f)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) R.o[j][i] = fmaf(f, v[i], R.o[j][i]);
+            }
         }
         if (shares) {
-            const long long gr = (long long)b * rows + r, rt = gr / P.tile_rows;
-            const int item = h * P.prefix_row_tiles + (int)rt, u0 = item * P.prefix_tiles;
-            R.pieces(P, u0, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, item,
-                     (int)(gr - rt * P.tile_rows), lane);
+            int item[N], u0[N], at[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const long long gr = (long long)b * rows + r0 + j * step, rt = gr / P.tile_rows;
+                item[j] = r0 + j * step < rows ? h * P.prefix_row_tiles + (int)rt : -1;
+                u0[j] = item[j] * P.prefix_tiles;
+                at[j] = (int)(gr - rt * P.tile_rows);
+            }
+            R.pieces(P, item, u0, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, at, lane);
         }
-        R.template store<E>(A, (long long)b * A.nq + r / A.group, h * A.group + r % A.group, lane);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int r = r0 + j * step;
+            if (r < rows) R.template store<E>(A, j, (long long)b * A.nq + r / A.group, h * A.group + r % A.group, lane);
+        }
     }
     if (cs > 1) cluster_barrier();   // no CTA leaves while its part is read
 }

@@ -687,10 +687,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
             RowSum<D / 32> R;
             if ((int)blockIdx.x < P.ctas) {
                 const int4 cut = P.cut[blockIdx.x];
-                R.pieces(P, cut.z, cut.w, *P.units, 0, i, lane);
+                R.pieces(P, {0}, {cut.z}, cut.w, *P.units, {i}, lane);
             }
             const long long r = (long long)rt * P.tile_rows + i, t = r / A.group;
-            R.template store<E>(A, (long long)b * A.nq + t, h * A.group + (int)(r - t * A.group), lane);
+            R.template store<E>(A, 0, (long long)b * A.nq + t, h * A.group + (int)(r - t * A.group), lane);
         }
 }
 
@@ -710,16 +710,16 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         if (attn_shares(A, P, attn_len(A, attn_row(A, b)))) {
             const long long r = tok * A.group + g, rt = r / P.tile_rows;
             const int item = h * P.prefix_row_tiles + (int)rt;
-            R.pieces(P, item * P.prefix_tiles, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, item,
-                     (int)(r - rt * P.tile_rows), lane);
+            R.pieces(P, {item}, {item * P.prefix_tiles}, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles,
+                     {(int)(r - rt * P.tile_rows)}, lane);
         }
         const int r = t * A.group + g, rt = r / W.tile_rows, pair = b * W.own_row_tiles + rt;
         const int tiles = own_tiles(A, W, pair);
         if (tiles > 0) {
             const int item = pair * A.kv_heads + h;
-            R.pieces(W, W.item_unit[item], tiles, U, item, r - rt * W.tile_rows, lane);
+            R.pieces(W, {item}, {W.item_unit[item]}, tiles, U, {r - rt * W.tile_rows}, lane);
         }
-        R.template store<E>(A, tok, qh, lane);
+        R.template store<E>(A, 0, tok, qh, lane);
     }
 }
 

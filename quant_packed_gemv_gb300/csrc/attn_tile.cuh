@@ -73,64 +73,99 @@ __host__ __device__ __forceinline__ long long piece_slot(const TilePlan& P, int 
     return P.keep ? (long long)c + item : 2LL * c + begins;
 }
 
-// One row's sums, by a warp: PER dims a lane.
-template <int PER> struct RowSum {
-    float m = -INFINITY, l = 0.0f, o[PER] = {};
+// The sums of N rows, by a warp: PER dims a lane.
+template <int PER, int N = 1> struct RowSum {
+    float m[N], l[N], o[N][PER];
+    __device__ RowSum() {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            m[j] = -INFINITY;
+            l[j] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) o[j][k] = 0.0f;
+        }
+    }
 
-    // Adds the pieces of an item (first unit u0, `tiles` of U units), row i of
-    // its tile: a lane each for their weights, then their dims four pieces at a
-    // time, all in the order of the units.
-    __device__ void pieces(const TilePlan& P, int u0, int tiles, int U, int item, int i, int lane) {
-        const int ctas = unit_ctas(P, U), c0 = unit_cta(u0, U, ctas), n = unit_cta(u0 + tiles - 1, U, ctas) - c0 + 1;
-        for (int p0 = 0; p0 < n; p0 += 32) {
-            const int some = min(32, n - p0);
-            const long long at = piece_slot(P, c0 + p0 + min(lane, some - 1), item, p0 + lane == 0) * P.tile_rows + i;
-            float2 ml = P.ml[at];
-            if (lane >= some || ml.y == 0.0f) ml = make_float2(-INFINITY, 0.0f);   // a piece without keys
-            const float mn = fmaxf(m, warp_max(ml.x));
-            const float old = m == -INFINITY ? 0.0f : ex2(m - mn), w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mn);
-            m = mn;
-            l = l * old + warp_sum(w * ml.y);
+    // Adds the pieces of each row's item (item[j] < 0: none; first unit u0[j],
+    // `tiles` of U units), row i[j] of its tile: a lane each for their weights,
+    // then their dims, all in the order of the units.  The loads of the rows, and
+    // of several pieces, are in flight together: each is a trip to L2.
+    __device__ void pieces(const TilePlan& P, const int (&item)[N], const int (&u0)[N], int tiles, int U, const int (&i)[N],
+                           int lane) {
+        constexpr int AHEAD = N * PER <= 4 ? 8 : 4;
+        const int ctas = unit_ctas(P, U);
+        int c0[N], n[N], most = 0;
 #pragma unroll
-            for (int k = 0; k < PER; ++k) o[k] *= old;
-            for (int p = 0; p < some; p += 4) {
-                float v[4][PER];
+        for (int j = 0; j < N; ++j) {
+            c0[j] = item[j] < 0 ? 0 : unit_cta(u0[j], U, ctas);
+            n[j] = item[j] < 0 ? 0 : unit_cta(u0[j] + tiles - 1, U, ctas) - c0[j] + 1;
+            most = max(most, n[j]);
+        }
+        for (int p0 = 0; p0 < most; p0 += 32) {
+            long long at[N];
+            float w[N];
+            float2 ml[N];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const long long row = __shfl_sync(0xFFFFFFFFu, at, min(p + q, some - 1));
-                    const float* src = P.o + row * (32 * PER) + PER * lane;
-                    if constexpr (PER == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(src);
-                        v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        v[q][0] = x.x; v[q][1] = x.y;
+            for (int j = 0; j < N; ++j) {
+                const bool in = p0 + lane < n[j];
+                at[j] = in ? piece_slot(P, c0[j] + p0 + lane, item[j], p0 + lane == 0) * P.tile_rows + i[j] : 0;
+                ml[j] = in ? P.ml[at[j]] : make_float2(-INFINITY, 0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (ml[j].y == 0.0f) ml[j].x = -INFINITY;   // a piece without keys
+                const float mn = fmaxf(m[j], warp_max(ml[j].x));
+                const float old = m[j] == -INFINITY ? 0.0f : ex2(m[j] - mn);
+                w[j] = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - mn);
+                m[j] = mn;
+                l[j] = l[j] * old + warp_sum(w[j] * ml[j].y);
+#pragma unroll
+                for (int k = 0; k < PER; ++k) o[j][k] *= old;
+            }
+            const int some = min(32, most - p0);
+            for (int p = 0; p < some; p += AHEAD) {
+                float v[N][AHEAD][PER];
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+#pragma unroll
+                    for (int q = 0; q < AHEAD; ++q) {
+                        // past the row's pieces: its weight is 0, and any piece will do
+                        const long long row = __shfl_sync(0xFFFFFFFFu, at[j], min(p + q, max(0, min(31, n[j] - p0 - 1))));
+                        const float* src = P.o + row * (32 * PER) + PER * lane;
+                        if constexpr (PER == 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(src);
+                            v[j][q][0] = x.x; v[j][q][1] = x.y; v[j][q][2] = x.z; v[j][q][3] = x.w;
+                        } else {
+                            const float2 x = *reinterpret_cast<const float2*>(src);
+                            v[j][q][0] = x.x; v[j][q][1] = x.y;
+                        }
                     }
-                }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float f = __shfl_sync(0xFFFFFFFFu, w, min(p + q, 31));
-                    if (p + q < some && f != 0.0f)
+                for (int j = 0; j < N; ++j)
 #pragma unroll
-                        for (int k = 0; k < PER; ++k) o[k] = fmaf(f, v[q][k], o[k]);
-                }
+                    for (int q = 0; q < AHEAD; ++q) {
+                        const float f = p + q < 32 ? __shfl_sync(0xFFFFFFFFu, w[j], (p + q) & 31) : 0.0f;
+                        if (f != 0.0f)
+#pragma unroll
+                            for (int k = 0; k < PER; ++k) o[j][k] = fmaf(f, v[j][q][k], o[j][k]);
+                    }
             }
         }
     }
 
-    // Row of the output: o / l, or zeros and lse = -inf where there was no key.
+    // Row j to the output: o / l, or zeros and lse = -inf where there was no key.
     template <class E>
-    __device__ void store(const AttnArgs& A, long long tok, int qh, int lane) const {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __device__ void store(const AttnArgs& A, int j, long long tok, int qh, int lane) const {
+        const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
         const long long off = tok * A.o_ts + (long long)qh * A.o_hs + PER * lane;
         if constexpr (PER == 4) {
-            attn_store4<E>(A, off, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+            attn_store4<E>(A, off, make_float4(o[j][0] * inv, o[j][1] * inv, o[j][2] * inv, o[j][3] * inv));
         } else if (A.o_f32) {
-            *reinterpret_cast<float2*>(static_cast<float*>(A.o) + off) = make_float2(o[0] * inv, o[1] * inv);
+            *reinterpret_cast<float2*>(static_cast<float*>(A.o) + off) = make_float2(o[j][0] * inv, o[j][1] * inv);
         } else {
-            *reinterpret_cast<uint32_t*>(static_cast<E*>(A.o) + off) = pack_pair<E>(o[0] * inv, o[1] * inv);
+            *reinterpret_cast<uint32_t*>(static_cast<E*>(A.o) + off) = pack_pair<E>(o[j][0] * inv, o[j][1] * inv);
         }
-        if (A.lse && lane == 0) A.lse[tok * A.heads + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (A.lse && lane == 0) A.lse[tok * A.heads + qh] = l[j] == 0.0f ? -INFINITY : (m[j] + log2f(l[j])) * 0.6931471805599453f;
     }
 };
 

@@ -8,6 +8,7 @@ fails loudly when libplm.so is missing.
 """
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -159,15 +160,15 @@ def load(build_if_missing=True):
     dbl, sz, i32, f32 = ctypes.c_double, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
     for name, res, args in (
             ("plm_rope_freqs", i32, [vp, i64, dbl, ctypes.POINTER(_RopeScaling), ctypes.POINTER(f32)]),
-            ("plm_rope", i32, [ctypes.POINTER(_RopeTensor), i64, vp, vp, i64, i64, i64, i32, f32, i32, vp]),
+            ("plm_rope", i32, [vp, i64, vp, vp, i64, i64, i64, i32, f32, i32, vp]),
             ("plm_kv_workspace_size", sz, [i64, i64]),
-            ("plm_kv_reserve", i32, [ctypes.POINTER(_KvState), vp, vp, i64, vp, i64, vp, sz, vp]),
-            ("plm_kv_fork", i32, [ctypes.POINTER(_KvState), vp, vp, vp, i64, vp, sz, vp]),
-            ("plm_kv_free", i32, [ctypes.POINTER(_KvState), vp, i64, vp]),
-            ("plm_kv_compact", i32, [ctypes.POINTER(_KvState), vp, vp, sz, vp]),
-            ("plm_kv_copy_pages", i32, [ctypes.POINTER(_KvState), vp, vp, i64, vp]),
+            ("plm_kv_reserve", i32, [vp, vp, vp, i64, vp, i64, vp, sz, vp]),
+            ("plm_kv_fork", i32, [vp, vp, vp, vp, i64, vp, sz, vp]),
+            ("plm_kv_free", i32, [vp, vp, i64, vp]),
+            ("plm_kv_compact", i32, [vp, vp, vp, sz, vp]),
+            ("plm_kv_copy_pages", i32, [vp, vp, vp, i64, vp]),
             ("plm_attn_workspace_size", sz, [i64] * 7),
-            ("plm_attn_shared_prefix", i32, [ctypes.POINTER(_AttnProblem), vp, sz, vp])):
+            ("plm_attn_shared_prefix", i32, [vp, vp, sz, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = res
     _lib = lib
@@ -458,10 +459,12 @@ def _ints(t, bits, name, shape=None):
     """Address of a contiguous CUDA tensor of 32- or 64-bit integers (None stays None)."""
     if t is None:
         return None
-    if not _types:
+    code = _types.get(t.dtype)
+    if code is None and not _types:
         import torch
         _type(torch.empty(0))
-    if _types.get(t.dtype) != -bits:
+        code = _types.get(t.dtype)
+    if code != -bits:
         raise ValueError("%s: expected int%d, got %s" % (name, bits, t.dtype))
     if shape is not None and t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
@@ -493,53 +496,61 @@ def plm_rope_freqs(rotary_dim, base, scaling="none", factor=1.0, trained=0.0, lo
     return (freqs if device is None else freqs.to(device)), scale.value
 
 
+# The structs of these calls are packed into bytes, which costs a fifth of
+# filling a ctypes structure: a decode step makes its calls in a few
+# microseconds of GPU time.
+_ROPE_TENSOR = struct.Struct("@11q3i4x")
+_KV_STATE = struct.Struct("@10q")
+_ATTN_PROBLEM = struct.Struct("@26qf2i4x")
+
+
 def plm_rope_tensor(x, y, slots=None, rotate=True):
-    """One tensor of a plm_rope call.  x [tokens][heads][head_dim]; y the same shape, or with slots (int64 [tokens])
-    the pages [pages][heads][page_tokens][head_dim] of a cache, as any strided view."""
-    xs = _rows(x, "x", 3)
+    """One tensor of a plm_rope call, to be kept as long as its addresses hold.  x [tokens][heads][head_dim]; y the
+    same shape, or with slots (int64 [tokens]) the pages [pages][heads][page_tokens][head_dim] of a cache, as any
+    strided view."""
+    xt, xh, _ = _rows(x, "x", 3)
+    shape = x.shape
+    tokens, heads, d = shape
     if slots is None:
-        ys = _rows(y, "y", 3)
-        if y.shape != x.shape:
-            raise ValueError("y: expected shape %s, got %s" % (tuple(x.shape), tuple(y.shape)))
-        page = (0, 0, 0)
-        yt, yh = ys[0], ys[1]
+        yt, yh, _ = _rows(y, "y", 3)
+        if y.shape != shape:
+            raise ValueError("y: expected shape %s, got %s" % (tuple(shape), tuple(y.shape)))
+        at = page_tokens = page_stride = pages = 0
     else:
-        ys = _rows(y, "y", 4)
-        if y.shape[1] != x.shape[1] or y.shape[3] != x.shape[2]:
-            raise ValueError("y: expected pages [.][%d][.][%d], got %s" % (x.shape[1], x.shape[2], tuple(y.shape)))
-        page = (y.shape[2], ys[0], y.shape[0])
-        yt, yh = ys[2], ys[1]
-    t = _RopeTensor(x.data_ptr() or None, y.data_ptr() or None, _ints(slots, 64, "slots", (x.shape[0],)),
-                    x.shape[1], xs[0], xs[1], yt, yh, page[0], page[1], page[2], _type(x), _type(y), 1 if rotate else 0)
-    t.shape = (x.shape[0], x.shape[2])
-    return t
+        page_stride, yh, yt, _ = _rows(y, "y", 4)
+        pages, yheads, page_tokens, yd = y.shape
+        if yheads != heads or yd != d:
+            raise ValueError("y: expected pages [.][%d][.][%d], got %s" % (heads, d, tuple(y.shape)))
+        at = _ints(slots, 64, "slots", (tokens,))
+    return (_ROPE_TENSOR.pack(x.data_ptr(), y.data_ptr(), at, heads, xt, xh, yt, yh, page_tokens, page_stride, pages,
+                              _type(x), _type(y), 1 if rotate else 0), tokens, d)
 
 
 def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, inverse=False, stream=None):
     """Turns the heads of the tensors (plm_rope_tensor) by their positions (int32 [tokens]); see include/plm.h."""
     lib = load()
-    tokens, d = tensors[0].shape if tensors else (positions.numel(), 0)
-    for t in tensors:
-        if t.shape != (tokens, d):
-            raise ValueError("the tensors differ in tokens or head size")
+    packed, tokens, d = tensors[0] if tensors else (b"", positions.numel(), 0)
+    if len(tensors) > 1:
+        for t in tensors:
+            if t[1] != tokens or t[2] != d:
+                raise ValueError("the tensors differ in tokens or head size")
+        packed = b"".join([t[0] for t in tensors])
     if freqs.numel() != rotary_dim // 2:
         raise ValueError("freqs: expected %d values, got %d" % (rotary_dim // 2, freqs.numel()))
     if tokens == 0 and tensors:
         return
-    arr = (_RopeTensor * len(tensors))(*tensors)
-    _check("plm_rope", lib.plm_rope(arr, len(tensors), _ints(positions, 32, "positions", (tokens,)),
-                                    _ints(freqs, 64, "freqs"), tokens, d, rotary_dim,
-                                    _LAYOUTS.get(layout, layout), scale, 1 if inverse else 0, _stream(stream)))
+    _check("plm_rope", lib.plm_rope(packed, len(tensors), _ints(positions, 32, "positions", (tokens,)),
+                                    _ints(freqs, 64, "freqs"), tokens, d, rotary_dim, _LAYOUTS.get(layout, layout),
+                                    scale, 1 if inverse else 0, _stream(stream)))
 
 
 def plm_kv_state(pool, table, lens, refs, page_tokens, status=None):
     """Page state over device tensors: pool [pages][...] of any type, table int32 [max_seqs][max_pages], lens int32
     [max_seqs], refs int32 [pages], status int32 [1] or None.  It holds addresses: keep the tensors."""
     pages, (seqs, width) = pool.shape[0], table.shape
-    s = _KvState(_addr(pool), pool.numel() // max(1, pages) * pool.element_size(), pages,
-                 _ints(table, 32, "table"), _ints(lens, 32, "lens", (seqs,)),
-                 _ints(refs, 32, "refs", (pages,)), _ints(status, 32, "status"), seqs, width, page_tokens)
-    return s
+    return _KV_STATE.pack(_addr(pool), pool.numel() // max(1, pages) * pool.element_size(), pages,
+                          _ints(table, 32, "table"), _ints(lens, 32, "lens", (seqs,)), _ints(refs, 32, "refs", (pages,)),
+                          _ints(status, 32, "status") or 0, seqs, width, page_tokens)
 
 
 def plm_kv_workspace_size(pages, n):
@@ -556,38 +567,37 @@ def plm_kv_reserve(kv, seqs, add, slots, workspace, stream=None):
     lib, n = load(), seqs.numel()
     if slots is not None and (slots.dim() != 2 or slots.shape[0] != n):
         raise ValueError("slots: expected [%d][.], got %s" % (n, tuple(slots.shape)))
-    _check("plm_kv_reserve", lib.plm_kv_reserve(ctypes.byref(kv), _ints(seqs, 32, "seqs"),
-                                                _ints(add, 32, "add", (n,)), n, _ints(slots, 64, "slots"),
-                                                0 if slots is None else slots.shape[1], _addr(workspace),
-                                                _bytes(workspace), _stream(stream)))
+    _check("plm_kv_reserve", lib.plm_kv_reserve(kv, _ints(seqs, 32, "seqs"), _ints(add, 32, "add", (n,)), n,
+                                                _ints(slots, 64, "slots"), 0 if slots is None else slots.shape[1],
+                                                _addr(workspace), _bytes(workspace), _stream(stream)))
 
 
 def plm_kv_fork(kv, parents, children, workspace, keep=None, stream=None):
     """Unused sequences children (int32 [n]) become copies of parents, of their first keep tokens if given."""
     lib, n = load(), parents.numel()
-    _check("plm_kv_fork", lib.plm_kv_fork(ctypes.byref(kv), _ints(parents, 32, "parents"),
-                                          _ints(children, 32, "children", (n,)), _ints(keep, 32, "keep", (n,)),
-                                          n, _addr(workspace), _bytes(workspace), _stream(stream)))
+    _check("plm_kv_fork", lib.plm_kv_fork(kv, _ints(parents, 32, "parents"), _ints(children, 32, "children", (n,)),
+                                          _ints(keep, 32, "keep", (n,)), n, _addr(workspace), _bytes(workspace),
+                                          _stream(stream)))
 
 
 def plm_kv_free(kv, seqs, stream=None):
     """The sequences (int32 [n]) give their pages back."""
     lib = load()
-    _check("plm_kv_free", lib.plm_kv_free(ctypes.byref(kv), _ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)))
+    _check("plm_kv_free", lib.plm_kv_free(kv, _ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)))
 
 
 def plm_kv_compact(kv, live, workspace, stream=None):
     """Packs the pages in use to the front of the pool; live (int32 [1] or None) gets their number."""
     lib = load()
-    _check("plm_kv_compact", lib.plm_kv_compact(ctypes.byref(kv), _ints(live, 32, "live"), _addr(workspace),
-                                                _bytes(workspace), _stream(stream)))
+    _check("plm_kv_compact", lib.plm_kv_compact(kv, _ints(live, 32, "live"), _addr(workspace), _bytes(workspace),
+                                                _stream(stream)))
 
 
 def plm_kv_copy_pages(kv, src, dst, stream=None):
     """Page dst[i] = page src[i] (int32 lists of the same length)."""
     lib, n = load(), src.numel()
-    _check("plm_kv_copy_pages", lib.plm_kv_copy_pages(ctypes.byref(kv), _ints(src, 32, "src"),
-                                                      _ints(dst, 32, "dst", (n,)), n, _stream(stream)))
+    _check("plm_kv_copy_pages", lib.plm_kv_copy_pages(kv, _ints(src, 32, "src"), _ints(dst, 32, "dst", (n,)), n,
+                                                      _stream(stream)))
 
 
 def plm_attn_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len):
@@ -600,30 +610,30 @@ def plm_attn_shared_prefix(q, o, k, v, table, lens, tokens, prefix_len, max_len,
     """Attention of q [batch*tokens][heads][head_dim] over the pages k, v [pages][kv_heads][page_tokens][head_dim]
     (strided views of one shape and strides) into o; the batch's first prefix_len tokens are shared (see include/plm.h)."""
     lib = load()
-    qs, os_, ks = _rows(q, "q", 3), _rows(o, "o", 3), _rows(k, "k", 4)
-    if o.shape != q.shape:
-        raise ValueError("o: expected shape %s, got %s" % (tuple(q.shape), tuple(o.shape)))
-    if v.shape != k.shape or _rows(v, "v", 4) != ks or v.dtype != k.dtype or q.dtype != k.dtype:
+    qt, qh, _ = _rows(q, "q", 3)
+    ot, oh, _ = _rows(o, "o", 3)
+    kp, kh, kt, _ = ks = _rows(k, "k", 4)
+    shape, kshape = q.shape, k.shape
+    if o.shape != shape:
+        raise ValueError("o: expected shape %s, got %s" % (tuple(shape), tuple(o.shape)))
+    if v.shape != kshape or v.stride() != ks or v.dtype != k.dtype or q.dtype != k.dtype or not v.is_cuda:
         raise ValueError("k and v have to agree in shape, strides and type, and q in type")
-    if k.shape[3] != q.shape[2]:
-        raise ValueError("k: expected heads of %d, got %d" % (q.shape[2], k.shape[3]))
-    n, heads, d = q.shape
+    n, heads, d = shape
+    pages, kv_heads, page_tokens, kd = kshape
+    if kd != d:
+        raise ValueError("k: expected heads of %d, got %d" % (d, kd))
     if tokens < 1 or n % tokens:
         raise ValueError("q: %d rows are no multiple of %d tokens" % (n, tokens))
     rows, width = table.shape
     batch = n // tokens
-    p = _AttnProblem(q.data_ptr() or None, o.data_ptr() or None, None, k.data_ptr() or None, v.data_ptr() or None,
-                     _ints(table, 32, "table"), _ints(lens, 32, "lens", (rows,)),
-                     _ints(seqs, 32, "seqs", (batch,)), batch, tokens, heads, k.shape[1], d, qs[0], qs[1], os_[0],
-                     os_[1], k.shape[2], k.shape[0], ks[0], ks[1], ks[2], width, rows, prefix_len, max_len, scale,
-                     _type(k), _type(o))
     if seqs is None and batch > rows:
         raise ValueError("table: %d rows for a batch of %d" % (rows, batch))
-    if lse is not None:
-        if _type(lse) != PLM_F32 or tuple(lse.shape) != (n, heads):
-            raise ValueError("lse: expected float32 %s" % ((n, heads),))
-        p.lse = _addr(lse)
+    if lse is not None and (_type(lse) != PLM_F32 or lse.shape != (n, heads)):
+        raise ValueError("lse: expected float32 %s" % ((n, heads),))
     if batch == 0:
         return
-    _check("plm_attn_shared_prefix", lib.plm_attn_shared_prefix(ctypes.byref(p), _addr(workspace), _bytes(workspace),
-                                                                _stream(stream)))
+    p = _ATTN_PROBLEM.pack(q.data_ptr(), o.data_ptr(), _addr(lse) or 0, k.data_ptr(), v.data_ptr(),
+                           _ints(table, 32, "table"), _ints(lens, 32, "lens", (rows,)),
+                           _ints(seqs, 32, "seqs", (batch,)) or 0, batch, tokens, heads, kv_heads, d, qt, qh, ot, oh,
+                           page_tokens, pages, kp, kh, kt, width, rows, prefix_len, max_len, scale, _type(k), _type(o))
+    _check("plm_attn_shared_prefix", lib.plm_attn_shared_prefix(p, _addr(workspace), _bytes(workspace), _stream(stream)))
