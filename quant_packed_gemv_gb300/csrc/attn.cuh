@@ -77,12 +77,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-
 // The cluster's CTAs: a barrier over all their threads, and shared memory of
 // the CTA of rank z at the place of `p` here (its own where n = 1).
 __device__ __forceinline__ void cluster_barrier() {
@@ -99,18 +93,12 @@ __device__ __forceinline__ float peer_f32(const float* p, int z, int n) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, z)) : "memory");
     return v;
 }
-template <int N>
-__device__ __forceinline__ void peer_dims(const float* p, int z, int n, float (&v)[N]) {
-    static_assert(N == 2 || N == 4, "dims per lane");
-    if (n == 1) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = p[i];
-    } else if constexpr (N == 4) {
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(peer_addr(p, z)) : "memory");
-    } else {
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(peer_addr(p, z)) : "memory");
-    }
+__device__ __forceinline__ float4 peer_f32x4(const float* p, int z, int n) {
+    if (n == 1) return *reinterpret_cast<const float4*>(p);
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_addr(p, z)) : "memory");
+    return v;
 }
 
 }  // namespace plm

@@ -65,6 +65,7 @@ template <int D, int NB> struct RowsSmem {
     struct Parts {
         float m[DW][ROWS], l[DW][ROWS];
         float o[DW][ROWS][PITCH];
+        Sums<ROWS, 8 * DW + MOST_CTAS, 1> sums;   // of the cluster's warps, then the prefix pieces
     };
     uint4 q[NB > 2 ? NB * (D / 32) * 32 : 1];
     union {
@@ -275,52 +276,55 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
         }
     }
     const int cs = gridDim.z;   // the cluster: the CTAs of this pair
+    // CTA z of it adds up rows z, z + cs, ..
+    constexpr int ROWS2 = NB == 1 ? 8 : NB == 2 ? 16 : 32;   // rows, to a power of two
+    const int mine = (rows - (int)blockIdx.z + cs - 1) / cs, parts = cs * DW;
+    auto& sums = sm.part.sums;
+    if ((int)threadIdx.x < mine) {
+        const int k = threadIdx.x, r = blockIdx.z + k * cs, gr = b * rows + r, t_ = r / A.group;
+        sums.place(A, k, (long long)b * A.nq + t_, h * A.group + r - t_ * A.group);
+        sums.pieces[0][k].n = 0;
+        if (shares) {
+            const int rt = gr >> P.tile_shift, item = h * P.prefix_row_tiles + rt;
+            sums.pieces[0][k] = item_pieces(P, item, item * P.prefix_tiles, P.prefix_tiles,
+                                            A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, gr & (P.tile_rows - 1));
+        }
+    }
     if (cs > 1) cluster_barrier();
     else __syncthreads();
     if (P.prefix_tiles > 0) grid_wait_prior();   // the tile kernel's results
-    // A warp adds up N rows at a time, 4 (2 at D = 64) dims a lane: the parts of
-    // the cluster's warps (at most 32, a lane each for their weights), then the
-    // pieces of the rows' prefix items, both in order.
-    constexpr int PER = D / 32, N = NB == 1 ? 2 : 4;
-    const int step = cs * DW;
-    for (int r0 = blockIdx.z + cs * warp; r0 < rows; r0 += N * step) {
-        RowSum<PER, N> R;
-        const int pz = lane / DW, pw = lane % DW;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int r = min(r0 + j * step, rows - 1);
-            const bool part = lane < cs * DW;
-            float pm = part ? peer_f32(&sm.part.m[pw][r], pz, cs) : -INFINITY;
-            const float pl = part ? peer_f32(&sm.part.l[pw][r], pz, cs) : 0.0f;
-            if (pl == 0.0f) pm = -INFINITY;   // no key
-            R.m[j] = warp_max(pm);
-            const float wgt = pm == -INFINITY ? 0.0f : ex2(pm - R.m[j]);
-            R.l[j] = warp_sum(wgt * pl);
-            for (int p = 0; p < cs * DW; ++p) {
-                const float f = __shfl_sync(0xFFFFFFFFu, wgt, p);
-                float v[PER];
-                peer_dims<PER>(&sm.part.o[p % DW][r][PER * lane], p / DW, cs, v);
-                if (f != 0.0f)
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) R.o[j][i] = fmaf(f, v[i], R.o[j][i]);
+    {   // a thread per (row, every so manieth part)
+        constexpr int SPAN = (DW * 32) / ROWS2;
+        const int k = threadIdx.x % ROWS2, from = threadIdx.x / ROWS2;
+        if (k < mine) {
+            const int r = blockIdx.z + k * cs;
+            bring(P, sums.pieces[0][k], sums.ml + parts, k, from, SPAN);
+            for (int p = from; p < parts; p += SPAN)
+                sums.ml[p][k] = make_float2(peer_f32(&sm.part.m[p % DW][r], p / DW, cs), peer_f32(&sm.part.l[p % DW][r], p / DW, cs));
+        }
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < mine; k0 += DW * 4) {
+        const int k = min(k0 + (int)threadIdx.x / 8, mine - 1);
+        weigh(A, sums, k, parts + sums.pieces[0][k].n, k0 + (int)threadIdx.x / 8 < mine, threadIdx.x & 7);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < mine * (D / 4); e += DW * 32) {
+        const int k = e / (D / 4), d = 4 * (e - k * (D / 4)), r = blockIdx.z + k * cs;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int p = 0; p < parts; ++p) {
+            const float f = sums.ml[p][k].x;
+            const float4 v = peer_f32x4(&sm.part.o[p % DW][r][d], p / DW, cs);
+            if (f != 0.0f) {
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
             }
         }
-        if (shares) {
-            int item[N], u0[N], at[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const long long gr = (long long)b * rows + r0 + j * step, rt = gr / P.tile_rows;
-                item[j] = r0 + j * step < rows ? h * P.prefix_row_tiles + (int)rt : -1;
-                u0[j] = item[j] * P.prefix_tiles;
-                at[j] = (int)(gr - rt * P.tile_rows);
-            }
-            R.pieces(P, item, u0, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, at, lane);
-        }
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int r = r0 + j * step;
-            if (r < rows) R.template store<E>(A, j, (long long)b * A.nq + r / A.group, h * A.group + r % A.group, lane);
-        }
+        add_pieces<D>(P, sums.pieces[0][k], sums.ml + parts, k, d, acc);
+        const float inv = sums.inv[k];
+        attn_store4<E>(A, sums.out[k] + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     }
     if (cs > 1) cluster_barrier();   // no CTA leaves while its part is read
 }

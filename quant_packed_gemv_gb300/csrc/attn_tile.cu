@@ -259,10 +259,9 @@ struct Walk {
 // Row i of a piece's row tile: the token (row of q) and query head, or false.
 __device__ __forceinline__ bool tile_row(const AttnArgs& A, const TilePlan& P, const Piece& S, int i, long long& tok,
                                          int& qh) {
-    const long long r = (long long)S.rt * P.tile_rows + i;
-    const long long all = (long long)A.nq * A.group * (P.job == 0 ? A.batch : 1);
-    if (r >= all) return false;
-    const long long t = r / A.group;
+    const unsigned r = ((unsigned)S.rt << P.tile_shift) + i;   // the rows fit 31 bits
+    if (r >= (unsigned)(A.nq * A.group * (P.job == 0 ? A.batch : 1))) return false;
+    const unsigned t = r / (unsigned)A.group;
     tok = (long long)S.b * A.nq + t;
     qh = S.h * A.group + (int)(r - t * A.group);
     return true;
@@ -657,70 +656,95 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
     }
 }
 
-// The items that are cut between CTAs (own keys alone): block (c, y) adds the
-// rows of the item that CTA c goes on with, if c - 1 began it.  The blocks
-// from P.ctas on write the rows of sequences without keys.
-constexpr int JOIN_Y = 32;   // a row per warp
-template <class E, int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
-    grid_launch_dependents();
-    grid_wait_prior();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int pair, h0, h1;
-    if ((int)blockIdx.x >= P.ctas) {
-        pair = blockIdx.x - P.ctas;
-        if (own_tiles(A, P, pair) > 0) return;
-        h0 = 0;
-        h1 = A.kv_heads;
-    } else {
-        const int c = blockIdx.x, U = *P.units;
-        const int4 cut = P.cut[c];
-        if (cut.x < 0 || unit_cta(cut.z, U, unit_ctas(P, U)) != c - 1) return;
-        pair = cut.x;
-        h0 = cut.y;
-        h1 = h0 + 1;
+constexpr int JR = 32;   // rows per block of 256 threads
+
+// Adds up a block's rows, whose places and pieces (of plan P, then of W) are set.
+template <class E, int D, int MOST, int SETS>
+__device__ __forceinline__ void add_rows(const AttnArgs& A, Sums<JR, MOST, SETS>& sums, int rows, const TilePlan& P, const TilePlan& W) {
+    __syncthreads();
+    const int k0 = threadIdx.x % JR, from = threadIdx.x / JR;
+    if (k0 < rows) {
+        bring(P, sums.pieces[0][k0], sums.ml, k0, from, 256 / JR);
+        if (SETS == 2) bring(W, sums.pieces[SETS - 1][k0], sums.ml + sums.pieces[0][k0].n, k0, from, 256 / JR);
     }
-    const int b = pair / P.own_row_tiles, rt = pair - b * P.own_row_tiles;
-    const int rows = (int)min((long long)P.tile_rows, (long long)A.nq * A.group - (long long)rt * P.tile_rows);
-    for (int h = h0; h < h1; ++h)
-        for (int i = blockIdx.y * 8 + warp; i < rows; i += JOIN_Y * 8) {
-            RowSum<D / 32> R;
-            if ((int)blockIdx.x < P.ctas) {
-                const int4 cut = P.cut[blockIdx.x];
-                R.pieces(P, {0}, {cut.z}, cut.w, *P.units, {i}, lane);
-            }
-            const long long r = (long long)rt * P.tile_rows + i, t = r / A.group;
-            R.template store<E>(A, 0, (long long)b * A.nq + t, h * A.group + (int)(r - t * A.group), lane);
-        }
+    __syncthreads();
+    {   // eight lanes a row
+        const int k = threadIdx.x / 8;
+        const bool in = k < rows;
+        weigh(A, sums, k, in ? sums.pieces[0][k].n + (SETS == 2 ? sums.pieces[SETS - 1][k].n : 0) : 0, in, threadIdx.x & 7);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
+        const int k = e / (D / 4), d = 4 * (e - k * (D / 4));
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        add_pieces<D>(P, sums.pieces[0][k], sums.ml, k, d, acc);
+        if (SETS == 2) add_pieces<D>(W, sums.pieces[SETS - 1][k], sums.ml + sums.pieces[0][k].n, k, d, acc);
+        const float inv = sums.inv[k];
+        attn_store4<E>(A, sums.out[k] + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
 }
 
-// All rows: the pieces of their prefix item and of their own item.
+// The items that are cut between CTAs (own keys alone): block (c, y) adds up
+// rows 32 y .. of the item that CTA c goes on with, if c - 1 began it.  The
+// blocks from P.ctas on write the rows of sequences without keys.
+template <class E, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
+    extern __shared__ __align__(16) uint8_t join_raw[];
+    auto& sums = *reinterpret_cast<Sums<JR, MOST_CTAS, 1>*>(join_raw);
+    grid_launch_dependents();
+    grid_wait_prior();
+    const bool cut_item = (int)blockIdx.x < P.ctas;
+    const int U = *P.units;
+    int4 cut = make_int4((int)blockIdx.x - P.ctas, 0, 0, 0);   // (sequence, row tile), head, first unit, units
+    int heads = 1;
+    if (cut_item) {
+        cut = P.cut[blockIdx.x];
+        if (cut.x < 0 || unit_cta(cut.z, U, unit_ctas(P, U)) != (int)blockIdx.x - 1) return;
+    } else {
+        if (own_tiles(A, P, cut.x) > 0) return;
+        heads = A.kv_heads;
+    }
+    const int b = cut.x / P.own_row_tiles, rt = cut.x - b * P.own_row_tiles, i0 = blockIdx.y * JR;
+    const unsigned r0 = ((unsigned)rt << P.tile_shift) + i0, all = A.nq * A.group;
+    const int rows = r0 < all ? (int)min((unsigned)JR, all - r0) : 0;
+    for (int h = cut.y; h < cut.y + heads; ++h) {
+        if ((int)threadIdx.x < rows) {
+            const int k = threadIdx.x, t = (r0 + k) / (unsigned)A.group;
+            sums.place(A, k, (long long)b * A.nq + t, h * A.group + (int)(r0 + k - t * A.group));
+            sums.pieces[0][k].n = 0;
+            if (cut_item) sums.pieces[0][k] = item_pieces(P, 0, cut.z, cut.w, U, i0 + k);
+        }
+        add_rows<E, D>(A, sums, rows, P, P);
+        __syncthreads();
+    }
+}
+
+// All rows: the pieces of their prefix item and of their own item.  A block
+// adds up JR rows of a sequence and head.
 template <class E, int D>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P,
                                                          const __grid_constant__ TilePlan W) {
+    extern __shared__ __align__(16) uint8_t merge_raw[];
+    auto& sums = *reinterpret_cast<Sums<JR, 2 * MOST_CTAS, 2>*>(merge_raw);
     grid_launch_dependents();
     grid_wait_prior();
-    const int lane = threadIdx.x & 31, U = *W.units;
-    const long long all = (long long)A.batch * A.nq * A.heads;
-    for (long long e = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5; e < all; e += (long long)gridDim.x * 8) {
-        const long long tok = e / A.heads;
-        const int qh = (int)(e - tok * A.heads), h = qh / A.group, g = qh - h * A.group;
-        const int b = (int)(tok / A.nq), t = (int)(tok - (long long)b * A.nq);
-        RowSum<D / 32> R;
+    const unsigned all = A.nq * A.group, chunks = (all + JR - 1) / JR;
+    const unsigned bh = blockIdx.x / chunks, b = bh / A.kv_heads, r0 = (blockIdx.x - bh * chunks) * JR;
+    const int h = bh - b * A.kv_heads, rows = (int)min((unsigned)JR, all - r0);
+    if ((int)threadIdx.x < rows) {
+        const int k = threadIdx.x;
+        const unsigned r = r0 + k, t = r / (unsigned)A.group, gr = b * all + r;
+        sums.place(A, k, (long long)b * A.nq + t, h * A.group + (int)(r - t * A.group));
+        sums.pieces[0][k].n = sums.pieces[1][k].n = 0;
         if (attn_shares(A, P, attn_len(A, attn_row(A, b)))) {
-            const long long r = tok * A.group + g, rt = r / P.tile_rows;
-            const int item = h * P.prefix_row_tiles + (int)rt;
-            R.pieces(P, {item}, {item * P.prefix_tiles}, P.prefix_tiles, A.kv_heads * P.prefix_row_tiles * P.prefix_tiles,
-                     {(int)(r - rt * P.tile_rows)}, lane);
+            const int item = h * P.prefix_row_tiles + (int)(gr >> P.tile_shift);
+            sums.pieces[0][k] = item_pieces(P, item, item * P.prefix_tiles, P.prefix_tiles,
+                                            A.kv_heads * P.prefix_row_tiles * P.prefix_tiles, gr & (P.tile_rows - 1));
         }
-        const int r = t * A.group + g, rt = r / W.tile_rows, pair = b * W.own_row_tiles + rt;
-        const int tiles = own_tiles(A, W, pair);
-        if (tiles > 0) {
-            const int item = pair * A.kv_heads + h;
-            R.pieces(W, {item}, {W.item_unit[item]}, tiles, U, {r - rt * W.tile_rows}, lane);
-        }
-        R.template store<E>(A, 0, tok, qh, lane);
+        const int pair = b * W.own_row_tiles + (int)(r >> W.tile_shift), tiles = own_tiles(A, W, pair), item = pair * A.kv_heads + h;
+        if (tiles > 0) sums.pieces[1][k] = item_pieces(W, item, W.item_unit[item], tiles, *W.units, r & (W.tile_rows - 1));
     }
+    add_rows<E, D>(A, sums, rows, P, W);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -765,14 +789,20 @@ cudaError_t tile_launch(const AttnArgs& A, const TilePlan& P, const CUtensorMap&
     if (e != cudaSuccess) return e;
     e = launch_kernel(attn_tile_kernel<E, D, NT>, dim3((unsigned)P.ctas), dim3(NT * 128 + 64), bytes, stream, A, P, km, vm, fault);
     if (e != cudaSuccess || P.job == 0 || P.keep) return e;
-    return launch_kernel(attn_join_kernel<E, D>, dim3((unsigned)(P.ctas + A.batch * P.own_row_tiles), JOIN_Y), dim3(256), 0, stream, A, P);
+    constexpr int sums = sizeof(Sums<JR, MOST_CTAS, 1>);
+    e = cudaFuncSetAttribute(attn_join_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sums);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(attn_join_kernel<E, D>, dim3((unsigned)(P.ctas + A.batch * P.own_row_tiles), (unsigned)(P.tile_rows / JR)),
+                         dim3(256), sums, stream, A, P);
 }
 
 template <class E, int D>
 cudaError_t merge_launch(const AttnArgs& A, const TilePlan& P, const TilePlan& W, cudaStream_t stream) {
-    const long long rows = (long long)A.batch * A.nq * A.heads, cap = 8LL * num_sms();
-    const long long ctas = (rows + 7) / 8 < cap ? (rows + 7) / 8 : cap;
-    return launch_kernel(attn_merge_kernel<E, D>, dim3((unsigned)ctas), dim3(256), 0, stream, A, P, W);
+    const long long blocks = (long long)A.batch * A.kv_heads * (((long long)A.nq * A.group + JR - 1) / JR);
+    constexpr int bytes = sizeof(Sums<JR, 2 * MOST_CTAS, 2>);
+    const cudaError_t e = cudaFuncSetAttribute(attn_merge_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(attn_merge_kernel<E, D>, dim3((unsigned)blocks), dim3(256), bytes, stream, A, P, W);
 }
 
 template <class E>
@@ -792,6 +822,7 @@ TilePlan tile_plan(const AttnArgs& A, int d, int job, bool share, void* ws, size
     T.job = job;
     T.keep = share;
     T.tile_rows = all > 128 ? 256 : 128;
+    T.tile_shift = all > 128 ? 8 : 7;
     const long long row_tiles = (all + T.tile_rows - 1) / T.tile_rows;
     T.prefix_tiles = share ? (A.prefix + TK - 1) / TK : 0;
     const long long items = (long long)A.kv_heads * row_tiles * (job == 0 ? 1 : A.batch);
@@ -801,7 +832,7 @@ TilePlan tile_plan(const AttnArgs& A, int d, int job, bool share, void* ws, size
         return T;
     }
     (job == 0 ? T.prefix_row_tiles : T.own_row_tiles) = (int)row_tiles;
-    const int sms = num_sms();
+    const int sms = num_sms() < MOST_CTAS ? num_sms() : MOST_CTAS;
     T.ctas = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
     const size_t slots = T.keep ? (size_t)(T.ctas + items) : 2 * (size_t)T.ctas;
     const size_t item_b = job == 1 && T.keep ? up256(4 * (size_t)items) : 0, cut_b = up256(sizeof(int4) * (size_t)T.ctas);

@@ -16,6 +16,7 @@ constexpr int TK = 128;   // keys per unit
 
 struct TilePlan {
     int tile_rows;         // rows per row tile (128 or 256)
+    int tile_shift;        // its logarithm
     int ctas;
     int prefix_tiles;      // units per prefix item; 0: no prefix job
     int prefix_row_tiles;  // row tiles of the prefix job (per head)
@@ -43,8 +44,8 @@ __device__ __forceinline__ int own_begin(const AttnArgs& A, const TilePlan& P, i
     return attn_shares(A, P, len) ? A.prefix : 0;
 }
 __device__ __forceinline__ int own_end(const AttnArgs& A, const TilePlan& P, int len, int rt) {
-    const long long last = min((long long)A.nq * A.group, (long long)(rt + 1) * P.tile_rows) - 1;
-    return attn_seen(A, len, (int)(last / A.group));
+    const unsigned last = min((unsigned)(A.nq * A.group), (unsigned)(rt + 1) << P.tile_shift) - 1;   // rows fit 31 bits
+    return attn_seen(A, len, (int)(last / (unsigned)A.group));
 }
 
 // Units of (sequence, row tile) `pair` of the own jobs, for one head.
@@ -58,10 +59,14 @@ __device__ __forceinline__ int own_tiles(const AttnArgs& A, const TilePlan& P, i
 // no share between two others is empty.
 __device__ __forceinline__ int unit_ctas(const TilePlan& P, int U) { return min(P.ctas, U); }
 
-// The CTA (of ctas) that holds unit u of U.
+// The CTA (of ctas) that holds unit u of U: the last c with U c / ctas <= u,
+// i.e. U c < (u + 1) ctas (an estimate, then exact steps: a 64-bit division is
+// slow where a row's sums wait for it).
 __device__ __forceinline__ int unit_cta(int u, int U, int ctas) {
-    int c = (int)((long long)u * ctas / U);
-    while ((long long)U * (c + 1) / ctas <= u) ++c;
+    const long long lim = (long long)(u + 1) * ctas;
+    int c = min(ctas - 1, (int)((float)lim / (float)U));
+    while (c > 0 && (long long)U * c >= lim) --c;
+    while (c + 1 < ctas && (long long)U * (c + 1) < lim) ++c;
     return c;
 }
 
@@ -73,101 +78,99 @@ __host__ __device__ __forceinline__ long long piece_slot(const TilePlan& P, int 
     return P.keep ? (long long)c + item : 2LL * c + begins;
 }
 
-// The sums of N rows, by a warp: PER dims a lane.
-template <int PER, int N = 1> struct RowSum {
-    float m[N], l[N], o[N][PER];
-    __device__ RowSum() {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            m[j] = -INFINITY;
-            l[j] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < PER; ++k) o[j][k] = 0.0f;
-        }
-    }
+// Adding up.  The sums of a row are sum_p w_p O_p and sum_p w_p l_p with w_p =
+// 2^(m_p - max m) over its parts p.  First all threads bring the rows' (m, l) into
+// shared memory, then eight lanes a row turn them into weights, then the
+// threads share the rows' dims, four each, and add the parts in order.  Every
+// step has all its loads in flight at once: a row waits for three trips to L2,
+// whatever its number of parts (a warp per row with the weights in lanes, or a
+// thread per row, took 6 to 15 us where the parts were many).
+// What costs time here otherwise is integer division, so each row's places are
+// worked out once.
+struct Pieces {
+    long long first, next;   // row in P.ml and P.o of piece 0, of piece 1
+    int step;                // rows from a piece to the next, after that
+    int n;
+    __device__ __forceinline__ long long at(int p) const { return p == 0 ? first : next + (long long)(p - 1) * step; }
+};
+// Of row i of an item (first unit u0, `tiles` of U units).
+__device__ __forceinline__ Pieces item_pieces(const TilePlan& P, int item, int u0, int tiles, int U, int i) {
+    const int ctas = unit_ctas(P, U), c0 = unit_cta(u0, U, ctas);
+    Pieces X;
+    X.n = unit_cta(u0 + tiles - 1, U, ctas) - c0 + 1;
+    X.first = piece_slot(P, c0, item, true) * P.tile_rows + i;
+    X.next = piece_slot(P, c0 + 1, item, false) * P.tile_rows + i;
+    X.step = P.keep ? P.tile_rows : 2 * P.tile_rows;
+    return X;
+}
 
-    // Adds the pieces of each row's item (item[j] < 0: none; first unit u0[j],
-    // `tiles` of U units), row i[j] of its tile: a lane each for their weights,
-    // then their dims, all in the order of the units.  The loads of the rows, and
-    // of several pieces, are in flight together: each is a trip to L2.
-    __device__ void pieces(const TilePlan& P, const int (&item)[N], const int (&u0)[N], int tiles, int U, const int (&i)[N],
-                           int lane) {
-        constexpr int AHEAD = N * PER <= 4 ? 8 : 4;
-        const int ctas = unit_ctas(P, U);
-        int c0[N], n[N], most = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            c0[j] = item[j] < 0 ? 0 : unit_cta(u0[j], U, ctas);
-            n[j] = item[j] < 0 ? 0 : unit_cta(u0[j] + tiles - 1, U, ctas) - c0[j] + 1;
-            most = max(most, n[j]);
-        }
-        for (int p0 = 0; p0 < most; p0 += 32) {
-            long long at[N];
-            float w[N];
-            float2 ml[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const bool in = p0 + lane < n[j];
-                at[j] = in ? piece_slot(P, c0[j] + p0 + lane, item[j], p0 + lane == 0) * P.tile_rows + i[j] : 0;
-                ml[j] = in ? P.ml[at[j]] : make_float2(-INFINITY, 0.0f);
-            }
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (ml[j].y == 0.0f) ml[j].x = -INFINITY;   // a piece without keys
-                const float mn = fmaxf(m[j], warp_max(ml[j].x));
-                const float old = m[j] == -INFINITY ? 0.0f : ex2(m[j] - mn);
-                w[j] = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - mn);
-                m[j] = mn;
-                l[j] = l[j] * old + warp_sum(w[j] * ml[j].y);
-#pragma unroll
-                for (int k = 0; k < PER; ++k) o[j][k] *= old;
-            }
-            const int some = min(32, most - p0);
-            for (int p = 0; p < some; p += AHEAD) {
-                float v[N][AHEAD][PER];
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-#pragma unroll
-                    for (int q = 0; q < AHEAD; ++q) {
-                        // past the row's pieces: its weight is 0, and any piece will do
-                        const long long row = __shfl_sync(0xFFFFFFFFu, at[j], min(p + q, max(0, min(31, n[j] - p0 - 1))));
-                        const float* src = P.o + row * (32 * PER) + PER * lane;
-                        if constexpr (PER == 4) {
-                            const float4 x = *reinterpret_cast<const float4*>(src);
-                            v[j][q][0] = x.x; v[j][q][1] = x.y; v[j][q][2] = x.z; v[j][q][3] = x.w;
-                        } else {
-                            const float2 x = *reinterpret_cast<const float2*>(src);
-                            v[j][q][0] = x.x; v[j][q][1] = x.y;
-                        }
-                    }
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-#pragma unroll
-                    for (int q = 0; q < AHEAD; ++q) {
-                        const float f = p + q < 32 ? __shfl_sync(0xFFFFFFFFu, w[j], (p + q) & 31) : 0.0f;
-                        if (f != 0.0f)
-#pragma unroll
-                            for (int k = 0; k < PER; ++k) o[j][k] = fmaf(f, v[j][q][k], o[j][k]);
-                    }
-            }
-        }
-    }
-
-    // Row j to the output: o / l, or zeros and lse = -inf where there was no key.
-    template <class E>
-    __device__ void store(const AttnArgs& A, int j, long long tok, int qh, int lane) const {
-        const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
-        const long long off = tok * A.o_ts + (long long)qh * A.o_hs + PER * lane;
-        if constexpr (PER == 4) {
-            attn_store4<E>(A, off, make_float4(o[j][0] * inv, o[j][1] * inv, o[j][2] * inv, o[j][3] * inv));
-        } else if (A.o_f32) {
-            *reinterpret_cast<float2*>(static_cast<float*>(A.o) + off) = make_float2(o[j][0] * inv, o[j][1] * inv);
-        } else {
-            *reinterpret_cast<uint32_t*>(static_cast<E*>(A.o) + off) = pack_pair<E>(o[j][0] * inv, o[j][1] * inv);
-        }
-        if (A.lse && lane == 0) A.lse[tok * A.heads + qh] = l[j] == 0.0f ? -INFINITY : (m[j] + log2f(l[j])) * 0.6931471805599453f;
+template <int ROWS, int MOST, int SETS> struct Sums {
+    float2 ml[MOST][ROWS];      // (m, l) of the parts, then the weight in x
+    float inv[ROWS];            // 1 / sum, 0 without keys
+    Pieces pieces[SETS][ROWS];
+    long long out[ROWS], lse[ROWS];   // places of the row in o and lse
+    __device__ __forceinline__ void place(const AttnArgs& A, int k, long long tok, int qh) {
+        out[k] = tok * A.o_ts + (long long)qh * A.o_hs;
+        lse[k] = tok * A.heads + qh;
     }
 };
+
+// Brings (m, l) of the pieces' row into `ml`: every `step`-th piece.
+template <int ROWS>
+__device__ __forceinline__ void bring(const TilePlan& P, const Pieces& X, float2 (*ml)[ROWS], int k, int from, int step) {
+    for (int p = from; p < X.n; p += step) ml[p][k] = P.ml[X.at(p)];
+}
+
+// Weights of row k from its n parts' (m, l), by eight neighbouring lanes (sub =
+// 0 .. 7, which all take part); the first writes 1 / sum and the row's lse.
+template <int ROWS, int MOST, int SETS>
+__device__ __forceinline__ void weigh(const AttnArgs& A, Sums<ROWS, MOST, SETS>& S, int k, int n, bool in, int sub) {
+    float m = -INFINITY, l = 0.0f;
+    if (in)
+        for (int p = sub; p < n; p += 8) {
+            const float2 v = S.ml[p][k];
+            if (v.y != 0.0f) m = fmaxf(m, v.x);   // l = 0: a part without keys
+        }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (in)
+        for (int p = sub; p < n; p += 8) {
+            const float2 v = S.ml[p][k];
+            const float w = v.y == 0.0f || v.x == -INFINITY ? 0.0f : ex2(v.x - m);
+            if (v.y != 0.0f) l += w * v.y;
+            S.ml[p][k].x = w;
+        }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    if (in && sub == 0) {
+        S.inv[k] = l == 0.0f ? 0.0f : 1.0f / l;
+        if (A.lse) A.lse[S.lse[k]] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+// acc += the pieces' dims d .. d + 3, weighted.
+template <int D, int ROWS>
+__device__ __forceinline__ void add_pieces(const TilePlan& P, const Pieces& X, const float2 (*w)[ROWS], int r, int d, float4& acc) {
+    constexpr int AHEAD = 8;   // loads in flight
+    for (int p = 0; p < X.n; p += AHEAD) {
+        float4 v[AHEAD];
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q)
+            v[q] = *reinterpret_cast<const float4*>(P.o + X.at(min(p + q, X.n - 1)) * D + d);
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+            const float f = p + q < X.n ? w[p + q][r].x : 0.0f;
+            if (f != 0.0f) {   // O of a part without weight may hold anything
+                acc.x = fmaf(f, v[q].x, acc.x);
+                acc.y = fmaf(f, v[q].y, acc.y);
+                acc.z = fmaf(f, v[q].z, acc.z);
+                acc.w = fmaf(f, v[q].w, acc.w);
+            }
+        }
+    }
+}
+
+constexpr int MOST_CTAS = 160;   // of the tile kernel: bounds a row's pieces
 
 // Plan of a launch of the tile kernel: of the prefix (job 0), or of the own
 // keys (job 1; share: the prefix is done apart).  Its workspace starts at ws
