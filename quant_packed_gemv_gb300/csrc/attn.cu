@@ -18,6 +18,7 @@ AttnArgs attn_args(const plm_attn_problem& p) {
     A.table = p.table; A.lens = p.lens; A.seqs = p.seqs;
     A.batch = (int)p.batch; A.nq = (int)p.tokens; A.heads = (int)p.heads; A.kv_heads = (int)p.kv_heads;
     A.group = A.heads / A.kv_heads;
+    A.group_inv = (65536u + A.group - 1) / A.group;
     A.q_ts = p.q_token_stride; A.q_hs = p.q_head_stride; A.o_ts = p.o_token_stride; A.o_hs = p.o_head_stride;
     A.page_stride = p.page_stride; A.kv_hs = p.kv_head_stride; A.kv_ts = p.kv_token_stride;
     A.table_stride = p.table_stride;

@@ -23,6 +23,7 @@ struct AttnArgs {
     const int* lens;
     const int* seqs;
     int batch, nq, heads, kv_heads, group;   // group = heads / kv_heads
+    unsigned group_inv;                      // 65536 / group, rounded up: r / group for r, group <= 32
     long long q_ts, q_hs, o_ts, o_hs;
     long long page_stride, kv_hs, kv_ts, table_stride;
     int page_shift, pages, rows;
@@ -30,6 +31,9 @@ struct AttnArgs {
     float scale;
     int o_f32;
 };
+
+// r / group for r <= 32 (an integer division is ~100 cycles in a row).
+__device__ __forceinline__ int small_row(const AttnArgs& A, int r) { return (int)(((unsigned)r * A.group_inv) >> 16); }
 
 // Table row of sequence b, or -1.
 __device__ __forceinline__ int attn_row(const AttnArgs& A, int b) {
@@ -78,7 +82,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 // The cluster's CTAs: a barrier over all their threads, and shared memory of
-// the CTA of rank z at the place of `p` here (its own where n = 1).
+// the CTA of rank z at the place of `p` here.
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -87,14 +91,12 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, int z) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(z));
     return a;
 }
-__device__ __forceinline__ float peer_f32(const float* p, int z, int n) {
-    if (n == 1) return *p;
+__device__ __forceinline__ float peer_f32(const float* p, int z) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(p, z)) : "memory");
     return v;
 }
-__device__ __forceinline__ float4 peer_f32x4(const float* p, int z, int n) {
-    if (n == 1) return *reinterpret_cast<const float4*>(p);
+__device__ __forceinline__ float4 peer_f32x4(const float* p, int z) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_addr(p, z)) : "memory");

@@ -101,43 +101,8 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
     const E* vbase = static_cast<const E*>(A.v) + head;
     const int mask = (1 << A.page_shift) - 1;
 
-    // Q as the B operand: row 8 nb + g, dims 32 c + 8 t ..; zeros past the rows
-    uint4 qf[QS ? 1 : NB][QS ? 1 : KC];
-    auto q_part = [&](int nb, int c) {
-        const int r = 8 * nb + g;
-        if (r >= rows) return make_uint4(0, 0, 0, 0);
-        return *reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + r / A.group) * A.q_ts +
-                                               (long long)(h * A.group + r % A.group) * A.q_hs + 8 * t + 32 * c);
-    };
-    if constexpr (QS) {
-        for (int i = warp; i < NB * KC; i += DW) sm.q[i * 32 + lane] = q_part(i / KC, i % KC);
-        __syncthreads();
-    } else {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int c = 0; c < KC; ++c) qf[nb][c] = q_part(nb, c);
-    }
-    int seen[NB][2];   // keys that rows 8 nb + 2t, + 1 see
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int rr = 8 * nb + 2 * t + i;
-            seen[nb][i] = rr < rows ? attn_seen(A, len, rr / A.group) : 0;
-        }
     const int all = attn_seen(A, len, 0);   // keys that every row sees
 
-    float m[NB][2], l[NB][2], o[NB][2 * VC * 2][4];   // o: D / 16 tiles of 16 dims x 8 rows
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        m[nb][0] = m[nb][1] = -INFINITY;
-        l[nb][0] = l[nb][1] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[nb][i][j] = 0.0f;
-    }
     const float sl2 = A.scale * LOG2E;
     const int streams = DW * gridDim.z, stream = blockIdx.z * DW + warp;
     const int blocks = (len + 15) >> 4;
@@ -174,6 +139,43 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
         const int next = page_of(blk + (i + 1) * streams);
         fetch(blk + i * streams, page, i);
         page = next;
+    }
+
+    // Q as the B operand: row 8 nb + g, dims 32 c + 8 t ..; zeros past the rows
+    uint4 qf[QS ? 1 : NB][QS ? 1 : KC];
+    auto q_part = [&](int nb, int c) {
+        const int r = 8 * nb + g;
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        const int tr = small_row(A, r);
+        return *reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + tr) * A.q_ts +
+                                               (long long)(h * A.group + r - tr * A.group) * A.q_hs + 8 * t + 32 * c);
+    };
+    if constexpr (QS) {
+        for (int i = warp; i < NB * KC; i += DW) sm.q[i * 32 + lane] = q_part(i / KC, i % KC);
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) qf[nb][c] = q_part(nb, c);
+    }
+    int seen[NB][2];   // keys that rows 8 nb + 2t, + 1 see
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int rr = 8 * nb + 2 * t + i;
+            seen[nb][i] = rr < rows ? attn_seen(A, len, small_row(A, rr)) : 0;
+        }
+    float m[NB][2], l[NB][2], o[NB][2 * VC * 2][4];   // o: D / 16 tiles of 16 dims x 8 rows
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[nb][i][j] = 0.0f;
     }
     for (int n = 0; blk < blocks; blk += streams, ++n) {
         const int j = blk << 4, ahead = blk + (Sm::STAGES - 1) * streams;
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
     const int mine = (rows - (int)blockIdx.z + cs - 1) / cs, parts = cs * DW;
     auto& sums = sm.part.sums;
     if ((int)threadIdx.x < mine) {
-        const int k = threadIdx.x, r = blockIdx.z + k * cs, gr = b * rows + r, t_ = r / A.group;
+        const int k = threadIdx.x, r = blockIdx.z + k * cs, gr = b * rows + r, t_ = small_row(A, r);
         sums.place(A, k, (long long)b * A.nq + t_, h * A.group + r - t_ * A.group);
         sums.pieces[0][k].n = 0;
         if (shares) {
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
             const int r = blockIdx.z + k * cs;
             bring(P, sums.pieces[0][k], sums.ml + parts, k, from, SPAN);
             for (int p = from; p < parts; p += SPAN)
-                sums.ml[p][k] = make_float2(peer_f32(&sm.part.m[p % DW][r], p / DW, cs), peer_f32(&sm.part.l[p % DW][r], p / DW, cs));
+                sums.ml[p][k] = make_float2(peer_f32(&sm.part.m[p % DW][r], p / DW), peer_f32(&sm.part.l[p % DW][r], p / DW));
         }
     }
     __syncthreads();
@@ -309,12 +311,14 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
         weigh(A, sums, k, parts + sums.pieces[0][k].n, k0 + (int)threadIdx.x / 8 < mine, threadIdx.x & 7);
     }
     __syncthreads();
+#pragma unroll 1
     for (int e = threadIdx.x; e < mine * (D / 4); e += DW * 32) {
-        const int k = e / (D / 4), d = 4 * (e - k * (D / 4)), r = blockIdx.z + k * cs;
+        const int k = e / (D / 4), d = 4 * (e % (D / 4)), r = blockIdx.z + k * cs;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
         for (int p = 0; p < parts; ++p) {
             const float f = sums.ml[p][k].x;
-            const float4 v = peer_f32x4(&sm.part.o[p % DW][r][d], p / DW, cs);
+            const float4 v = peer_f32x4(&sm.part.o[p % DW][r][d], p / DW);
             if (f != 0.0f) {
                 acc.x = fmaf(f, v.x, acc.x);
                 acc.y = fmaf(f, v.y, acc.y);
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
                 acc.w = fmaf(f, v.w, acc.w);
             }
         }
-        add_pieces<D>(P, sums.pieces[0][k], sums.ml + parts, k, d, acc);
+        add_pieces<D, Sm::ROWS>(P, sums.pieces[0][k], &sums.ml[parts][k], d, acc);
         const float inv = sums.inv[k];
         attn_store4<E>(A, sums.out[k] + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     }

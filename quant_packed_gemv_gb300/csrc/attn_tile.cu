@@ -94,6 +94,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
                  "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                  : PLM_R16(r, 0), PLM_R16(r, 16) : "r"(a));
 }
+// Eight columns, loaded at once; stored.
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : PLM_R4(r, 0), PLM_R4(r, 4) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(a), PLM_I4(r, 0), PLM_I4(r, 4) : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
                  "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
@@ -152,14 +162,17 @@ struct Piece {
 };
 
 // Walks the CTA's share of the units; every warp for itself, by all its lanes.
+// Not inlined, and nothing outside the loops over units unrolled far: a CTA runs
+// that code once or twice, and fetching it is what it costs (at 140 KB of code the
+// start and end of a piece took 10 us).
 struct Walk {
     int u, end;        // the next unit, the end of the share
     int prefix_row;    // prefix: table row that holds it
     int pair, T, h;    // own: (sequence, row tile), its units per head, head
     int item_u0;       // own: first unit of the item
 
-    // Returns the number of all units.
-    __device__ int start(const AttnArgs& A, const TilePlan& P, int lane) {
+    // Returns the number of all units.  tables: page tables will be read.
+    __device__ __noinline__ int start(const AttnArgs& A, const TilePlan& P, int lane, bool tables) {
         int U;
         if (P.job == 0) {
             U = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
@@ -177,7 +190,7 @@ struct Walk {
         end = mine ? (int)((long long)U * (blockIdx.x + 1) / ctas) : U;
         pair = prefix_row = -1;
         T = h = item_u0 = 0;
-        if (P.job == 0)   // the first sequence that takes part
+        if (P.job == 0 && tables)   // the first sequence that takes part
             for (int b0 = 0; b0 < A.batch && prefix_row < 0; b0 += 32) {
                 const int b = b0 + lane, row = b < A.batch ? attn_row(A, b) : -1;
                 const unsigned hit = __ballot_sync(0xFFFFFFFFu, row >= 0 && attn_shares(A, P, attn_len(A, row)));
@@ -213,7 +226,7 @@ struct Walk {
         }
     }
 
-    __device__ bool next(const AttnArgs& A, const TilePlan& P, int lane, Piece& S) {
+    __device__ __noinline__ bool next(const AttnArgs& A, const TilePlan& P, int lane, Piece& S) {
         if (u >= end) return false;
         if (P.job == 0) {
             S.item = u / P.prefix_tiles;
@@ -238,7 +251,7 @@ struct Walk {
                 }
             }
             const int t0 = u - item_u0;
-            S.b = pair / P.own_row_tiles;
+            S.b = own_seq(P, pair);
             S.rt = pair - S.b * P.own_row_tiles;
             S.h = h;
             S.row = attn_row(A, S.b);
@@ -317,7 +330,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
     Walk W;
     Piece S;
     if (warp == TMA_WARP) {
-        const int U = W.start(A, P, lane);
+        const int U = W.start(A, P, lane, true);
         bool first = true;
         // ---------------------------------------------------- pages -> K, V
         const int bt = min(1 << A.page_shift, TK), per = TK / bt;   // tokens per box, boxes per 64 dims
@@ -363,7 +376,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             if (first && !P.keep) P.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);   // no units
         }
     } else if (warp == MMA_WARP) {
-        W.start(A, P, lane);
+        W.start(A, P, lane, false);
         // ------------------------------------------------------- the products
         constexpr uint32_t ID_S = idesc<E>(128, false), ID_O = idesc<E>(D, true);
         // the operands' descriptors; a place in shared memory adds bytes / 16
@@ -407,6 +420,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             if (ok) ok = wait_full(n0);
             if (!ok) break;
             tc_after();
+#pragma unroll 1
             for (int t = 0; t < NT; ++t) product_s(t, NT == 2 ? t : step & 1, n0 % L::SLOTS);
             free_slot(n0 % L::SLOTS);
             for (int i = 0; ok && i < S.tiles; ++i, ++step) {
@@ -422,7 +436,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 if (NT == 1) ok = wait_full(vt);
                 if (!ok) break;
                 const int left = S.keys - (S.key0 + i * TK);
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < NT; ++t) {
                     const int sb = NT == 2 ? t : step & 1;
                     // P of this unit; for NT = 2 its arrivals also say that V and the next K have landed
@@ -450,7 +464,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             ++pieces;
         }
     } else {
-        W.start(A, P, lane);
+        W.start(A, P, lane, false);
         // ------------------------------------- the softmax, a row per thread
         const int t = warp >> 2, i = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -469,22 +483,33 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             constexpr int CH = D / 8, AT = 32 / CH;   // 16-byte chunks of a row, rows at a time
             const int c = lane % CH;
             uint8_t* dst = sm + t * L::QTILE + (c >> 3) * L::HALF;
-#pragma unroll 8
-            for (int k = 0; k < 32 / AT; ++k) {
-                const int r = k * AT + lane / CH;
-                const long long off = __shfl_sync(0xFFFFFFFFu, mine, r);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (off >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + off) + c);
-                v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
-                *reinterpret_cast<uint4*>(dst + (32 * (warp & 3) + r) * 128 + (((c ^ r) & 7) << 4)) = v;
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32 / AT; k0 += 8) {   // eight loads in flight
+                uint4 v[8];
+                bool have_row[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const long long off = __shfl_sync(0xFFFFFFFFu, mine, (k0 + k) * AT + lane / CH);
+                    have_row[k] = off >= 0;
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + (off >= 0 ? off : 0)) + c);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = (k0 + k) * AT + lane / CH;
+                    uint4 u = have_row[k] ? v[k] : make_uint4(0, 0, 0, 0);
+                    u.x ^= sign; u.y ^= sign; u.z ^= sign; u.w ^= sign;
+                    *reinterpret_cast<uint4*>(dst + (32 * (warp & 3) + r) * 128 + (((c ^ r) & 7) << 4)) = u;
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_ready[t]);
         };
         bool have = W.next(A, P, lane, S);
-        if (have) load_q(S);
         while (have && ok) {
+            load_q(S);
+            Piece next;   // worked out while the first S is on its way
+            const bool more = W.next(A, P, lane, next);
             const bool in = tile_row(A, P, S, t * 128 + i, tok, qh);
             int seen = S.keys;   // keys that the row sees
             if (P.job == 1 && in) seen = attn_seen(A, attn_len(A, S.row), (int)(tok - (long long)S.b * A.nq));
@@ -504,7 +529,19 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 if (!ok) break;
                 tc_after();
                 const int left = seen - (S.key0 + u * TK);
-                const bool part = __any_sync(0xFFFFFFFFu, left < TK);
+                if (__any_sync(0xFFFFFFFFu, left < TK)) {
+                    // keys that some row does not see: -inf in their place (rare)
+#pragma unroll 1
+                    for (int c = 0; c < TK; c += 8) {
+                        uint32_t r[8];
+                        tmem_ld8(sa + c, r);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (c + k >= left) r[k] = 0xFF800000u;
+                        tmem_st8(sa + c, r);
+                    }
+                    tmem_st_wait();
+                }
                 // the row's S in halves of 64: the second is read twice, which
                 // saves 64 registers
                 float s[64];
@@ -514,10 +551,6 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                     tmem_ld32(sa + c0 + 32, r + 32);
                     tmem_ld_wait(r);
                     tmem_ld_wait(r + 32);
-                    if (part)
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c0 + c >= left) s[c] = -INFINITY;
                 };
                 float mx = -INFINITY, my = -INFINITY;
                 auto half_max = [&] {
@@ -542,14 +575,13 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                         if (!ok) break;
                         tc_after();
                         const uint32_t oa = tmem + lanes + TM_O + D * t;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 8) {
+                            uint32_t r[8];
+                            tmem_ld8(oa + c, r);
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t r[32];
-                            tmem_ld32(oa + c, r);
-                            tmem_ld_wait(r);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * keep);
-                            tmem_st32(oa + c, r);
+                            for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * keep);
+                            tmem_st8(oa + c, r);
                         }
                     }
                     l *= keep;
@@ -602,6 +634,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             const long long slot_row = piece_slot(P, blockIdx.x, S.item, S.begins) * P.tile_rows + t * 128 + i;
             const long long mine = final ? (in ? tok * A.o_ts + (long long)qh * A.o_hs : -1) : slot_row * D;
             constexpr int CW = D / 2, CH = CW / 4, AT = 32 / CH;   // dims and chunks of a half, rows at a time
+            const bool wide = !final || A.o_f32;
+            uint8_t* out = final ? static_cast<uint8_t*>(A.o) : reinterpret_cast<uint8_t*>(P.o);
             // (a bounded wait, as every other: a barrier of the warps would hang if
             // one of them gave up)
             auto all_warps = [&](int nth) {
@@ -614,26 +648,36 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             float4* stage = reinterpret_cast<float4*>(sm + t * L::QTILE + (warp & 3) * (32 * CW * 4));
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                for (int c = 0; c < CW; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld8(oa + h * CW + c, r);
+                    tmem_ld8(oa + h * CW + c + 8, r + 8);
 #pragma unroll
-                for (int c = 0; c < CW; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(oa + h * CW + c, r);
-                    tmem_ld_wait(r);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
+                    for (int k = 0; k < 16; k += 4)
                         stage[lane * CH + (((c + k) / 4) ^ (lane & (CH - 1)))] =
                             make_float4(__uint_as_float(r[k]) * f, __uint_as_float(r[k + 1]) * f,
                                         __uint_as_float(r[k + 2]) * f, __uint_as_float(r[k + 3]) * f);
                 }
                 __syncwarp();
                 const int c = lane % CH;
-#pragma unroll 4
-                for (int k = 0; k < 32 / AT; ++k) {
-                    const int r = k * AT + lane / CH;
-                    const long long off = __shfl_sync(0xFFFFFFFFu, mine, r);
-                    const float4 v = stage[r * CH + (c ^ (r & (CH - 1)))];
-                    if (!final) *reinterpret_cast<float4*>(P.o + off + h * CW + 4 * c) = v;
-                    else if (off >= 0) attn_store4<E>(A, off + h * CW + 4 * c, v);
+#pragma unroll 1
+                for (int k0 = 0; k0 < 32 / AT; k0 += 4) {
+                    float4 v[4];
+                    long long off[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = (k0 + k) * AT + lane / CH;
+                        v[k] = stage[r * CH + (c ^ (r & (CH - 1)))];
+                        off[k] = __shfl_sync(0xFFFFFFFFu, mine, r);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (off[k] >= 0) {
+                            const long long at = off[k] + h * CW + 4 * c;
+                            if (wide) *reinterpret_cast<float4*>(out + 4 * at) = v[k];
+                            else *reinterpret_cast<uint2*>(out + 2 * at) = make_uint2(pack_pair<E>(v[k].x, v[k].y), pack_pair<E>(v[k].z, v[k].w));
+                        }
                 }
                 __syncwarp();
             }
@@ -641,8 +685,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
             else if (in && A.lse) A.lse[tok * A.heads + qh] = l == 0.0f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
             ok = all_warps(1);   // the tile is free
             if (!ok) break;
-            have = W.next(A, P, lane, S);
-            if (have) load_q(S);
+            have = more;
+            S = next;
             // O has been read: the next piece's first product (after its P) may overwrite it
             tc_before();
         }
@@ -674,11 +718,12 @@ __device__ __forceinline__ void add_rows(const AttnArgs& A, Sums<JR, MOST, SETS>
         weigh(A, sums, k, in ? sums.pieces[0][k].n + (SETS == 2 ? sums.pieces[SETS - 1][k].n : 0) : 0, in, threadIdx.x & 7);
     }
     __syncthreads();
+#pragma unroll 1
     for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
-        const int k = e / (D / 4), d = 4 * (e - k * (D / 4));
+        const int k = e / (D / 4), d = 4 * (e % (D / 4));
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        add_pieces<D>(P, sums.pieces[0][k], sums.ml, k, d, acc);
-        if (SETS == 2) add_pieces<D>(W, sums.pieces[SETS - 1][k], sums.ml + sums.pieces[0][k].n, k, d, acc);
+        add_pieces<D, JR>(P, sums.pieces[0][k], &sums.ml[0][k], d, acc);
+        if (SETS == 2) add_pieces<D, JR>(W, sums.pieces[SETS - 1][k], &sums.ml[sums.pieces[0][k].n][k], d, acc);
         const float inv = sums.inv[k];
         attn_store4<E>(A, sums.out[k] + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     }
@@ -704,7 +749,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         if (own_tiles(A, P, cut.x) > 0) return;
         heads = A.kv_heads;
     }
-    const int b = cut.x / P.own_row_tiles, rt = cut.x - b * P.own_row_tiles, i0 = blockIdx.y * JR;
+    const int b = own_seq(P, cut.x), rt = cut.x - b * P.own_row_tiles, i0 = blockIdx.y * JR;
     const unsigned r0 = ((unsigned)rt << P.tile_shift) + i0, all = A.nq * A.group;
     const int rows = r0 < all ? (int)min((unsigned)JR, all - r0) : 0;
     for (int h = cut.y; h < cut.y + heads; ++h) {

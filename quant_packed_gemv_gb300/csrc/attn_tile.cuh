@@ -38,19 +38,22 @@ __device__ __forceinline__ bool attn_shares(const AttnArgs& A, const TilePlan& P
     return P.prefix_tiles > 0 && len - A.nq + 1 >= A.prefix;
 }
 
+// Sequence of a (sequence, row tile).
+__device__ __forceinline__ int own_seq(const TilePlan& P, int pair) { return P.own_row_tiles == 1 ? pair : pair / P.own_row_tiles; }
+
 // First own key of a sequence, and the end of the keys that row tile rt of it
 // sees.
 __device__ __forceinline__ int own_begin(const AttnArgs& A, const TilePlan& P, int len) {
     return attn_shares(A, P, len) ? A.prefix : 0;
 }
 __device__ __forceinline__ int own_end(const AttnArgs& A, const TilePlan& P, int len, int rt) {
-    const unsigned last = min((unsigned)(A.nq * A.group), (unsigned)(rt + 1) << P.tile_shift) - 1;   // rows fit 31 bits
-    return attn_seen(A, len, (int)(last / (unsigned)A.group));
+    if (rt + 1 == P.own_row_tiles) return len;   // its last row is the last query's
+    return attn_seen(A, len, (int)((((unsigned)(rt + 1) << P.tile_shift) - 1) / (unsigned)A.group));
 }
 
 // Units of (sequence, row tile) `pair` of the own jobs, for one head.
 __device__ __forceinline__ int own_tiles(const AttnArgs& A, const TilePlan& P, int pair) {
-    const int b = pair / P.own_row_tiles, rt = pair - b * P.own_row_tiles;
+    const int b = own_seq(P, pair), rt = pair - b * P.own_row_tiles;
     const int len = attn_len(A, attn_row(A, b));
     return max(0, own_end(A, P, len, rt) - own_begin(A, P, len) + TK - 1) / TK;
 }
@@ -148,18 +151,18 @@ __device__ __forceinline__ void weigh(const AttnArgs& A, Sums<ROWS, MOST, SETS>&
     }
 }
 
-// acc += the pieces' dims d .. d + 3, weighted.
+// acc += the dims d .. d + 3 of the pieces, weighted (w: ROWS apart).
 template <int D, int ROWS>
-__device__ __forceinline__ void add_pieces(const TilePlan& P, const Pieces& X, const float2 (*w)[ROWS], int r, int d, float4& acc) {
+__device__ __forceinline__ void add_pieces(const TilePlan& P, const Pieces& X, const float2* w, int d, float4& acc) {
     constexpr int AHEAD = 8;   // loads in flight
+#pragma unroll 1
     for (int p = 0; p < X.n; p += AHEAD) {
         float4 v[AHEAD];
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q)
-            v[q] = *reinterpret_cast<const float4*>(P.o + X.at(min(p + q, X.n - 1)) * D + d);
+        for (int q = 0; q < AHEAD; ++q) v[q] = *reinterpret_cast<const float4*>(P.o + X.at(min(p + q, X.n - 1)) * D + d);
 #pragma unroll
         for (int q = 0; q < AHEAD; ++q) {
-            const float f = p + q < X.n ? w[p + q][r].x : 0.0f;
+            const float f = p + q < X.n ? w[(p + q) * ROWS].x : 0.0f;
             if (f != 0.0f) {   // O of a part without weight may hold anything
                 acc.x = fmaf(f, v[q].x, acc.x);
                 acc.y = fmaf(f, v[q].y, acc.y);
