@@ -133,14 +133,6 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
         cp_commit();
     };
 
-    int blk = first + stream, page = page_of(blk);
-#pragma unroll
-    for (int i = 0; i < Sm::STAGES - 1; ++i) {
-        const int next = page_of(blk + (i + 1) * streams);
-        fetch(blk + i * streams, page, i);
-        page = next;
-    }
-
     // Q as the B operand: row 8 nb + g, dims 32 c + 8 t ..; zeros past the rows
     uint4 qf[QS ? 1 : NB][QS ? 1 : KC];
     auto q_part = [&](int nb, int c) {
@@ -167,6 +159,15 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
             const int rr = 8 * nb + 2 * t + i;
             seen[nb][i] = rr < rows ? attn_seen(A, len, small_row(A, rr)) : 0;
         }
+
+    int blk = first + stream, page = page_of(blk);
+#pragma unroll
+    for (int i = 0; i < Sm::STAGES - 1; ++i) {
+        const int next = page_of(blk + (i + 1) * streams);
+        fetch(blk + i * streams, page, i);
+        page = next;
+    }
+
     float m[NB][2], l[NB][2], o[NB][2 * VC * 2][4];   // o: D / 16 tiles of 16 dims x 8 rows
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {

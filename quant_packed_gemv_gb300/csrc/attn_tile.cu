@@ -162,9 +162,8 @@ struct Piece {
 };
 
 // Walks the CTA's share of the units; every warp for itself, by all its lanes.
-// Not inlined, and nothing outside the loops over units unrolled far: a CTA runs
-// that code once or twice, and fetching it is what it costs (at 140 KB of code the
-// start and end of a piece took 10 us).
+// (Outside the loops over units little is unrolled: a CTA runs that code once or
+// twice, and most of its cost is to fetch it.)
 struct Walk {
     int u, end;        // the next unit, the end of the share
     int prefix_row;    // prefix: table row that holds it
@@ -172,7 +171,7 @@ struct Walk {
     int item_u0;       // own: first unit of the item
 
     // Returns the number of all units.  tables: page tables will be read.
-    __device__ __noinline__ int start(const AttnArgs& A, const TilePlan& P, int lane, bool tables) {
+    __device__ int start(const AttnArgs& A, const TilePlan& P, int lane, bool tables) {
         int U;
         if (P.job == 0) {
             U = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
@@ -226,7 +225,7 @@ struct Walk {
         }
     }
 
-    __device__ __noinline__ bool next(const AttnArgs& A, const TilePlan& P, int lane, Piece& S) {
+    __device__ bool next(const AttnArgs& A, const TilePlan& P, int lane, Piece& S) {
         if (u >= end) return false;
         if (P.job == 0) {
             S.item = u / P.prefix_tiles;
@@ -347,6 +346,10 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 }
             }
             first = false;
+            // The first piece's Q comes before the ring is filled: 160 KB an SM are
+            // 4 us of HBM, and Q, the code and the constants would queue behind them
+            if (n == 0)
+                for (int t = 0; ok && t < NT; ++t) ok = warp_wait(&q_ready[t], 0);
             for (int i = 0; ok && i < S.tiles; ++i) {
                 const int j = S.key0 + i * TK + box * bt;
                 int page = A.pages;   // out of range: the box is filled with zeros
@@ -861,6 +864,24 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 }  // namespace
 
+// CTAs of the prefix launch.  With a multiple of the items, s each, no CTA holds
+// pieces of two items; a piece costs its start and end (~3 units) and each piece
+// of an item makes its sums longer (~1/4 unit).  One GB300, 61 streams behind
+// 8176 (4 items of 64 units): 152 CTAs 23.9 us, 128 22.6, 64 18.1; 48 x 5 tokens
+// behind 8192 (32 items of 64): 152 CTAs 88 us, 128 81.
+static int prefix_ctas(long long items, long long tiles, int sms) {
+    const long long units = items * tiles, all = units < sms ? units : sms, share = (units + all - 1) / all;
+    long long best = all, cost = 4 * (share + 3) + tiles / share + 1;
+    for (long long s = 1; s <= tiles && s * items <= sms; ++s) {
+        const long long c = 4 * ((tiles + s - 1) / s) + s;
+        if (c <= cost) {
+            cost = c;
+            best = s * items;
+        }
+    }
+    return (int)best;
+}
+
 TilePlan tile_plan(const AttnArgs& A, int d, int job, bool share, void* ws, size_t* bytes) {
     const long long mine = (long long)A.nq * A.group, all = job == 0 ? mine * A.batch : mine;
     TilePlan T = {};
@@ -879,6 +900,7 @@ TilePlan tile_plan(const AttnArgs& A, int d, int job, bool share, void* ws, size
     (job == 0 ? T.prefix_row_tiles : T.own_row_tiles) = (int)row_tiles;
     const int sms = num_sms() < MOST_CTAS ? num_sms() : MOST_CTAS;
     T.ctas = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
+    if (job == 0) T.ctas = prefix_ctas(items, T.prefix_tiles, sms);
     const size_t slots = T.keep ? (size_t)(T.ctas + items) : 2 * (size_t)T.ctas;
     const size_t item_b = job == 1 && T.keep ? up256(4 * (size_t)items) : 0, cut_b = up256(sizeof(int4) * (size_t)T.ctas);
     const size_t ml_b = up256(slots * T.tile_rows * sizeof(float2));

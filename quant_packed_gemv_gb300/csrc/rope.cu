@@ -7,12 +7,16 @@
 // bits as a signed number are turns in [-1/2, 1/2), and sincospi of twice
 // that needs no range reduction.
 //
-// Bound: HBM (each value read and written once, ~1 operation per byte).
-// A CTA takes TB tokens: its threads first put the TB * R/2 (c, s) pairs into
-// shared memory (one sincospi each, shared by all heads), then walk the
-// tokens' head rows.  A unit is V pairs (or 2V values past the rotary part):
-// V = 8 gives 16-byte accesses of 16-bit types; smaller V where the rotary
-// size, a stride or a pointer is not a multiple of that.
+// Bound: HBM (each value read and written once, ~1 operation per byte); next is
+// the issue of the address and conversion work around the two FMAs a pair.  A CTA
+// takes TB tokens: its threads first put the TB * R/2 (c, s) pairs into shared
+// memory (one sincospi each, shared by all heads) and work out where each token
+// goes in the cache, then walk the head rows of one tensor after the other, in
+// a loop made for its types.  A unit is V pairs (or 2V values past the rotary
+// part): V = 8 gives 16-byte accesses of 16-bit types; smaller V where the rotary
+// size, a stride or a pointer is not a multiple of that.  A thread steps from unit
+// to unit by additions.  (With the types, the tensor and 64-bit divisions for the
+// slots looked up per unit, the kernel ran at 70 % of the copy rate.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,10 +32,10 @@ namespace {
 
 constexpr int RT = 256;          // threads per CTA
 constexpr int ROPE_CS = 1024;    // (c, s) pairs of a CTA's tokens at most
+constexpr int ROPE_TB = 4;       // tokens of a CTA at most
 
 struct RopeArgs {
     plm_rope_tensor t[PLM_ROPE_MAX_TENSORS];
-    int head0[PLM_ROPE_MAX_TENSORS + 1];   // first head of each tensor in the joint head index
     int count;
     const int32_t* positions;
     const unsigned long long* freqs;
@@ -74,22 +78,67 @@ __device__ __forceinline__ void store_as(E* p, const float (&v)[N]) {
     }
 }
 
-template <int W, int N>
-__device__ __forceinline__ void load_any(const void* base, long long off, int type, float (&v)[N]) {
-    if (type == PLM_F32) load_as<W>(static_cast<const float*>(base) + off, v);
-    else if (type == PLM_F16) load_as<W>(static_cast<const __half*>(base) + off, v);
-    else load_as<W>(static_cast<const __nv_bfloat16*>(base) + off, v);
-}
-template <int W, int N>
-__device__ __forceinline__ void store_any(void* base, long long off, int type, const float (&v)[N]) {
-    if (type == PLM_F32) store_as<W>(static_cast<float*>(base) + off, v);
-    else if (type == PLM_F16) store_as<W>(static_cast<__half*>(base) + off, v);
-    else store_as<W>(static_cast<__nv_bfloat16*>(base) + off, v);
+// The head rows of one tensor, of types X to Y.
+template <int V, bool HALF, class X, class Y>
+__device__ __forceinline__ void rope_rows(const plm_rope_tensor& T, long long t0, int nt, int d, int pairs, const float* cs_c,
+                                          const float* cs_s, const long long* place, int first, int step) {
+    const int upr = d / (2 * V), rot_units = T.rotate ? pairs / V : 0;   // units per head row, turned ones
+    const int heads = (int)T.heads;
+    const X* const x = static_cast<const X*>(T.x) + t0 * T.x_token_stride;
+    Y* const y = static_cast<Y*>(T.y);
+    const long long xt = T.x_token_stride, xh = T.x_head_stride, yh = T.y_head_stride;
+    const bool paged = T.slots != nullptr;
+    int row = first / upr, un = first - row * upr, t = row / heads, h = row - t * heads;
+    const int row_step = step / upr, un_step = step - row_step * upr, t_step = row_step / heads, h_step = row_step - t_step * heads;
+    while (t < nt) {
+        const long long base = place[t];
+        if (!paged || base >= 0) {
+            const X* const xp = x + t * xt + h * xh;
+            Y* const yp = y + base + h * yh;
+            if (un < rot_units) {
+                float c[V], s[V], v[2 * V];
+                if (HALF) {
+                    load_as<V>(xp + un * V, *reinterpret_cast<float (*)[V]>(v));
+                    load_as<V>(xp + pairs + un * V, *reinterpret_cast<float (*)[V]>(v + V));
+                } else {
+                    load_as<V>(xp + 2 * un * V, v);
+                }
+                load_as<V>(cs_c + t * pairs + un * V, c);
+                load_as<V>(cs_s + t * pairs + un * V, s);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float& a = v[HALF ? i : 2 * i];
+                    float& b = v[HALF ? V + i : 2 * i + 1];
+                    const float p = a * c[i] - b * s[i], q = b * c[i] + a * s[i];
+                    a = p;
+                    b = q;
+                }
+                if (HALF) {
+                    store_as<V>(yp + un * V, *reinterpret_cast<float (*)[V]>(v));
+                    store_as<V>(yp + pairs + un * V, *reinterpret_cast<float (*)[V]>(v + V));
+                } else {
+                    store_as<V>(yp + 2 * un * V, v);
+                }
+            } else {
+                float v[2 * V];
+                load_as<V>(xp + 2 * un * V, v);
+                store_as<V>(yp + 2 * un * V, v);
+            }
+        }
+        un += un_step;
+        int carry = 0;
+        if (un >= upr) { un -= upr; carry = 1; }
+        h += h_step + carry;
+        t += t_step;
+        while (h >= heads) { h -= heads; ++t; }
+    }
 }
 
+// CTA (x, y): tokens x * TB .., tensors y, y + gridDim.y, ..
 template <int V, bool HALF>
-__global__ void __launch_bounds__(RT) rope_kernel(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(RT, 6) rope_kernel(const __grid_constant__ RopeArgs A) {
     __shared__ __align__(16) float cs_c[ROPE_CS], cs_s[ROPE_CS];
+    __shared__ long long place[PLM_ROPE_MAX_TENSORS][ROPE_TB];   // a token's offset in y, -1: not written
     grid_launch_dependents();
     grid_wait_prior();
     const long long t0 = (long long)blockIdx.x * A.tb;
@@ -104,62 +153,35 @@ __global__ void __launch_bounds__(RT) rope_kernel(const __grid_constant__ RopeAr
         cs_c[i] = c * A.scale;
         cs_s[i] = A.inverse ? -s * A.scale : s * A.scale;
     }
-    __syncthreads();
-    const int upr = A.d / (2 * V);                    // units per head row
-    const int heads = A.head0[A.count];
-    const int units = nt * heads * upr;
-    const int rot_units = pairs / V;
-    for (int u = blockIdx.y * RT + threadIdx.x; u < units; u += RT * gridDim.y) {
-        const int row = u / upr, un = u - row * upr;
-        const int t = row / heads, hj = row - t * heads;
-        int j = 0;
-        while (hj >= A.head0[j + 1]) ++j;
+    for (int i = threadIdx.x; i < nt * A.count; i += RT) {
+        const int j = i / nt, t = i - j * nt;
         const plm_rope_tensor& T = A.t[j];
-        const int h = hj - A.head0[j];
-        const long long tok = t0 + t;
-        const long long xo = tok * T.x_token_stride + h * T.x_head_stride;
-        long long yo = h * T.y_head_stride;
+        long long yo = (t0 + t) * T.y_token_stride;
         if (T.slots) {
-            const long long slot = __ldg(T.slots + tok);
-            if (slot < 0 || slot >= T.pages * T.page_tokens) continue;
-            const long long page = slot / T.page_tokens;
-            yo += page * T.page_stride + (slot - page * T.page_tokens) * T.y_token_stride;
-        } else {
-            yo += tok * T.y_token_stride;
+            const long long slot = __ldg(T.slots + t0 + t);
+            yo = -1;
+            if (slot >= 0 && slot < T.pages * T.page_tokens) {
+                const long long page = slot / T.page_tokens;
+                yo = page * T.page_stride + (slot - page * T.page_tokens) * T.y_token_stride;
+            }
         }
-        if (un < rot_units && T.rotate) {
-            float c[V], s[V], a[V], b[V];
-            load_as<V>(cs_c + t * pairs + un * V, c);
-            load_as<V>(cs_s + t * pairs + un * V, s);
-            if (HALF) {
-                load_any<V>(T.x, xo + un * V, T.x_type, a);
-                load_any<V>(T.x, xo + pairs + un * V, T.x_type, b);
-            } else {
-                float v[2 * V];
-                load_any<V>(T.x, xo + 2 * un * V, T.x_type, v);
-#pragma unroll
-                for (int i = 0; i < V; ++i) { a[i] = v[2 * i]; b[i] = v[2 * i + 1]; }
-            }
-            float p[V], q[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                p[i] = a[i] * c[i] - b[i] * s[i];
-                q[i] = b[i] * c[i] + a[i] * s[i];
-            }
-            if (HALF) {
-                store_any<V>(T.y, yo + un * V, T.y_type, p);
-                store_any<V>(T.y, yo + pairs + un * V, T.y_type, q);
-            } else {
-                float v[2 * V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) { v[2 * i] = p[i]; v[2 * i + 1] = q[i]; }
-                store_any<V>(T.y, yo + 2 * un * V, T.y_type, v);
-            }
-        } else {
-            float v[2 * V];
-            load_any<V>(T.x, xo + 2 * un * V, T.x_type, v);
-            store_any<V>(T.y, yo + 2 * un * V, T.y_type, v);
-        }
+        place[j][t] = yo;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int j = blockIdx.y; j < A.count; j += gridDim.y) {
+        const plm_rope_tensor& T = A.t[j];
+        auto rows = [&](auto x, auto y) {
+            rope_rows<V, HALF, decltype(x), decltype(y)>(T, t0, nt, A.d, pairs, cs_c, cs_s, place[j], threadIdx.x, RT);
+        };
+        auto from = [&](auto x) {
+            if (T.y_type == PLM_F32) rows(x, float());
+            else if (T.y_type == PLM_F16) rows(x, __half());
+            else rows(x, __nv_bfloat16());
+        };
+        if (T.x_type == PLM_F32) from(float());
+        else if (T.x_type == PLM_F16) from(__half());
+        else from(__nv_bfloat16());
     }
 }
 
@@ -195,10 +217,7 @@ cudaError_t launch_rope(const plm_rope_tensor* tensors, int count, const int32_t
                         cudaStream_t stream) {
     RopeArgs A = {};
     A.count = count;
-    for (int j = 0; j < count; ++j) {
-        A.t[j] = tensors[j];
-        A.head0[j + 1] = A.head0[j] + (int)tensors[j].heads;
-    }
+    for (int j = 0; j < count; ++j) A.t[j] = tensors[j];
     A.positions = positions;
     A.freqs = reinterpret_cast<const unsigned long long*>(freqs);
     A.tokens = tokens;
@@ -208,20 +227,16 @@ cudaError_t launch_rope(const plm_rope_tensor* tensors, int count, const int32_t
     A.inverse = inverse;
     const int V = rope_fits(A, 8) ? 8 : rope_fits(A, 4) ? 4 : rope_fits(A, 2) ? 2 : 1;
     // Tokens per CTA: enough (c, s) pairs to occupy its threads, while every
-    // SM still gets CTAs; few tokens are spread over CTAs by heads instead.
+    // SM still gets CTAs; few tokens are spread over CTAs by tensors instead.
     const int sms = num_sms();
-    int tb = 2 * RT / rotary_dim;
+    // (Four tokens: 2 and 8 measured 66 and 56 us where 4 takes 55, on 16381 x 40
+    // heads of 128 in bf16; 53 and 57 us on f32 into pages.)
+    int tb = 2 * RT / rotary_dim < 4 ? 2 * RT / rotary_dim : ROPE_TB;
     if (tb > tokens / (2 * sms)) tb = (int)(tokens / (2 * sms));
-    while (tb > 1 && (long long)tb * A.head0[count] * (head_dim / (2 * V)) > (1 << 20)) tb /= 2;   // int unit index
     if (tb < 1) tb = 1;
     A.tb = tb;
     const long long gx = (tokens + tb - 1) / tb;
-    const long long units = (long long)tb * A.head0[count] * (head_dim / (2 * V));
-    long long gy = (units + RT - 1) / RT;                 // CTAs that one unit per thread needs
-    const long long room = 4LL * sms / gx;
-    if (gy > room) gy = room;
-    if (gy < 1) gy = 1;
-    const dim3 grid((unsigned)gx, (unsigned)gy);
+    const dim3 grid((unsigned)gx, gx < 2 * sms ? (unsigned)count : 1u);
     switch (V) {
         case 8: return rope_launch<8>(A, layout, grid, stream);
         case 4: return rope_launch<4>(A, layout, grid, stream);
