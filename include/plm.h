@@ -749,6 +749,19 @@ size_t plm_attn_workspace_size(int64_t batch, int64_t tokens, int64_t heads, int
 plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, size_t workspace_bytes,
                                   cudaStream_t stream);
 
+/*
+ * For bindings in which each argument of a call costs: an entry point above
+ * with its arguments in one block of 8-byte fields, in the order of its
+ * declaration (pointers, sizes and the stream as they are, an int as int64_t,
+ * plm_rope's scale as a double), without the pointer to its struct or structs,
+ * which follow the fields in the block itself.  entry: 0 plm_rope, 1
+ * plm_kv_reserve, 2 plm_kv_fork, 3 plm_kv_free, 4 plm_kv_compact, 5
+ * plm_kv_copy_pages, 6 plm_attn_shared_prefix; PLM_ERR_INVALID_ARG otherwise
+ * and for a null block.  args is 8-byte aligned HOST memory, read during the
+ * call only.
+ */
+plm_status plm_call(int entry, const void* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/plm.h"
 #include "plm_device.cuh"
@@ -698,6 +699,34 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
         p->page_stride % 8 || p->kv_head_stride % 8 || p->kv_token_stride % 8)
         return PLM_ERR_MISALIGNED;
     return cuda_status(plm::launch_attn(*p, workspace, stream));
+}
+
+plm_status plm_call(int entry, const void* args) {
+    if (!args) return PLM_ERR_INVALID_ARG;
+    const int64_t* a = static_cast<const int64_t*>(args);
+    auto ptr = [&](int i) { return reinterpret_cast<void*>(a[i]); };
+    auto ints = [&](int i) { return static_cast<const int32_t*>(ptr(i)); };
+    auto stream = [&](int i) { return static_cast<cudaStream_t>(ptr(i)); };
+    auto kv = [&](int i) { return reinterpret_cast<const plm_kv_state*>(a + i); };
+    switch (entry) {
+        case 0: {
+            double scale;
+            std::memcpy(&scale, a + 7, sizeof scale);
+            return plm_rope(reinterpret_cast<const plm_rope_tensor*>(a + 10), a[0], ints(1),
+                            static_cast<const uint64_t*>(ptr(2)), a[3], a[4], a[5], (int)a[6], (float)scale, (int)a[8],
+                            stream(9));
+        }
+        case 1:
+            return plm_kv_reserve(kv(8), ints(0), ints(1), a[2], static_cast<int64_t*>(ptr(3)), a[4], ptr(5), (size_t)a[6],
+                                  stream(7));
+        case 2: return plm_kv_fork(kv(7), ints(0), ints(1), ints(2), a[3], ptr(4), (size_t)a[5], stream(6));
+        case 3: return plm_kv_free(kv(3), ints(0), a[1], stream(2));
+        case 4: return plm_kv_compact(kv(4), static_cast<int32_t*>(ptr(0)), ptr(1), (size_t)a[2], stream(3));
+        case 5: return plm_kv_copy_pages(kv(4), ints(0), ints(1), a[2], stream(3));
+        case 6:
+            return plm_attn_shared_prefix(reinterpret_cast<const plm_attn_problem*>(a + 3), ptr(0), (size_t)a[1], stream(2));
+        default: return PLM_ERR_INVALID_ARG;
+    }
 }
 
 }  // extern "C"

@@ -167,6 +167,7 @@ def load(build_if_missing=True):
             ("plm_kv_free", i32, [vp, vp, i64, vp]),
             ("plm_kv_compact", i32, [vp, vp, vp, sz, vp]),
             ("plm_kv_copy_pages", i32, [vp, vp, vp, i64, vp]),
+            ("plm_call", i32, [i32, vp]),
             ("plm_attn_workspace_size", sz, [i64] * 7),
             ("plm_attn_shared_prefix", i32, [vp, vp, sz, vp])):
         getattr(lib, name).argtypes = args
@@ -468,7 +469,9 @@ def _ints(t, bits, name, shape=None):
         raise ValueError("%s: expected int%d, got %s" % (name, bits, t.dtype))
     if shape is not None and t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
-    return _addr(t)
+    if not (t.is_cuda and t.is_contiguous()):
+        return _addr(t)   # says why
+    return t.data_ptr()
 
 
 def _rows(t, name, dims):
@@ -496,39 +499,55 @@ def plm_rope_freqs(rotary_dim, base, scaling="none", factor=1.0, trained=0.0, lo
     return (freqs if device is None else freqs.to(device)), scale.value
 
 
-# The structs of these calls are packed into bytes, which costs a fifth of
-# filling a ctypes structure: a decode step makes its calls in a few
-# microseconds of GPU time.
+# These calls are packed: their structs and arguments go to plm_call as bytes,
+# which costs a fifth of filling ctypes structures and converting arguments one by
+# one.  A decode step makes them for a few microseconds of GPU time each.
 _ROPE_TENSOR = struct.Struct("@11q3i4x")
 _KV_STATE = struct.Struct("@10q")
 _ATTN_PROBLEM = struct.Struct("@26qf2i4x")
+_ROPE_CALL = struct.Struct("@7qd2q")
+_RESERVE_CALL, _FORK_CALL, _FREE_CALL, _COMPACT_CALL, _COPY_CALL, _ATTN_CALL = (
+    struct.Struct("@%dq" % n) for n in (8, 7, 3, 4, 4, 3))
+_ROPE, _RESERVE, _FORK, _FREE, _COMPACT, _COPY, _ATTN = range(7)
+_NAMES = ("plm_rope", "plm_kv_reserve", "plm_kv_fork", "plm_kv_free", "plm_kv_compact", "plm_kv_copy_pages",
+          "plm_attn_shared_prefix")
+
+
+def _call(entry, args):
+    status = (_lib or load()).plm_call(entry, args)
+    if status != PLM_OK:
+        raise PlmError(_NAMES[entry], status, _lib)
 
 
 def plm_rope_tensor(x, y, slots=None, rotate=True):
     """One tensor of a plm_rope call, to be kept as long as its addresses hold.  x [tokens][heads][head_dim]; y the
     same shape, or with slots (int64 [tokens]) the pages [pages][heads][page_tokens][head_dim] of a cache, as any
     strided view."""
-    xt, xh, _ = _rows(x, "x", 3)
-    shape = x.shape
+    xs, shape, ys, xtype, ytype = x.stride(), x.shape, y.stride(), _types.get(x.dtype, -1), _types.get(y.dtype, -1)
+    if len(xs) != 3 or xs[2] != 1 or len(ys) != (3 if slots is None else 4) or ys[-1] != 1 or xtype < 0 or ytype < 0 or not (
+            x.is_cuda and y.is_cuda):   # an error, or a dimension of one: look closer
+        _rows(x, "x", 3)
+        _rows(y, "y", 3 if slots is None else 4)
+        xtype, ytype = _type(x), _type(y)
+    xt, xh, _ = xs
     tokens, heads, d = shape
     if slots is None:
-        yt, yh, _ = _rows(y, "y", 3)
+        yt, yh, _ = ys
         if y.shape != shape:
             raise ValueError("y: expected shape %s, got %s" % (tuple(shape), tuple(y.shape)))
         at = page_tokens = page_stride = pages = 0
     else:
-        page_stride, yh, yt, _ = _rows(y, "y", 4)
+        page_stride, yh, yt, _ = ys
         pages, yheads, page_tokens, yd = y.shape
         if yheads != heads or yd != d:
             raise ValueError("y: expected pages [.][%d][.][%d], got %s" % (heads, d, tuple(y.shape)))
         at = _ints(slots, 64, "slots", (tokens,))
     return (_ROPE_TENSOR.pack(x.data_ptr(), y.data_ptr(), at, heads, xt, xh, yt, yh, page_tokens, page_stride, pages,
-                              _type(x), _type(y), 1 if rotate else 0), tokens, d)
+                              xtype, ytype, 1 if rotate else 0), tokens, d)
 
 
 def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, inverse=False, stream=None):
     """Turns the heads of the tensors (plm_rope_tensor) by their positions (int32 [tokens]); see include/plm.h."""
-    lib = load()
     packed, tokens, d = tensors[0] if tensors else (b"", positions.numel(), 0)
     if len(tensors) > 1:
         for t in tensors:
@@ -539,17 +558,17 @@ def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, in
         raise ValueError("freqs: expected %d values, got %d" % (rotary_dim // 2, freqs.numel()))
     if tokens == 0 and tensors:
         return
-    _check("plm_rope", lib.plm_rope(packed, len(tensors), _ints(positions, 32, "positions", (tokens,)),
-                                    _ints(freqs, 64, "freqs"), tokens, d, rotary_dim, _LAYOUTS.get(layout, layout),
-                                    scale, 1 if inverse else 0, _stream(stream)))
+    _call(_ROPE, _ROPE_CALL.pack(len(tensors), _ints(positions, 32, "positions", (tokens,)), _ints(freqs, 64, "freqs"),
+                                 tokens, d, rotary_dim, _LAYOUTS.get(layout, layout), scale, 1 if inverse else 0,
+                                 _stream(stream)) + packed)
 
 
 def plm_kv_state(pool, table, lens, refs, page_tokens, status=None):
     """Page state over device tensors: pool [pages][...] of any type, table int32 [max_seqs][max_pages], lens int32
     [max_seqs], refs int32 [pages], status int32 [1] or None.  It holds addresses: keep the tensors."""
     pages, (seqs, width) = pool.shape[0], table.shape
-    return _KV_STATE.pack(_addr(pool), pool.numel() // max(1, pages) * pool.element_size(), pages,
-                          _ints(table, 32, "table"), _ints(lens, 32, "lens", (seqs,)), _ints(refs, 32, "refs", (pages,)),
+    return _KV_STATE.pack(_addr(pool), pool.nbytes // pages if pages else 0, pages, _ints(table, 32, "table"),
+                          _ints(lens, 32, "lens", (seqs,)), _ints(refs, 32, "refs", (pages,)),
                           _ints(status, 32, "status") or 0, seqs, width, page_tokens)
 
 
@@ -558,46 +577,45 @@ def plm_kv_workspace_size(pages, n):
     return load().plm_kv_workspace_size(pages, n)
 
 
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _ws(workspace):
+    """Address and size of a workspace tensor (None: 0, 0)."""
+    return (0, 0) if workspace is None else (_addr(workspace), workspace.nbytes)
 
 
 def plm_kv_reserve(kv, seqs, add, slots, workspace, stream=None):
     """Sequences seqs grow by add tokens (int32 [n]); slots int64 [n][most] or None gets the new tokens' slots."""
-    lib, n = load(), seqs.numel()
-    if slots is not None and (slots.dim() != 2 or slots.shape[0] != n):
-        raise ValueError("slots: expected [%d][.], got %s" % (n, tuple(slots.shape)))
-    _check("plm_kv_reserve", lib.plm_kv_reserve(kv, _ints(seqs, 32, "seqs"), _ints(add, 32, "add", (n,)), n,
-                                                _ints(slots, 64, "slots"), 0 if slots is None else slots.shape[1],
-                                                _addr(workspace), _bytes(workspace), _stream(stream)))
+    n, most = seqs.numel(), 0
+    if slots is not None:
+        rows, most = slots.shape
+        if rows != n:
+            raise ValueError("slots: expected [%d][.], got %s" % (n, tuple(slots.shape)))
+    ws, size = _ws(workspace)
+    _call(_RESERVE, _RESERVE_CALL.pack(_ints(seqs, 32, "seqs"), _ints(add, 32, "add", (n,)), n, _ints(slots, 64, "slots") or 0,
+                                       most, ws, size, _stream(stream)) + kv)
 
 
 def plm_kv_fork(kv, parents, children, workspace, keep=None, stream=None):
     """Unused sequences children (int32 [n]) become copies of parents, of their first keep tokens if given."""
-    lib, n = load(), parents.numel()
-    _check("plm_kv_fork", lib.plm_kv_fork(kv, _ints(parents, 32, "parents"), _ints(children, 32, "children", (n,)),
-                                          _ints(keep, 32, "keep", (n,)), n, _addr(workspace), _bytes(workspace),
-                                          _stream(stream)))
+    n, (ws, size) = parents.numel(), _ws(workspace)
+    _call(_FORK, _FORK_CALL.pack(_ints(parents, 32, "parents"), _ints(children, 32, "children", (n,)),
+                                 _ints(keep, 32, "keep", (n,)) or 0, n, ws, size, _stream(stream)) + kv)
 
 
 def plm_kv_free(kv, seqs, stream=None):
     """The sequences (int32 [n]) give their pages back."""
-    lib = load()
-    _check("plm_kv_free", lib.plm_kv_free(kv, _ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)))
+    _call(_FREE, _FREE_CALL.pack(_ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)) + kv)
 
 
 def plm_kv_compact(kv, live, workspace, stream=None):
     """Packs the pages in use to the front of the pool; live (int32 [1] or None) gets their number."""
-    lib = load()
-    _check("plm_kv_compact", lib.plm_kv_compact(kv, _ints(live, 32, "live"), _addr(workspace), _bytes(workspace),
-                                                _stream(stream)))
+    ws, size = _ws(workspace)
+    _call(_COMPACT, _COMPACT_CALL.pack(_ints(live, 32, "live") or 0, ws, size, _stream(stream)) + kv)
 
 
 def plm_kv_copy_pages(kv, src, dst, stream=None):
     """Page dst[i] = page src[i] (int32 lists of the same length)."""
-    lib, n = load(), src.numel()
-    _check("plm_kv_copy_pages", lib.plm_kv_copy_pages(kv, _ints(src, 32, "src"), _ints(dst, 32, "dst", (n,)), n,
-                                                      _stream(stream)))
+    n = src.numel()
+    _call(_COPY, _COPY_CALL.pack(_ints(src, 32, "src"), _ints(dst, 32, "dst", (n,)), n, _stream(stream)) + kv)
 
 
 def plm_attn_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len):
@@ -609,11 +627,15 @@ def plm_attn_shared_prefix(q, o, k, v, table, lens, tokens, prefix_len, max_len,
                            stream=None):
     """Attention of q [batch*tokens][heads][head_dim] over the pages k, v [pages][kv_heads][page_tokens][head_dim]
     (strided views of one shape and strides) into o; the batch's first prefix_len tokens are shared (see include/plm.h)."""
-    lib = load()
-    qt, qh, _ = _rows(q, "q", 3)
-    ot, oh, _ = _rows(o, "o", 3)
-    kp, kh, kt, _ = ks = _rows(k, "k", 4)
-    shape, kshape = q.shape, k.shape
+    qs, os_, ks, shape, kshape = q.stride(), o.stride(), k.stride(), q.shape, k.shape
+    ktype, otype = _types.get(k.dtype, -1), _types.get(o.dtype, -1)
+    if len(qs) != 3 or len(os_) != 3 or len(ks) != 4 or qs[2] != 1 or os_[2] != 1 or ks[3] != 1 or ktype < 0 or otype < 0 or not (
+            q.is_cuda and o.is_cuda and k.is_cuda):   # an error, or a dimension of one: look closer
+        _rows(q, "q", 3)
+        _rows(o, "o", 3)
+        _rows(k, "k", 4)
+        ktype, otype = _type(k), _type(o)
+    (qt, qh, _), (ot, oh, _), (kp, kh, kt, _) = qs, os_, ks
     if o.shape != shape:
         raise ValueError("o: expected shape %s, got %s" % (tuple(shape), tuple(o.shape)))
     if v.shape != kshape or v.stride() != ks or v.dtype != k.dtype or q.dtype != k.dtype or not v.is_cuda:
@@ -632,8 +654,9 @@ def plm_attn_shared_prefix(q, o, k, v, table, lens, tokens, prefix_len, max_len,
         raise ValueError("lse: expected float32 %s" % ((n, heads),))
     if batch == 0:
         return
+    ws, size = _ws(workspace)
     p = _ATTN_PROBLEM.pack(q.data_ptr(), o.data_ptr(), _addr(lse) or 0, k.data_ptr(), v.data_ptr(),
                            _ints(table, 32, "table"), _ints(lens, 32, "lens", (rows,)),
                            _ints(seqs, 32, "seqs", (batch,)) or 0, batch, tokens, heads, kv_heads, d, qt, qh, ot, oh,
-                           page_tokens, pages, kp, kh, kt, width, rows, prefix_len, max_len, scale, _type(k), _type(o))
-    _check("plm_attn_shared_prefix", lib.plm_attn_shared_prefix(p, _addr(workspace), _bytes(workspace), _stream(stream)))
+                           page_tokens, pages, kp, kh, kt, width, rows, prefix_len, max_len, scale, ktype, otype)
+    _call(_ATTN, _ATTN_CALL.pack(ws, size, _stream(stream)) + p)

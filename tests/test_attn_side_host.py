@@ -173,3 +173,34 @@ def test_attention_refusals():
     need = size(4, 1, 16, 8, 128, 64, 100)
     if need:
         assert st(b=need - 1) == BAD and st(w=None) == BAD and st(w=A + 16) == MIS
+
+
+def test_packed_calls_are_the_same_calls():
+    # the block form refuses what the entry points refuse, with the same status (nothing is launched)
+    import struct
+    call = lambda entry, args: P.raw_status("plm_call", entry, args)  # noqa: E731
+    assert call(7, b"\0" * 64) == BAD and call(-1, b"\0" * 64) == BAD and call(0, None) == BAD
+
+    def q8(*v):
+        return struct.pack("@%dq" % len(v), *v)
+
+    def rope(count=1, pos=A, freqs=A, tokens=4, d=128, rot=128, layout=0, t=None):
+        return call(0, struct.pack("@7qd2q", count, pos, freqs, tokens, d, rot, layout, 1.0, 0, 0) + bytes(t or rope_tensor()))
+    assert rope(count=0) == BAD and rope(pos=0) == BAD and rope(rot=3) == BAD and rope(layout=2) == BAD
+    assert rope(freqs=A + 4) == MIS and rope(t=rope_tensor(x=A + 2)) == MIS and rope(tokens=0) == P.PLM_OK
+    ws, s = q.plm_kv_workspace_size(64, 4), bytes(kv())
+    assert call(1, q8(A, A, 4, A + 4, 2, A, ws, 0) + s) == MIS and call(1, q8(0, A, 4, 0, 0, A, ws, 0) + s) == BAD
+    assert call(1, q8(A, A, 0, 0, 0, A, ws, 0) + s) == P.PLM_OK
+    assert call(2, q8(A, A, A + 1, 4, A, ws, 0) + s) == MIS and call(2, q8(A, A, 0, 4, A, 3, 0) + s) == BAD
+    assert call(3, q8(A + 2, 4, 0) + s) == MIS and call(3, q8(A, 0, 0) + s) == P.PLM_OK
+    assert call(4, q8(A + 2, A, ws, 0) + s) == MIS and call(4, q8(0, 0, ws, 0) + s) == BAD
+    assert call(5, q8(A, 0, 4, 0) + s) == BAD and call(5, q8(A, A, 0, 0) + s) == P.PLM_OK
+    a = lambda **kw: bytes(P._AttnProblem.from_address(ctypes.addressof(attn(**kw)._obj)))  # noqa: E731
+    assert call(6, q8(A, 1 << 40, 0) + a(k=A + 8)) == MIS and call(6, q8(A, 1 << 40, 0) + a(head_dim=96)) == UNS
+    assert call(6, q8(A, 1 << 40, 0) + a(batch=0)) == P.PLM_OK
+
+
+def test_the_bindings_blocks_have_the_structs_layout():
+    for ctype, packed in ((P._RopeTensor, P._ROPE_TENSOR), (P._KvState, P._KV_STATE), (P._AttnProblem, P._ATTN_PROBLEM)):
+        values = list(range(1, len(ctype._fields_) + 1))
+        assert ctypes.sizeof(ctype) == packed.size and bytes(ctype(*values)) == packed.pack(*values)
