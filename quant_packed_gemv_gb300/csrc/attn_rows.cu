@@ -61,7 +61,8 @@ __device__ __forceinline__ uint32_t words(const uint4& u, int i) { return i == 0
 // O [rows][D + 4] (padded against conflicts).
 template <int D, int NB> struct RowsSmem {
     static constexpr int ROWS = 8 * NB, PITCH = D + 4;
-    static constexpr int STAGES = D == 64 ? 4 : 2, STAGE = 16 * D * 2;   // bytes of 16 keys' K, or V
+    static constexpr int STAGES = (D == 64 ? 2 : 1) * (NB == 1 ? 2 : 3);
+    static constexpr int STAGE = 16 * D * 2;   // bytes of 16 keys' K, or V
     struct Parts {
         float m[DW][ROWS], l[DW][ROWS];
         float o[DW][ROWS][PITCH];
@@ -81,7 +82,7 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 template <class E, int D, int NB>
-__global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
+__global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     using Sm = RowsSmem<D, NB>;
     constexpr int KC = D / 32, VC = D / 64;   // 16-byte chunks per lane of a K row, of a V row
     constexpr bool QS = NB > 2;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
     if ((int)threadIdx.x < mine) {
         const int k = threadIdx.x, r = blockIdx.z + k * cs, gr = b * rows + r, t_ = small_row(A, r);
         sums.place(A, k, (long long)b * A.nq + t_, h * A.group + r - t_ * A.group);
-        sums.pieces[0][k].n = 0;
+        sums.pieces[0][k] = Pieces{0, 0, 0, 0};
         if (shares) {
             const int rt = gr >> P.tile_shift, item = h * P.prefix_row_tiles + rt;
             sums.pieces[0][k] = item_pieces(P, item, item * P.prefix_tiles, P.prefix_tiles,
@@ -312,24 +313,42 @@ __global__ void __launch_bounds__(DW * 32, NB <= 3 ? 3 : 2) attn_rows_kernel(con
         weigh(A, sums, k, parts + sums.pieces[0][k].n, k0 + (int)threadIdx.x / 8 < mine, threadIdx.x & 7);
     }
     __syncthreads();
+    constexpr int N = NB == 1 ? 1 : 2;   // 8 rows at most fill the threads once or twice
 #pragma unroll 1
-    for (int e = threadIdx.x; e < mine * (D / 4); e += DW * 32) {
-        const int k = e / (D / 4), d = 4 * (e % (D / 4)), r = blockIdx.z + k * cs;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) {
-            const float f = sums.ml[p][k].x;
-            const float4 v = peer_f32x4(&sm.part.o[p % DW][r][d], p / DW);
-            if (f != 0.0f) {
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            }
+    for (int e0 = threadIdx.x; e0 < mine * (D / 4); e0 += N * DW * 32) {
+        int k[N], d[N];
+        float4 acc[N];
+        const Pieces* X[N];
+        const float2* w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = min(e0 + i * DW * 32, mine * (D / 4) - 1);
+            k[i] = e / (D / 4);
+            d[i] = 4 * (e % (D / 4));
+            X[i] = &sums.pieces[0][k[i]];
+            w[i] = &sums.ml[parts][k[i]];
+            acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        add_pieces<D, Sm::ROWS>(P, sums.pieces[0][k], &sums.ml[parts][k], d, acc);
-        const float inv = sums.inv[k];
-        attn_store4<E>(A, sums.out[k] + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float f = sums.ml[p][k[i]].x;
+                const float4 v = peer_f32x4(&sm.part.o[p % DW][blockIdx.z + k[i] * cs][d[i]], p / DW);
+                if (f != 0.0f) {
+                    acc[i].x = fmaf(f, v.x, acc[i].x);
+                    acc[i].y = fmaf(f, v.y, acc[i].y);
+                    acc[i].z = fmaf(f, v.z, acc[i].z);
+                    acc[i].w = fmaf(f, v.w, acc[i].w);
+                }
+            }
+        if (shares) add_pieces<D, Sm::ROWS>(P, X, w, d, acc);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e0 + i * DW * 32 < mine * (D / 4)) {
+                const float inv = sums.inv[k[i]];
+                attn_store4<E>(A, sums.out[k[i]] + d[i], make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+            }
     }
     if (cs > 1) cluster_barrier();   // no CTA leaves while its part is read
 }
@@ -354,10 +373,11 @@ cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t s
     return rows <= 24 ? rows_launch<E, D, 3>(A, P, cs, stream) : rows_launch<E, D, 4>(A, P, cs, stream);
 }
 
-// CTAs of a pair (at most 8: 32 warps): while the pairs alone leave warps idle (12 fit an SM), and
-// every warp still gets two blocks of 16 keys.
+// CTAs of a pair (at most 8: 32 warps): as many as the GPU holds at once (a second
+// wave costs a whole start and end: 12 x 9 tokens behind 512, 30 us where one wave
+// takes 17), while every warp still gets two blocks of 16 keys.
 int rows_cluster(const AttnArgs& A, int keys) {
-    const long long pairs = (long long)A.batch * A.kv_heads, room = 3LL * num_sms();
+    const long long pairs = (long long)A.batch * A.kv_heads, room = (A.nq * A.group <= 8 ? 3LL : 2LL) * num_sms();
     int cs = 1;
     while (cs < 8 && pairs * cs * 2 <= room && keys > 2 * 16 * DW * cs) cs *= 2;
     return cs;

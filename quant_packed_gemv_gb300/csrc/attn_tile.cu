@@ -724,11 +724,11 @@ __device__ __forceinline__ void add_rows(const AttnArgs& A, Sums<JR, MOST, SETS>
 #pragma unroll 1
     for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
         const int k = e / (D / 4), d = 4 * (e % (D / 4));
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        add_pieces<D, JR>(P, sums.pieces[0][k], &sums.ml[0][k], d, acc);
-        if (SETS == 2) add_pieces<D, JR>(W, sums.pieces[SETS - 1][k], &sums.ml[sums.pieces[0][k].n][k], d, acc);
+        float4 acc[1] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+        add_pieces<D, JR>(P, {&sums.pieces[0][k]}, {&sums.ml[0][k]}, {d}, acc);
+        if (SETS == 2) add_pieces<D, JR>(W, {&sums.pieces[SETS - 1][k]}, {&sums.ml[sums.pieces[0][k].n][k]}, {d}, acc);
         const float inv = sums.inv[k];
-        attn_store4<E>(A, sums.out[k] + d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        attn_store4<E>(A, sums.out[k] + d, make_float4(acc[0].x * inv, acc[0].y * inv, acc[0].z * inv, acc[0].w * inv));
     }
 }
 
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         if ((int)threadIdx.x < rows) {
             const int k = threadIdx.x, t = (r0 + k) / (unsigned)A.group;
             sums.place(A, k, (long long)b * A.nq + t, h * A.group + (int)(r0 + k - t * A.group));
-            sums.pieces[0][k].n = 0;
+            sums.pieces[0][k] = Pieces{0, 0, 0, 0};
             if (cut_item) sums.pieces[0][k] = item_pieces(P, 0, cut.z, cut.w, U, i0 + k);
         }
         add_rows<E, D>(A, sums, rows, P, P);
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         const int k = threadIdx.x;
         const unsigned r = r0 + k, t = r / (unsigned)A.group, gr = b * all + r;
         sums.place(A, k, (long long)b * A.nq + t, h * A.group + (int)(r - t * A.group));
-        sums.pieces[0][k].n = sums.pieces[1][k].n = 0;
+        sums.pieces[0][k] = sums.pieces[1][k] = Pieces{0, 0, 0, 0};
         if (attn_shares(A, P, attn_len(A, attn_row(A, b)))) {
             const int item = h * P.prefix_row_tiles + (int)(gr >> P.tile_shift);
             sums.pieces[0][k] = item_pieces(P, item, item * P.prefix_tiles, P.prefix_tiles,
@@ -865,16 +865,16 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 }  // namespace
 
 // CTAs of the prefix launch.  With a multiple of the items, s each, no CTA holds
-// pieces of two items; a piece costs its start and end (~3 units) and each piece
-// of an item makes its sums longer (~1/4 unit).  One GB300, 61 streams behind
-// 8176 (4 items of 64 units): 152 CTAs 23.9 us, 128 22.6, 64 18.1; 48 x 5 tokens
-// behind 8192 (32 items of 64): 152 CTAs 88 us, 128 81.
+// pieces of two items; a piece costs its start and end (~3 units), and every eight
+// pieces of an item a round of loads (~2 units) in the sums that follow.  One GB300,
+// 61 streams behind 8176 (4 items of 64 units): 152 CTAs 23.9 us, 128 22.6, 64
+// 18.1; 48 x 5 tokens behind 8192 (32 items of 64): 152 CTAs 88 us, 128 81.
 static int prefix_ctas(long long items, long long tiles, int sms) {
     const long long units = items * tiles, all = units < sms ? units : sms, share = (units + all - 1) / all;
-    long long best = all, cost = 4 * (share + 3) + tiles / share + 1;
+    long long best = all, cost = 4 * (share + 3) + 8 * ((tiles / share + 8) / 8);
     for (long long s = 1; s <= tiles && s * items <= sms; ++s) {
-        const long long c = 4 * ((tiles + s - 1) / s) + s;
-        if (c <= cost) {
+        const long long c = 4 * ((tiles + s - 1) / s) + 8 * ((s + 7) / 8);
+        if (c < cost) {
             cost = c;
             best = s * items;
         }

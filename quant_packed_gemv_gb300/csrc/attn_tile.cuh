@@ -91,7 +91,7 @@ __host__ __device__ __forceinline__ long long piece_slot(const TilePlan& P, int 
 // What costs time here otherwise is integer division, so each row's places are
 // worked out once.
 struct Pieces {
-    long long first, next;   // row in P.ml and P.o of piece 0, of piece 1
+    long long first, next;   // row in P.ml and P.o of piece 0 (0 if there is none), of piece 1
     int step;                // rows from a piece to the next, after that
     int n;
     __device__ __forceinline__ long long at(int p) const { return p == 0 ? first : next + (long long)(p - 1) * step; }
@@ -151,25 +151,34 @@ __device__ __forceinline__ void weigh(const AttnArgs& A, Sums<ROWS, MOST, SETS>&
     }
 }
 
-// acc += the dims d .. d + 3 of the pieces, weighted (w: ROWS apart).
-template <int D, int ROWS>
-__device__ __forceinline__ void add_pieces(const TilePlan& P, const Pieces& X, const float2* w, int d, float4& acc) {
-    constexpr int AHEAD = 8;   // loads in flight
+// acc[i] += the dims d[i] .. d[i] + 3 of the pieces X[i], weighted (w: ROWS apart).
+template <int D, int ROWS, int N>
+__device__ __forceinline__ void add_pieces(const TilePlan& P, const Pieces* const (&X)[N], const float2* const (&w)[N],
+                                           const int (&d)[N], float4 (&acc)[N]) {
+    constexpr int AHEAD = 8;   // loads in flight of each
+    int most = X[0]->n;
+#pragma unroll
+    for (int i = 1; i < N; ++i) most = max(most, X[i]->n);
 #pragma unroll 1
-    for (int p = 0; p < X.n; p += AHEAD) {
-        float4 v[AHEAD];
+    for (int p = 0; p < most; p += AHEAD) {
+        float4 v[N][AHEAD];
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q) v[q] = *reinterpret_cast<const float4*>(P.o + X.at(min(p + q, X.n - 1)) * D + d);
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            const float f = p + q < X.n ? w[(p + q) * ROWS].x : 0.0f;
-            if (f != 0.0f) {   // O of a part without weight may hold anything
-                acc.x = fmaf(f, v[q].x, acc.x);
-                acc.y = fmaf(f, v[q].y, acc.y);
-                acc.z = fmaf(f, v[q].z, acc.z);
-                acc.w = fmaf(f, v[q].w, acc.w);
+            for (int q = 0; q < AHEAD; ++q)   // past the last piece: the last again, without weight
+                v[i][q] = *reinterpret_cast<const float4*>(P.o + X[i]->at(max(0, min(p + q, X[i]->n - 1))) * D + d[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                const float f = p + q < X[i]->n ? w[i][(p + q) * ROWS].x : 0.0f;
+                if (f != 0.0f) {   // O of a part without weight may hold anything
+                    acc[i].x = fmaf(f, v[i][q].x, acc[i].x);
+                    acc[i].y = fmaf(f, v[i][q].y, acc[i].y);
+                    acc[i].z = fmaf(f, v[i][q].z, acc[i].z);
+                    acc[i].w = fmaf(f, v[i][q].w, acc[i].w);
+                }
             }
-        }
     }
 }
 
