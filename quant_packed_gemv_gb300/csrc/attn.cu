@@ -1,7 +1,7 @@
 // Attention over a paged cache (plm_attn_shared_prefix): which kernels a call
 // runs.
 //
-// Decode (at most 32 rows per sequence and head): attn_rows.cu, a cluster per
+// Decode (at most 96 rows per sequence and head): attn_rows.cu, a cluster per
 // (sequence, head); a shared prefix is first done for the whole batch by the
 // tile kernel (attn_tile.cu), and the rows kernel adds its results at the end.
 // More rows: the tile kernel does the own keys too, and a last kernel adds what
@@ -43,7 +43,10 @@ struct Choice {
 Choice choose(const AttnArgs& A, int d, void* ws) {
     const long long mine = (long long)A.nq * A.group;
     Choice c = {};
-    c.rows = mine <= 32;
+    // Up to 96 rows the rows kernel, in chunks of 32 that read the keys again: 40 x 68
+    // rows over 2000 keys take 90 us there and 138 in the tile kernel, 5 x 80 rows behind
+    // 1024 26 and 36, 24 x 80 behind 8192 150 and 144; 8 x 112 behind 4096 52 and 44.
+    c.rows = mine <= 96;
     c.share = A.prefix > 0 && A.batch > 1;
     if (!c.rows && c.share) {
         // a sequence's rows fill their own tiles well: its prefix keys are then

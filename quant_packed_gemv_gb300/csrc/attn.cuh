@@ -23,7 +23,7 @@ struct AttnArgs {
     const int* lens;
     const int* seqs;
     int batch, nq, heads, kv_heads, group;   // group = heads / kv_heads
-    unsigned group_inv;                      // 65536 / group, rounded up: r / group for r, group <= 32
+    unsigned group_inv;                      // 65536 / group, rounded up: r / group for r, group < 256
     long long q_ts, q_hs, o_ts, o_hs;
     long long page_stride, kv_hs, kv_ts, table_stride;
     int page_shift, pages, rows;
@@ -32,7 +32,7 @@ struct AttnArgs {
     int o_f32;
 };
 
-// r / group for r <= 32 (an integer division is ~100 cycles in a row).
+// r / group for r < 256 (an integer division is ~100 cycles in a row).
 __device__ __forceinline__ int small_row(const AttnArgs& A, int r) { return (int)(((unsigned)r * A.group_inv) >> 16); }
 
 // Table row of sequence b, or -1.

@@ -1,5 +1,5 @@
-// Paged attention for up to 32 query rows per (sequence, key/value head):
-// decode, and a few drafted tokens (plm_attn_shared_prefix).
+// Paged attention for few query rows per (sequence, key/value head), in chunks
+// of up to 32: decode, and some drafted tokens (plm_attn_shared_prefix).
 //
 // Mathematics.  With R = tokens * group rows, each block of 16 keys is two
 // small products: S^T = K Q^T (16 keys x 8 rows, sums over d) and O^T += V^T
@@ -94,7 +94,9 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     if (P.prefix_tiles == 0) grid_wait_prior();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int b = blockIdx.x / A.kv_heads, h = blockIdx.x - b * A.kv_heads;
-    const int rows = A.nq * A.group;
+    // rows r0 .. r0 + rows - 1 of the sequence and head (grid y: chunks of them)
+    const int total = A.nq * A.group, chunk = (total + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int r0 = blockIdx.y * chunk, rows = min(chunk, total - r0);
     const int row = attn_row(A, b), len = attn_len(A, row);
     const int* tab = A.table + (long long)max(row, 0) * A.table_stride;
     const long long head = (long long)h * A.kv_hs;
@@ -102,11 +104,11 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const E* vbase = static_cast<const E*>(A.v) + head;
     const int mask = (1 << A.page_shift) - 1;
 
-    const int all = attn_seen(A, len, 0);   // keys that every row sees
+    const int all = attn_seen(A, len, small_row(A, r0));   // keys that every row sees
 
     const float sl2 = A.scale * LOG2E;
     const int streams = DW * gridDim.z, stream = blockIdx.z * DW + warp;
-    const int blocks = (len + 15) >> 4;
+    const int blocks = (attn_seen(A, len, small_row(A, r0 + rows - 1)) + 15) >> 4;   // that the last row sees
     const bool shares = attn_shares(A, P, len);
     const int first = shares ? A.prefix >> 4 : 0;   // the prefix is a multiple of 16
 
@@ -139,9 +141,9 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     auto q_part = [&](int nb, int c) {
         const int r = 8 * nb + g;
         if (r >= rows) return make_uint4(0, 0, 0, 0);
-        const int tr = small_row(A, r);
+        const int tr = small_row(A, r0 + r);
         return *reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + tr) * A.q_ts +
-                                               (long long)(h * A.group + r - tr * A.group) * A.q_hs + 8 * t + 32 * c);
+                                               (long long)(h * A.group + r0 + r - tr * A.group) * A.q_hs + 8 * t + 32 * c);
     };
     if constexpr (QS) {
         for (int i = warp; i < NB * KC; i += DW) sm.q[i * 32 + lane] = q_part(i / KC, i % KC);
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int rr = 8 * nb + 2 * t + i;
-            seen[nb][i] = rr < rows ? attn_seen(A, len, small_row(A, rr)) : 0;
+            seen[nb][i] = rr < rows ? attn_seen(A, len, small_row(A, r0 + rr)) : 0;
         }
 
     int blk = first + stream, page = page_of(blk);
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
     const int mine = (rows - (int)blockIdx.z + cs - 1) / cs, parts = cs * DW;
     auto& sums = sm.part.sums;
     if ((int)threadIdx.x < mine) {
-        const int k = threadIdx.x, r = blockIdx.z + k * cs, gr = b * rows + r, t_ = small_row(A, r);
+        const int k = threadIdx.x, r = r0 + blockIdx.z + k * cs, gr = b * total + r, t_ = small_row(A, r);
         sums.place(A, k, (long long)b * A.nq + t_, h * A.group + r - t_ * A.group);
         sums.pieces[0][k] = Pieces{0, 0, 0, 0};
         if (shares) {
@@ -354,8 +356,8 @@ __global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(con
 }
 
 template <class E, int D, int NB>
-cudaError_t rows_launch(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t stream) {
-    const dim3 grid((unsigned)(A.batch * A.kv_heads), 1, (unsigned)cs);
+cudaError_t rows_launch(const AttnArgs& A, const TilePlan& P, int chunks, int cs, cudaStream_t stream) {
+    const dim3 grid((unsigned)(A.batch * A.kv_heads), (unsigned)chunks, (unsigned)cs);
     constexpr int bytes = sizeof(RowsSmem<D, NB>);
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<E, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -366,18 +368,18 @@ cudaError_t rows_launch(const AttnArgs& A, const TilePlan& P, int cs, cudaStream
 }
 
 template <class E, int D>
-cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int cs, cudaStream_t stream) {
-    const int rows = A.nq * A.group;
-    if (rows <= 8) return rows_launch<E, D, 1>(A, P, cs, stream);
-    if (rows <= 16) return rows_launch<E, D, 2>(A, P, cs, stream);
-    return rows <= 24 ? rows_launch<E, D, 3>(A, P, cs, stream) : rows_launch<E, D, 4>(A, P, cs, stream);
+cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int chunks, int cs, cudaStream_t stream) {
+    const int rows = (A.nq * A.group + chunks - 1) / chunks;
+    if (rows <= 8) return rows_launch<E, D, 1>(A, P, chunks, cs, stream);
+    if (rows <= 16) return rows_launch<E, D, 2>(A, P, chunks, cs, stream);
+    return rows <= 24 ? rows_launch<E, D, 3>(A, P, chunks, cs, stream) : rows_launch<E, D, 4>(A, P, chunks, cs, stream);
 }
 
 // CTAs of a pair (at most 8: 32 warps): as many as the GPU holds at once (a second
 // wave costs a whole start and end: 12 x 9 tokens behind 512, 30 us where one wave
 // takes 17), while every warp still gets two blocks of 16 keys.
-int rows_cluster(const AttnArgs& A, int keys) {
-    const long long pairs = (long long)A.batch * A.kv_heads, room = (A.nq * A.group <= 8 ? 3LL : 2LL) * num_sms();
+int rows_cluster(const AttnArgs& A, int chunks, int keys) {
+    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = (A.nq * A.group <= 8 ? 3LL : 2LL) * num_sms();
     int cs = 1;
     while (cs < 8 && pairs * cs * 2 <= room && keys > 2 * 16 * DW * cs) cs *= 2;
     return cs;
@@ -387,9 +389,9 @@ int rows_cluster(const AttnArgs& A, int keys) {
 
 cudaError_t launch_attn_rows(const AttnArgs& A, const TilePlan* plan, int type, int d, cudaStream_t stream) {
     const TilePlan P = plan ? *plan : TilePlan{};
-    const int cs = rows_cluster(A, plan ? A.cap - A.prefix : A.cap);
-    if (type == PLM_F16) return d == 64 ? rows_nb<__half, 64>(A, P, cs, stream) : rows_nb<__half, 128>(A, P, cs, stream);
-    return d == 64 ? rows_nb<__nv_bfloat16, 64>(A, P, cs, stream) : rows_nb<__nv_bfloat16, 128>(A, P, cs, stream);
+    const int chunks = (A.nq * A.group + 31) / 32, cs = rows_cluster(A, chunks, plan ? A.cap - A.prefix : A.cap);
+    if (type == PLM_F16) return d == 64 ? rows_nb<__half, 64>(A, P, chunks, cs, stream) : rows_nb<__half, 128>(A, P, chunks, cs, stream);
+    return d == 64 ? rows_nb<__nv_bfloat16, 64>(A, P, chunks, cs, stream) : rows_nb<__nv_bfloat16, 128>(A, P, chunks, cs, stream);
 }
 
 }  // namespace plm

@@ -195,7 +195,7 @@ cudaError_t launch_attn_tile(const AttnArgs& A, const TilePlan& P, int type, int
 cudaError_t launch_attn_merge(const AttnArgs& A, const TilePlan& prefix, const TilePlan& own, int type, int d,
                               cudaStream_t stream);
 
-// At most 32 query rows per sequence and key/value head; P: prefix results to
+// Few query rows per sequence and key/value head; P: prefix results to
 // add, or null.
 cudaError_t launch_attn_rows(const AttnArgs& A, const TilePlan* P, int type, int d, cudaStream_t stream);
 
