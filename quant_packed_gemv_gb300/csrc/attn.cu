@@ -48,11 +48,22 @@ Choice choose(const AttnArgs& A, int d, void* ws) {
     // 1024 26 and 36, 24 x 80 behind 8192 150 and 144; 8 x 112 behind 4096 52 and 44.
     c.rows = mine <= 96;
     c.share = A.prefix > 0 && A.batch > 1;
-    if (!c.rows && c.share) {
-        // a sequence's rows fill their own tiles well: its prefix keys are then
-        // read at no loss, and nothing has to be added afterwards
-        const long long tile = mine > 128 ? 256 : 128, full = (mine + tile - 1) / tile * tile;
-        if (5 * mine >= 4 * full) c.share = false;
+    if (c.share && c.rows) {
+        // The prefix apart costs a launch and longer sums, ~7 us.  Read by every sequence
+        // it takes its bytes at ~6 TB/s, or the 16-key blocks that a warp of a full
+        // cluster goes through.  One GB300: 4 streams behind 1024 tokens 9.3 us unshared
+        // and 11.0 shared, 149 behind 64 11 and 20; 16 behind 1024 15.7 and 11.3, 2
+        // behind 8192 22 and 17, 12 x 28 rows behind 3104 33 and 24.
+        const double bytes = (A.batch - 1.0) * A.prefix * A.kv_heads * 4 * d * ((mine + 31) / 32);
+        const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7);
+        c.share = (bytes / 6e6 > chain ? bytes / 6e6 : chain) > 7.0;
+    } else if (c.share) {
+        // The same in units of the tile kernel: those of the prefix in every sequence's
+        // own tiles, less those of the batch's rows together; its launch and the sums
+        // over all rows are worth ~3000 (96 x 490 rows behind 15360: 566 us unshared, 659
+        // shared; 24 x 140 rows behind 8192 saves 9000).
+        const long long tile = mine > 128 ? 256 : 128, each = (mine + tile - 1) / tile, all = (mine * A.batch + 255) / 256;
+        c.share = (A.batch * each - all) * (double)A.kv_heads * A.prefix / TK > 3000;
     }
     size_t a = 0, b = 0;
     if (c.share) c.prefix = tile_plan(A, d, 0, true, ws, &a);
