@@ -167,7 +167,7 @@ struct Piece {
 struct Walk {
     int u, end;        // the next unit, the end of the share
     int prefix_row;    // prefix: table row that holds it
-    int pair, T, h;    // own: (sequence, row tile), its units per head, head
+    int b, rt, T, h;   // own: sequence, row tile, its units per head, head
     int item_u0;       // own: first unit of the item
 
     // Returns the number of all units.  tables: page tables will be read.
@@ -176,9 +176,8 @@ struct Walk {
         if (P.job == 0) {
             U = A.kv_heads * P.prefix_row_tiles * P.prefix_tiles;
         } else {
-            const int pairs = A.batch * P.own_row_tiles;
             int sum = 0;
-            for (int p = lane; p < pairs; p += 32) sum += own_tiles(A, P, p);
+            for (int b = lane; b < A.batch; b += 32) sum += seq_tiles(A, P, attn_len(A, attn_row(A, b)));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
             U = sum * A.kv_heads;
@@ -187,8 +186,8 @@ struct Walk {
         const bool mine = (int)blockIdx.x < ctas;
         u = mine ? (int)((long long)U * blockIdx.x / ctas) : U;
         end = mine ? (int)((long long)U * (blockIdx.x + 1) / ctas) : U;
-        pair = prefix_row = -1;
-        T = h = item_u0 = 0;
+        b = prefix_row = -1;
+        rt = T = h = item_u0 = 0;
         if (P.job == 0 && tables)   // the first sequence that takes part
             for (int b0 = 0; b0 < A.batch && prefix_row < 0; b0 += 32) {
                 const int b = b0 + lane, row = b < A.batch ? attn_row(A, b) : -1;
@@ -198,13 +197,11 @@ struct Walk {
         return U;
     }
 
-    // The pair, head and item of own unit u.
+    // The sequence, row tile, head and item of own unit u.
     __device__ void locate(const AttnArgs& A, const TilePlan& P, int lane) {
-        const int pairs = A.batch * P.own_row_tiles;
         int acc = 0;
-        for (int p0 = 0; p0 < pairs; p0 += 32) {
-            const int p = p0 + lane;
-            const int n = p < pairs ? own_tiles(A, P, p) : 0;
+        for (int b0 = 0; b0 < A.batch; b0 += 32) {
+            const int n = b0 + lane < A.batch ? seq_tiles(A, P, attn_len(A, attn_row(A, b0 + lane))) : 0;
             int x = n * A.kv_heads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -214,9 +211,13 @@ struct Walk {
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, acc + x > u);
             if (hit) {
                 const int w = __ffs(hit) - 1;
-                pair = p0 + w;
-                T = __shfl_sync(0xFFFFFFFFu, n, w);
-                const int first = acc + __shfl_sync(0xFFFFFFFFu, x, w) - T * A.kv_heads;
+                b = b0 + w;
+                int first = acc + __shfl_sync(0xFFFFFFFFu, x, w) - __shfl_sync(0xFFFFFFFFu, n, w) * A.kv_heads;
+                for (rt = 0;; ++rt) {   // ends: u lies in one of the sequence's row tiles
+                    T = own_tiles(A, P, b * P.own_row_tiles + rt);
+                    if (u - first < T * A.kv_heads) break;
+                    first += T * A.kv_heads;
+                }
                 h = (u - first) / T;
                 item_u0 = first + h * T;
                 return;
@@ -241,17 +242,20 @@ struct Walk {
             S.keys = A.prefix;
             S.row = prefix_row;
         } else {
-            if (pair < 0) locate(A, P, lane);
+            if (b < 0) locate(A, P, lane);
             else if (u == item_u0 + T) {   // the next item
                 item_u0 = u;
                 if (++h == A.kv_heads) {
                     h = 0;
-                    do { T = own_tiles(A, P, ++pair); } while (T == 0);   // u < end <= U: there is one
+                    do {   // u < end <= U: there is one
+                        if (++rt == P.own_row_tiles) { rt = 0; ++b; }
+                        T = own_tiles(A, P, b * P.own_row_tiles + rt);
+                    } while (T == 0);
                 }
             }
             const int t0 = u - item_u0;
-            S.b = own_seq(P, pair);
-            S.rt = pair - S.b * P.own_row_tiles;
+            S.b = b;
+            S.rt = rt;
             S.h = h;
             S.row = attn_row(A, S.b);
             const int len = attn_len(A, S.row);
@@ -261,7 +265,7 @@ struct Walk {
             S.whole = S.begins && S.tiles == T;
             S.key0 = own_begin(A, P, len) + t0 * TK;
             S.keys = own_end(A, P, len, S.rt);
-            S.item = A.kv_heads * pair + h;
+            S.item = A.kv_heads * (b * P.own_row_tiles + rt) + h;
         }
         u += S.tiles;
         return true;
@@ -342,7 +346,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                 if (P.keep) {
                     if (S.begins) P.item_unit[S.item] = S.unit0;
                 } else if (first) {
-                    P.cut[blockIdx.x] = make_int4(S.begins ? -1 : W.pair, S.h, S.unit0, W.T);
+                    P.cut[blockIdx.x] = make_int4(S.begins ? -1 : S.b * P.own_row_tiles + S.rt, S.h, S.unit0, W.T);
                 }
             }
             first = false;

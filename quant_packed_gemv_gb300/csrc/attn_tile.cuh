@@ -58,6 +58,21 @@ __device__ __forceinline__ int own_tiles(const AttnArgs& A, const TilePlan& P, i
     return max(0, own_end(A, P, len, rt) - own_begin(A, P, len) + TK - 1) / TK;
 }
 
+// The same of all a sequence's row tiles (by additions: the last row of tile rt is
+// query ((rt + 1) tile_rows - 1) / group).
+__device__ __forceinline__ int seq_tiles(const AttnArgs& A, const TilePlan& P, int len) {
+    const int begin = own_begin(A, P, len), q = P.tile_rows / A.group, r = P.tile_rows - q * A.group;
+    int sum = 0, t = -1, left = A.group - 1;   // t group + left: the last row so far (-1: none)
+    for (int rt = 0; rt < P.own_row_tiles; ++rt) {
+        t += q;
+        left += r;
+        if (left >= A.group) { left -= A.group; ++t; }
+        const int end = rt + 1 == P.own_row_tiles ? len : attn_seen(A, len, t);
+        sum += max(0, end - begin + TK - 1) / TK;
+    }
+    return sum;
+}
+
 // CTAs that get units: with fewer units than CTAs the others stay idle, so that
 // no share between two others is empty.
 __device__ __forceinline__ int unit_ctas(const TilePlan& P, int U) { return min(P.ctas, U); }
