@@ -475,7 +475,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         // ------------------------------------- the softmax, a row per thread
         const int t = warp >> 2, i = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const float sl2 = fabsf(A.scale) * LOG2E, raise_at = RAISE / sl2;
+        // a scale of 0 counts as 1e-30: every finite score then is as good as 0, and
+        // -inf (a hidden key, a row's first maximum) stays -inf
+        const float sl2 = fmaxf(fabsf(A.scale) * LOG2E, 1e-30f), raise_at = RAISE / sl2;
         int step = 0;   // units so far
         int pieces = 0;
         long long tok;

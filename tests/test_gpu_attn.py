@@ -171,6 +171,47 @@ def test_sharp_and_rising_scores(dtype, nq, prefix):
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("nq,prefix", [(1, 0), (1, 512), (40, 512), (130, 0), (130, 512)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_scales_of_zero_and_below(dtype, nq, prefix):
+    c = Case([600 + nq, 516 + nq, 130, 0], nq, 8, 2, 64, prefix, 16, T[dtype], seed=11)
+    scale, c.scale = c.scale, 0.0      # the mean of the values
+    c.check(*c.run())
+    c.scale = -scale                   # as the opposite queries under the opposite scale
+    o, lse = c.run()
+    c.q.neg_()
+    c.scale = scale
+    c.check(o, lse)
+
+
+@pytest.mark.parametrize("hidden", [100, 128, 300])
+def test_prompts_with_scores_of_minus_infinity(hidden):
+    # the first keys score -inf for positive queries, as if they were not there
+    nq, n = 130, 400
+    c = Case([n], nq, 2, 1, 128, 0, 16, torch.bfloat16, seed=6)
+    c.q.copy_(c.q.abs() + 0.1)
+    whole = Case([n], nq, 2, 1, 128, 0, 16, torch.bfloat16, seed=6)
+    for j in range(hidden):
+        c.k[c.rows[0][j // 16], :, j % 16] = -math.inf
+    o, lse = c.run()
+    pages = c.rows[0][:n // 16]
+    take = lambda x: x[pages].transpose(1, 2).reshape(-1, 128)[:n].double()  # noqa: E731
+    k, v, x = take(whole.k)[hidden:], take(c.v)[hidden:], c.q.double()
+    s, size = x @ k.T * c.scale, x.abs() @ k.abs().T * c.scale
+    seen = torch.arange(hidden, n, device="cuda")[None] <= torch.arange(n - nq, n, device="cuda")[:, None]
+    s, size = s.masked_fill(~seen[:, None], -math.inf), size.masked_fill(~seen[:, None], 0.0).amax(-1)
+    some = seen.any(-1)
+    p = torch.softmax(s, -1).nan_to_num(0.0)
+    want, A = p @ v, p @ v.abs()
+    e = 2 * ((128 + 4) * 2.0 ** -24 + 2.0 ** -22) * (1 + size)
+    tol = (2.0 ** -8 + e[..., None] + 2 * n * 2.0 ** -24) * A + 1e-30
+    tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    assert bool(((o.double() - want).abs() <= tol).all())
+    assert bool((o[~some] == 0).all()) and bool((lse[~some] == -math.inf).all())
+    ref = torch.logsumexp(s, -1)[some]
+    assert bool(((lse.double()[some] - ref).abs() <= e[some] + n * 2.0 ** -24 + 2.0 ** -22 * (1 + ref.abs())).all())
+
+
 def test_scores_of_minus_infinity():
     # keys of -inf score -inf for positive queries: as if hidden; a row of nothing else is empty
     c = Case([40, 20], 1, 2, 1, 64, 0, 16, torch.bfloat16, seed=5)
