@@ -377,11 +377,16 @@ cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int chunks, int cs, cu
 
 // CTAs of a pair (at most 8: 32 warps): as many as the GPU holds at once (a second
 // wave costs a whole start and end: 12 x 9 tokens behind 512, 30 us where one wave
-// takes 17), while every warp still gets two blocks of 16 keys.
+// takes 17), while every warp still gets two blocks of 16 keys.  Long rows up to 16
+// are cut into CTAs of 1024 keys and more whatever their number: the GPU hands them
+// out as others end, so that sequences of unequal lengths even out (20 of up to
+// 16000 keys, 8 heads of 128: 132 us in one wave, 115 so; 64 of up to 4000: 97 and
+// 90; half the keys: 91; 4 tokens each, 3000: 85 and 78; 7 tokens: 73 and 75).
 int rows_cluster(const AttnArgs& A, int chunks, int keys) {
-    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = (A.nq * A.group <= 8 ? 3LL : 2LL) * num_sms();
+    const int rows = A.nq * A.group, cut = rows <= 16 ? 2048 : 0x7FFFFFFF;
+    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = (rows <= 8 ? 3LL : 2LL) * num_sms();
     int cs = 1;
-    while (cs < 8 && pairs * cs * 2 <= room && keys > 2 * 16 * DW * cs) cs *= 2;
+    while (cs < 8 && keys > 2 * 16 * DW * cs && (pairs * cs * 2 <= room || keys / cs > cut)) cs *= 2;
     return cs;
 }
 
