@@ -22,7 +22,9 @@
 // its own by cp.async, 16-byte chunks XORed so that the fragment loads are free
 // of bank conflicts; keys past the end are filled with zeros and not read.  The
 // warps of a CTA and the CTAs of a cluster take the blocks in turn and add
-// their parts through shared memory, in a fixed order.
+// their parts through shared memory, in a fixed order.  One GB300, 8 heads of 128
+// in bf16: 64 sequences of up to 4000 keys, 90 us (5.8 TB/s); 256 of up to 2000,
+// 182 us with a cold L2 (5.7 TB/s); 4 of 1100, 9.3 us, which is latency.
 #include "attn_tile.cuh"
 
 namespace plm {

@@ -21,6 +21,9 @@
 // Work: equal shares of units per CTA (attn_tile.cuh), one CTA per SM.
 // Bound: the tensor cores from ~270 rows per head on, HBM below.  Every wait
 // is bounded; one that runs out records a fault and the kernel winds down.
+// One GB300, bf16, 32 query heads on 8 of 128: 8 x 509 tokens behind 16384, 790 us
+// (1.4 PFLOP/s with the join); 256 tokens' prefix of 32768, 115 us (1.2 PFLOP/s).
+// The tensor pipe then waits for the starts and ends of pieces.
 #include <cuda.h>
 
 #include <cstring>

@@ -17,6 +17,8 @@
 // size, a stride or a pointer is not a multiple of that.  A thread steps from unit
 // to unit by additions.  (With the types, the tensor and 64-bit divisions for the
 // slots looked up per unit, the kernel ran at 70 % of the copy rate.)
+// One GB300: 16381 tokens x 40 heads of 128, bf16: 55 us, 6.1 TB/s (91 % of a
+// copy); 8191 x 48 heads, f32 to bf16 pages: 53.5 us, 5.6 TB/s; one token 2.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
