@@ -33,7 +33,7 @@ struct Plan {
     int* first;    // [n] index of the item's first new page in `fresh`
     int* need;     // [n] new pages of the item; -1: a bad item
     int* fresh;    // [pages] new pages in ascending order; compact: the holes
-    int* src;      // [max(pages, n)] pages to copy from
+    int* src;      // [max(pages, n)] pages to copy from; reserve: [n] the items' lengths before
     int* dst;      // fork: [n] pages to copy to; compact: map of moved pages [pages]
 };
 
@@ -128,7 +128,9 @@ struct ReserveArgs {
     long long slots_stride;
 };
 
-// One item, by a warp: its new table entries, counts, length and slots.
+// One item, by a warp: its new table entries, counts, length and slots.  The length
+// before is the plan's, for which the row was found long enough: of a sequence listed
+// twice, the other item may have raised it since.
 __device__ void reserve_item(const ReserveArgs& A, long long i, bool done, int lane) {
     const plm_kv_state& S = A.S;
     const int need = A.P.need[i];
@@ -139,7 +141,7 @@ __device__ void reserve_item(const ReserveArgs& A, long long i, bool done, int l
         return;
     }
     const int s = A.seqs[i];
-    const long long old = S.lens[s], add = A.add[i];
+    const long long old = A.P.src[i], add = A.add[i];
     int* row = S.table + (long long)s * S.max_pages;
     const long long have = pages_for(old, S.page_tokens);
     const int* fresh = A.P.fresh + A.P.first[i];
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(PT) reserve_plan_kernel(const __grid_constant_
             need = -1;
             if (s >= 0 && s < S.max_seqs && add >= 0) {
                 const long long old = S.lens[s], now = old + add;
+                A.P.src[i] = (int)old;
                 if (old >= 0 && now <= 0x7FFFFFFFLL && pages_for(now, S.page_tokens) <= S.max_pages &&
                     (!A.slots || add <= A.slots_stride))
                     need = (int)(pages_for(now, S.page_tokens) - pages_for(old, S.page_tokens));

@@ -187,6 +187,28 @@ def test_many_items_and_a_sequence_listed_twice_in_free():
     g.same(m)
 
 
+@pytest.mark.parametrize("n,form", [(2, "one launch"), (40, "one launch"), (40, "two launches")])
+def test_a_sequence_listed_twice_in_reserve_stays_inside_its_row(n, form):
+    # its state is then undefined, but nothing else: each item alone fills the last row, and what lies behind the
+    # table, the other rows and the counts of pages that were in use stay as they are
+    seqs, width, ps, pages = 3, 4, 16, 400
+    i32 = dict(dtype=torch.int32, device="cuda")
+    behind = torch.full((seqs * width + 4096,), 77, **i32)
+    table = behind[:seqs * width].view(seqs, width)
+    table[:] = -1
+    lens, refs = torch.zeros(seqs, **i32), torch.zeros(pages, **i32)
+    table[0, 0], lens[0], refs[0] = 0, 5, 1
+    kv, ws = q.plm_kv_state(torch.zeros(pages, 4, **i32), table, lens, refs, ps), torch.empty(q.plm_kv_workspace_size(pages, n), dtype=torch.uint8, device="cuda")
+    slots = torch.empty(n, 64 if form == "one launch" else 4096, dtype=torch.int64, device="cuda")
+    q.plm_kv_reserve(kv, ints([seqs - 1] * n), ints([64] * n), slots, ws)
+    assert bool((behind[seqs * width:] == 77).all())
+    assert table[:2].tolist() == [[0, -1, -1, -1], [-1] * 4] and lens.tolist() == [5, 0, 64]
+    row = table[2].tolist()
+    assert all(1 <= p <= 4 * n for p in row) and refs[:4 * n + 1].tolist() == [1] * (4 * n + 1)
+    got = slots[:, :64]     # every item's slots lie in pages that it was given, or that a later one put in the row
+    assert bool(((got >= ps) & (got < (4 * n + 1) * ps)).all()) and bool((slots[:, 64:] == -1).all())
+
+
 def test_copy_pages():
     for words in (4, 1024, 1028, 70000):
         pool = torch.randint(-9, 9, (50, words), dtype=torch.int32, device="cuda")
