@@ -59,23 +59,23 @@ Plan plan_at(void* ws, long long pages, long long n) {
 }
 
 // Exclusive prefix sum of v over the CTA's PT threads; total gets the sum.
-__device__ int cta_scan(int v, int& total) {
-    __shared__ int sums[33];
+template <class T> __device__ T cta_scan(T v, T& total) {
+    __shared__ T sums[33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();   // sums of an earlier scan have been read
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int w = sums[lane], z = w;
+        T w = sums[lane], z = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, z, o);
+            const T y = __shfl_up_sync(0xFFFFFFFFu, z, o);
             if (lane >= o) z += y;
         }
         sums[lane] = z - w;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(PT) reserve_plan_kernel(const __grid_constant_
     grid_launch_dependents();
     grid_wait_prior();
     const plm_kv_state& S = A.S;
-    int want = 0;
+    long long want = 0;   // rows of 2^21 pages: 1024 items can ask for 2^31
     for (long long i0 = 0; i0 < A.n; i0 += PT) {
         const long long i = i0 + threadIdx.x;
         int need = 0;
@@ -185,12 +185,12 @@ __global__ void __launch_bounds__(PT) reserve_plan_kernel(const __grid_constant_
             A.P.need[i] = need;
             if (need < 0) flag(S, PLM_KV_BAD_ITEM);
         }
-        int total;
-        const int at = cta_scan(need > 0 ? need : 0, total);
-        if (i < A.n) A.P.first[i] = want + at;
-        want = min((long long)want + total, 0x3FFFFFFFLL);
+        long long total;
+        const long long at = want + cta_scan<long long>(max(need, 0), total);
+        if (i < A.n) A.P.first[i] = (int)at;   // read only if all fit: it is at most S.pages then
+        want += total;
     }
-    const bool done = find_free(S, want, A.P.fresh) == want;
+    const bool done = want <= S.pages && find_free(S, (int)want, A.P.fresh) == want;
     if (threadIdx.x == 0) {
         if (!done) flag(S, PLM_KV_OUT_OF_PAGES);
         A.P.head[1] = done;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(PT) fork_plan_kernel(const __grid_constant__ F
             if (need < 0) flag(S, PLM_KV_BAD_ITEM);
         }
         int total;
-        const int at = want + cta_scan(need > 0, total);
+        const int at = want + cta_scan<int>(need > 0, total);
         if (i < A.n) {
             A.P.first[i] = at;
             if (need > 0) A.P.src[at] = last;
@@ -364,10 +364,10 @@ __global__ void __launch_bounds__(PT) compact_plan_kernel(const __grid_constant_
         const bool in = p < S.pages, used = in && S.refs[p] > 0;
         const bool hole = in && !used && p < live, move = used && p >= live;
         int total;
-        int at = holes + cta_scan(hole, total);
+        int at = holes + cta_scan<int>(hole, total);
         if (hole) A.P.fresh[at] = (int)p;
         holes += total;
-        at = high + cta_scan(move, total);
+        at = high + cta_scan<int>(move, total);
         if (move) A.P.src[at] = (int)p;
         high += total;
     }

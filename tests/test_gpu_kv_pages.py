@@ -158,6 +158,19 @@ def test_out_of_pages_changes_nothing():
     assert m.status == q.PLM_KV_OUT_OF_PAGES and m.lens == [14, 13, 4, 4]
 
 
+@pytest.mark.parametrize("n", [1024, 2048])
+def test_wishes_that_pass_32_bits_together_change_nothing(n):
+    # 2^21 pages for each of n sequences: 2^31 of them for 1024, 2^32 for 2048, and the pool has 64
+    width, pages = 1 << 21, 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens, refs, status = torch.empty(n, width, **i32), torch.zeros(n, **i32), torch.zeros(pages, **i32), torch.zeros(1, **i32)
+    kv = q.plm_kv_state(torch.zeros(pages, 4, **i32), table, lens, refs, 1, status)
+    ws, table[:, 0] = torch.empty(q.plm_kv_workspace_size(pages, n), dtype=torch.uint8, device="cuda"), -1
+    q.plm_kv_reserve(kv, torch.arange(n, **i32), torch.full((n,), width, **i32), None, ws)
+    assert int(status) == q.PLM_KV_OUT_OF_PAGES
+    assert not lens.any() and not refs.any() and bool((table[:, 0] == -1).all())
+
+
 def test_fork_without_room_changes_nothing():
     m = Model(9, 4, 8, 4)
     g = Gpu(m, 4)
