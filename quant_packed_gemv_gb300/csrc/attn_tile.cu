@@ -343,7 +343,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
         int n = 0;                                                  // tiles loaded: slot n % SLOTS
         const int part = lane / per, box = lane - part * per;
         const bool active = part < D / 64;
-        while (ok && W.next(A, P, lane, S)) {
+        // (goes on without loads once a wait has run out: the sums that follow find their
+        // places by what is written here for each item)
+        while (W.next(A, P, lane, S)) {
             const int* tab = A.table + (long long)max(S.row, 0) * A.table_stride;
             if (P.job == 1 && lane == 0) {
                 if (P.keep) {

@@ -75,14 +75,15 @@ __device__ __forceinline__ int seq_tiles(const AttnArgs& A, const TilePlan& P, i
 
 // CTAs that get units: with fewer units than CTAs the others stay idle, so that
 // no share between two others is empty.
-__device__ __forceinline__ int unit_ctas(const TilePlan& P, int U) { return min(P.ctas, U); }
+__host__ __device__ __forceinline__ int unit_ctas(const TilePlan& P, int U) { return min(P.ctas, U); }
 
 // The CTA (of ctas) that holds unit u of U: the last c with U c / ctas <= u,
 // i.e. U c < (u + 1) ctas (an estimate, then exact steps: a 64-bit division is
-// slow where a row's sums wait for it).
-__device__ __forceinline__ int unit_cta(int u, int U, int ctas) {
-    const long long lim = (long long)(u + 1) * ctas;
-    int c = min(ctas - 1, (int)((float)lim / (float)U));
+// slow where a row's sums wait for it).  0 .. ctas - 1 whatever u is, so that a wrong
+// unit never leads outside the slots.
+__host__ __device__ __forceinline__ int unit_cta(int u, int U, int ctas) {
+    const long long lim = ((long long)u + 1) * ctas;
+    int c = (int)fmaxf(0.0f, fminf((float)(ctas - 1), (float)lim / (float)U));
     while (c > 0 && (long long)U * c >= lim) --c;
     while (c + 1 < ctas && (long long)U * (c + 1) < lim) ++c;
     return c;
@@ -109,10 +110,10 @@ struct Pieces {
     long long first, next;   // row in P.ml and P.o of piece 0 (0 if there is none), of piece 1
     int step;                // rows from a piece to the next, after that
     int n;
-    __device__ __forceinline__ long long at(int p) const { return p == 0 ? first : next + (long long)(p - 1) * step; }
+    __host__ __device__ __forceinline__ long long at(int p) const { return p == 0 ? first : next + (long long)(p - 1) * step; }
 };
 // Of row i of an item (first unit u0, `tiles` of U units).
-__device__ __forceinline__ Pieces item_pieces(const TilePlan& P, int item, int u0, int tiles, int U, int i) {
+__host__ __device__ __forceinline__ Pieces item_pieces(const TilePlan& P, int item, int u0, int tiles, int U, int i) {
     const int ctas = unit_ctas(P, U), c0 = unit_cta(u0, U, ctas);
     Pieces X;
     X.n = unit_cta(u0 + tiles - 1, U, ctas) - c0 + 1;
