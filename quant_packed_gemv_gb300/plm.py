@@ -520,9 +520,8 @@ def _call(entry, args):
 
 
 def plm_rope_tensor(x, y, slots=None, rotate=True):
-    """One tensor of a plm_rope call, to be kept as long as its addresses hold.  x [tokens][heads][head_dim]; y the
-    same shape, or with slots (int64 [tokens]) the pages [pages][heads][page_tokens][head_dim] of a cache, as any
-    strided view."""
+    """One tensor of a plm_rope call; it holds x, y and slots.  x [tokens][heads][head_dim]; y the same shape, or with
+    slots (int64 [tokens]) the pages [pages][heads][page_tokens][head_dim] of a cache, as any strided view."""
     xs, shape, ys, xtype, ytype = x.stride(), x.shape, y.stride(), _types.get(x.dtype, -1), _types.get(y.dtype, -1)
     if len(xs) != 3 or xs[2] != 1 or len(ys) != (3 if slots is None else 4) or ys[-1] != 1 or xtype < 0 or ytype < 0 or not (
             x.is_cuda and y.is_cuda):   # an error, or a dimension of one: look closer
@@ -543,12 +542,12 @@ def plm_rope_tensor(x, y, slots=None, rotate=True):
             raise ValueError("y: expected pages [.][%d][.][%d], got %s" % (heads, d, tuple(y.shape)))
         at = _ints(slots, 64, "slots", (tokens,))
     return (_ROPE_TENSOR.pack(x.data_ptr(), y.data_ptr(), at, heads, xt, xh, yt, yh, page_tokens, page_stride, pages,
-                              xtype, ytype, 1 if rotate else 0), tokens, d)
+                              xtype, ytype, 1 if rotate else 0), tokens, d, (x, y, slots))
 
 
 def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, inverse=False, stream=None):
     """Turns the heads of the tensors (plm_rope_tensor) by their positions (int32 [tokens]); see include/plm.h."""
-    packed, tokens, d = tensors[0] if tensors else (b"", positions.numel(), 0)
+    packed, tokens, d, _ = tensors[0] if tensors else (b"", positions.numel(), 0, None)
     if len(tensors) > 1:
         for t in tensors:
             if t[1] != tokens or t[2] != d:
@@ -565,11 +564,11 @@ def plm_rope(tensors, positions, freqs, rotary_dim, layout="half", scale=1.0, in
 
 def plm_kv_state(pool, table, lens, refs, page_tokens, status=None):
     """Page state over device tensors: pool [pages][...] of any type, table int32 [max_seqs][max_pages], lens int32
-    [max_seqs], refs int32 [pages], status int32 [1] or None.  It holds addresses: keep the tensors."""
+    [max_seqs], refs int32 [pages], status int32 [1] or None.  It holds the tensors."""
     pages, (seqs, width) = pool.shape[0], table.shape
-    return _KV_STATE.pack(_addr(pool), pool.nbytes // pages if pages else 0, pages, _ints(table, 32, "table"),
-                          _ints(lens, 32, "lens", (seqs,)), _ints(refs, 32, "refs", (pages,)),
-                          _ints(status, 32, "status") or 0, seqs, width, page_tokens)
+    return (_KV_STATE.pack(_addr(pool), pool.nbytes // pages if pages else 0, pages, _ints(table, 32, "table"),
+                           _ints(lens, 32, "lens", (seqs,)), _ints(refs, 32, "refs", (pages,)),
+                           _ints(status, 32, "status") or 0, seqs, width, page_tokens), (pool, table, lens, refs, status))
 
 
 def plm_kv_workspace_size(pages, n):
@@ -591,31 +590,31 @@ def plm_kv_reserve(kv, seqs, add, slots, workspace, stream=None):
             raise ValueError("slots: expected [%d][.], got %s" % (n, tuple(slots.shape)))
     ws, size = _ws(workspace)
     _call(_RESERVE, _RESERVE_CALL.pack(_ints(seqs, 32, "seqs"), _ints(add, 32, "add", (n,)), n, _ints(slots, 64, "slots") or 0,
-                                       most, ws, size, _stream(stream)) + kv)
+                                       most, ws, size, _stream(stream)) + kv[0])
 
 
 def plm_kv_fork(kv, parents, children, workspace, keep=None, stream=None):
     """Unused sequences children (int32 [n]) become copies of parents, of their first keep tokens if given."""
     n, (ws, size) = parents.numel(), _ws(workspace)
     _call(_FORK, _FORK_CALL.pack(_ints(parents, 32, "parents"), _ints(children, 32, "children", (n,)),
-                                 _ints(keep, 32, "keep", (n,)) or 0, n, ws, size, _stream(stream)) + kv)
+                                 _ints(keep, 32, "keep", (n,)) or 0, n, ws, size, _stream(stream)) + kv[0])
 
 
 def plm_kv_free(kv, seqs, stream=None):
     """The sequences (int32 [n]) give their pages back."""
-    _call(_FREE, _FREE_CALL.pack(_ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)) + kv)
+    _call(_FREE, _FREE_CALL.pack(_ints(seqs, 32, "seqs"), seqs.numel(), _stream(stream)) + kv[0])
 
 
 def plm_kv_compact(kv, live, workspace, stream=None):
     """Packs the pages in use to the front of the pool; live (int32 [1] or None) gets their number."""
     ws, size = _ws(workspace)
-    _call(_COMPACT, _COMPACT_CALL.pack(_ints(live, 32, "live") or 0, ws, size, _stream(stream)) + kv)
+    _call(_COMPACT, _COMPACT_CALL.pack(_ints(live, 32, "live") or 0, ws, size, _stream(stream)) + kv[0])
 
 
 def plm_kv_copy_pages(kv, src, dst, stream=None):
     """Page dst[i] = page src[i] (int32 lists of the same length)."""
     n = src.numel()
-    _call(_COPY, _COPY_CALL.pack(_ints(src, 32, "src"), _ints(dst, 32, "dst", (n,)), n, _stream(stream)) + kv)
+    _call(_COPY, _COPY_CALL.pack(_ints(src, 32, "src"), _ints(dst, 32, "dst", (n,)), n, _stream(stream)) + kv[0])
 
 
 def plm_attn_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len):

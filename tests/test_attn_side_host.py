@@ -204,3 +204,42 @@ def test_the_bindings_blocks_have_the_structs_layout():
     for ctype, packed in ((P._RopeTensor, P._ROPE_TENSOR), (P._KvState, P._KV_STATE), (P._AttnProblem, P._ATTN_PROBLEM)):
         values = list(range(1, len(ctype._fields_) + 1))
         assert ctypes.sizeof(ctype) == packed.size and bytes(ctype(*values)) == packed.pack(*values)
+
+
+class Stub:
+    """What the binding asks of a CUDA tensor."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype, self.nbytes = shape, dtype, math.prod(shape) * 4
+        self.strides = [math.prod(shape[i + 1:]) for i in range(len(shape))]
+
+    def stride(self):
+        return self.strides
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+def test_arguments_made_ahead_hold_their_tensors():
+    # else a temporary's memory may be the next temporary's before the call is made
+    import gc
+    import weakref
+    made = {"x": Stub((4, 2, 64), torch.float32), "y": Stub((9, 2, 16, 64), torch.bfloat16), "slots": Stub((4,), torch.int64),
+            "pool": Stub((8, 16), torch.int32), "table": Stub((2, 4), torch.int32), "lens": Stub((2,), torch.int32),
+            "refs": Stub((8,), torch.int32), "status": Stub((1,), torch.int32)}
+    part = q.plm_rope_tensor(made["x"], made["y"], slots=made["slots"])
+    state = q.plm_kv_state(made["pool"], made["table"], made["lens"], made["refs"], 16, made["status"])
+    seen = {k: weakref.ref(v) for k, v in made.items()}
+    made.clear()
+    gc.collect()
+    assert [k for k, v in seen.items() if v() is None] == []
+    del part, state
+    gc.collect()
+    assert [k for k, v in seen.items() if v() is not None] == []

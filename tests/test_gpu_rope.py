@@ -154,6 +154,19 @@ def test_offsets_past_32_bits():
     assert torch.equal(pool[0, :, 5], x[2].bfloat16()) and bool((pool[-1, :, 1:15] == 0).all())
 
 
+def test_temporaries_of_a_nested_call():
+    # each part's input is made, and forgotten, within the call: none may take another's place
+    x = torch.randn(3, 50, 4, 64, device="cuda")
+    y, want = torch.empty(3, 50, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 50, 4, 64, dtype=torch.bfloat16, device="cuda")
+    pos, freqs = torch.arange(50, dtype=torch.int32, device="cuda"), q.plm_rope_freqs(64, 1e4, device="cuda")[0]
+    held = [x[i].bfloat16() for i in range(3)]
+    for i in range(3):
+        q.plm_rope([q.plm_rope_tensor(held[i], want[i])], pos, freqs, 64)
+    q.plm_rope([q.plm_rope_tensor(x[0].bfloat16(), y[0]), q.plm_rope_tensor(x[1].bfloat16(), y[1]),
+                q.plm_rope_tensor(x[2].bfloat16(), y[2])], pos, freqs, 64)
+    assert torch.equal(y, want)
+
+
 def test_side_stream_and_empty_call():
     side = torch.cuda.Stream()
     x = torch.randn(1000, 8, 128, device="cuda")
