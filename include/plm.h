@@ -644,7 +644,8 @@ plm_status plm_rope(const plm_rope_tensor* tensors, int64_t count, const int32_t
  * suffice for all the others, none is done.
  * Sequences (for fork: children) are distinct within a call, and a fork's
  * parents are not its children; the state is undefined otherwise, but no
- * memory outside it is touched.
+ * memory outside it is touched.  A call of n = 0 items does nothing; its lists
+ * may be null.
  */
 #define PLM_KV_OUT_OF_PAGES 1
 #define PLM_KV_BAD_ITEM 2

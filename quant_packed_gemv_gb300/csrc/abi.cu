@@ -605,7 +605,7 @@ plm_status plm_kv_reserve(const plm_kv_state* kv, const int32_t* seqs, const int
                           int64_t slots_stride, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     plm_status s = check_kv(kv);
     if (s != PLM_OK) return s;
-    if (!seqs || !add || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if ((n != 0 && (!seqs || !add)) || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
     if (slots && !in_range(slots_stride, 1, kMaxIndex)) return PLM_ERR_INVALID_ARG;
     s = check_kv_workspace(kv, n, workspace, workspace_bytes);
     if (s != PLM_OK) return s;
@@ -620,7 +620,7 @@ plm_status plm_kv_fork(const plm_kv_state* kv, const int32_t* parents, const int
     plm_status s = check_kv(kv);
     if (s == PLM_OK) s = check_pool(kv);
     if (s != PLM_OK) return s;
-    if (!parents || !children || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if ((n != 0 && (!parents || !children)) || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
     s = check_kv_workspace(kv, n, workspace, workspace_bytes);
     if (s != PLM_OK) return s;
     if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(keep, 4)) return PLM_ERR_MISALIGNED;
@@ -631,7 +631,7 @@ plm_status plm_kv_fork(const plm_kv_state* kv, const int32_t* parents, const int
 plm_status plm_kv_free(const plm_kv_state* kv, const int32_t* seqs, int64_t n, cudaStream_t stream) {
     plm_status s = check_kv(kv);
     if (s != PLM_OK) return s;
-    if (!seqs || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if ((n != 0 && !seqs) || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
     if (!aligned(seqs, 4)) return PLM_ERR_MISALIGNED;
     if (n == 0) return PLM_OK;
     return cuda_status(plm::launch_kv_free(*kv, seqs, n, stream));
@@ -652,7 +652,7 @@ plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const i
     plm_status s = check_kv(kv);
     if (s == PLM_OK) s = check_pool(kv);
     if (s != PLM_OK) return s;
-    if (!src || !dst || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if ((n != 0 && (!src || !dst)) || !in_range(n, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
     if (!aligned(src, 4) || !aligned(dst, 4)) return PLM_ERR_MISALIGNED;
     if (n == 0) return PLM_OK;
     return cuda_status(plm::launch_kv_copy_pages(*kv, src, dst, n, stream));

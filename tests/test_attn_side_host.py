@@ -243,3 +243,17 @@ def test_arguments_made_ahead_hold_their_tensors():
     del part, state
     gc.collect()
     assert [k for k, v in seen.items() if v() is not None] == []
+
+
+def test_page_calls_without_items():
+    # a step in which no sequence grows, splits or ends: torch gives an empty list's address as null
+    ws, s = q.plm_kv_workspace_size(64, 0), ctypes.byref(kv())
+    assert P.raw_status("plm_kv_reserve", s, None, None, 0, None, 0, A, ws, None) == P.PLM_OK
+    assert P.raw_status("plm_kv_fork", s, None, None, None, 0, A, ws, None) == P.PLM_OK
+    assert P.raw_status("plm_kv_free", s, None, 0, None) == P.PLM_OK
+    assert P.raw_status("plm_kv_copy_pages", s, None, None, 0, None) == P.PLM_OK
+    for n in (1, -1):   # else the lists are wanted
+        assert P.raw_status("plm_kv_reserve", s, None, None, n, None, 0, A, 1 << 30, None) == BAD
+        assert P.raw_status("plm_kv_fork", s, None, None, None, n, A, 1 << 30, None) == BAD
+        assert P.raw_status("plm_kv_free", s, None, n, None) == BAD
+        assert P.raw_status("plm_kv_copy_pages", s, None, A, n, None) == BAD

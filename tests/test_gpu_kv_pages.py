@@ -222,6 +222,21 @@ def test_a_sequence_listed_twice_in_reserve_stays_inside_its_row(n, form):
     assert bool(((got >= ps) & (got < (4 * n + 1) * ps)).all()) and bool((slots[:, 64:] == -1).all())
 
 
+def test_calls_without_items():
+    m = Model(20, 4, 8, 4)
+    g = Gpu(m, 4)
+    none = ints([])
+    m.reserve([1], [9], 9)
+    q.plm_kv_reserve(g.kv, ints([1]), ints([9]), None, g.ws)
+    q.plm_kv_reserve(g.kv, none, none, None, g.ws)
+    q.plm_kv_reserve(g.kv, none, none, torch.empty(0, 3, dtype=torch.int64, device="cuda"), g.ws)
+    q.plm_kv_fork(g.kv, none, none, g.ws)
+    q.plm_kv_fork(g.kv, none, none, g.ws, keep=none)
+    q.plm_kv_free(g.kv, none)
+    q.plm_kv_copy_pages(g.kv, none, none)
+    g.same(m)
+
+
 def test_copy_pages():
     for words in (4, 1024, 1028, 70000):
         pool = torch.randint(-9, 9, (50, words), dtype=torch.int32, device="cuda")
