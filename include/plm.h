@@ -607,9 +607,10 @@ plm_status plm_rope_freqs(uint64_t* freqs, int64_t rotary_dim, double base, cons
  *   positions int32 [tokens], freqs uint64 [rotary_dim / 2]: device memory.
  * Pointers are aligned to their elements.  PLM_ERR_INVALID_ARG: null
  * pointers, count outside 1..8, sizes < 1 (tokens = 0 is allowed: nothing is
- * done), tokens or heads past int32, head_dim > 1024, rotary_dim odd, < 2 or
- * > head_dim, unknown layout or type, page sizes < 1 with slots, y = x with
- * another stride or type.  Distinct tensors must not overlap otherwise.
+ * done), tokens past int32, more than 65536 heads (all tensors together),
+ * head_dim odd or > 1024, rotary_dim odd, < 2 or > head_dim, unknown layout or
+ * type, page sizes < 1 with slots, y = x with another stride or type, or with
+ * slots.  Distinct tensors must not overlap otherwise.
  */
 #define PLM_ROPE_MAX_TENSORS 8
 typedef struct {

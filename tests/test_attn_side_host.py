@@ -257,3 +257,14 @@ def test_page_calls_without_items():
         assert P.raw_status("plm_kv_fork", s, None, None, None, n, A, 1 << 30, None) == BAD
         assert P.raw_status("plm_kv_free", s, None, n, None) == BAD
         assert P.raw_status("plm_kv_copy_pages", s, None, A, n, None) == BAD
+
+
+def test_rope_limits_as_stated():
+    # more than 65536 heads together; an odd head size, whatever its rotary part
+    def st(*tensors, d=128, rot=128):
+        return P.raw_status("plm_rope", (P._RopeTensor * len(tensors))(*tensors), len(tensors), A, A, 0, d, rot, 0, 1.0, 0, None)
+    many = lambda n: rope_tensor(heads=n)  # noqa: E731
+    assert st(many(65536)) == P.PLM_OK and st(many(65537)) == BAD
+    assert st(many(32768), many(32768)) == P.PLM_OK and st(many(32768), many(32769)) == BAD
+    assert st(*[many(8192)] * 8) == P.PLM_OK and st(*[many(8193)] * 8) == BAD
+    assert st(many(8), d=127, rot=64) == BAD and st(many(8), d=1024, rot=1024) == P.PLM_OK and st(many(8), d=1026, rot=64) == BAD
