@@ -77,6 +77,10 @@ template <int D, int NB> struct RowsSmem {
     };
 };
 
+// CTAs of 8 nb rows that an SM holds at once: registers bound the first, shared
+// memory the others (228 KB, of which a CTA takes 1 KB for itself).
+__host__ __device__ constexpr int rows_ctas(int d, int nb) { return nb == 1 ? 3 : nb == 4 && d == 128 ? 1 : 2; }
+
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -84,7 +88,7 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 template <class E, int D, int NB>
-__global__ void __launch_bounds__(DW * 32, NB == 1 ? 3 : 2) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
+__global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TilePlan P) {
     using Sm = RowsSmem<D, NB>;
     constexpr int KC = D / 32, VC = D / 64;   // 16-byte chunks per lane of a K row, of a V row
     constexpr bool QS = NB > 2;
@@ -361,6 +365,7 @@ template <class E, int D, int NB>
 cudaError_t rows_launch(const AttnArgs& A, const TilePlan& P, int chunks, int cs, cudaStream_t stream) {
     const dim3 grid((unsigned)(A.batch * A.kv_heads), (unsigned)chunks, (unsigned)cs);
     constexpr int bytes = sizeof(RowsSmem<D, NB>);
+    static_assert(rows_ctas(D, NB) * (bytes + 1024) <= 228 * 1024, "the CTAs of an SM");
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<E, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
@@ -384,9 +389,16 @@ cudaError_t rows_nb(const AttnArgs& A, const TilePlan& P, int chunks, int cs, cu
 // out as others end, so that sequences of unequal lengths even out (20 of up to
 // 16000 keys, 8 heads of 128: 132 us in one wave, 115 so; 64 of up to 4000: 97 and
 // 90; half the keys: 91; 4 tokens each, 3000: 85 and 78; 7 tokens: 73 and 75).
-int rows_cluster(const AttnArgs& A, int chunks, int keys) {
-    const int rows = A.nq * A.group, cut = rows <= 16 ? 2048 : 0x7FFFFFFF;
-    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = (rows <= 8 ? 3LL : 2LL) * num_sms();
+// Where an SM holds one CTA (25 to 32 rows of 128), a third more than fit at once
+// still pays, as those of short sequences end early, and more does not.  Sequences x
+// tokens, 4 query heads each on 8 heads, up to 3000 keys: 12 x 8 as 96 CTAs 50 us, as
+// 192 39; 8 x 8 as 128 31, as 256 41; 18 x 8 as 144 50, as 288 57; 4 x 8 over 8000 as
+// 128 41, as 256 70; 7 heads on 2, over 2000: 40 x 4 as 80 39, as 160 29; 60 x 4 as
+// 120 40, as 240 46.
+int rows_cluster(const AttnArgs& A, int d, int chunks, int keys) {
+    const int rows = A.nq * A.group, cut = rows <= 16 ? 2048 : 0x7FFFFFFF, sms = num_sms();
+    const int ctas = rows_ctas(d, ((rows + chunks - 1) / chunks + 7) / 8);
+    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = ctas == 1 ? sms + sms / 3 : (long long)ctas * sms;
     int cs = 1;
     while (cs < 8 && keys > 2 * 16 * DW * cs && (pairs * cs * 2 <= room || keys / cs > cut)) cs *= 2;
     return cs;
@@ -396,7 +408,7 @@ int rows_cluster(const AttnArgs& A, int chunks, int keys) {
 
 cudaError_t launch_attn_rows(const AttnArgs& A, const TilePlan* plan, int type, int d, cudaStream_t stream) {
     const TilePlan P = plan ? *plan : TilePlan{};
-    const int chunks = (A.nq * A.group + 31) / 32, cs = rows_cluster(A, chunks, plan ? A.cap - A.prefix : A.cap);
+    const int chunks = (A.nq * A.group + 31) / 32, cs = rows_cluster(A, d, chunks, plan ? A.cap - A.prefix : A.cap);
     if (type == PLM_F16) return d == 64 ? rows_nb<__half, 64>(A, P, chunks, cs, stream) : rows_nb<__half, 128>(A, P, chunks, cs, stream);
     return d == 64 ? rows_nb<__nv_bfloat16, 64>(A, P, chunks, cs, stream) : rows_nb<__nv_bfloat16, 128>(A, P, chunks, cs, stream);
 }
