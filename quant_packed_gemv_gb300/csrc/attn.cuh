@@ -35,14 +35,11 @@ struct AttnArgs {
 // r / group for r < 256 (an integer division is ~100 cycles in a row).
 __device__ __forceinline__ int small_row(const AttnArgs& A, int r) { return (int)(((unsigned)r * A.group_inv) >> 16); }
 
-// Table row of sequence b, or -1.
-__device__ __forceinline__ int attn_row(const AttnArgs& A, int b) {
-    const int r = A.seqs ? A.seqs[b] : b;
-    return r >= 0 && r < A.rows ? r : -1;
-}
-__device__ __forceinline__ int attn_len(const AttnArgs& A, int row) {
-    return row < 0 ? 0 : max(0, min(A.lens[row], A.cap));
-}
+// Table row of sequence b, or -1; its length.
+__device__ __forceinline__ int attn_row_of(const AttnArgs& A, int r) { return r >= 0 && r < A.rows ? r : -1; }
+__device__ __forceinline__ int attn_row(const AttnArgs& A, int b) { return attn_row_of(A, A.seqs ? A.seqs[b] : b); }
+__device__ __forceinline__ int attn_cut(const AttnArgs& A, int len) { return max(0, min(len, A.cap)); }
+__device__ __forceinline__ int attn_len(const AttnArgs& A, int row) { return row < 0 ? 0 : attn_cut(A, A.lens[row]); }
 // Keys that query t of a sequence of len tokens sees.
 __device__ __forceinline__ int attn_seen(const AttnArgs& A, int len, int t) { return max(0, len - A.nq + t + 1); }
 

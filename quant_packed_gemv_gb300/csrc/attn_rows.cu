@@ -96,14 +96,17 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
     Sm& sm = *reinterpret_cast<Sm*>(rows_raw);
     grid_launch_dependents();
     // after the tile kernel there is nothing to wait for yet: it starts this
-    // kernel once the work before it has finished
+    // kernel once the work before it has finished.  What that work wrote (lengths,
+    // tables, q, pages) is then read from L2 (.cg): without a wait, a line that this
+    // SM's L1 holds from before need not be fresh (200 x 2 tokens, nothing shared: the
+    // table from L2 37 us, by L1 35)
     if (P.prefix_tiles == 0) grid_wait_prior();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int b = blockIdx.x / A.kv_heads, h = blockIdx.x - b * A.kv_heads;
     // rows r0 .. r0 + rows - 1 of the sequence and head (grid y: chunks of them)
     const int total = A.nq * A.group, chunk = (total + (int)gridDim.y - 1) / (int)gridDim.y;
     const int r0 = blockIdx.y * chunk, rows = min(chunk, total - r0);
-    const int row = attn_row(A, b), len = attn_len(A, row);
+    const int row = attn_row_of(A, A.seqs ? __ldcg(A.seqs + b) : b), len = row < 0 ? 0 : attn_cut(A, __ldcg(A.lens + row));
     const int* tab = A.table + (long long)max(row, 0) * A.table_stride;
     const long long head = (long long)h * A.kv_hs;
     const E* kbase = static_cast<const E*>(A.k) + head;
@@ -123,7 +126,11 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
     constexpr int CH = D / 8;
     const int cc = lane % CH, cr = lane / CH;
     const uint32_t ring = smem_u32(&sm.ring[warp][0][0][0]);
-    auto page_of = [&](int blk) -> int { return blk < blocks ? __ldg(tab + ((blk << 4) >> A.page_shift)) : -1; };
+    auto page_of = [&](int blk) -> int {
+        if (blk >= blocks) return -1;
+        const int* at = tab + ((blk << 4) >> A.page_shift);
+        return P.prefix_tiles > 0 ? __ldcg(at) : __ldg(at);
+    };
     auto fetch = [&](int blk, int page, int slot) {
         if (blk < blocks) {
             const int j = blk << 4;
@@ -148,8 +155,8 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
         const int r = 8 * nb + g;
         if (r >= rows) return make_uint4(0, 0, 0, 0);
         const int tr = small_row(A, r0 + r);
-        return *reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + tr) * A.q_ts +
-                                               (long long)(h * A.group + r0 + r - tr * A.group) * A.q_hs + 8 * t + 32 * c);
+        return __ldcg(reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + tr) * A.q_ts +
+                                                     (long long)(h * A.group + r0 + r - tr * A.group) * A.q_hs + 8 * t + 32 * c));
     };
     if constexpr (QS) {
         for (int i = warp; i < NB * KC; i += DW) sm.q[i * 32 + lane] = q_part(i / KC, i % KC);
