@@ -58,12 +58,19 @@ Choice choose(const AttnArgs& A, int d, void* ws) {
         const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7);
         c.share = (bytes / 6e6 > chain ? bytes / 6e6 : chain) > 7.0;
     } else if (c.share) {
-        // The same in units of the tile kernel: those of the prefix in every sequence's
-        // own tiles, less those of the batch's rows together; its launch and the sums
-        // over all rows are worth ~3000 (96 x 490 rows behind 15360: 566 us unshared, 659
-        // shared; 24 x 140 rows behind 8192 saves 9000).
+        // What it saves: the prefix's units in every sequence's own tiles, less those of the
+        // batch's rows together.  A unit of two row tiles takes the whole GPU 8 + d / 32 ns,
+        // one of a single tile 0.57 of that.  What it costs: a launch, and two more trips of
+        // every row's O through memory.  So it pays where a sequence's rows fill its tiles
+        // badly.  One GB300, us unshared and shared; 8 heads of 128: 24 x 140 rows behind 8192
+        // 173 and 158, behind 2048 78 and 98; 24 x 180 behind 8192 176 and 180; 24 x 112 97 and
+        // 113 (4096); 60 x 128 97 and 182 (2048); 96 x 490 2105 and 2442 (15360), on 2 heads 528
+        // and 628; 40 x 130 on 2 103 and 90 (10240); 60 x 100 on 2 204 and 182 (32768); 8 heads
+        // of 64, 60 x 140 behind 8192 320 and 255.
         const long long tile = mine > 128 ? 256 : 128, each = (mine + tile - 1) / tile, all = (mine * A.batch + 255) / 256;
-        c.share = (A.batch * each - all) * (double)A.kv_heads * A.prefix / TK > 3000;
+        const double unit = 1e-3 * (8 + d / 32.0) * A.kv_heads * A.prefix / TK;
+        const double saved = unit * (A.batch * each * (tile == 256 ? 1.0 : 0.57) - all);
+        c.share = saved > 6.0 + 1.25e-5 * d * A.batch * mine * A.kv_heads;
     }
     size_t a = 0, b = 0;
     if (c.share) c.prefix = tile_plan(A, d, 0, true, ws, &a);

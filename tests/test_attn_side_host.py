@@ -268,3 +268,13 @@ def test_rope_limits_as_stated():
     assert st(many(32768), many(32768)) == P.PLM_OK and st(many(32768), many(32769)) == BAD
     assert st(*[many(8192)] * 8) == P.PLM_OK and st(*[many(8193)] * 8) == BAD
     assert st(many(8), d=127, rot=64) == BAD and st(many(8), d=1024, rot=1024) == P.PLM_OK and st(many(8), d=1026, rot=64) == BAD
+
+
+def test_when_the_prefix_of_many_rows_is_done_apart():
+    # more than 96 rows; measured on both sides (csrc/attn.cu).  Done apart, a call needs more workspace than without
+    def apart(batch, tokens, group, kv_heads, d, prefix):
+        size = lambda p: q.plm_attn_workspace_size(batch, tokens, group * kv_heads, kv_heads, d, p, prefix + tokens + 100)  # noqa: E731
+        return size(prefix) != size(0)
+    assert not apart(60, 32, 4, 8, 128, 2048) and not apart(96, 70, 7, 8, 128, 15360) and not apart(96, 70, 7, 2, 128, 15360)
+    assert not apart(24, 28, 4, 8, 128, 4096) and not apart(60, 28, 4, 8, 64, 2048) and not apart(8, 509, 4, 8, 128, 16384)
+    assert apart(24, 35, 4, 8, 128, 8192) and apart(40, 26, 5, 2, 128, 10240) and apart(60, 35, 4, 8, 64, 8192) and apart(60, 25, 4, 2, 128, 32768)

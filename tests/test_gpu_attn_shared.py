@@ -45,9 +45,9 @@ def test_few_rows_of_a_batch_behind_a_short_prefix(dtype, batch, nq, hq, hkv, d,
     c.check(*c.run())
 
 
-# more than 96 rows: the own keys in the tile kernel too.  One row tile of 128 rows, one of 256, two of 256
-MANY = [(24, 28, 32, 8, 128, 4096), (24, 112, 8, 8, 64, 4096), (60, 15, 14, 2, 64, 5632), (100, 20, 5, 1, 128, 6656), (40, 26, 10, 2, 128, 10240),
-        (10, 150, 16, 8, 128, 6144)]
+# more than 96 rows: the own keys in the tile kernel too.  A sequence's rows in one tile of 128, one of 256, two of 256
+MANY = [(60, 14, 14, 2, 64, 10240), (23, 20, 10, 2, 128, 20480), (10, 129, 8, 8, 64, 8192), (24, 35, 32, 8, 64, 5632), (40, 26, 10, 2, 128, 10240),
+        (10, 140, 16, 8, 128, 8192)]
 
 
 @pytest.mark.parametrize("batch,nq,hq,hkv,d,prefix", MANY)
@@ -62,7 +62,7 @@ def test_many_rows(batch, nq, hq, hkv, d, prefix, dtype, page, order):
     c.check(*c.run(o_type=torch.float32 if page == 64 else None))
 
 
-@pytest.mark.parametrize("nq,batch,prefix", [(1, 5, 5248), (7, 5, 2688), (28, 24, 4096)])
+@pytest.mark.parametrize("nq,batch,prefix", [(1, 5, 5248), (7, 5, 2688), (33, 24, 8192)])
 def test_nobody_shares(nq, batch, prefix):
     # all too short or idle: the kernels of the prefix find no row to read it from
     r = random.Random(nq)
@@ -80,7 +80,7 @@ def test_large_pages_alone(page, nq, dtype):
     c.check(*c.run())
 
 
-@pytest.mark.parametrize("nq,batch,prefix", [(1, 6, 5248), (7, 6, 2688), (28, 24, 4096)])
+@pytest.mark.parametrize("nq,batch,prefix", [(1, 6, 5248), (7, 6, 2688), (33, 24, 8192)])
 def test_the_same_bits_every_time_apart(nq, batch, prefix):
     r = random.Random(nq)
     c = Case([prefix + r.randrange(nq, 300) for _ in range(batch)], nq, 32, 8, 128, prefix, 16, torch.bfloat16, seed=nq)
@@ -132,7 +132,7 @@ def grow(nq, batch, prefix, steps, seed=3):
     return o, lse
 
 
-@pytest.mark.parametrize("nq,batch,prefix,steps", [(1, 8, 5248, 40), (1, 90, 1024, 30), (7, 8, 2688, 20), (28, 24, 4096, 6)])
+@pytest.mark.parametrize("nq,batch,prefix,steps", [(1, 8, 5248, 40), (1, 90, 1024, 30), (7, 8, 2688, 20), (33, 24, 8192, 4)])
 def test_the_same_bits_in_every_launch_mode_apart(nq, batch, prefix, steps):
     # with early launch the kernel of the own keys starts beside that of the prefix, and reads what earlier calls wrote
     runs, before = [], q.plm_set_overlap(q.PLM_OVERLAP_OFF)
