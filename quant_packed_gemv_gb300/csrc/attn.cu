@@ -1,11 +1,11 @@
 // Attention over a paged cache (plm_attn_shared_prefix): which kernels a call
 // runs.
 //
-// Decode (at most 96 rows per sequence and head): attn_rows.cu, a cluster per
-// (sequence, head); a shared prefix is first done for the whole batch by the
-// tile kernel (attn_tile.cu), and the rows kernel adds its results at the end.
-// More rows: the tile kernel does the own keys too, and a last kernel adds what
-// was cut.
+// Few rows per sequence and head (decode, drafted tokens: up to 32, up to 96 over
+// few keys): attn_rows.cu, a cluster per (sequence, head).  More rows: the tile kernel
+// (attn_tile.cu), and a last kernel that adds what was cut.  A shared prefix goes
+// either with each sequence's own keys or, where that pays, first and for the whole
+// batch through the tile kernel; its results are then added at the end.
 #include "attn_tile.cuh"
 
 namespace plm {
@@ -40,24 +40,37 @@ struct Choice {
     size_t bytes;  // workspace, SIZE_MAX: too many units
 };
 
-Choice choose(const AttnArgs& A, int d, void* ws) {
+// bound: what the lengths are bounded by (A.cap may be less: the table's rows end
+// first; the workspace is sized without knowing them).
+Choice choose(const AttnArgs& A, int d, long long bound, void* ws) {
     const long long mine = (long long)A.nq * A.group;
+    const bool common = A.prefix > 0 && A.batch > 1;
     Choice c = {};
-    // Up to 96 rows the rows kernel, in chunks of 32 that read the keys again: 40 x 68
-    // rows over 2000 keys take 90 us there and 138 in the tile kernel, 5 x 80 rows behind
-    // 1024 26 and 36, 24 x 80 behind 8192 150 and 144; 8 x 112 behind 4096 52 and 44.
-    c.rows = mine <= 96;
-    c.share = A.prefix > 0 && A.batch > 1;
-    if (c.share && c.rows) {
+    if (mine <= 96) {
         // The prefix apart costs a launch and longer sums, ~7 us.  Read by every sequence
         // it takes its bytes at ~6 TB/s, or the 16-key blocks that a warp of a full
-        // cluster goes through.  One GB300: 4 streams behind 1024 tokens 9.3 us unshared
-        // and 11.0 shared, 149 behind 64 11 and 20; 16 behind 1024 15.7 and 11.3, 2
-        // behind 8192 22 and 17, 12 x 28 rows behind 3104 33 and 24.
+        // cluster goes through.  One GB300, us unshared and shared: 4 streams behind 1024
+        // tokens 9.8 and 11.1, 149 behind 64 16 and 25; 16 behind 1024 15.9 and 11.6, 2
+        // behind 8192 22 and 19, 12 x 28 rows behind 3072 59 and 32.
         const double bytes = (A.batch - 1.0) * A.prefix * A.kv_heads * 4 * d * ((mine + 31) / 32);
         const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7);
-        c.share = (bytes / 6e6 > chain ? bytes / 6e6 : chain) > 7.0;
-    } else if (c.share) {
+        c.share = common && (bytes / 6e6 > chain ? bytes / 6e6 : chain) > 7.0;
+        // Beyond 32 rows the rows kernel goes over the keys again for each chunk of 32, which
+        // pays as long as they are few, and for longer where its CTAs leave room on the GPU;
+        // the prefix apart, and its sums, count as 512 keys.  One GB300, 8 heads of 128, us
+        // here and in the tile kernel: 24 x 40 rows over 4000 keys 74 and 97, over 16000 254 and
+        // 178; 24 x 64 over 2000 74 and 81, over 3000 101 and 81; 60 x 72 over 2000 136 and 137,
+        // over 3000 184 and 152; 2 x 64 over 4000 23 and 27, 5 x 72 over 3000 24 and 28; 60 x 80
+        // over 1000 154 and 114, 8 x 80 27 and 30, over 3000 56 and 39; 8 x 96 behind 4096 51
+        // and 41.  Heads of 64: 24 x 64 over 4000 57 and 71, 24 x 80 over 1000 31 and 40, over
+        // 4000 82 and 68, 3 x 80 19 and 22.
+        const long long keys = c.share ? bound - A.prefix + 512 : bound;
+        const long long ctas = (mine + 31) / 32 * A.batch * A.kv_heads, room = attn_rows_room(d, (int)mine);
+        const bool half = 2 * ctas <= room, whole = ctas <= room && !c.share;
+        const int most = mine <= 48 ? 4096 : mine <= 72 ? (half ? 4096 : 2048) : half && d == 64 ? 3072 : whole ? 1536 : 512;
+        c.rows = mine <= 32 || keys <= most * (128 / d);
+    }
+    if (!c.rows) {
         // What it saves: the prefix's units in every sequence's own tiles, less those of the
         // batch's rows together.  A unit of two row tiles takes the whole GPU 8 + d / 32 ns,
         // one of a single tile 0.57 of that.  What it costs: a launch, and two more trips of
@@ -70,7 +83,7 @@ Choice choose(const AttnArgs& A, int d, void* ws) {
         const long long tile = mine > 128 ? 256 : 128, each = (mine + tile - 1) / tile, all = (mine * A.batch + 255) / 256;
         const double unit = 1e-3 * (8 + d / 32.0) * A.kv_heads * A.prefix / TK;
         const double saved = unit * (A.batch * each * (tile == 256 ? 1.0 : 0.57) - all);
-        c.share = saved > 6.0 + 1.25e-5 * d * A.batch * mine * A.kv_heads;
+        c.share = common && saved > 6.0 + 1.25e-5 * d * A.batch * mine * A.kv_heads;
     }
     size_t a = 0, b = 0;
     if (c.share) c.prefix = tile_plan(A, d, 0, true, ws, &a);
@@ -89,13 +102,13 @@ size_t attn_workspace_bytes(long long batch, long long tokens, long long heads, 
     A.group = A.heads / A.kv_heads;
     A.prefix = (int)prefix_len;
     A.cap = (int)max_len;
-    return choose(A, (int)head_dim, nullptr).bytes;
+    return choose(A, (int)head_dim, max_len, nullptr).bytes;
 }
 
 cudaError_t launch_attn(const plm_attn_problem& p, void* ws, cudaStream_t stream) {
     const AttnArgs A = attn_args(p);
     const int d = (int)p.head_dim;
-    const Choice c = choose(A, d, ws);
+    const Choice c = choose(A, d, p.max_len, ws);
     if (c.share) {
         const cudaError_t e = launch_attn_tile(A, c.prefix, p.type, d, stream);
         if (e != cudaSuccess) return e;

@@ -215,4 +215,8 @@ cudaError_t launch_attn_merge(const AttnArgs& A, const TilePlan& prefix, const T
 // add, or null.
 cudaError_t launch_attn_rows(const AttnArgs& A, const TilePlan* P, int type, int d, cudaStream_t stream);
 
+// CTAs of that kernel that the GPU takes well at once, for so many rows a sequence
+// and head.
+long long attn_rows_room(int d, int rows);
+
 }  // namespace plm

@@ -278,3 +278,11 @@ def test_when_the_prefix_of_many_rows_is_done_apart():
     assert not apart(60, 32, 4, 8, 128, 2048) and not apart(96, 70, 7, 8, 128, 15360) and not apart(96, 70, 7, 2, 128, 15360)
     assert not apart(24, 28, 4, 8, 128, 4096) and not apart(60, 28, 4, 8, 64, 2048) and not apart(8, 509, 4, 8, 128, 16384)
     assert apart(24, 35, 4, 8, 128, 8192) and apart(40, 26, 5, 2, 128, 10240) and apart(60, 35, 4, 8, 64, 8192) and apart(60, 25, 4, 2, 128, 32768)
+
+
+def test_where_the_rows_kernel_ends():
+    # 33 to 96 rows; measured on both sides (csrc/attn.cu).  Alone it needs no workspace, the tile kernel does
+    size = lambda batch, tokens, d, keys: q.plm_attn_workspace_size(batch, tokens, 32, 8, d, 0, keys)  # noqa: E731
+    assert size(24, 8, 128, 90000) == 0 and size(24, 10, 128, 4000) == 0 and size(24, 16, 128, 2000) == 0 and size(5, 20, 128, 500) == 0
+    assert size(24, 10, 128, 16000) > 0 and size(24, 16, 128, 3000) > 0 and size(60, 20, 128, 4000) > 0 and size(60, 24, 128, 2000) > 0
+    assert size(24, 16, 64, 4000) == 0 and size(24, 20, 64, 1000) == 0 and size(24, 20, 64, 4000) > 0 and size(8, 25, 128, 100) > 0

@@ -20,7 +20,7 @@ def apart(c, prefix=None, most=None):
 
 # query heads, key/value heads, head size, tokens: 5 to 96 rows per sequence and key/value head
 FEW = [(14, 2, 64, 1), (14, 2, 64, 3), (14, 2, 64, 13), (16, 8, 128, 1), (32, 8, 128, 4), (32, 8, 128, 7), (5, 1, 128, 1), (5, 1, 128, 6),
-       (8, 8, 64, 1), (8, 8, 64, 20), (8, 8, 64, 96), (12, 2, 128, 4)]
+       (8, 8, 64, 1), (8, 8, 64, 20), (8, 8, 64, 96), (12, 2, 128, 4), (32, 8, 128, 10), (16, 8, 128, 36)]
 
 
 @pytest.mark.parametrize("hq,hkv,d,nq", FEW)
@@ -69,6 +69,16 @@ def test_nobody_shares(nq, batch, prefix):
     c = Case([r.choice((0, 1, 100, 300)) for _ in range(batch - 1)] + [120], nq, 32, 8, 128, 0, 16, torch.bfloat16, seed=nq)
     assert apart(c, prefix, prefix + 400)
     c.check(*c.run(max_len=prefix + 400, prefix=prefix))
+
+
+@pytest.mark.parametrize("nq", [18, 36, 48])
+@pytest.mark.parametrize("prefix", [0, 512])
+def test_a_bound_far_above_the_table(nq, prefix):
+    # the kernels are chosen, and the workspace sized, by the bound; the rows of the table end long before it
+    c = Case([prefix + nq + 9, prefix + 200, 0, 30, prefix + nq], nq, 8, 4, 128, prefix, 16, torch.bfloat16, seed=nq + prefix)
+    assert q.plm_attn_workspace_size(5, nq, 8, 4, 128, prefix, 600) != q.plm_attn_workspace_size(5, nq, 8, 4, 128, prefix, 90000)
+    c.check(*c.run())
+    c.check(*c.run(max_len=90000))
 
 
 @pytest.mark.parametrize("page", [128, 256, 1024])
