@@ -643,6 +643,10 @@ plm_status plm_rope(const plm_rope_tensor* tensors, int64_t count, const int32_t
  * timing.  An item that cannot be done (a sequence out of range, a row too
  * short, a child in use) is left out and flagged; if the free pages do not
  * suffice for all the others, none is done.
+ * The lengths are these calls' to write: the next reserve counts a sequence's
+ * pages from its length, so one lowered by hand loses those past it.  Tokens
+ * are taken back (drafts that were not accepted) by a fork that keeps the
+ * others, into an unused sequence, and a free of the first.
  * Sequences (for fork: children) are distinct within a call, and a fork's
  * parents are not its children; the state is undefined otherwise, but no
  * memory outside it is touched.  A call of n = 0 items does nothing; its lists

@@ -171,6 +171,25 @@ def test_wishes_that_pass_32_bits_together_change_nothing(n):
     assert not lens.any() and not refs.any() and bool((table[:, 0] == -1).all())
 
 
+def test_tokens_are_taken_back_by_fork_and_free():
+    # drafts that were not accepted: whole pages past the kept tokens become free, the page they end in is copied
+    m = Model(40, 8, 10, 4)
+    g = Gpu(m, 8)
+    steps = [("reserve", [0, 1, 2], [9, 16, 6]), ("reserve", [0, 1, 2], [7, 7, 7])]
+    for _, seqs, add in steps:
+        q.plm_kv_reserve(g.kv, ints(seqs), ints(add), None, g.ws)
+        m.reserve(seqs, add, 99)
+    used = sum(r > 0 for r in m.refs)
+    old, new, keep = [0, 1, 2], [5, 6, 7], [10, 16, 13]   # 1, 0 and all of the 7 drafts stay
+    q.plm_kv_fork(g.kv, ints(old), ints(new), g.ws, keep=ints(keep))
+    q.plm_kv_free(g.kv, ints(old))
+    m.fork(old, new, keep)
+    m.free(old)
+    g.same(m)
+    assert m.status == 0 and m.lens == [0, 0, 0, 0, 0, 10, 16, 13]
+    assert sum(r > 0 for r in m.refs) == 3 + 4 + 4 < used and sum(m.refs) == 3 + 4 + 4
+
+
 def test_fork_without_room_changes_nothing():
     m = Model(9, 4, 8, 4)
     g = Gpu(m, 4)
