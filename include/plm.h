@@ -50,7 +50,7 @@
 extern "C" {
 #endif
 
-#define PLM_ABI_VERSION 1
+#define PLM_ABI_VERSION 1   /* raised when an entry point changes; new ones leave it */
 
 typedef enum {
     PLM_OK = 0,
@@ -698,9 +698,9 @@ plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const i
 
 /*
  * Attention over a paged cache for a batch whose sequences share their first
- * prefix_len tokens (the same pages in every row): those are read once for
- * all the batch.  prefix_len = 0 is plain paged attention; what is computed
- * does not depend on it.
+ * prefix_len tokens (the same pages in every row): where that pays, those are
+ * read once for all the batch, else with each sequence's own.  prefix_len = 0
+ * is plain paged attention; what is computed does not depend on it.
  * Query t of sequence b (row b * tokens + t of q) stands at position
  * len_b - tokens + t, where len_b counts all its tokens, the new ones
  * included, and sees the keys j <= that position:
@@ -708,7 +708,8 @@ plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const i
  * A query that sees no key (or only scores of -inf) has o = 0, lse = -inf.
  * Query head h reads key/value head h / (heads / kv_heads).
  * Scores, maxima, sums and the output are held in f32; the probabilities are
- * rounded to the cache's type for the second product (their sum is not).
+ * rounded to the cache's type for the second product (their sum is not), also
+ * for an output of f32: the tensor cores take both operands in one type.
  *   q [batch*tokens][heads][head_dim] of `type`, strides in elements;
  *   o the same shape of o_type (type or PLM_F32) with its own strides;
  *   lse f32 [batch*tokens][heads], or null;
@@ -731,6 +732,8 @@ plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const i
  * below 256.  PLM_ERR_INVALID_ARG: null pointers, sizes < 1, heads not a
  * multiple of kv_heads, unknown types, a workspace below
  * plm_attn_workspace_size bytes.  batch = 0 does nothing.
+ * plm_attn_workspace_size: bytes for a call of these sizes on the current
+ * device; 0 where none are needed, and for sizes that the call refuses.
  */
 typedef struct {
     const void* q;

@@ -23,8 +23,8 @@
 // of bank conflicts; keys past the end are filled with zeros and not read.  The
 // warps of a CTA and the CTAs of a cluster take the blocks in turn and add
 // their parts through shared memory, in a fixed order.  One GB300, 8 heads of 128
-// in bf16: 64 sequences of up to 4000 keys, 90 us (5.8 TB/s); 256 of up to 2000,
-// 182 us with a cold L2 (5.7 TB/s); 4 of 1100, 9.3 us, which is latency.
+// in bf16: 64 sequences of up to 4000 keys, 95 us (5.5 TB/s); 256 of up to 2000,
+// 176 us (6.0 TB/s), 182 with a cold L2; 4 of 1100, 9.3 us, which is latency.
 #include "attn_tile.cuh"
 
 namespace plm {
@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
                 p[i] = ex2(s[nb][i] - base);
                 l[nb][i & 1] += p[i];
             }
+            // rounded to the cache's type (attn.cuh); l has the whole p
             pb[nb][0] = transpose8x8(pack_pair<E>(p[0], p[1]));
             pb[nb][1] = transpose8x8(pack_pair<E>(p[2], p[3]));
         }

@@ -21,8 +21,8 @@
 // Work: equal shares of units per CTA (attn_tile.cuh), one CTA per SM.
 // Bound: the tensor cores from ~270 rows per head on, HBM below.  Every wait
 // is bounded; one that runs out records a fault and the kernel winds down.
-// One GB300, bf16, 32 query heads on 8 of 128: 8 x 509 tokens behind 16384, 790 us
-// (1.4 PFLOP/s with the join); 256 tokens' prefix of 32768, 115 us (1.2 PFLOP/s).
+// One GB300, bf16, 32 query heads on 8 of 128: 8 x 509 tokens behind 16384, 820 us
+// (1.37 PFLOP/s with the join), 8192 tokens behind nothing 1000 us; 256 tokens' prefix of 32768, 115 us (1.2 PFLOP/s).
 // The tensor pipe then waits for the starts and ends of pieces.
 #include <cuda.h>
 
@@ -616,7 +616,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ Til
                         p0 = ex2(p0); p1 = ex2(p1); p2 = ex2(p2); p3 = ex2(p3);
                         la = f2_add(la, f2(p0, p1));
                         lb = f2_add(lb, f2(p2, p3));
-                        pk[k / 2] = pack_pair<E>(p0, p1);
+                        pk[k / 2] = pack_pair<E>(p0, p1);   // rounded to the cache's type (attn.cuh); l has the whole p
                         pk[k / 2 + 1] = pack_pair<E>(p2, p3);
                     }
                     tmem_st32(sa + c / 2, pk);

@@ -5,8 +5,10 @@
 // in step.  A call that hands out pages counts what its items need (a prefix
 // sum over the items), then walks the counts in index order until it has
 // found that many free pages.  Both are done by one CTA: 1024 threads read
-// 64 K counts (256 KB) in a few microseconds, and the walk ends early.  What
-// follows touches each item, table row and page independently and runs on the
+// 64 K counts (256 KB) in a few microseconds.  As the lowest free pages are handed
+// out, those below are in use, and the walk reads about as many counts as there are
+// live pages; packing reads all.  (Millions of small pages would take one CTA a
+// millisecond.)  What follows touches each item, table row and page independently and runs on the
 // whole GPU; reference counts change by integer atomics, whose order does not
 // show.  Bound: HBM for the calls that move pages (each moved page read and
 // written once), launch latency for the others.  One GB300: packing 3000 pages of
