@@ -727,7 +727,7 @@ plm_status plm_kv_copy_pages(const plm_kv_state* kv, const int32_t* src, const i
  * queries of the same call that stand before them (0 * inf).
  * PLM_ERR_UNSUPPORTED: head_dim other than 64 or 128, page_tokens not a
  * power of two from 16 on, 2^31 units of 128 rows x 128 keys or more (by
- * max_len).  PLM_ERR_MISALIGNED: q, k, v below 16 bytes (o
+ * max_len; for the own keys only beyond 96 rows a sequence and head).  PLM_ERR_MISALIGNED: q, k, v below 16 bytes (o
  * too), a stride of q, o, k, v not a multiple of 16 bytes, the workspace
  * below 256.  PLM_ERR_INVALID_ARG: null pointers, sizes < 1, heads not a
  * multiple of kv_heads, unknown types, a workspace below

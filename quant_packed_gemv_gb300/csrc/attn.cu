@@ -64,11 +64,15 @@ Choice choose(const AttnArgs& A, int d, long long bound, void* ws) {
         // over 1000 154 and 114, 8 x 80 27 and 30, over 3000 56 and 39; 8 x 96 behind 4096 51
         // and 41.  Heads of 64: 24 x 64 over 4000 57 and 71, 24 x 80 over 1000 31 and 40, over
         // 4000 82 and 68, 3 x 80 19 and 22.
-        const long long keys = c.share ? bound - A.prefix + 512 : bound;
-        const long long ctas = (mine + 31) / 32 * A.batch * A.kv_heads, room = attn_rows_room(d, (int)mine);
-        const bool half = 2 * ctas <= room, whole = ctas <= room && !c.share;
-        const int most = mine <= 48 ? 4096 : mine <= 72 ? (half ? 4096 : 2048) : half && d == 64 ? 3072 : whole ? 1536 : 512;
-        c.rows = mine <= 32 || keys <= most * (128 / d);
+        c.rows = true;
+        if (mine > 32) {
+            const long long keys = c.share ? bound - A.prefix + 512 : bound, pairs = (long long)A.batch * A.kv_heads;
+            const long long ctas = (mine + 31) / 32 * pairs, room = attn_rows_room(d, (int)mine);
+            const bool half = 2 * ctas <= room, whole = ctas <= room && !c.share;
+            const int most = mine <= 48 ? 4096 : mine <= 72 ? (half ? 4096 : 2048) : half && d == 64 ? 3072 : whole ? 1536 : 512;
+            // (what the tile kernel cannot count the rows kernel can)
+            c.rows = keys <= most * (128 / d) || pairs * ((bound + TK - 1) / TK) > 0x7FFFFFFFLL;
+        }
     }
     if (!c.rows) {
         // What it saves: the prefix's units in every sequence's own tiles, less those of the

@@ -286,3 +286,13 @@ def test_where_the_rows_kernel_ends():
     assert size(24, 8, 128, 90000) == 0 and size(24, 10, 128, 4000) == 0 and size(24, 16, 128, 2000) == 0 and size(5, 20, 128, 500) == 0
     assert size(24, 10, 128, 16000) > 0 and size(24, 16, 128, 3000) > 0 and size(60, 20, 128, 4000) > 0 and size(60, 24, 128, 2000) > 0
     assert size(24, 16, 64, 4000) == 0 and size(24, 20, 64, 1000) == 0 and size(24, 20, 64, 4000) > 0 and size(8, 25, 128, 100) > 0
+
+
+def test_few_rows_of_very_many_keys_are_not_refused():
+    # 2^32 units of the tile kernel by the bound: up to 96 rows there is a kernel without them.  (k is misaligned, which
+    # is checked after: nothing is launched)
+    st = lambda tokens, **kw: P.raw_status("plm_attn_shared_prefix", attn(batch=1 << 16, rows=1 << 16, tokens=tokens, heads=16,  # noqa: E731
+                                           kv_heads=8, prefix_len=0, max_len=1 << 20, k=A + 8, **kw), A, 1 << 50, None)
+    for tokens in (1, 16, 20, 48):
+        assert st(tokens) == MIS
+    assert st(49) == UNS

@@ -71,6 +71,16 @@ def test_nobody_shares(nq, batch, prefix):
     c.check(*c.run(max_len=prefix + 400, prefix=prefix))
 
 
+@pytest.mark.parametrize("hq,hkv,nq,d,most", [(40, 1, 1, 128, 5000), (10, 2, 7, 64, 9000), (64, 1, 1, 128, 4500), (8, 1, 8, 128, 4500), (3, 1, 21, 64, 8500),
+                                              (96, 1, 1, 128, 2000), (5, 1, 19, 64, 7000), (24, 2, 8, 128, 1700)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_middling_rows_over_many_keys(hq, hkv, nq, d, most, dtype):
+    # 33 to 96 rows a sequence and head whose keys are too many for the kernel of few rows
+    c = Case([most, 0, most - 1, 3, most // 2 + 5, 130], nq, hq, hkv, d, 0, 32, T[dtype], order="tokens first", seed=nq + most)
+    assert q.plm_attn_workspace_size(6, nq, hq, hkv, d, 0, most) > 0
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("nq", [18, 36, 48])
 @pytest.mark.parametrize("prefix", [0, 512])
 def test_a_bound_far_above_the_table(nq, prefix):
