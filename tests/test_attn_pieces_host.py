@@ -24,7 +24,7 @@ static unsigned state = 12345;
 static int below(int n) { state = state * 1664525u + 1013904223u; return (int)((state >> 8) % (unsigned)n); }
 
 int main() {
-    for (int round = 0; round < 400; ++round) {
+    for (int trial = 0; trial < 400; ++trial) {
         TilePlan P = {};
         P.tile_rows = below(2) ? 256 : 128;
         P.ctas = 1 + below(MOST_CTAS);
