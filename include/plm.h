@@ -759,13 +759,188 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
                                   cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * What a decode step needs besides: the residual sum and norm before a
+ * product, a cache in 8 bits with the attention that reads it, and the choice
+ * of the next token.  The PocketLLM pages name the norm, the cache and the
+ * sampler as parts of the engine around the packed matmul and give no layouts
+ * for them.  The general rules above hold.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Residual sum and root-mean-square norm, m rows of k values:
+ *   h = x + residual, rounded to the residual's type   (no residual: h = x)
+ *   y = (h / sqrt(sum h^2 / k + eps)) * weight
+ * in f32.  The norm is of h as it is rounded, whether or not it is stored.
+ * Wanted outputs (at least one of xq and y, others null):
+ *   sum [m][k] of r_type: h, the next residual;
+ *   xq  q8_K [m][k/256]: what plm_quantize_q8K makes of y in f32, bit for bit
+ *       (k a multiple of 256);
+ *   y   [m][k] of y_type, rounded once from f32.
+ * weight [k] of w_type, or null (1).  Strides are in elements from row to row,
+ * rows are dense.  Every pointer is aligned to its elements (xq: 4 bytes);
+ * whole 16-byte accesses are made where pointers, strides and k allow them.
+ * sum may be x or residual, and y x or residual (an output that is also an
+ * input has the input's type and stride); nothing else may overlap.  m = 0
+ * does nothing.  PLM_ERR_INVALID_ARG: null x, neither xq nor y, sum without
+ * residual, m < 0, k < 1, m or k past int32, eps negative or NaN, unknown types, a
+ * row stride below k with m > 1, xq with k % 256 != 0, an output in place of an input of
+ * another type or stride, sum = y.
+ */
+typedef struct {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* sum;
+    void* xq;
+    void* y;
+    int64_t m, k;
+    int64_t x_stride, residual_stride, sum_stride, y_stride;
+    float eps;
+    int32_t x_type, r_type, w_type, y_type;
+} plm_rmsnorm_problem;
+
+plm_status plm_rmsnorm(const plm_rmsnorm_problem* p, cudaStream_t stream);
+
+/*
+ * A cache in 8 bits ("kv8").  A head's row of head_dim values is cut into
+ * blocks of 32.  A block is 32 codes (int8, -127 .. 127) and an exponent e
+ * (one byte): value = code * 2^(e - 127), and 0 where e = 0.  2^(e - 127) is the
+ * smallest power of two, 2^-100 at least, with which no code exceeds 127 after rounding to
+ * nearest (ties to even); a block of zeros has e = 0.  So every value is exact in f32 and
+ * bf16, and a block's error is at most half of 2^(e - 127).  Values beyond +-2^120 are cut
+ * to it, NaN is stored as 0.
+ * Pages, slots and tables are those of the cache above.  Element (page, head,
+ * token, i) of the codes lies at page * page_stride + head * head_stride +
+ * token * token_stride + i from their base, the exponent of block j at page *
+ * exp_page_stride + head * exp_head_stride + token * (head_dim / 32) + j from
+ * theirs: codes and exponents of a page may lie in one pool, so that the page
+ * calls move them together.
+ */
+typedef struct {
+    void* rows;                                 /* [tokens][heads][head_dim] of `type`, the last axis dense */
+    int8_t* codes;
+    uint8_t* exps;
+    const int64_t* slots;                       /* [tokens] */
+    int64_t heads;
+    int64_t row_token_stride, row_head_stride;
+    int64_t page_tokens, pages;
+    int64_t page_stride, head_stride, token_stride;   /* of the codes */
+    int64_t exp_page_stride, exp_head_stride;
+    int32_t type;                               /* PLM_F32, PLM_F16, PLM_BF16 */
+    int32_t rotate;                             /* write: turn the rows by their positions first */
+} plm_kv8_tensor;
+
+/*
+ * Writes the rows of up to PLM_ROPE_MAX_TENSORS tensors into 8-bit pages in one
+ * launch: typically k (turned) and v of one product.  The turning is that of
+ * plm_rope (positions, freqs, rotary_dim, layout, scale, in f32); positions and
+ * freqs may be null, and the other three are not looked at, where no tensor has
+ * rotate != 0.  A token whose slot is negative or >= pages * page_tokens is not written.
+ * PLM_ERR_INVALID_ARG: null pointers, count outside 1..8, tokens < 0 or past
+ * int32, head_dim not a multiple of 32 or outside 32..1024, sizes < 1, more than
+ * 65536 heads (all tensors together), unknown type, a rotary part as plm_rope
+ * refuses it.  PLM_ERR_MISALIGNED: rows or slots below their element, codes
+ * below 4 bytes, a code stride not a multiple of 4.  tokens = 0 does nothing.
+ * Distinct slots must not share bytes, and a slot is given once in a call.
+ */
+plm_status plm_kv8_write(const plm_kv8_tensor* tensors, int64_t count, const int32_t* positions, const uint64_t* freqs,
+                         int64_t tokens, int64_t head_dim, int64_t rotary_dim, int layout, float scale,
+                         cudaStream_t stream);
+
+/*
+ * Reads slots back into rows, one rounding to `type` (none for f32 and bf16).
+ * A token whose slot is negative or out of range reads as zeros.  `rotate` is
+ * not looked at.  Errors as plm_kv8_write.
+ */
+plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t tokens, int64_t head_dim,
+                        cudaStream_t stream);
+
+/*
+ * plm_attn_shared_prefix over 8-bit pages: the same sums, lengths, tables,
+ * prefix and refusals, with k and v the pages' values in `type` (that of q:
+ * exact in bf16; in f16 a block counts as zeros below 2^(e - 127) = 2^-24, and
+ * values beyond f16 are undefined).
+ *   k, v codes, k_exps, v_exps their exponents, both with the strides given (in bytes).
+ * PLM_ERR_MISALIGNED: as there, and codes, exponents or one of their strides
+ * not a multiple of 16 bytes.  More than 96 rows a sequence and head, and a
+ * prefix that is done apart, are read back into the workspace as 16-bit pages
+ * first (2 * 2 * head_dim bytes a key and key/value head), as that is faster.
+ */
+typedef struct {
+    const void* q;
+    void* o;
+    float* lse;
+    const int8_t* k;
+    const int8_t* v;
+    const uint8_t* k_exps;
+    const uint8_t* v_exps;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* seqs;
+    int64_t batch, tokens, heads, kv_heads, head_dim;
+    int64_t q_token_stride, q_head_stride, o_token_stride, o_head_stride;
+    int64_t page_tokens, pages, page_stride, kv_head_stride, kv_token_stride, exp_page_stride, exp_head_stride;
+    int64_t table_stride, rows;
+    int64_t prefix_len, max_len;
+    float scale;
+    int32_t type, o_type;
+} plm_attn_kv8_problem;
+
+size_t plm_attn_kv8_workspace_size(int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                   int64_t prefix_len, int64_t max_len);
+plm_status plm_attn_kv8(const plm_attn_kv8_problem* p, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The next token of each of m rows of n logits, from given random numbers.
+ * With T = temperature[i], top = the row's largest logit, w_j =
+ * exp((x_j - top) / T), and the tokens in descending order of their logits
+ * (equal ones: lowest index first):
+ *   top_k[i] >= 1: the first top_k of them, else all;
+ *   top_p[i] < 1:  of those, the ones before which less than top_p of their
+ *                  w's sum lies (always the first);
+ *   min_p[i] > 0:  of those, the ones with w >= min_p (always the largest logits);
+ * tokens[i] is the first in the order of the indices at which the w's kept so far
+ * add up to more than u[i] of all the kept; prob[i] is its w over their sum.
+ * u is cut to 0 .. 1; u = 1 gives the last one kept with a weight.
+ * Greedy (the largest logit, lowest index, prob 1): T <= 0 or NaN, or u null.
+ * A NaN logit counts as -inf; -inf is never taken; with +inf in the row its
+ * +inf are equal and the others nothing.  A row without a token has tokens = -1, prob = 0.
+ * temperature, top_k, top_p, min_p: [m] on the device, or null: 1, off, off,
+ * off.  A NaN top_p or min_p is off, min_p above 1 counts as 1.
+ * The w's are held in fixed point, 2^-40 of the largest (relative error 2^-30): their
+ * sums do not depend on an order, and tokens below 2^-40 of the largest have no weight.
+ * logits [m][n] of `type`, `stride` elements from row to row, aligned to their
+ * elements; tokens int32 [m], prob f32 [m] or null.  PLM_ERR_INVALID_ARG: null
+ * logits or tokens, m < 0 or past 2^24, n < 1 or past 2^22, an unknown type, a stride below n
+ * with m > 1.  PLM_ERR_MISALIGNED: a pointer below its element.  m = 0 does
+ * nothing.
+ */
+typedef struct {
+    const void* logits;
+    const float* u;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* tokens;
+    float* prob;
+    int64_t m, n, stride;
+    int32_t type;
+} plm_sample_problem;
+
+plm_status plm_sample(const plm_sample_problem* p, cudaStream_t stream);
+
+/*
  * For bindings in which each argument of a call costs: an entry point above
  * with its arguments in one block of 8-byte fields, in the order of its
  * declaration (pointers, sizes and the stream as they are, an int as int64_t,
  * plm_rope's scale as a double), without the pointer to its struct or structs,
  * which follow the fields in the block itself.  entry: 0 plm_rope, 1
  * plm_kv_reserve, 2 plm_kv_fork, 3 plm_kv_free, 4 plm_kv_compact, 5
- * plm_kv_copy_pages, 6 plm_attn_shared_prefix; PLM_ERR_INVALID_ARG otherwise
+ * plm_kv_copy_pages, 6 plm_attn_shared_prefix, 8 plm_rmsnorm, 9 plm_kv8_write, 10
+ * plm_kv8_read, 11 plm_attn_kv8, 12 plm_sample; PLM_ERR_INVALID_ARG otherwise
  * and for a null block.  args is 8-byte aligned HOST memory, read during the
  * call only.
  */

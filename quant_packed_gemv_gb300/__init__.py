@@ -1,7 +1,8 @@
 """GB300 (sm_103a) packed K-quant matmul: q8_K activation quantization and
 q2_K .. q6_K decode GEMV and prefill GEMM behind a C ABI (include/plm.h),
-and the attention side of a decoder between those products: rotary positions,
-the pages of a key/value cache, attention over a shared prefix."""
+and the rest of a decoder's step: residual sums and norms, rotary positions,
+the pages of a key/value cache in 16 or 8 bits, attention over them with a
+shared prefix, the choice of the next token."""
 from .plm import (  # noqa: F401
     PlmError, load, library_path, plm_abi_version, plm_set_overlap,
     PLM_OVERLAP_OFF, PLM_OVERLAP_LAUNCH, PLM_OVERLAP_PREFETCH, plm_device_fault, plm_selftest_bounded_wait, plm_probe_mma_rates,
@@ -16,6 +17,8 @@ from .plm import (  # noqa: F401
     plm_q4K_x16_size, plm_q4K_to_x16, plm_gemv_q4K_x16, plm_q6K_x16_size, plm_q6K_to_x16, plm_gemv_q6K_x16,
     plm_rope_freqs, plm_rope_tensor, plm_rope, plm_kv_state, plm_kv_workspace_size, plm_kv_reserve, plm_kv_fork,
     plm_kv_free, plm_kv_compact, plm_kv_copy_pages, plm_attn_workspace_size, plm_attn_shared_prefix,
+    plm_rmsnorm, plm_kv8_page_bytes, plm_kv8_views, plm_kv8_tensor, plm_kv8_write, plm_kv8_read, plm_attn_kv8_workspace_size,
+    plm_attn_kv8, plm_sample,
     PLM_F32, PLM_F16, PLM_BF16, PLM_ROPE_HALF, PLM_ROPE_INTERLEAVED, PLM_KV_OUT_OF_PAGES, PLM_KV_BAD_ITEM,
     QK, Q4K_BYTES, Q6K_BYTES, Q8K_BYTES, GEMV_MAX_M,
 )

@@ -701,6 +701,135 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
     return cuda_status(plm::launch_attn(*p, workspace, stream));
 }
 
+plm_status plm_rmsnorm(const plm_rmsnorm_problem* p, cudaStream_t stream) {
+    if (!p || !p->x || (!p->xq && !p->y) || (p->sum && !p->residual)) return PLM_ERR_INVALID_ARG;
+    if (!in_range(p->m, 0, kMaxIndex) || !in_range(p->k, 1, kMaxIndex) || !(p->eps >= 0.0f)) return PLM_ERR_INVALID_ARG;
+    struct Part { const void* p; int64_t stride; int type; };
+    const Part x = {p->x, p->x_stride, p->x_type}, r = {p->residual, p->residual_stride, p->r_type}, w = {p->weight, p->k, p->w_type},
+               s = {p->sum, p->sum_stride, p->r_type}, y = {p->y, p->y_stride, p->y_type};
+    for (const Part& a : {x, r, w, s, y})
+        if (a.p && (!type_size(a.type) || (p->m > 1 && a.stride < p->k))) return PLM_ERR_INVALID_ARG;
+    if (p->xq && p->k % plm::QK) return PLM_ERR_INVALID_ARG;
+    // an output in the place of an input: the same rows
+    for (const Part& out : {s, y})
+        for (const Part& in : {x, r})
+            if (out.p && out.p == in.p && (out.type != in.type || (p->m > 1 && out.stride != in.stride))) return PLM_ERR_INVALID_ARG;
+    if (s.p && s.p == y.p) return PLM_ERR_INVALID_ARG;
+    for (const Part& a : {x, r, w, s, y})
+        if (a.p && !aligned(a.p, type_size(a.type))) return PLM_ERR_MISALIGNED;
+    if (!aligned(p->xq, 4)) return PLM_ERR_MISALIGNED;
+    if (p->m == 0) return PLM_OK;
+    return cuda_status(plm::launch_rmsnorm(*p, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// What writing and reading 8-bit pages have in common.
+plm_status check_kv8(const plm_kv8_tensor* tensors, int64_t count, int64_t tokens, int64_t head_dim) {
+    if (!tensors || !in_range(count, 1, PLM_ROPE_MAX_TENSORS) || !in_range(tokens, 0, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+    if (!in_range(head_dim, 32, 1024) || head_dim % 32) return PLM_ERR_INVALID_ARG;
+    int64_t heads = 0;
+    for (int64_t j = 0; j < count; ++j) {
+        const plm_kv8_tensor& t = tensors[j];
+        if (!t.rows || !t.codes || !t.exps || !t.slots || !type_size(t.type) || !in_range(t.heads, 1, 65536)) return PLM_ERR_INVALID_ARG;
+        if (!in_range(t.page_tokens, 1, kMaxIndex) || !in_range(t.pages, 1, kMaxIndex)) return PLM_ERR_INVALID_ARG;
+        heads += t.heads;
+    }
+    if (heads > 65536) return PLM_ERR_INVALID_ARG;
+    for (int64_t j = 0; j < count; ++j) {
+        const plm_kv8_tensor& t = tensors[j];
+        if (!aligned(t.rows, type_size(t.type)) || !aligned(t.slots, 8) || !aligned(t.codes, 4)) return PLM_ERR_MISALIGNED;
+        if (t.page_stride % 4 || t.head_stride % 4 || t.token_stride % 4) return PLM_ERR_MISALIGNED;
+    }
+    return PLM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+plm_status plm_kv8_write(const plm_kv8_tensor* tensors, int64_t count, const int32_t* positions, const uint64_t* freqs,
+                         int64_t tokens, int64_t head_dim, int64_t rotary_dim, int layout, float scale, cudaStream_t stream) {
+    const plm_status s = check_kv8(tensors, count, tokens, head_dim);
+    if (s == PLM_ERR_INVALID_ARG) return s;
+    bool turned = false;
+    for (int64_t j = 0; j < count; ++j) turned |= tensors[j].rotate != 0;
+    if (turned && (!positions || !freqs || !in_range(rotary_dim, 2, head_dim) || rotary_dim % 2 ||
+                   (layout != PLM_ROPE_HALF && layout != PLM_ROPE_INTERLEAVED)))
+        return PLM_ERR_INVALID_ARG;
+    if (s != PLM_OK) return s;
+    if (turned && (!aligned(positions, 4) || !aligned(freqs, 8))) return PLM_ERR_MISALIGNED;
+    if (tokens == 0) return PLM_OK;
+    return cuda_status(plm::launch_kv8_write(tensors, (int)count, positions, freqs, tokens, (int)head_dim,
+                                             turned ? (int)rotary_dim : 0, layout, scale, stream));
+}
+
+plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t tokens, int64_t head_dim, cudaStream_t stream) {
+    const plm_status s = check_kv8(tensors, count, tokens, head_dim);
+    if (s != PLM_OK) return s;
+    if (tokens == 0) return PLM_OK;
+    return cuda_status(plm::launch_kv8_read(tensors, (int)count, tokens, (int)head_dim, stream));
+}
+
+size_t plm_attn_kv8_workspace_size(int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                   int64_t prefix_len, int64_t max_len) {
+    if (!in_range(batch, 1, kMaxIndex) || !in_range(tokens, 1, kMaxIndex) || !in_range(heads, 1, kMaxIndex) ||
+        !in_range(kv_heads, 1, heads) || heads % kv_heads || (head_dim != 64 && head_dim != 128) ||
+        !in_range(max_len, 1, kMaxIndex) || !in_range(prefix_len, 0, max_len))
+        return 0;
+    if (batch * tokens > kMaxIndex / heads) return 0;
+    const size_t need = plm::attn_kv8_workspace_bytes(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len);
+    return need == SIZE_MAX ? 0 : need;
+}
+
+plm_status plm_attn_kv8(const plm_attn_kv8_problem* p, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!p || !p->q || !p->o || !p->k || !p->v || !p->k_exps || !p->v_exps || !p->table || !p->lens) return PLM_ERR_INVALID_ARG;
+    if (!in_range(p->batch, 0, kMaxIndex) || !in_range(p->tokens, 1, kMaxIndex) || !in_range(p->heads, 1, kMaxIndex) ||
+        !in_range(p->kv_heads, 1, p->heads) || p->heads % p->kv_heads || p->head_dim < 1)
+        return PLM_ERR_INVALID_ARG;
+    if (p->batch * p->tokens > kMaxIndex / p->heads) return PLM_ERR_INVALID_ARG;
+    if ((p->type != PLM_F16 && p->type != PLM_BF16) || (p->o_type != p->type && p->o_type != PLM_F32))
+        return PLM_ERR_INVALID_ARG;
+    if (!in_range(p->pages, 1, kMaxIndex) || !in_range(p->rows, 1, kMaxIndex) || p->page_tokens < 1 ||
+        !in_range(p->table_stride, 1, kMaxIndex) || !in_range(p->max_len, 1, kMaxIndex) ||
+        !in_range(p->prefix_len, 0, p->max_len) || p->prefix_len % p->page_tokens)
+        return PLM_ERR_INVALID_ARG;
+    if (p->page_stride < 0 || p->kv_head_stride < 0 || p->kv_token_stride < 0 || p->exp_page_stride < 0 || p->exp_head_stride < 0)
+        return PLM_ERR_INVALID_ARG;
+    if ((p->head_dim != 64 && p->head_dim != 128) || !in_range(p->page_tokens, 16, 1 << 30) ||
+        (p->page_tokens & (p->page_tokens - 1)))
+        return PLM_ERR_UNSUPPORTED;
+    if (p->batch == 0) return PLM_OK;
+    const size_t need = plm::attn_kv8_workspace_bytes(p->batch, p->tokens, p->heads, p->kv_heads, p->head_dim,
+                                                      p->prefix_len, p->max_len);
+    if (need == SIZE_MAX) return PLM_ERR_UNSUPPORTED;
+    if (need && (!workspace || workspace_bytes < need)) return PLM_ERR_INVALID_ARG;
+    const int64_t oe = p->o_type == PLM_F32 ? 4 : 8;   // elements of 16 bytes
+    for (const void* a : {p->q, (const void*)p->o, (const void*)p->k, (const void*)p->v, (const void*)p->k_exps, (const void*)p->v_exps})
+        if (!aligned(a, 16)) return PLM_ERR_MISALIGNED;
+    for (const void* a : {(const void*)p->lse, (const void*)p->table, (const void*)p->lens, (const void*)p->seqs})
+        if (!aligned(a, 4)) return PLM_ERR_MISALIGNED;
+    if (!aligned(workspace, 256)) return PLM_ERR_MISALIGNED;
+    if (p->q_token_stride % 8 || p->q_head_stride % 8 || p->o_token_stride % oe || p->o_head_stride % oe ||
+        p->page_stride % 16 || p->kv_head_stride % 16 || p->kv_token_stride % 16 || p->exp_page_stride % 16 ||
+        p->exp_head_stride % 16)
+        return PLM_ERR_MISALIGNED;
+    return cuda_status(plm::launch_attn_kv8(*p, workspace, stream));
+}
+
+plm_status plm_sample(const plm_sample_problem* p, cudaStream_t stream) {
+    if (!p || !p->logits || !p->tokens || !type_size(p->type)) return PLM_ERR_INVALID_ARG;
+    if (!in_range(p->m, 0, 1 << 24) || !in_range(p->n, 1, 1 << 22) || (p->m > 1 && p->stride < p->n)) return PLM_ERR_INVALID_ARG;
+    if (!aligned(p->logits, type_size(p->type))) return PLM_ERR_MISALIGNED;
+    for (const void* a : {(const void*)p->u, (const void*)p->temperature, (const void*)p->top_k, (const void*)p->top_p,
+                          (const void*)p->min_p, (const void*)p->tokens, (const void*)p->prob})
+        if (!aligned(a, 4)) return PLM_ERR_MISALIGNED;
+    if (p->m == 0) return PLM_OK;
+    return cuda_status(plm::launch_sample(*p, stream));
+}
+
 plm_status plm_call(int entry, const void* args) {
     if (!args) return PLM_ERR_INVALID_ARG;
     const int64_t* a = static_cast<const int64_t*>(args);
@@ -725,6 +854,17 @@ plm_status plm_call(int entry, const void* args) {
         case 5: return plm_kv_copy_pages(kv(4), ints(0), ints(1), a[2], stream(3));
         case 6:
             return plm_attn_shared_prefix(reinterpret_cast<const plm_attn_problem*>(a + 3), ptr(0), (size_t)a[1], stream(2));
+        case 8: return plm_rmsnorm(reinterpret_cast<const plm_rmsnorm_problem*>(a + 1), stream(0));
+        case 9: {
+            double scale;
+            std::memcpy(&scale, a + 7, sizeof scale);
+            return plm_kv8_write(reinterpret_cast<const plm_kv8_tensor*>(a + 9), a[0], ints(1), static_cast<const uint64_t*>(ptr(2)),
+                                 a[3], a[4], a[5], (int)a[6], (float)scale, stream(8));
+        }
+        case 10: return plm_kv8_read(reinterpret_cast<const plm_kv8_tensor*>(a + 4), a[0], a[1], a[2], stream(3));
+        case 11:
+            return plm_attn_kv8(reinterpret_cast<const plm_attn_kv8_problem*>(a + 3), ptr(0), (size_t)a[1], stream(2));
+        case 12: return plm_sample(reinterpret_cast<const plm_sample_problem*>(a + 1), stream(0));
         default: return PLM_ERR_INVALID_ARG;
     }
 }

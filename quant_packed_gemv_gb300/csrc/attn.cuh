@@ -32,6 +32,13 @@ struct AttnArgs {
     int o_f32;
 };
 
+// The same over 8-bit pages: k and v are codes, their strides in bytes.
+struct AttnArgs8 : AttnArgs {
+    const uint8_t* k_exps;
+    const uint8_t* v_exps;
+    long long exp_page, exp_hs;
+};
+
 // r / group for r < 256 (an integer division is ~100 cycles in a row).
 __device__ __forceinline__ int small_row(const AttnArgs& A, int r) { return (int)(((unsigned)r * A.group_inv) >> 16); }
 
@@ -69,6 +76,40 @@ template <> __device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float l
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+
+// Four codes as two pairs of values, exact: c as 1024 + (c + 128) less 1152; or as
+// 128 + (c mod 128) less 128, or less 256 where c < 0.
+template <class E> __device__ __forceinline__ void codes_to_pairs(uint32_t w, uint32_t& lo, uint32_t& hi);
+template <> __device__ __forceinline__ void codes_to_pairs<__half>(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u, less = 0x64806480u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(less));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(less));
+}
+template <> __device__ __forceinline__ void codes_to_pairs<__nv_bfloat16>(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w & 0x7F7F7F7Fu, n = w & 0x80808080u, one = 0x43434343u;
+    const uint32_t a0 = __byte_perm(u, one, 0x4140), a1 = __byte_perm(u, one, 0x4342);
+    const uint32_t b0 = __byte_perm(n, one, 0x4140), b1 = __byte_perm(n, one, 0x4342);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a0), "r"(b0));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(a1), "r"(b1));
+}
+template <class E> __device__ __forceinline__ uint32_t mul_pairs(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t mul_pairs<__half>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t mul_pairs<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The powers of two of two exponents, in the cache's type (f16: 0 below 2^-24, 2^15 at most).
+template <class E> __device__ __forceinline__ uint32_t exps_to_pair(uint32_t e0, uint32_t e1);
+template <> __device__ __forceinline__ uint32_t exps_to_pair<__half>(uint32_t e0, uint32_t e1) {
+    return pack_pair<__half>(fminf(__uint_as_float(e0 << 23), 32768.0f), fminf(__uint_as_float(e1 << 23), 32768.0f));
+}
+template <> __device__ __forceinline__ uint32_t exps_to_pair<__nv_bfloat16>(uint32_t e0, uint32_t e1) { return e0 << 7 | e1 << 23; }
 
 // Four values of an output row, at element offset off (a multiple of 4).
 template <class E>

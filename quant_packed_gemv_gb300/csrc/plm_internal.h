@@ -172,5 +172,18 @@ cudaError_t launch_kv_copy_pages(const plm_kv_state& S, const int* src, const in
 size_t attn_workspace_bytes(long long batch, long long tokens, long long heads, long long kv_heads, long long head_dim,
                             long long prefix_len, long long max_len);
 cudaError_t launch_attn(const plm_attn_problem& p, void* ws, cudaStream_t stream);
+// The same over 8-bit pages.
+size_t attn_kv8_workspace_bytes(long long batch, long long tokens, long long heads, long long kv_heads, long long head_dim,
+                                long long prefix_len, long long max_len);
+cudaError_t launch_attn_kv8(const plm_attn_kv8_problem& p, void* ws, cudaStream_t stream);
+
+// 8-bit pages: rows in and out, checked arguments.
+cudaError_t launch_kv8_write(const plm_kv8_tensor* tensors, int count, const int32_t* positions, const uint64_t* freqs,
+                             long long tokens, int head_dim, int rotary_dim, int layout, float scale, cudaStream_t stream);
+cudaError_t launch_kv8_read(const plm_kv8_tensor* tensors, int count, long long tokens, int head_dim, cudaStream_t stream);
+
+// Residual sum and norm; the next token of each row; checked arguments.
+cudaError_t launch_rmsnorm(const plm_rmsnorm_problem& p, cudaStream_t stream);
+cudaError_t launch_sample(const plm_sample_problem& p, cudaStream_t stream);
 
 }  // namespace plm

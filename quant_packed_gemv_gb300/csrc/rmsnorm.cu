@@ -1,0 +1,240 @@
+// Residual sum, root-mean-square norm and the q8_K blocks of the result
+// (plm_rmsnorm).
+//
+// Mathematics.  h = x + r (rounded to r's type); inv = 1 / sqrt(sum h^2 / k +
+// eps); y = (h inv) w; per 256 values q8_K as plm_quantize_q8K makes it.
+//
+// Layout.  A row is cut into chunks of 256 values; a warp holds up to four of
+// its row's chunks in registers from the first read to the last write, so
+// each value passes memory once.  A lane holds values 4 lane .. + 3 of each
+// half of a chunk: whole 512-byte lines per access.  Chunk sums go through
+// shared memory and every warp adds them in the same order, which depends on k
+// alone: a row's bits do not depend on m or on the launch.
+#include "plm_device.cuh"
+#include "plm_internal.h"
+#include "values.cuh"
+
+namespace plm {
+
+namespace {
+
+constexpr int NORM_WARPS = 16;    // of a row at most
+constexpr int HELD = 4;           // chunks of a warp in registers at most
+
+struct NormArgs {
+    plm_rmsnorm_problem p;
+    int warps;                    // per row
+    bool x4, r4, s4, y4, w4;      // four values in one access
+};
+
+// (fused by hand: left to the compiler, the kernels round differently)
+__device__ __forceinline__ float sum8(const float4& a, const float4& b) {
+    const float s = fmaf(a.w, a.w, fmaf(a.z, a.z, fmaf(a.y, a.y, __fmul_rn(a.x, a.x))));
+    const float t = fmaf(b.w, b.w, fmaf(b.z, b.z, fmaf(b.y, b.y, __fmul_rn(b.x, b.x))));
+    return __fadd_rn(s, t);
+}
+
+// The q8_K block of a warp's chunk v (values 4 lane .. and 128 + 4 lane ..): the
+// arithmetic of q8K_quantize_warp, with the reductions as single instructions.
+__device__ __forceinline__ void put_q8K(uint8_t* blk, const float (&v)[8], int lane) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, top);
+    uint32_t idx = 0x7FFFFFFFu;
+    float mine = 0.0f;
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+        if ((__float_as_uint(v[i]) & 0x7FFFFFFFu) == amax) {
+            idx = 4 * lane + (i & 3) + (i < 4 ? 0 : 128);
+            mine = v[i];
+        }
+    idx = __reduce_min_sync(0xFFFFFFFFu, idx);   // the first occurrence
+    const float mx = __shfl_sync(0xFFFFFFFFu, mine, (idx & 127) >> 2);
+    int q[8];
+    float d = 0.0f;
+    if (amax != 0) {
+        const float iscale = __fdiv_rn(-128.0f, mx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = min(127, __float2int_rn(__fmul_rn(iscale, v[i])));
+        d = __fdiv_rn(1.0f, iscale);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = 0;
+    }
+    uint32_t w0, w1;
+    pack_codes8(q, w0, w1);
+    uint32_t* words = reinterpret_cast<uint32_t*>(blk);
+    words[1 + lane] = w0;
+    words[33 + lane] = w1;
+    // sums of 16 codes: four lanes each, in both halves
+    int s0 = q[0] + q[1] + q[2] + q[3], s1 = q[4] + q[5] + q[6] + q[7];
+    int both = s0 + s1 * 65536;   // both sums in one word
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
+    s0 = (int)(short)(both & 0xFFFF);
+    s1 = (both - s0) >> 16;
+    const int n0 = __shfl_down_sync(0xFFFFFFFFu, s0, 4), n1 = __shfl_down_sync(0xFFFFFFFFu, s1, 4);
+    if ((lane & 7) == 0) {   // sums 2h, 2h + 1 of each half
+        words[65 + (lane >> 3)] = ((uint32_t)s0 & 0xFFFFu) | ((uint32_t)n0 << 16);
+        words[69 + (lane >> 3)] = ((uint32_t)s1 & 0xFFFFu) | ((uint32_t)n1 << 16);
+    }
+    if (lane == 0) words[0] = __float_as_uint(d);
+}
+
+struct Row {
+    const NormArgs& A;
+    long long xo, ro, so, yo;   // the row's element offsets
+    long long r;
+    int lane;
+
+    __device__ Row(const NormArgs& a, long long row, int ln)
+        : A(a), xo(row * a.p.x_stride), ro(row * a.p.residual_stride), so(row * a.p.sum_stride), yo(row * a.p.y_stride), r(row), lane(ln) {}
+
+    // Of four values from i on, how many there are (0 or less: none)
+    __device__ __forceinline__ int left(int i) const { return (int)(A.p.k - i < 4 ? A.p.k - i : 4); }
+    // h of a half chunk, from value i on
+    __device__ __forceinline__ float4 h(int i) const {
+        const int n = left(i);
+        float4 v = load_four(A.p.x, A.p.x_type, xo + i, n, A.x4);
+        if (A.p.residual) {
+            const float4 b = load_four(A.p.residual, A.p.r_type, ro + i, n, A.r4);
+            v.x = value_rounded(v.x + b.x, A.p.r_type);
+            v.y = value_rounded(v.y + b.y, A.p.r_type);
+            v.z = value_rounded(v.z + b.z, A.p.r_type);
+            v.w = value_rounded(v.w + b.w, A.p.r_type);
+        }
+        return v;
+    }
+    __device__ __forceinline__ void keep(int i, const float4& v) const {
+        if (A.p.sum) store_four(A.p.sum, A.p.r_type, so + i, left(i), A.s4, v);
+    }
+    __device__ __forceinline__ float4 w(int i) const {
+        if (!A.p.weight) return make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+        return load_four(A.p.weight, A.p.w_type, i, left(i), A.w4);
+    }
+    // The outputs of chunk c
+    __device__ __forceinline__ void put(long long c, const float4& a, const float4& b, const float4& wa, const float4& wb, float inv) const {
+        const float v[8] = {a.x * inv * wa.x, a.y * inv * wa.y, a.z * inv * wa.z, a.w * inv * wa.w,
+                            b.x * inv * wb.x, b.y * inv * wb.y, b.z * inv * wb.z, b.w * inv * wb.w};
+        const int i = (int)(c * QK) + 4 * lane;
+        if (A.p.y) {
+            store_four(A.p.y, A.p.y_type, yo + i, left(i), A.y4, make_float4(v[0], v[1], v[2], v[3]));
+            store_four(A.p.y, A.p.y_type, yo + i + 128, left(i + 128), A.y4, make_float4(v[4], v[5], v[6], v[7]));
+        }
+        if (A.p.xq) put_q8K(static_cast<uint8_t*>(A.p.xq) + (r * (A.p.k / QK) + c) * Q8K_BYTES, v, lane);
+    }
+    __device__ __forceinline__ float inverse(float sum) const {
+        return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)A.p.k) + A.p.eps));
+    }
+};
+
+// A row per A.warps warps, NCH chunks each.
+template <int NCH>
+__global__ void __launch_bounds__(NORM_WARPS * 32) rmsnorm_kernel(const __grid_constant__ NormArgs A) {
+    __shared__ float sums[NORM_WARPS * HELD];   // of the rows' chunks
+    grid_launch_dependents();
+    grid_wait_prior();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = (int)(blockDim.x >> 5) / A.warps;
+    const int mine = warp / A.warps, part = warp - mine * A.warps, chunks = (int)((A.p.k + QK - 1) / QK);
+    const long long r = (long long)blockIdx.x * rows + mine;
+    const bool in = r < A.p.m;
+    const Row row(A, in ? r : 0, lane);
+    float4 a[NCH], b[NCH];
+    float* own = sums + mine * A.warps * NCH;
+    if (in) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const int c = part + j * A.warps, i = c * QK + 4 * lane;
+            a[j] = b[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c < chunks) {
+                a[j] = row.h(i);
+                b[j] = row.h(i + 128);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const int c = part + j * A.warps, i = c * QK + 4 * lane;
+            const float s = warp_sum(sum8(a[j], b[j]));
+            if (lane == 0) own[c] = s;   // (0 past the row)
+            if (c < chunks) {
+                row.keep(i, a[j]);
+                row.keep(i + 128, b[j]);
+            }
+        }
+    }
+    __syncthreads();
+    if (!in) return;
+    float s = lane < chunks ? own[lane] : 0.0f;
+    if (lane + 32 < chunks) s += own[lane + 32];
+    const float inv = row.inverse(warp_sum(s));
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        const int c = part + j * A.warps, i = c * QK + 4 * lane;
+        if (c < chunks) row.put(c, a[j], b[j], row.w(i), row.w(i + 128), inv);
+    }
+}
+
+// Rows too long for the registers: read twice.
+__global__ void __launch_bounds__(NORM_WARPS * 32) rmsnorm_long_kernel(const __grid_constant__ NormArgs A) {
+    __shared__ float sums[NORM_WARPS];
+    grid_launch_dependents();
+    grid_wait_prior();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Row row(A, blockIdx.x, lane);
+    const long long chunks = (A.p.k + QK - 1) / QK;
+    float s = 0.0f;
+    for (long long c = warp; c < chunks; c += NORM_WARPS) {
+        const int i = (int)(c * QK) + 4 * lane;
+        const float4 a = row.h(i), b = i + 128 < A.p.k ? row.h(i + 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        s += warp_sum(sum8(a, b));
+        row.keep(i, a);
+        if (i + 128 < A.p.k) row.keep(i + 128, b);
+    }
+    if (lane == 0) sums[warp] = s;
+    __syncthreads();
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NORM_WARPS; ++i) s += sums[i];
+    const float inv = row.inverse(s);
+    for (long long c = warp; c < chunks; c += NORM_WARPS) {
+        const int i = (int)(c * QK) + 4 * lane;
+        auto again = [&](int at) {   // the sum may have taken the place of what it is made of
+            return A.p.sum ? load_four(A.p.sum, A.p.r_type, row.so + at, row.left(at), A.s4) : row.h(at);
+        };
+        const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const bool two = i + 128 < A.p.k;
+        const float4 a = again(i), b = two ? again(i + 128) : z;
+        row.put(c, a, b, row.w(i), two ? row.w(i + 128) : z, inv);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const plm_rmsnorm_problem& p, cudaStream_t stream) {
+    NormArgs A = {};
+    A.p = p;
+    const bool even = p.k % 4 == 0;
+    auto four = [&](const void* q, long long stride, int type) { return even && four_aligned(q, p.m > 1 ? stride : 0, type); };
+    A.x4 = four(p.x, p.x_stride, p.x_type);
+    A.r4 = four(p.residual, p.residual_stride, p.r_type);
+    A.s4 = four(p.sum, p.sum_stride, p.r_type);
+    A.y4 = four(p.y, p.y_stride, p.y_type);
+    A.w4 = four(p.weight, 0, p.w_type);
+    const long long chunks = (p.k + QK - 1) / QK;
+    if (chunks > NORM_WARPS * HELD) {
+        A.warps = NORM_WARPS;
+        return launch_kernel(rmsnorm_long_kernel, dim3((unsigned)p.m), dim3(NORM_WARPS * 32), 0, stream, A);
+    }
+    // chunks a warp: few rows are spread over warps, many keep more loads of a warp in flight
+    int held = 1;
+    while (held < HELD && (chunks > NORM_WARPS * held || (chunks > held && p.m * chunks >= 16LL * num_sms() * held))) held *= 2;
+    A.warps = (int)((chunks + held - 1) / held);
+    const int rows = A.warps >= 4 ? 1 : 8 / A.warps;   // of a CTA
+    const dim3 grid((unsigned)((p.m + rows - 1) / rows)), block((unsigned)(32 * A.warps * rows));
+    if (held == 1) return launch_kernel(rmsnorm_kernel<1>, grid, block, 0, stream, A);
+    if (held == 2) return launch_kernel(rmsnorm_kernel<2>, grid, block, 0, stream, A);
+    return launch_kernel(rmsnorm_kernel<4>, grid, block, 0, stream, A);
+}
+
+}  // namespace plm

@@ -82,6 +82,34 @@ class _AttnProblem(ctypes.Structure):
                 [("scale", ctypes.c_float), ("type", ctypes.c_int32), ("o_type", ctypes.c_int32)])
 
 
+class _RmsnormProblem(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("x", "residual", "weight", "sum", "xq", "y")] +
+                [(f, ctypes.c_int64) for f in ("m", "k", "x_stride", "residual_stride", "sum_stride", "y_stride")] +
+                [("eps", ctypes.c_float)] + [(f, ctypes.c_int32) for f in ("x_type", "r_type", "w_type", "y_type")])
+
+
+class _Kv8Tensor(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("rows", "codes", "exps", "slots")] +
+                [(f, ctypes.c_int64) for f in ("heads", "row_token_stride", "row_head_stride", "page_tokens", "pages", "page_stride",
+                                               "head_stride", "token_stride", "exp_page_stride", "exp_head_stride")] +
+                [("type", ctypes.c_int32), ("rotate", ctypes.c_int32)])
+
+
+class _AttnKv8Problem(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("q", "o", "lse", "k", "v", "k_exps", "v_exps", "table", "lens", "seqs")] +
+                [(f, ctypes.c_int64) for f in ("batch", "tokens", "heads", "kv_heads", "head_dim", "q_token_stride",
+                                               "q_head_stride", "o_token_stride", "o_head_stride", "page_tokens",
+                                               "pages", "page_stride", "kv_head_stride", "kv_token_stride",
+                                               "exp_page_stride", "exp_head_stride", "table_stride", "rows",
+                                               "prefix_len", "max_len")] +
+                [("scale", ctypes.c_float), ("type", ctypes.c_int32), ("o_type", ctypes.c_int32)])
+
+
+class _SampleProblem(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("logits", "u", "temperature", "top_k", "top_p", "min_p", "tokens", "prob")] +
+                [(f, ctypes.c_int64) for f in ("m", "n", "stride")] + [("type", ctypes.c_int32)])
+
+
 _lib = None
 
 
@@ -169,7 +197,13 @@ def load(build_if_missing=True):
             ("plm_kv_copy_pages", i32, [vp, vp, vp, i64, vp]),
             ("plm_call", i32, [i32, vp]),
             ("plm_attn_workspace_size", sz, [i64] * 7),
-            ("plm_attn_shared_prefix", i32, [vp, vp, sz, vp])):
+            ("plm_attn_shared_prefix", i32, [vp, vp, sz, vp]),
+            ("plm_rmsnorm", i32, [vp, vp]),
+            ("plm_kv8_write", i32, [vp, i64, vp, vp, i64, i64, i64, i32, f32, vp]),
+            ("plm_kv8_read", i32, [vp, i64, i64, i64, vp]),
+            ("plm_attn_kv8_workspace_size", sz, [i64] * 7),
+            ("plm_attn_kv8", i32, [vp, vp, sz, vp]),
+            ("plm_sample", i32, [vp, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = res
     _lib = lib
@@ -508,9 +542,15 @@ _ATTN_PROBLEM = struct.Struct("@26qf2i4x")
 _ROPE_CALL = struct.Struct("@7qd2q")
 _RESERVE_CALL, _FORK_CALL, _FREE_CALL, _COMPACT_CALL, _COPY_CALL, _ATTN_CALL = (
     struct.Struct("@%dq" % n) for n in (8, 7, 3, 4, 4, 3))
+_RMSNORM_PROBLEM = struct.Struct("@12qf4i4x")
+_KV8_TENSOR = struct.Struct("@14q2i")
+_ATTN_KV8_PROBLEM = struct.Struct("@30qf2i4x")
+_SAMPLE_PROBLEM = struct.Struct("@11qi4x")
+_ONE, _KV8_WRITE_CALL, _KV8_READ_CALL = struct.Struct("@q"), struct.Struct("@7qdq"), struct.Struct("@4q")
 _ROPE, _RESERVE, _FORK, _FREE, _COMPACT, _COPY, _ATTN = range(7)
+_RMSNORM, _KV8_WRITE, _KV8_READ, _ATTN_KV8, _SAMPLE = range(8, 13)
 _NAMES = ("plm_rope", "plm_kv_reserve", "plm_kv_fork", "plm_kv_free", "plm_kv_compact", "plm_kv_copy_pages",
-          "plm_attn_shared_prefix")
+          "plm_attn_shared_prefix", "", "plm_rmsnorm", "plm_kv8_write", "plm_kv8_read", "plm_attn_kv8", "plm_sample")
 
 
 def _call(entry, args):
@@ -659,3 +699,188 @@ def plm_attn_shared_prefix(q, o, k, v, table, lens, tokens, prefix_len, max_len,
                            _ints(seqs, 32, "seqs", (batch,)) or 0, batch, tokens, heads, kv_heads, d, qt, qh, ot, oh,
                            page_tokens, pages, kp, kh, kt, width, rows, prefix_len, max_len, scale, ktype, otype)
     _call(_ATTN, _ATTN_CALL.pack(ws, size, _stream(stream)) + p)
+
+
+# ---------------------------------------------------------------------------
+# The residual sum and norm before a product, a cache in 8 bits and the
+# attention over it, the next token.
+# ---------------------------------------------------------------------------
+def _matrix(t, name, shape=None):
+    """Row stride and type of a CUDA tensor [m][k] with dense rows."""
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1 or not t.is_cuda:
+        _rows(t, name, 2)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return st[0], _types[t.dtype] if _types.get(t.dtype, -1) >= 0 else _type(t)
+
+
+def plm_rmsnorm(x, weight, eps, residual=None, sum=None, xq=None, y=None, stream=None):
+    """h = x + residual (into sum if given, of the residual's type; sum may be x or residual); h / sqrt(mean h^2 + eps) *
+    weight into xq as q8_K blocks (contiguous bytes) and / or into y; x [m][k], weight [k] or None (see include/plm.h)."""
+    shape = x.shape
+    xs, xt = _matrix(x, "x")
+    m, k = shape
+    rs = rt = ss = ys = yt = wt = st = 0
+    r = w = o = b = yo = 0
+    if residual is not None:
+        rs, rt = _matrix(residual, "residual", shape)
+        r = residual.data_ptr()
+    if sum is not None:
+        ss, st = _matrix(sum, "sum", shape)
+        if residual is None or st != rt:
+            raise ValueError("sum: there is none without a residual, and it has the residual's type")
+        o = sum.data_ptr()
+    if weight is not None:
+        if weight.shape != (k,):
+            raise ValueError("weight: expected shape (%d,), got %s" % (k, tuple(weight.shape)))
+        w, wt = _addr(weight), _type(weight)
+    if xq is not None:
+        if xq.nbytes != m * (k // QK) * Q8K_BYTES:
+            raise ValueError("xq: expected %d bytes, got %d" % (m * (k // QK) * Q8K_BYTES, xq.nbytes))
+        b = _addr(xq)
+    if y is not None:
+        ys, yt = _matrix(y, "y", shape)
+        yo = y.data_ptr()
+    if m == 0:
+        return
+    _call(_RMSNORM, _ONE.pack(_stream(stream)) + _RMSNORM_PROBLEM.pack(x.data_ptr(), r, w, o, b, yo, m, k, xs, rs, ss, ys, eps, xt, rt, wt, yt))
+
+
+def plm_kv8_page_bytes(kv_heads, page_tokens, head_dim):
+    """Bytes of a page of plm_kv8_views: keys and values, codes and exponents."""
+    return 2 * kv_heads * page_tokens * (head_dim + head_dim // 32)
+
+
+def plm_kv8_views(pool, kv_heads, page_tokens, head_dim):
+    """(k, v, k_exps, v_exps) of a pool uint8 [pages][page bytes]: codes int8 [pages][kv_heads][page_tokens][head_dim],
+    exponents uint8 [pages][kv_heads][page_tokens][head_dim / 32].  A page holds the keys' codes, the values' codes, then the
+    exponents of both, so that the page calls (plm_kv_state over the same pool) move them together."""
+    import torch
+    n, size = kv_heads * page_tokens * head_dim, plm_kv8_page_bytes(kv_heads, page_tokens, head_dim)
+    if head_dim % 32 or pool.dim() != 2 or pool.shape[1] < size or pool.dtype != torch.uint8 or pool.stride(1) != 1:
+        raise ValueError("pool: expected uint8 [.][%d or more], and heads of a multiple of 32" % size)
+    e, pitch, at = n // 32, pool.stride(0), pool.storage_offset()
+    cs, es = (pitch, page_tokens * head_dim, head_dim, 1), (pitch, page_tokens * (head_dim // 32), head_dim // 32, 1)
+    pages, codes = pool.shape[0], pool.view(torch.int8)
+    code = lambda o: codes.as_strided((pages, kv_heads, page_tokens, head_dim), cs, at + o)  # noqa: E731
+    exps = lambda o: pool.as_strided((pages, kv_heads, page_tokens, head_dim // 32), es, at + o)  # noqa: E731
+    return code(0), code(n), exps(2 * n), exps(2 * n + e)
+
+
+def _kv8_pages(codes, exps, name):
+    """Strides of 8-bit pages: of the codes, and the exponents' first two."""
+    import torch
+    if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
+        raise ValueError("%s: expected int8 codes and uint8 exponents" % name)
+    cs, es = _rows(codes, name, 4), _rows(exps, name + " exponents", 4)
+    blocks = codes.shape[3] // 32
+    if codes.shape[3] % 32 or exps.shape != codes.shape[:3] + (blocks,) or (es[2] != blocks and codes.shape[2] > 1):
+        raise ValueError("%s: expected exponents [pages][heads][page_tokens][head_dim / 32], a head's tokens dense" % name)
+    return cs, es
+
+
+def plm_kv8_tensor(rows, codes, exps, slots, rotate=True):
+    """One tensor of a plm_kv8_write or plm_kv8_read call; it holds the tensors.  rows [tokens][heads][head_dim], codes and
+    exps as plm_kv8_views gives them (any strided views), slots int64 [tokens]."""
+    rt, rh, _ = _rows(rows, "rows", 3)
+    cs, es = _kv8_pages(codes, exps, "codes")
+    tokens, heads, d = rows.shape
+    pages, cheads, page_tokens, cd = codes.shape
+    if cheads != heads or cd != d:
+        raise ValueError("codes: expected pages [.][%d][.][%d], got %s" % (heads, d, tuple(codes.shape)))
+    return (_KV8_TENSOR.pack(rows.data_ptr(), codes.data_ptr(), exps.data_ptr(), _ints(slots, 64, "slots", (tokens,)), heads, rt, rh,
+                             page_tokens, pages, cs[0], cs[1], cs[2], es[0], es[1], _type(rows), 1 if rotate else 0),
+            tokens, d, (rows, codes, exps, slots), rotate)
+
+
+def _kv8_join(tensors):
+    if not tensors:
+        raise ValueError("no tensors")
+    tokens, d = tensors[0][1:3]
+    for t in tensors:
+        if t[1] != tokens or t[2] != d:
+            raise ValueError("the tensors differ in tokens or head size")
+    return b"".join([t[0] for t in tensors]), tokens, d
+
+
+def plm_kv8_write(tensors, positions=None, freqs=None, rotary_dim=0, layout="half", scale=1.0, stream=None):
+    """Writes the tensors' rows (plm_kv8_tensor) to their slots in 8 bits, those with rotate turned by their positions
+    (int32 [tokens]) first; see include/plm.h."""
+    packed, tokens, d = _kv8_join(tensors)
+    if any(t[4] for t in tensors) and (positions is None or freqs is None or freqs.numel() != rotary_dim // 2):
+        raise ValueError("a tensor that rotates needs positions, and %d frequencies" % (rotary_dim // 2))
+    if tokens == 0:
+        return
+    _call(_KV8_WRITE, _KV8_WRITE_CALL.pack(len(tensors), _ints(positions, 32, "positions", (tokens,)) or 0, _ints(freqs, 64, "freqs") or 0,
+                                           tokens, d, rotary_dim, _LAYOUTS.get(layout, layout), scale, _stream(stream)) + packed)
+
+
+def plm_kv8_read(tensors, stream=None):
+    """Reads the tensors' slots (plm_kv8_tensor) into their rows; a slot out of range reads as zeros."""
+    packed, tokens, d = _kv8_join(tensors)
+    if tokens == 0:
+        return
+    _call(_KV8_READ, _KV8_READ_CALL.pack(len(tensors), tokens, d, _stream(stream)) + packed)
+
+
+def plm_attn_kv8_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len):
+    """Workspace bytes of plm_attn_kv8 (0: none needed, or invalid arguments)."""
+    return load().plm_attn_kv8_workspace_size(batch, tokens, heads, kv_heads, head_dim, prefix_len, max_len)
+
+
+def plm_attn_kv8(q, o, k, v, k_exps, v_exps, table, lens, tokens, prefix_len, max_len, scale, workspace, lse=None, seqs=None,
+                 stream=None):
+    """plm_attn_shared_prefix over 8-bit pages (plm_kv8_views, or strided views like them); see include/plm.h."""
+    shape, kshape = q.shape, k.shape
+    (qt, qh, _), (ot, oh, _) = _rows(q, "q", 3), _rows(o, "o", 3)
+    cs, es = _kv8_pages(k, k_exps, "k")
+    if o.shape != shape:
+        raise ValueError("o: expected shape %s, got %s" % (tuple(shape), tuple(o.shape)))
+    if (v.shape != kshape or v.stride() != cs or v.dtype != k.dtype or v_exps.shape != k_exps.shape or v_exps.stride() != es or
+            v_exps.dtype != k_exps.dtype or not (v.is_cuda and v_exps.is_cuda)):
+        raise ValueError("keys and values have to agree in shapes, strides and types")
+    n, heads, d = shape
+    pages, kv_heads, page_tokens, kd = kshape
+    if kd != d:
+        raise ValueError("k: expected heads of %d, got %d" % (d, kd))
+    if tokens < 1 or n % tokens:
+        raise ValueError("q: %d rows are no multiple of %d tokens" % (n, tokens))
+    rows, width = table.shape
+    batch = n // tokens
+    if seqs is None and batch > rows:
+        raise ValueError("table: %d rows for a batch of %d" % (rows, batch))
+    if lse is not None and (_type(lse) != PLM_F32 or lse.shape != (n, heads)):
+        raise ValueError("lse: expected float32 %s" % ((n, heads),))
+    if batch == 0:
+        return
+    ws, size = _ws(workspace)
+    p = _ATTN_KV8_PROBLEM.pack(q.data_ptr(), o.data_ptr(), _addr(lse) or 0, k.data_ptr(), v.data_ptr(), k_exps.data_ptr(),
+                               v_exps.data_ptr(), _ints(table, 32, "table"), _ints(lens, 32, "lens", (rows,)),
+                               _ints(seqs, 32, "seqs", (batch,)) or 0, batch, tokens, heads, kv_heads, d, qt, qh, ot, oh,
+                               page_tokens, pages, cs[0], cs[1], cs[2], es[0], es[1], width, rows, prefix_len, max_len, scale,
+                               _type(q), _type(o))
+    _call(_ATTN_KV8, _ATTN_CALL.pack(ws, size, _stream(stream)) + p)
+
+
+def _per_row(t, name, m, code):
+    """Address of one value a row on the device, or 0."""
+    if t is None:
+        return 0
+    if t.shape != (m,) or (_type(t) if code == PLM_F32 else code) != code:
+        raise ValueError("%s: expected float32 (%d,), got %s %s" % (name, m, t.dtype, tuple(t.shape)))
+    return _addr(t)
+
+
+def plm_sample(logits, tokens, u=None, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, stream=None):
+    """tokens (int32 [m]) = the next token of each row of logits [m][n] by the row's random number u in 0 .. 1 (None:
+    the largest logit) and what else is given, all [m] on the device, top_k int32, the others float32; prob gets the
+    probability with which it was met (see include/plm.h)."""
+    stride, code = _matrix(logits, "logits")
+    m, n = logits.shape
+    f = [_per_row(t, name, m, PLM_F32) for t, name in ((u, "u"), (temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (prob, "prob"))]
+    k, out = _ints(top_k, 32, "top_k", (m,)) or 0, _ints(tokens, 32, "tokens", (m,))
+    if m == 0:
+        return
+    _call(_SAMPLE, _ONE.pack(_stream(stream)) +
+          _SAMPLE_PROBLEM.pack(logits.data_ptr(), f[0], f[1], k, f[2], f[3], out, f[4], m, n, stride, code))
