@@ -11,15 +11,14 @@
 //   A border (the k-th largest logit; the one at which the sum of the w's in
 // descending order reaches p of all) is found without sorting the row: f is the
 // bin of a histogram, which says in which bins the border lies.  If few logits lie
-// from there upwards they are sorted and everything is decided among them (the
-// rule for top-k).  Else the logits of the border's bin are, and the sum of those
-// above it is formed exactly (a top-p of flat rows).  Where neither applies the
-// bins are cut again by the logits' bits until a bin is a single value.
+// from there upwards they are put in order and everything is decided among them
+// (the rule for top-k).  Else the logits of the border's bin are, and the sum of
+// those above it is formed exactly (a top-p of flat rows).  Where neither applies
+// the bins are cut again by the logits' bits until a bin is a single value.
 //
-// Layout.  A cluster of CTAs takes a row, each a piece of it in shared memory as
-// integers that order as the logits do; so the row is read once.  What does not
-// fit is read again from L2.  A warp has consecutive logits, so the sums of the
-// warps say in which of them the token is.
+// Layout.  A cluster of CTAs takes a row, each a piece of it in shared memory, so
+// the row is read once.  What does not fit is read again from L2.  A warp has
+// consecutive logits, so the sums of the warps say in which of them the token is.
 #include "plm_device.cuh"
 #include "plm_internal.h"
 #include "values.cuh"
@@ -30,11 +29,13 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int MOST_THREADS = 1024, MOST_WARPS = MOST_THREADS / 32;
+constexpr int MOST_THREADS = 1024, MOST_WARPS = MOST_THREADS / 32;   // of a CTA; 512 at least
 constexpr int BINS = 2560;                   // f of a logit with a weight: t below 40
-constexpr int LIST = 1024;                   // logits that are sorted at most
+constexpr int COARSE = 16, GROUPS = BINS / COARSE;   // bins that are first looked at together
+constexpr int LIST = 1024;                   // logits that are put in order at most
+constexpr int BUCKETS = 512;
 constexpr int MOST_CS = 8;                   // CTAs of a row at most
-constexpr uint32_t LOWEST = 0x007FFFFFu;     // the key of -inf; 0: no logit
+constexpr uint32_t LOWEST = 0x007FFFFFu;     // the key of -inf
 constexpr float MAGIC = 12582912.0f;         // 1.5 2^23: adding it rounds to a whole number
 
 struct SampleArgs {
@@ -43,65 +44,70 @@ struct SampleArgs {
     bool four;                               // rows in accesses of four
 };
 
-// 2^(40 - i/64)
+// 2^(40 - i/64), less 2^-41 of it, so that all are below 2^40
 __device__ const u64 EXP_TABLE[64] = {
-    0x10000000000ULL, 0x0FD3E0C0CF5ULL, 0x0FA83B2DB72ULL, 0x0F7D0DF730BULL, 0x0F5257D1525ULL, 0x0F281773C5AULL,
-    0x0EFE4B99BDDULL, 0x0ED4F301EDAULL, 0x0EAC0C6E7DDULL, 0x0E8396A503CULL, 0x0E5B906E77DULL, 0x0E33F8972BFULL,
-    0x0E0CCDEEC2BULL, 0x0DE60F4825EULL, 0x0DBFBB797DBULL, 0x0D99D15C279ULL, 0x0D744FCCAD7ULL, 0x0D4F35AABD0ULL,
-    0x0D2A81D91F1ULL, 0x0D06333DAEFULL, 0x0CE248C1520ULL, 0x0CBEC14FEF2ULL, 0x0C9B9BD866EULL, 0x0C78D74C8ACULL,
-    0x0C5672A1155ULL, 0x0C346CCDA25ULL, 0x0C12C4CCA66ULL, 0x0BF1799B67AULL, 0x0BD08A39F58ULL, 0x0BAFF5AB213ULL,
-    0x0B8FBAF4763ULL, 0x0B6FD91E329ULL, 0x0B504F333FAULL, 0x0B311C412A9ULL, 0x0B123F581D3ULL, 0x0AF3B78AD69ULL,
-    0x0AD583EEA43ULL, 0x0AB7A39B5A9ULL, 0x0A9A15AB4EAULL, 0x0A7CD93B4E9ULL, 0x0A5FED6A9B1ULL, 0x0A43515AE0AULL,
-    0x0A27043030CULL, 0x0A0B0510FB9ULL, 0x09EF5326092ULL, 0x09D3ED9A72DULL, 0x09B8D39B9D5ULL, 0x099E0459321ULL,
-    0x09837F0518EULL, 0x096942D3720ULL, 0x094F4EFA8FFULL, 0x0935A2B2F14ULL, 0x091C3D373ABULL, 0x09031DC4314ULL,
-    0x08EA4398B46ULL, 0x08D1ADF5B7EULL, 0x08B95C1E3EBULL, 0x08A14D57549ULL, 0x088980E8093ULL, 0x0871F61969FULL,
-    0x085AAC367CCULL, 0x0843A28C3ADULL, 0x082CD8698ACULL, 0x08164D1F3BCULL,
+    0xFFFFFFFFFFull, 0xFD3E0C0CF4ull, 0xFA83B2DB71ull, 0xF7D0DF730Aull, 0xF5257D1524ull, 0xF281773C59ull,
+    0xEFE4B99BDCull, 0xED4F301ED9ull, 0xEAC0C6E7DCull, 0xE8396A503Bull, 0xE5B906E77Cull, 0xE33F8972BEull,
+    0xE0CCDEEC2Aull, 0xDE60F4825Dull, 0xDBFBB797DAull, 0xD99D15C278ull, 0xD744FCCAD6ull, 0xD4F35AABCFull,
+    0xD2A81D91F0ull, 0xD06333DAEEull, 0xCE248C151Full, 0xCBEC14FEF2ull, 0xC9B9BD866Dull, 0xC78D74C8ABull,
+    0xC5672A1154ull, 0xC346CCDA24ull, 0xC12C4CCA66ull, 0xBF1799B67Aull, 0xBD08A39F57ull, 0xBAFF5AB212ull,
+    0xB8FBAF4762ull, 0xB6FD91E328ull, 0xB504F333F9ull, 0xB311C412A8ull, 0xB123F581D2ull, 0xAF3B78AD68ull,
+    0xAD583EEA42ull, 0xAB7A39B5A8ull, 0xA9A15AB4EAull, 0xA7CD93B4E9ull, 0xA5FED6A9B0ull, 0xA43515AE09ull,
+    0xA27043030Bull, 0xA0B0510FB9ull, 0x9EF5326091ull, 0x9D3ED9A72Cull, 0x9B8D39B9D5ull, 0x99E0459320ull,
+    0x9837F0518Dull, 0x96942D371Full, 0x94F4EFA8FEull, 0x935A2B2F13ull, 0x91C3D373AAull, 0x9031DC4314ull,
+    0x8EA4398B45ull, 0x8D1ADF5B7Eull, 0x8B95C1E3EAull, 0x8A14D57549ull, 0x88980E8092ull, 0x871F61969Eull,
+    0x85AAC367CCull, 0x843A28C3ACull, 0x82CD8698ABull, 0x8164D1F3BBull,
 };
 
-// Logits as integers in their order; NaN is -inf, -0 is 0.
+// Logits as integers in their order, and back.
 __device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return x != x ? LOWEST : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+    const uint32_t b = __float_as_uint(x);
+    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float logit_of(uint32_t key) {   // of 0: NaN
-    return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
+__device__ __forceinline__ float logit_of(uint32_t key) {
+    return __uint_as_float(key ^ ((uint32_t)((int)~key >> 31) | 0x80000000u));
 }
+__device__ __forceinline__ float nothing() { return __uint_as_float(0x7FFFFFFFu); }   // NaN: no logit
 
 struct alignas(16) SampleSmem {
-    u64 table[64];
+    u64 table[64][16];                           // a copy for every pair of banks
     u64 part[2][MOST_WARPS], slot[2][MOST_CS];   // of an exchange, in turn
-    u64 own[MOST_WARPS];                         // the warps' sums of kept w's
+    u64 own[2][MOST_WARPS];                      // the warps' sums, in turn
     u64 scan[2][MOST_WARPS];
     u64 sums[MOST_CS * MOST_WARPS];              // the same of all warps of the row
+    u64 group_sum[GROUPS];                       // of the row's logits, by the bins' middles
     u64 found_sum;
+    uint32_t group[GROUPS];                      // the row's logits
+    uint32_t near[MOST_CS][32];                  // of a group's bins and those beside it, by CTA
     uint32_t found[8];
     int listed;                                  // logits in `list`
-    alignas(16) uint32_t hist[BINS];
-    u64 list[LIST], sorted[LIST];                // key, and the index's complement below
+    union {
+        alignas(16) uint32_t hist[BINS];
+        struct {
+            u64 sorted[LIST];                    // key, and the index's complement below
+            uint32_t bucket[BUCKETS];
+        };
+    };
+    u64 list[LIST];
 };
 
+// (in parts whose sums fit 32 bits: an instruction each)
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+    const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)v & 0x7FFFFFFu);
+    const uint32_t b = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(v >> 27) & 0x7FFFFFFu);
+    const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(v >> 54));
+    return a + ((u64)b << 27) + ((u64)c << 54);
 }
-__device__ __forceinline__ u64 warp_max64(u64 v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const u64 w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = w > v ? w : v;
-    }
-    return v;
-}
-__device__ __forceinline__ u64 warp_scan64(u64 v, int lane) {   // inclusive
+template <class T> __device__ __forceinline__ T warp_scan(T v, int lane) {   // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const u64 w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        const T w = __shfl_up_sync(0xFFFFFFFFu, v, o);
         if (lane >= o) v += w;
     }
     return v;
 }
 
+// Shared memory of CTA z of the cluster.
 __device__ __forceinline__ uint32_t at_peer(const void* p, int z) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(z));
@@ -112,21 +118,27 @@ __device__ __forceinline__ u64 peer64(const u64* p, int z) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at_peer(p, z)) : "memory");
     return v;
 }
-__device__ __forceinline__ void to_peer64(u64* p, int z, u64 v) {
-    asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at_peer(p, z)), "l"(v) : "memory");
+__device__ __forceinline__ uint32_t peer32(const void* p, int z) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at_peer(p, z)) : "memory");
+    return v;
 }
 __device__ __forceinline__ uint4 peer128(const uint32_t* p, int z) {
     uint4 v;
     asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at_peer(p, z)) : "memory");
     return v;
 }
-__device__ __forceinline__ int peer_int(const int* p, int z) {
-    int v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at_peer(p, z)) : "memory");
-    return v;
+__device__ __forceinline__ void to_peer64(u64* p, int z, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at_peer(p, z)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void add_at_peer(u64* p, int z, u64 v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" :: "r"(at_peer(p, z)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void add_at_peer(uint32_t* p, int z, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" :: "r"(at_peer(p, z)), "r"(v) : "memory");
 }
 
-// v part of 1: floor and ceiling of v a for 0 <= a < 1 (f32), v below 2^63.
+// Floor and ceiling of v a for 0 <= a < 1, v below 2^63.
 __device__ __forceinline__ u64 share_of(u64 v, float a, bool up) {
     const uint32_t b = __float_as_uint(a);
     const int e = (int)(b >> 23);                       // a = m 2^(e - 150)
@@ -146,41 +158,56 @@ __device__ __forceinline__ u64 share_of(u64 v, float a, bool up) {
     }
     return q + (up && rest);
 }
+// w / all, w <= all: the f32 quotient, corrected once.
+__device__ __forceinline__ float quotient(u64 w, u64 all) {
+    const float w1 = __ull2float_rn(w), w2 = __ll2float_rn((long long)(w - (u64)w1));
+    const float a1 = __ull2float_rn(all), a2 = __ll2float_rn((long long)(all - (u64)a1));
+    const float q = __fdiv_rn(w1, a1), rest = fmaf(-q, a1, w1) + fmaf(-q, a2, w2);
+    return q + __fdiv_rn(rest, a1);
+}
 
 // A row as one CTA of its cluster sees it.
 struct Sampler {
     const SampleArgs& A;
     SampleSmem& sm;
-    uint32_t* keys;             // of this warp's logits, the first `held`
+    float* held;                // this warp's logits, the first A.held
     long long row;
-    int lane, warp, nw, nt, cs, rank, first, turn;   // first: index of the warp's first logit
-    uint32_t kmax;
+    int lane, warp, nw, nt, cs, rank, first;         // first: index of the warp's first logit
+    int turn, owned;
+    float top, u;
     float base, c_hi, c_lo, ref, ref64;              // t = ref - (x - base) (c_hi + c_lo)
-    bool infinite;                                   // the largest logits are +inf: they are 0, the others no logits
+    bool infinite;                                   // the largest logits are +inf: they are 0, the others nothing
 
-    // Four logits from index i on, as keys
-    __device__ __forceinline__ uint4 load(int i) const {
+    // Four logits from index i on; -0 becomes 0
+    __device__ __forceinline__ float4 load(int i) const {
         const long long n = A.p.n - i;
-        const float4 v = load_four(A.p.logits, A.p.type, row * A.p.stride + i, n < 4 ? (int)n : 4, A.four && n >= 4);
-        return make_uint4(n > 0 ? key_of(v.x) : 0, n > 1 ? key_of(v.y) : 0, n > 2 ? key_of(v.z) : 0, n > 3 ? key_of(v.w) : 0);
+        float4 v = load_four(A.p.logits, A.p.type, row * A.p.stride + i, n < 4 ? (int)n : 4, A.four && n >= 4);
+        v.x = n > 0 ? v.x + 0.0f : nothing();
+        v.y = n > 1 ? v.y + 0.0f : nothing();
+        v.z = n > 2 ? v.z + 0.0f : nothing();
+        v.w = n > 3 ? v.w + 0.0f : nothing();
+        return v;
     }
-    __device__ __forceinline__ uint32_t finite(uint32_t k) const { return k == key_of(INFINITY) ? key_of(0.0f) : 0; }
-    // The lane's four of the warp's 128 from place i on
-    __device__ __forceinline__ uint4 four(int i) const {
-        if (i < A.held) return *reinterpret_cast<const uint4*>(keys + i + 4 * lane);
-        uint4 k = load(first + i + 4 * lane);
-        if (infinite) k = make_uint4(finite(k.x), finite(k.y), finite(k.z), finite(k.w));
-        return k;
+    __device__ __forceinline__ float finite(float x) const { return x == INFINITY ? 0.0f : nothing(); }
+    // The lane's four of a warp's 128 from place i on; that warp's first logit has index `from`
+    __device__ __forceinline__ float4 four(const float* theirs, int from, int i) const {
+        if (i < A.held) return *reinterpret_cast<const float4*>(theirs + i + 4 * lane);
+        float4 v = load(from + i + 4 * lane);
+        if (infinite) v = make_float4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
+        return v;
     }
+    __device__ __forceinline__ int length(int from) const { return (int)min((long long)A.seg, (long long)A.p.n - from); }
+    // f(logit, index) of all of this warp's
     template <class F> __device__ __forceinline__ void each(F f) const {
-        const int end = (int)min((long long)A.seg, (long long)A.p.n - first);
+        const int end = length(first);
 #pragma unroll 2
         for (int i = 0; i < end; i += 128) {
-            const uint4 k = four(i);
-            f(k.x, i + 4 * lane);
-            f(k.y, i + 4 * lane + 1);
-            f(k.z, i + 4 * lane + 2);
-            f(k.w, i + 4 * lane + 3);
+            const float4 v = four(held, first, i);
+            const int j = first + i + 4 * lane;
+            f(v.x, j);
+            f(v.y, j + 1);
+            f(v.z, j + 2);
+            f(v.w, j + 3);
         }
     }
     __device__ __forceinline__ void together() const {
@@ -189,74 +216,398 @@ struct Sampler {
         else __syncthreads();
     }
 
-    // 64 t rounded, MAGIC added: its bits count in steps of 1.  No less for a smaller logit.
+    // 64 t rounded, MAGIC added: its bits count in steps of 1.  No less for a smaller
+    // logit; NaN for none.  (x: less base; p: times c_hi)
     __device__ __forceinline__ float steps(float p) const { return fmaf(p, -64.0f, ref64); }
-    __device__ __forceinline__ float product(uint32_t k) const { return (logit_of(k) - base) * c_hi; }
     __device__ __forceinline__ bool weighs(float s) const { return s < MAGIC + (float)BINS; }   // (false for NaN)
-    __device__ __forceinline__ int bin(uint32_t k) const {   // BINS where there is no weight
-        const float s = steps(product(k));
-        return weighs(s) ? (int)(__float_as_uint(s) - __float_as_uint(MAGIC)) : BINS;
+    __device__ __forceinline__ int bin_of(float s) const { return (int)(__float_as_uint(s) - __float_as_uint(MAGIC)); }
+    __device__ __forceinline__ int bin(float x) const {   // BINS where there is no weight
+        const float s = steps((x - base) * c_hi);
+        return weighs(s) ? bin_of(s) : BINS;
     }
     // 2^(40 - f/64 - r)
     __device__ __forceinline__ u64 power(uint32_t f, float r) const {
-        const float e = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);   // 2^-r - 1
-        const u64 v = sm.table[f & 63];
-        // v e in steps of 2^11: below 2^22 of them
-        const float s = fmaf((float)(uint32_t)(v >> 17) * 64.0f, e, MAGIC);
-        return (v + (u64)((long long)(int)(__float_as_uint(s) - __float_as_uint(MAGIC)) * 2048)) >> (f >> 6);
+        const float e = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);   // 2^-r - 1, below 2^-7
+        const u64 v = sm.table[f & 63][lane & 15];
+        // v e in steps of 2^11, with v's 24 leading bits: v / 2^11 as f32
+        const float lead = __uint_as_float(((uint32_t)(v >> 16) & 0x7FFFFFu) | (uint32_t)(127 + 28) << 23);
+        const int more = bin_of(fmaf(lead, e, MAGIC));
+        return (v + (u64)((long long)more * 2048)) >> (f >> 6);
     }
-    __device__ __forceinline__ u64 weight(uint32_t k) const {   // 0 where there is none
-        const float x = logit_of(k) - base, p = x * c_hi, s = steps(p);
-        if (!weighs(s)) return 0;
+    __device__ __forceinline__ u64 middle(int f) const { return sm.table[f & 63][lane & 15] >> (f >> 6); }
+    __device__ __forceinline__ u64 weight(float x, float p, float s) const {
         const float y = fmaf(s - MAGIC, -0.015625f, ref);       // ref - f/64, exact
         const float r = fmaf(x, -c_lo, (y - p) - fmaf(x, c_hi, -p));
-        return power(__float_as_uint(s) - __float_as_uint(MAGIC), r);
+        return power(bin_of(s), r);
+    }
+    __device__ __forceinline__ u64 weight(float logit) const {   // 0 where there is none
+        const float x = logit - base, p = x * c_hi, s = steps(p);
+        return weighs(s) ? weight(x, p, s) : 0;
     }
 
-    // Sum or maximum of the threads' v over the row.
+    // Sum, or maximum (of 32 bits), of the threads' v over the row.
     template <bool MAX> __device__ u64 exchange(u64 v) {
         const int b = turn & 1;
         ++turn;
-        v = MAX ? warp_max64(v) : warp_sum64(v);
+        auto warps = [](u64 x) { return MAX ? (u64)__reduce_max_sync(0xFFFFFFFFu, (uint32_t)x) : warp_sum64(x); };
+        v = warps(v);
         if (lane == 0) sm.part[b][warp] = v;
         __syncthreads();
-        if (cs == 1 || warp == 0) {
-            v = lane < nw ? sm.part[b][lane] : 0;
-            v = MAX ? warp_max64(v) : warp_sum64(v);
-        }
+        if (cs == 1 || warp == 0) v = warps(lane < nw ? sm.part[b][lane] : 0);
         if (cs == 1) return v;
         if (warp == 0 && lane < cs) to_peer64(&sm.slot[b][rank], lane, v);
         together();
-        v = lane < cs ? sm.slot[b][lane] : 0;
-        return MAX ? warp_max64(v) : warp_sum64(v);
+        return warps(lane < cs ? sm.slot[b][lane] : 0);
+    }
+    // Exclusive sum of the threads' value over the CTA, and the sum of all.
+    __device__ __forceinline__ u64 block_scan(u64 v, u64& all) {
+        const u64 in = warp_scan(v, lane);
+        __syncthreads();   // (what was there has been read)
+        if (lane == 31) sm.scan[0][warp] = in;
+        __syncthreads();
+        const u64 x = lane < nw ? sm.scan[0][lane] : 0;
+        all = warp_sum64(x);
+        return in - v + warp_sum64(lane < warp ? x : 0);
     }
 
-    // The largest (up) or smallest key in [lo, hi] whose bin is >= b (<= b), of
-    // which there is one: the bins fall as the keys rise.  A lane tries a key each.
-    __device__ uint32_t edge(int b, uint32_t lo, uint32_t hi, bool up) const {
-        while (lo < hi) {
-            const uint32_t step = (hi - lo) / 32 + 1, off = step * lane;   // (below 2^32)
-            const bool in = off <= hi - lo;
-            const uint32_t k = up ? hi - off : lo + off;
-            const unsigned yes = __ballot_sync(0xFFFFFFFFu, in && (up ? bin(k) >= b : bin(k) <= b));
-            const int first_yes = __ffs(yes) - 1;
-            // the one looked for lies at that key, or between it and the one tried before
-            if (first_yes < 0) {   // beyond the last key tried
-                const uint32_t far = (hi - lo) / step * step;
-                if (up) hi -= far;
-                else lo += far;
-                if (step == 1) break;
-            } else {
-                const uint32_t at = step * first_yes, before = first_yes ? at - step + 1 : 0;
-                const uint32_t a = up ? hi - at : lo + before, z = up ? hi - before : lo + at;
-                lo = a;
-                hi = z;
-                if (first_yes == 0) return up ? hi : lo;
-            }
+    // The key of the largest logit whose bin is >= b (the bins fall as the keys
+    // rise), b <= BINS.  It lies close to where f32 arithmetic puts it; a lane tries
+    // a key each.
+    __device__ uint32_t up_to(int b) const {
+        if (bin(top) >= b) return key_of(top);
+        uint32_t lo = LOWEST, hi = key_of(top);      // it is lo or above, and below hi
+        auto reaches = [&](uint32_t k) { return bin(logit_of(k)) >= b; };
+        const uint32_t guess = min(max(key_of(base + (ref - ((float)b - 0.5f) * 0.015625f) / c_hi), LOWEST + 32), 0xFF800000u);
+        const uint32_t k = guess + 15 - lane;
+        int yes = __ffs(__ballot_sync(0xFFFFFFFFu, k < hi && reaches(k))) - 1;
+        if (guess < hi) {
+            if (yes > 0) return guess + 15 - yes;
+            if (yes == 0) lo = guess + 15;
+            else hi = guess - 16;
+        }
+        while (hi - lo > 1) {
+            const uint32_t far = hi - lo, step = (far + 31) / 32, off = step * (lane + 1);   // (far < 2^32 - 2^23)
+            yes = __ffs(__ballot_sync(0xFFFFFFFFu, off >= far || reaches(hi - off))) - 1;
+            const uint32_t z = hi - step * yes;
+            lo = (uint32_t)(max((u64)lo + step, (u64)z) - step);
+            hi = z;
         }
         return lo;
     }
 
+    // Adds the histogram's bins up in groups, at every CTA (complete after a barrier).
+    __device__ __forceinline__ void add_groups(bool sum) {
+        __syncthreads();
+        for (int at = 0; at < BINS; at += 4 * nt) {   // four bins a thread, a group in four lanes
+            const int b = at + 4 * (int)threadIdx.x;
+            if (b >= BINS) break;                     // (whole warps)
+            const uint4 c = *reinterpret_cast<const uint4*>(sm.hist + b);
+            uint32_t n = c.x + c.y + c.z + c.w;
+            u64 v = 0;
+            if (sum && n) v = c.x * middle(b) + c.y * middle(b + 1) + c.z * middle(b + 2) + c.w * middle(b + 3);
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+                if (sum) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            }
+            for (int z = lane & 3; n && z < cs; z += 4)   // (a lane of the group for every fourth CTA)
+                if (cs == 1) {
+                    sm.group[b / COARSE] = n;
+                    sm.group_sum[b / COARSE] = v;
+                } else {
+                    add_at_peer(&sm.group[b / COARSE], z, n);
+                    if (sum) add_at_peer(&sm.group_sum[b / COARSE], z, v);
+                }
+        }
+    }
+    // Where the histogram has the border (by the bins' middles, for sums): its bin (BINS:
+    // nowhere), the logits down to it and in it, and in its neighbours; for warp 0.
+    struct Place { int b; uint32_t live, down_to, there, above, below; };
+    // For sums the border may be some bins off, the more so the fewer logits have most of
+    // the sum (a bin's w's are up to 2^(1/128) off its middle).  So the list takes in groups of bins
+    // around, as far as they fit: `wide` not from the top.  False: nothing fits.
+    __device__ bool window(const Place& P, int& first_bin, int& last_bin, bool& wide) const {
+        constexpr int AROUND = 8;
+        const int g = P.b / COARSE;
+        // lanes 0 .. 7: groups g + lane + 1 and what is down to them; lanes 8 .. 15: g - 1 - (lane - 8)
+        const int mine = lane < AROUND ? g + 1 + lane : g - 1 - (lane - AROUND);
+        const uint32_t n = lane < 2 * AROUND && mine >= 0 && mine < GROUPS ? sm.group[mine] : 0;
+        const uint32_t in = warp_scan(n, lane), up = in - __shfl_sync(0xFFFFFFFFu, in, AROUND - 1);   // of each side, to the lane
+        uint32_t to_end = 0;   // from the border's bin to its group's end
+        for (int i = lane; i < GROUPS; i += 32) to_end += i <= g ? sm.group[i] : 0;
+        to_end = __reduce_add_sync(0xFFFFFFFFu, to_end) - P.down_to;
+        const uint32_t down = P.down_to + to_end;   // logits to the end of the border's group
+        wide = P.down_to + P.below > (uint32_t)LIST;
+        if (!wide) {
+            first_bin = 0;
+            last_bin = P.b + 1;
+            if (down <= (uint32_t)LIST) {
+                const int more = __popc(__ballot_sync(0xFFFFFFFFu, lane < AROUND && down + in <= (uint32_t)LIST));
+                last_bin = max(last_bin, (g + more) * COARSE + COARSE - 1);
+            }
+        } else {
+            const uint32_t group = sm.group[g];
+            if (group <= (uint32_t)LIST) {
+                // as many groups on both sides as fit together
+                const uint32_t below = __shfl_sync(0xFFFFFFFFu, in, lane & (AROUND - 1)), above = __shfl_sync(0xFFFFFFFFu, up, AROUND + (lane & (AROUND - 1)));
+                const int more = __popc(__ballot_sync(0xFFFFFFFFu, lane < AROUND && group + below + above <= (uint32_t)LIST));
+                first_bin = (g - more) * COARSE;
+                last_bin = (g + more) * COARSE + COARSE - 1;
+                if (more == 0) {   // the neighbours, where the border is at the group's end
+                    if (P.b == first_bin && group + P.above <= (uint32_t)LIST) first_bin = P.b - 1;
+                    if (P.b == last_bin && group + P.below <= (uint32_t)LIST) last_bin = P.b + 1;
+                }
+            } else {
+                const bool one = P.below + P.there + P.above > (uint32_t)LIST;
+                if (P.there > (uint32_t)LIST) return false;
+                first_bin = one ? P.b : P.b - 1;
+                last_bin = one ? P.b : P.b + 1;
+            }
+        }
+        first_bin = max(first_bin, 0);
+        last_bin = min(last_bin, BINS - 1);
+        return true;
+    }
+    __device__ Place locate(bool sum, u64 target) const {
+        constexpr int L = GROUPS / 32;
+        Place P = {BINS, 0, 0, 0, 0, 0};
+        int group = -1;
+        u64 at = 0;
+        uint32_t at_n = 0;
+        if (warp < cs) {   // the group; its bins of CTA `warp`, in lanes 1 .. 16, the neighbours beside them
+            uint32_t n[L], mine_n = 0;
+            u64 v[L], mine = 0;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                n[i] = sm.group[lane * L + i];
+                v[i] = sum ? sm.group_sum[lane * L + i] : n[i];
+                mine += v[i];
+                mine_n += n[i];
+            }
+            const u64 in = warp_scan(mine, lane);
+            u64 pre = in - mine;
+            int found = -1;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                if (found < 0 && n[i] && pre < target && pre + v[i] >= target) found = i;
+                if (found < 0) pre += v[i];
+            }
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, found >= 0);
+            P.live = __reduce_add_sync(0xFFFFFFFFu, mine_n);
+            if (who) {
+                const int l = __ffs(who) - 1, i = __shfl_sync(0xFFFFFFFFu, found, l);
+                at = __shfl_sync(0xFFFFFFFFu, pre, l);
+                group = l * L + i;
+                uint32_t above = lane < l ? mine_n : 0;
+#pragma unroll
+                for (int k = 0; k < L; ++k) above += lane == l && k < i ? n[k] : 0;
+                at_n = __reduce_add_sync(0xFFFFFFFFu, above);
+                const int b = group * COARSE + lane - 1;
+                uint32_t c = 0;
+                if (lane < COARSE + 2 && b >= 0 && b < BINS) c = cs > 1 ? peer32(&sm.hist[b], warp) : sm.hist[b];
+                sm.near[warp][lane] = c;
+            }
+        }
+        __syncthreads();
+        if (warp == 0 && group >= 0) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int z = 0; z < MOST_CS; ++z) c += z < cs ? sm.near[z][lane] : 0;
+            const bool inside = lane >= 1 && lane <= COARSE;
+            const u64 w = inside && c ? (sum ? c * middle(group * COARSE + lane - 1) : c) : 0, down = warp_scan(w, lane);
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, inside && c && at + down - w < target && at + down >= target);
+            if (hit) {
+                const int h = __ffs(hit) - 1;
+                P.b = group * COARSE + h - 1;
+                P.there = __shfl_sync(0xFFFFFFFFu, c, h);
+                P.above = __shfl_sync(0xFFFFFFFFu, c, h - 1);
+                P.below = __shfl_sync(0xFFFFFFFFu, c, h + 1);
+                P.down_to = at_n + __reduce_add_sync(0xFFFFFFFFu, inside && lane <= h ? c : 0);
+            }
+        }
+        return P;
+    }
+
+    // Puts the logits of lo .. hi on this CTA's list, and the w's of those above
+    // into the warps' sums; the logits on all lists (more than LIST: they are not whole),
+    // and on that of CTA `lane`.
+    __device__ int collect(float lo, float hi, int& parts) {
+        u64 above = 0;
+        const int end = length(first);
+        for (int i = 0; i < end; i += 128) {
+            const float4 v = four(held, first, i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            if (!__any_sync(0xFFFFFFFFu, v.x >= lo || v.y >= lo || v.z >= lo || v.w >= lo)) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (x[j] > hi) above += weight(x[j]);
+                const bool in = x[j] >= lo && x[j] <= hi;
+                const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
+                if (!who) continue;
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&sm.listed, __popc(who));
+                at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1));
+                if (in && at < LIST) sm.list[at] = (u64)key_of(x[j]) << 32 | (0xFFFFFFFFu - (uint32_t)(first + i + 4 * lane + j));
+            }
+        }
+        put_own(warp_sum64(above));
+        together();
+        const int n = lane < cs ? (cs > 1 ? (int)peer32(&sm.listed, lane) : sm.listed) : 0;
+        parts = min(n, LIST + 1);
+        return __reduce_add_sync(0xFFFFFFFFu, parts);
+    }
+    // Values threadIdx.x and threadIdx.x + nt of all lists (0 past the n)
+    __device__ void bring(int n, int parts, u64 (&e)[2]) const {
+        int end[MOST_CS];   // of the lists, one after the other
+#pragma unroll
+        for (int z = 0; z < MOST_CS; ++z) end[z] = __shfl_sync(0xFFFFFFFFu, parts, z) + (z ? end[z ? z - 1 : 0] : 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = threadIdx.x + k * nt;
+            int z = 0, from = 0;
+#pragma unroll
+            for (int j = 0; j < MOST_CS - 1; ++j)
+                if (i >= end[j]) {
+                    z = j + 1;
+                    from = end[j];
+                }
+            e[k] = i >= n ? 0 : cs > 1 ? peer64(&sm.list[i - from], z) : sm.list[i];
+        }
+    }
+    // The n <= LIST distinct values that the threads hold into sm.sorted, in descending
+    // order.  bucket: of a value, BUCKETS of them, no less for a smaller one.
+    template <class B> __device__ void order(int n, const u64 (&e)[2], B bucket) {
+        __syncthreads();
+        if (threadIdx.x < BUCKETS) sm.bucket[threadIdx.x] = 0;
+        __syncthreads();
+        int b[2];
+        uint32_t place[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            b[k] = e[k] ? bucket(e[k]) : 0;
+            place[k] = e[k] ? atomicAdd(&sm.bucket[b[k]], 1u) : 0;
+        }
+        __syncthreads();
+        const uint32_t c = threadIdx.x < BUCKETS ? sm.bucket[threadIdx.x] : 0, in = warp_scan(c, lane);
+        if (lane == 31) sm.scan[0][warp] = in;
+        __syncthreads();
+        if (threadIdx.x < BUCKETS) sm.bucket[threadIdx.x] = in - c + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? (uint32_t)sm.scan[0][lane] : 0);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (e[k]) sm.sorted[sm.bucket[b[k]] + place[k]] = e[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (e[k]) {   // its place in its bucket
+                const uint32_t from = sm.bucket[b[k]], to = b[k] + 1 < BUCKETS ? sm.bucket[b[k] + 1] : n;
+                place[k] = from;
+                for (uint32_t i = from; i < to; ++i) place[k] += sm.sorted[i] > e[k];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (e[k]) sm.sorted[place[k]] = e[k];
+        __syncthreads();
+    }
+
+    // The warps' sums of the whole row into sm.sums.
+    __device__ void tell(u64 mine) {
+        put_own(mine);
+        together();
+        gather();
+    }
+    __device__ void put_own(u64 mine) {   // (what a turn ago was written may still be read)
+        ++owned;
+        if (lane == 0) sm.own[owned & 1][warp] = mine;
+    }
+    __device__ void gather() {
+        for (int i = threadIdx.x; i < cs * nw; i += nt) {
+            const int z = i / nw;
+            sm.sums[i] = cs > 1 ? peer64(&sm.own[owned & 1][i - z * nw], z) : sm.own[owned & 1][i];
+        }
+        __syncthreads();
+    }
+    // The first index at which the sum of f over the row exceeds `target`, which is
+    // less than the whole; in all lanes of one warp, -1 in the others.  The warps' sums
+    // are in sm.sums.  f: logit, index.
+    template <class F> __device__ int find(F f, u64 target) {
+        // the warp that has it
+        u64 pre = 0;
+        int who = -1;
+        for (int i0 = 0; i0 < cs * nw && who < 0; i0 += 32) {
+            const u64 v = i0 + lane < cs * nw ? sm.sums[i0 + lane] : 0, all = warp_sum64(v);
+            if (pre + all > target) {
+                const u64 in = warp_scan(v, lane);
+                const int l = __ffs(__ballot_sync(0xFFFFFFFFu, pre + in > target)) - 1;
+                who = i0 + l;
+                pre += __shfl_sync(0xFFFFFFFFu, in - v, l);
+            } else {
+                pre += all;
+            }
+        }
+        if (who < 0 || who / nw != rank) return -1;
+        // its logits: 128 a warp of this CTA, in rounds
+        const int w = who - rank * nw, at = who * A.seg, end = length(at);
+        const float* const theirs = held + (w - warp) * A.held;
+        for (int i0 = 0; i0 < end; i0 += 128 * nw) {
+            const int i = i0 + 128 * warp, j = at + i + 4 * lane;
+            float4 x = make_float4(nothing(), nothing(), nothing(), nothing());
+            if (i < end) x = four(theirs, at, i);
+            const u64 a = f(x.x, j), b = f(x.y, j + 1), c = f(x.z, j + 2), d = f(x.w, j + 3), mine = warp_sum64(a + b + c + d);
+            __syncthreads();   // (what was there has been read)
+            if (lane == 0) sm.scan[0][warp] = mine;
+            __syncthreads();
+            const u64 v = lane < nw ? sm.scan[0][lane] : 0, here = pre + warp_sum64(lane < warp ? v : 0);
+            if (here <= target && target < here + mine) {
+                const u64 in = warp_scan(a + b + c + d, lane), before = here + in - (a + b + c + d);
+                const int l = __ffs(__ballot_sync(0xFFFFFFFFu, here + in > target)) - 1;
+                const int k = before + a > target ? 0 : before + a + b > target ? 1 : before + a + b + c > target ? 2 : 3;
+                return __shfl_sync(0xFFFFFFFFu, j + k, l);
+            }
+            const u64 all = warp_sum64(v);
+            if (pre + all > target) return -1;   // (in another warp)
+            pre += all;
+        }
+        return -1;
+    }
+    // The place in the kept w's that u points at
+    __device__ u64 target_of(u64 all) const { return u < 1.0f ? share_of(all, u, false) : all - 1; }
+    __device__ void put(int token, float prob) const {
+        A.p.tokens[row] = token;
+        if (A.p.prob) A.p.prob[row] = prob;
+    }
+    // The token, of the logits above `border` and those equal to it up to index
+    // `last`; the warps' sums of their w's are in sm.sums.
+    __device__ void finish(float border, int last) {
+        u64 all = 0;
+        for (int i = lane; i < cs * nw; i += 32) all += sm.sums[i];
+        all = warp_sum64(all);
+        const int at = find([&](float x, int i) -> u64 { return x > border || (x == border && i <= last) ? weight(x) : 0; }, target_of(all));
+        if (at >= 0 && lane == 0) {
+            float x = value_at(A.p.logits, A.p.type, row * A.p.stride + at) + 0.0f;
+            if (infinite) x = finite(x);
+            put(at, quotient(weight(x), all));
+        }
+    }
+
+    // ------------------------------------------------ rows that the histogram does not settle
+    // The w's sum of the logits from `from` on.
+    __device__ u64 total(float from) {
+        u64 v = 0;
+        each([&](float x, int) {
+            if (x >= from) v += weight(x);
+        });
+        return exchange<false>(v);
+    }
+    // The index of the logit equal to `border` that `before` equal ones precede.
+    __device__ int tie_at(float border, u64 before) {
+        u64 mine = 0;
+        each([&](float x, int) { mine += x == border; });
+        tell(warp_sum64(mine));
+        const int at = find([&](float x, int) -> u64 { return x == border; }, before);
+        return (int)(0xFFFFFFFFu - (uint32_t)exchange<true>(at < 0 ? 0 : 0xFFFFFFFFu - (uint32_t)at));
+    }
     // Empties the histogram, once every CTA has read it.
     __device__ __forceinline__ void empty() const {
         together();
@@ -267,7 +618,6 @@ struct Sampler {
     __device__ __forceinline__ uint4 counts(int b) const {
         if (cs == 1) return *reinterpret_cast<const uint4*>(sm.hist + b);
         uint4 c = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
         for (int z = 0; z < cs; ++z) {
             const uint4 v = peer128(sm.hist + b, z);
             c.x += v.x;
@@ -277,41 +627,38 @@ struct Sampler {
         }
         return c;
     }
-    __device__ __forceinline__ uint32_t count_of(int b) const {
-        const uint4 c = counts(b & ~3);
-        return (b & 3) == 0 ? c.x : (b & 3) == 1 ? c.y : (b & 3) == 2 ? c.z : c.w;
-    }
     // Exclusive sums of the threads' pair over the CTA.
-    __device__ __forceinline__ void block_scan(u64& a, u64& b) {
-        const u64 ai = warp_scan64(a, lane), bi = warp_scan64(b, lane);
+    __device__ __forceinline__ void block_scan_two(u64& a, u64& b) {
+        const u64 ai = warp_scan(a, lane), bi = warp_scan(b, lane);
         __syncthreads();   // (what was there has been read)
         if (lane == 31) {
             sm.scan[0][warp] = ai;
             sm.scan[1][warp] = bi;
         }
         __syncthreads();
-        u64 x = lane < warp ? sm.scan[0][lane] : 0, y = lane < warp ? sm.scan[1][lane] : 0;
+        const u64 x = lane < warp ? sm.scan[0][lane] : 0, y = lane < warp ? sm.scan[1][lane] : 0;
         a = ai - a + warp_sum64(x);
         b = bi - b + warp_sum64(y);
     }
 
-    struct Border { uint32_t key; uint32_t ties, of; };   // ties kept of `of`
+    struct Border { uint32_t key, ties, of; };   // ties kept of `of`
 
     // The border of the row at which the count (mass = false) or the w's sum of
     // the logits in descending order reaches `target` >= 1 (which they do).  Below
     // `floor_` nothing counts, and of the logits equal to it `missing` do not.
     __device__ Border select(bool mass, u64 target, uint32_t floor_, uint32_t missing) {
-        uint32_t hi = kmax, lo = floor_;
+        uint32_t hi = key_of(top), lo = floor_;
         bool by_t = true;
         for (;;) {
             int shift = 0;
             while (((hi - lo) >> shift) >= (uint32_t)BINS) ++shift;
-            auto place = [&](uint32_t k) { return by_t ? min(bin(k), BINS - 1) : (int)((hi - k) >> shift); };
+            auto place = [&](uint32_t k) { return by_t ? min(bin(logit_of(k)), BINS - 1) : (int)((hi - k) >> shift); };
             empty();
             u64 mine = 0;
-            each([&](uint32_t k, int) {
-                if (k > hi) mine += mass ? weight(k) : 1;
-                else if (k >= lo) atomicAdd(&sm.hist[place(k)], 1u);
+            const float hi_x = logit_of(hi), lo_x = logit_of(lo);
+            each([&](float x, int) {
+                if (x > hi_x) mine += mass ? weight(x) : 1;
+                else if (x >= lo_x) atomicAdd(&sm.hist[place(key_of(x))], 1u);
             });
             const u64 above = exchange<false>(mine);
             // a thread's bins, four at a time: how many, and the bounds of their sums
@@ -337,8 +684,8 @@ struct Sampler {
                             w0 = power(b, 0.0079f);
                         } else {
                             const uint32_t k1 = hi - ((uint32_t)b << shift), left = k1 - lo, k0 = left >> shift ? k1 - (1u << shift) + 1 : lo;
-                            w1 = weight(k1);
-                            w0 = k0 == k1 ? w1 : weight(k0);
+                            w1 = weight(logit_of(k1));
+                            w0 = k0 == k1 ? w1 : weight(logit_of(k0));
                             if (k0 != k1) {   // w is right to 2^-28, and may fall by that where it should rise
                                 w1 += (w1 >> 26) + 1;
                                 w0 -= w0 >> 26;
@@ -351,7 +698,7 @@ struct Sampler {
                     down += least[j];
                 }
                 u64 up_at = up, down_at = down;
-                block_scan(up_at, down_at);
+                block_scan_two(up_at, down_at);
                 if (threadIdx.x == nt - 1) { sm.sums[0] = up_at + up; sm.sums[1] = down_at + down; }
                 up_at += up_run;
                 down_at += down_run;
@@ -382,189 +729,32 @@ struct Sampler {
                 Border B;
                 B.key = hi - b1;
                 B.of = count;
-                const u64 w = mass ? weight(B.key) : 1;
+                const u64 w = mass ? weight(logit_of(B.key)) : 1;
                 const u64 need = target > before && w ? (target - before + w - 1) / w : 1;
                 B.ties = (uint32_t)(need < 1 ? 1 : need > count ? count : need);
                 return B;
             }
             const uint32_t wide = hi - lo;
             if (by_t) {
-                const uint32_t top = edge(b1, lo, hi, true);
-                if (b2 < BINS - 1) lo = edge(b2, lo, hi, false);
-                hi = top;
+                hi = up_to(b1);
+                lo = max(lo, up_to(b2 + 1) + 1);
                 by_t = false;
                 continue;
             }
-            const uint32_t top = hi - ((uint32_t)b1 << shift), k2 = hi - ((uint32_t)b2 << shift);
+            const uint32_t k1 = hi - ((uint32_t)b1 << shift), k2 = hi - ((uint32_t)b2 << shift);
             lo = (k2 - lo) >> shift ? k2 - (1u << shift) + 1 : lo;
-            hi = top;
+            hi = k1;
             if (hi - lo > wide / 4) {   // bounds that tell the bins apart badly: halve what is left
                 const uint32_t mid = lo + (hi - lo) / 2;
+                const float mid_x = logit_of(mid);
                 u64 v = 0;
-                each([&](uint32_t k, int) {
-                    if (k > mid) v += mass ? weight(k) : 1;
+                each([&](float x, int) {
+                    if (x > mid_x) v += mass ? weight(x) : 1;
                 });
                 if (exchange<false>(v) >= target) lo = mid + 1;
                 else hi = mid;
             }
         }
-    }
-
-    // The w's sum of the logits from `from` on.
-    __device__ u64 total(uint32_t from) {
-        u64 v = 0;
-        each([&](uint32_t k, int) {
-            if (k >= from) v += weight(k);
-        });
-        return exchange<false>(v);
-    }
-
-    // The index of the logit equal to `key` that `before` equal ones precede.
-    __device__ int tie_at(uint32_t key, u64 before) {
-        u64 mine = 0;
-        each([&](uint32_t k, int) { mine += k == key; });
-        mine = warp_sum64(mine);
-        tell(mine);
-        u64 pre = 0;
-        for (int i = lane; i < rank * nw + warp; i += 32) pre += sm.sums[i];
-        pre = warp_sum64(pre);
-        int at = 0x7FFFFFFF;
-        if (before >= pre && before < pre + mine)
-            at = find([&](uint32_t k, int) -> u64 { return k == key; }, before - pre);
-        return (int)(0xFFFFFFFFu - (uint32_t)exchange<true>(at == 0x7FFFFFFF ? 0 : 0xFFFFFFFFu - (uint32_t)at));
-    }
-
-    // The warps' sums of the whole row into sm.sums.
-    __device__ void tell(u64 mine) {
-        if (lane == 0) sm.own[warp] = mine;
-        together();
-        gather();
-        together();   // (sm.own may be written again)
-    }
-    __device__ void gather() {
-        for (int i = threadIdx.x; i < cs * nw; i += nt) {
-            const int z = i / nw;
-            sm.sums[i] = cs > 1 ? peer64(&sm.own[i - z * nw], z) : sm.own[i];
-        }
-        __syncthreads();
-    }
-
-    // The index at which the sum of f over this warp's logits exceeds `target`.
-    template <class F> __device__ int find(F f, u64 target) const {
-        const int end = (int)min((long long)A.seg, (long long)A.p.n - first);
-        u64 pre = 0;
-        for (int i = 0; i < end; i += 128) {
-            const uint4 k = four(i);
-            const u64 a = f(k.x, i + 4 * lane), b = f(k.y, i + 4 * lane + 1), c = f(k.z, i + 4 * lane + 2), d = f(k.w, i + 4 * lane + 3);
-            const u64 in = warp_scan64(a + b + c + d, lane);
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, pre + in > target);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                const u64 before = pre + in - (a + b + c + d);
-                const int j = before + a > target ? 0 : before + a + b > target ? 1 : before + a + b + c > target ? 2 : 3;
-                return first + i + __shfl_sync(0xFFFFFFFFu, 4 * lane + j, l);
-            }
-            pre += __shfl_sync(0xFFFFFFFFu, in, 31);
-        }
-        return 0x7FFFFFFF;
-    }
-
-    __device__ void put(int token, float prob) const {
-        A.p.tokens[row] = token;
-        if (A.p.prob) A.p.prob[row] = prob;
-    }
-    __device__ u64 target_of(u64 all) const {   // the place in the kept w's that u points at
-        const float u = fmaxf(A.p.u[row], 0.0f);
-        return u < 1.0f ? share_of(all, u, false) : all - 1;
-    }
-
-    // The token, of the logits above `key` and those equal to it up to index
-    // `last`; the warps' sums of their w's are in sm.sums.
-    __device__ void finish(uint32_t key, int last) {
-        u64 all = 0;
-        for (int i = lane; i < cs * nw; i += 32) all += sm.sums[i];
-        all = warp_sum64(all);
-        const u64 target = target_of(all);
-        u64 pre = 0;
-        for (int i = lane; i < rank * nw + warp; i += 32) pre += sm.sums[i];
-        pre = warp_sum64(pre);
-        if (target < pre || target >= pre + sm.sums[rank * nw + warp]) return;
-        const int at = find([&](uint32_t k, int i) -> u64 { return k > key || (k == key && first + i <= last) ? weight(k) : 0; }, target - pre);
-        if (lane == 0) {
-            uint32_t k = key_of(value_at(A.p.logits, A.p.type, row * A.p.stride + at));
-            if (infinite) k = finite(k);
-            put(at, (float)((double)weight(k) / (double)all));
-        }
-    }
-
-    // Sorts sm.sorted[0 .. n), n a power of two of 32 .. LIST, downwards.
-    __device__ void sort(int n) {
-        // a thread has the values at threadIdx.x and, where nt < n, threadIdx.x + nt
-        const int i0 = threadIdx.x, i1 = i0 + nt;
-        u64 a = i0 < n ? sm.sorted[i0] : 0, b = i1 < n ? sm.sorted[i1] : 0;
-        auto keep = [](u64 mine, u64 other, bool larger) { return (mine > other) == larger ? mine : other; };
-        for (int k = 2; k <= n; k <<= 1)
-            for (int j = k >> 1; j > 0; j >>= 1) {
-                const bool a_max = ((i0 & k) == 0) == ((i0 & j) == 0), b_max = ((i1 & k) == 0) == ((i1 & j) == 0);
-                if (j < 32) {
-                    const u64 x = __shfl_xor_sync(0xFFFFFFFFu, a, j), y = __shfl_xor_sync(0xFFFFFFFFu, b, j);
-                    a = keep(a, x, a_max);
-                    b = keep(b, y, b_max);
-                } else {
-                    __syncthreads();
-                    if (i0 < n) sm.sorted[i0] = a;
-                    if (i1 < n) sm.sorted[i1] = b;
-                    __syncthreads();
-                    if (i0 < n) a = keep(a, sm.sorted[i0 ^ j], a_max);
-                    if (i1 < n) b = keep(b, sm.sorted[i1 ^ j], b_max);
-                }
-            }
-        __syncthreads();
-        if (i0 < n) sm.sorted[i0] = a;
-        if (i1 < n) sm.sorted[i1] = b;
-        __syncthreads();
-    }
-    static __device__ __forceinline__ int rounded_up(int n) { return n <= 32 ? 32 : 1 << (32 - __clz(n - 1)); }
-
-    // Puts the logits of [lo, hi] on this CTA's list, and the w's of those above
-    // into the warps' sums; the logits on all lists (more than LIST: they are not whole).
-    __device__ int collect(uint32_t lo, uint32_t hi) {
-        u64 above = 0;
-        const int end = (int)min((long long)A.seg, (long long)A.p.n - first);
-        for (int i = 0; i < end; i += 128) {
-            const uint4 v = four(i);
-            const uint32_t k[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (k[j] > hi) above += weight(k[j]);
-                const bool in = k[j] >= lo && k[j] <= hi;
-                const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
-                if (!who) continue;
-                int at = 0;
-                if (lane == 0) at = atomicAdd(&sm.listed, __popc(who));
-                at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1));
-                if (in && at < LIST) sm.list[at] = (u64)k[j] << 32 | (0xFFFFFFFFu - (uint32_t)(first + i + 4 * lane + j));
-            }
-        }
-        above = warp_sum64(above);
-        if (lane == 0) sm.own[warp] = above;
-        together();
-        int n = lane < cs ? (cs > 1 ? peer_int(&sm.listed, lane) : sm.listed) : 0;
-        return __reduce_add_sync(0xFFFFFFFFu, min(n, LIST + 1));
-    }
-    // All lists into sm.sorted, sorted; the place after the last.
-    __device__ int bring(int n) {
-        const int size = rounded_up(n);
-        int at = 0;
-        for (int z = 0; z < cs; ++z) {
-            const int m = cs > 1 ? peer_int(&sm.listed, z) : sm.listed;
-            for (int i = threadIdx.x; i < m; i += nt) sm.sorted[at + i] = cs > 1 ? peer64(&sm.list[i], z) : sm.list[i];
-            at += m;
-        }
-        for (int i = n + threadIdx.x; i < size; i += nt) sm.sorted[i] = 0;
-        __syncthreads();
-        sort(size);
-        return size;
     }
 };
 
@@ -582,46 +772,66 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
     S.cs = gridDim.z;
     S.rank = blockIdx.z;
     S.first = (int)min((long long)(S.rank * S.nw + S.warp) * A.seg, (long long)A.p.n);
-    S.turn = 0;
+    S.turn = S.owned = 0;
     S.infinite = false;
-    S.keys = reinterpret_cast<uint32_t*>(sample_raw + sizeof(SampleSmem)) + S.warp * A.held;
-    if (threadIdx.x < 64) sm.table[threadIdx.x] = EXP_TABLE[threadIdx.x];
+    S.held = reinterpret_cast<float*>(sample_raw + sizeof(SampleSmem)) + S.warp * A.held;
+    for (int i = threadIdx.x; i < 64 * 16; i += S.nt) sm.table[i / 16][i % 16] = EXP_TABLE[i / 16];
+    for (int i = threadIdx.x; i < GROUPS; i += S.nt) sm.group[i] = sm.group_sum[i] = 0;
     if (threadIdx.x == 0) sm.listed = 0;
     for (int i = threadIdx.x; i < BINS / 4; i += S.nt) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
     grid_wait_prior();
+    const float T = A.p.temperature ? A.p.temperature[S.row] : 1.0f;
+    const int k = A.p.top_k ? A.p.top_k[S.row] : 0;
+    const float p = A.p.top_p ? A.p.top_p[S.row] : 1.0f, low = A.p.min_p ? A.p.min_p[S.row] : 0.0f;
+    S.u = A.p.u ? fmaxf(A.p.u[S.row], 0.0f) : 0.0f;
     // the row, and its largest logit
-    uint32_t best = 0;
+    float best = -INFINITY;
     {
-        const int end = (int)min((long long)A.seg, (long long)A.p.n - S.first);
-#pragma unroll 4
-        for (int i = 0; i < end; i += 128) {
-            const uint4 k = S.load(S.first + i + 4 * S.lane);
-            if (i < A.held) *reinterpret_cast<uint4*>(S.keys + i + 4 * S.lane) = k;
-            best = max(best, max(max(k.x, k.y), max(k.z, k.w)));
+        const int end = S.length(S.first);
+        constexpr int AHEAD = 5;   // loads in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < end; i0 += 128 * AHEAD) {
+            float4 v[AHEAD];
+            if (A.four && A.p.type == PLM_F32 && i0 + 128 * AHEAD <= end) {   // whole: nothing between the loads
+                const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(A.p.logits) + S.row * A.p.stride + S.first + i0) + S.lane;
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) v[j] = at[32 * j];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) v[j] = make_float4(v[j].x + 0.0f, v[j].y + 0.0f, v[j].z + 0.0f, v[j].w + 0.0f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j)
+                    v[j] = i0 + 128 * j < end ? S.load(S.first + i0 + 128 * j + 4 * S.lane) : make_float4(nothing(), nothing(), nothing(), nothing());
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int i = i0 + 128 * j;
+                if (i < min(end, A.held)) *reinterpret_cast<float4*>(S.held + i + 4 * S.lane) = v[j];
+                best = fmaxf(fmaxf(best, fmaxf(v[j].x, v[j].y)), fmaxf(v[j].z, v[j].w));   // (NaN counts for nothing)
+            }
         }
     }
-    S.kmax = (uint32_t)S.exchange<true>(best);
+    const uint32_t most = (uint32_t)S.exchange<true>(key_of(best));
+    S.top = logit_of(most);
     const bool leader = S.rank == 0 && threadIdx.x == 0;
-    const float T = A.p.temperature ? A.p.temperature[S.row] : 1.0f;
-    if (S.kmax <= LOWEST) {
+    if (most <= LOWEST) {
         if (leader) S.put(-1, 0.0f);
     } else if (!(T > 0.0f) || !A.p.u) {
         uint32_t at = 0;   // the first index, as its complement
-        S.each([&](uint32_t k, int i) {
-            if (k == S.kmax) at = max(at, 0xFFFFFFFFu - (uint32_t)(S.first + i));
+        S.each([&](float x, int i) {
+            if (x == S.top) at = max(at, 0xFFFFFFFFu - (uint32_t)i);
         });
         at = (uint32_t)S.exchange<true>(at);
         if (leader) S.put((int)(0xFFFFFFFFu - at), 1.0f);
     } else {
-        if (S.kmax == key_of(INFINITY)) {
+        if (S.top == INFINITY) {
             S.infinite = true;
-            const int end = min(A.held, (int)min((long long)A.seg, (long long)A.p.n - S.first));
+            const int end = min(A.held, S.length(S.first));
             for (int i = 4 * S.lane; i < end; i += 128)
-                for (int j = i; j < i + 4; ++j) S.keys[j] = S.finite(S.keys[j]);
-            S.kmax = key_of(0.0f);
+                for (int j = i; j < i + 4; ++j) S.held[j] = S.finite(S.held[j]);
+            S.top = 0.0f;
             __syncwarp();
         }
-        const float top = logit_of(S.kmax);
         {   // c = log2(e) / T as a pair of f32: the quotient and what it leaves
             const float l_hi = 1.44269502f, l_lo = 1.92596299e-8f;   // log2(e)
             const float q = fminf(__fdiv_rn(l_hi, T), 3e38f);
@@ -629,191 +839,154 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
             S.c_lo = q < 1e37f && T < 1e37f && T > 1e-30f ? __fdiv_rn(fmaf(-q, T, l_hi) + l_lo, T) : 0.0f;
         }
         // Logits near the top differ from it exactly; else the reference is 0
-        S.base = fabsf(top * S.c_hi) < 80.0f ? 0.0f : top;
-        S.ref = ceilf((top - S.base) * S.c_hi * 64.0f) * 0.015625f;
+        S.base = fabsf(S.top * S.c_hi) < 80.0f ? 0.0f : S.top;
+        S.ref = ceilf((S.top - S.base) * S.c_hi * 64.0f) * 0.015625f;
         S.ref64 = S.ref * 64.0f + MAGIC;
-        const int k = A.p.top_k ? A.p.top_k[S.row] : 0;
-        const float p = A.p.top_p ? A.p.top_p[S.row] : 1.0f, low = A.p.min_p ? A.p.min_p[S.row] : 0.0f;
         const bool by_k = k > 0 && k < A.p.n, by_p = p < 1.0f;
-        // the lowest key with a weight; min_p: of the smallest f32 that is at least max + T ln(min_p)
-        uint32_t floor_ = S.edge(BINS - 1, LOWEST + 1, S.kmax, false);
+        // min_p: the smallest f32 that is at least max + T ln(min_p)
+        uint32_t floor_ = LOWEST + 1;
         if (low > 0.0f) {
-            if (threadIdx.x == 0)
-                sm.found[7] = S.infinite ? S.kmax : min(key_of(__double2float_ru((double)top + (double)T * log((double)fminf(low, 1.0f)))), S.kmax);
+            if (threadIdx.x == 0) {
+                const double at = (double)S.top + (double)T * log((double)fminf(low, 1.0f));   // (NaN: T is infinite, min_p 1)
+                sm.found[7] = S.infinite ? key_of(0.0f) : at == at ? min(key_of(__double2float_ru(at) + 0.0f), key_of(S.top)) : floor_;
+            }
             __syncthreads();
-            floor_ = max(floor_, sm.found[7]);
+            floor_ = sm.found[7];
             __syncthreads();
         }
         uint32_t border = floor_;   // what is kept: the keys above, and those equal up to index `last`
         int last = 0x7FFFFFFF;
         enum { AGAIN, LISTED, WIDE, DONE } how = DONE;
-        u64 sum = 0;
         if (by_k || by_p) {
             // The histogram; for top_p alone also the sum of all w's
             u64 mine = 0;
-            S.each([&](uint32_t x, int) {
-                const int b = S.bin(x);
-                if (b < BINS) atomicAdd(&sm.hist[b], 1u);
-                if (!by_k) mine += S.weight(x);
+            S.each([&](float logit, int) {
+                const float x = logit - S.base, v = x * S.c_hi, s = S.steps(v);
+                if (S.weighs(s)) {
+                    atomicAdd(&sm.hist[S.bin_of(s)], 1u);
+                    if (!by_k) mine += S.weight(x, v, s);
+                }
             });
-            sum = S.exchange<false>(mine);
+            S.add_groups(!by_k);
+            const u64 sum = S.exchange<false>(mine);
             u64 target = by_k ? k : share_of(sum, fmaxf(p, 0.0f), true);
             if (target < 1) target = 1;
-            if (target > sum && !by_k) target = sum;
-            // the bin in which the count, or by the bins' middles the sum, reaches it
-            if (threadIdx.x == 0) { sm.found[0] = BINS; sm.found[1] = 0; sm.found[2] = 0; sm.found[3] = 0; }
-            u64 run = 0, run_n = 0;
-            for (int at = 0; at < BINS; at += 4 * S.nt) {
-                const int b0 = at + 4 * (int)threadIdx.x;
-                const uint4 c = b0 < BINS ? S.counts(b0) : make_uint4(0, 0, 0, 0);
-                const uint32_t n[4] = {c.x, c.y, c.z, c.w};
-                u64 v[4], in = 0, in_n = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] = by_k ? n[j] : n[j] ? n[j] * S.power(b0 + j, 0.0f) : 0;
-                    in += v[j];
-                    in_n += n[j];
+            const Sampler::Place P = S.locate(!by_k, target);
+            if (S.warp == 0) {
+                // The list: down to the border's bin for top_k, with what is around for top_p
+                uint32_t lo = LOWEST + 1, hi = key_of(S.top);
+                int first_bin = 0, last_bin = P.b;
+                bool wide = false, far = P.b >= BINS || (by_k && P.down_to > (uint32_t)LIST);
+                if (!far && !by_k) far = !S.window(P, first_bin, last_bin, wide);
+                if (!far) {
+                    lo = S.up_to(last_bin + 1) + 1;
+                    if (wide) hi = S.up_to(first_bin);
                 }
-                u64 pre = in, pre_n = in_n;
-                S.block_scan(pre, pre_n);
-                if (threadIdx.x == S.nt - 1) { sm.sums[0] = pre + in; sm.sums[1] = pre_n + in_n; }
-                pre += run;
-                pre_n += run_n;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pre_n += n[j];
-                    if (n[j] && pre < target && pre + v[j] >= target) {
-                        sm.found[0] = b0 + j;
-                        sm.found[1] = (uint32_t)pre_n;   // logits down to this bin
-                        sm.found[2] = n[j];
-                    }
-                    pre += v[j];
+                if (S.lane == 0) {
+                    sm.found[0] = lo;
+                    sm.found[1] = hi;
+                    sm.found[2] = wide;
+                    sm.found[3] = far;
+                    sm.found[4] = P.live;
+                    sm.found[5] = last_bin;
                 }
-                __syncthreads();
-                run += sm.sums[0];
-                run_n += sm.sums[1];
             }
-            const int b = (int)sm.found[0];
-            const uint32_t down_to = sm.found[1], there = sm.found[2];
-            if (by_k && run_n <= (u64)k) {
+            __syncthreads();
+            uint32_t lo = sm.found[0];
+            const uint32_t hi = sm.found[1], live = sm.found[4], bins = sm.found[5] + 1;
+            how = sm.found[3] ? AGAIN : sm.found[2] ? WIDE : LISTED;
+            __syncthreads();
+            if (by_k && live <= (uint32_t)k) {
                 how = by_p ? AGAIN : DONE;                 // top_k leaves all that have a weight
-            } else if (b >= BINS) {
-                how = AGAIN;                               // (rounding has put it past the last bin)
-            } else {
-                // for top_p the border may be a bin further down, or up, than the middles say
-                uint32_t lo = S.edge(b, LOWEST + 1, S.kmax, false), hi = S.kmax;
-                how = LISTED;
-                if (!by_k) {
-                    const uint32_t below = b + 1 < BINS ? S.count_of(b + 1) : 0, above = b ? S.count_of(b - 1) : 0;
-                    if (down_to + below <= (uint32_t)LIST) {
-                        lo = S.edge(min(b + 1, BINS - 1), LOWEST + 1, S.kmax, false);
-                    } else {
-                        how = WIDE;
-                        const bool three = below + there + above <= (uint32_t)LIST;
-                        if (three) lo = S.edge(min(b + 1, BINS - 1), LOWEST + 1, S.kmax, false);
-                        hi = S.edge(three ? max(b - 1, 0) : b, LOWEST + 1, S.kmax, true);
-                    }
-                }
+            } else if (how != AGAIN) {
                 // what min_p leaves out need not be looked at, but counts in what top_p is of
                 if (!(by_k && by_p) && floor_ > lo) lo = floor_;
+                int n = 0, parts;
                 if (lo > hi) {                             // min_p seems to leave less than top_p
-                    how = S.total(floor_) <= target ? DONE : AGAIN;
-                } else if (by_k && down_to > (uint32_t)LIST) {
-                    how = AGAIN;
+                    how = S.total(logit_of(floor_)) <= target ? DONE : AGAIN;
                 } else {
-                    const int n = S.collect(lo, hi);
-                    if (n > LIST || n == 0) {
+                    n = S.collect(logit_of(lo), logit_of(hi), parts);
+                    if (n > LIST || n == 0) how = AGAIN;
+                }
+                if (how == LISTED || how == WIDE) {
+                    u64 e[2], w[2], above = 0;
+                    S.bring(n, parts, e);
+                    if (how == WIDE) {
+                        S.gather();
+                        for (int i = S.lane; i < S.cs * S.nw; i += 32) above += sm.sums[i];
+                        above = warp_sum64(above);
+                        const uint32_t step = (hi - lo) / BUCKETS + 1;
+                        S.order(n, e, [&](u64 v) { return (int)((hi - (uint32_t)(v >> 32)) / step); });
+                    } else {
+                        const uint32_t step = (bins + BUCKETS - 1) / BUCKETS;
+                        S.order(n, e, [&](u64 v) { return min(S.bin(logit_of((uint32_t)(v >> 32))) / (int)step, BUCKETS - 1); });
+                    }
+                    // a thread's two values of the list, in descending order
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int i = 2 * threadIdx.x + j;
+                        e[j] = i < n ? sm.sorted[i] : 0;
+                        w[j] = i < n && (!by_k || i < k) ? S.weight(logit_of((uint32_t)(e[j] >> 32))) : 0;
+                    }
+                    u64 listed;
+                    const u64 pre = S.block_scan(w[0] + w[1], listed);
+                    if (by_k) {
+                        target = by_p ? share_of(listed, fmaxf(p, 0.0f), true) : listed;
+                        if (target < 1) target = 1;
+                    }
+                    // (by the middles of the bins the border may seem to lie where it does not; a list that min_p has
+                    // cut short need not reach it)
+                    if (!by_k && (above >= target || (above + listed < target && lo > floor_))) {
                         how = AGAIN;
                     } else {
-                        S.bring(n);
-                        u64 above = 0;
+                        const bool keep0 = w[0] && above + pre < target && (uint32_t)(e[0] >> 32) >= floor_;
+                        const bool keep1 = w[1] && above + pre + w[0] < target && (uint32_t)(e[1] >> 32) >= floor_;
+                        const int kept = __syncthreads_count(keep0) + __syncthreads_count(keep1);   // the first so many
                         if (how == WIDE) {
-                            S.gather();
-                            for (int i = S.lane; i < S.cs * S.nw; i += 32) above += sm.sums[i];
-                            above = warp_sum64(above);
-                        }
-                        // a thread's values of the list, in descending order
-                        u64 w[2], key[2];
-                        for (int round = 0; round < 2; ++round) {
-                            const int i = 2 * threadIdx.x + round;
-                            key[round] = i < n ? sm.sorted[i] : 0;
-                            w[round] = i < n && (!by_k || i < k) ? S.weight((uint32_t)(key[round] >> 32)) : 0;
-                        }
-                        u64 pre = w[0] + w[1], none = 0;
-                        const u64 pair = pre;
-                        S.block_scan(pre, none);
-                        if (threadIdx.x == S.nt - 1) sm.found_sum = pre + pair;
-                        __syncthreads();
-                        const u64 listed = sm.found_sum;
-                        if (by_k) {
-                            sum = listed;
-                            target = by_p ? share_of(sum, fmaxf(p, 0.0f), true) : sum;
-                            if (target < 1) target = 1;
-                        }
-                        // (by the middles of the bins the border may seem to lie where it does not; a list that min_p
-                        // has cut short need not reach it)
-                        if (!by_k && (above >= target || (above + listed < target && lo > floor_))) {
-                            how = AGAIN;
-                        } else {
-                            const bool keep0 = w[0] && above + pre < target && (uint32_t)(key[0] >> 32) >= floor_;
-                            const bool keep1 = w[1] && above + pre + w[0] < target && (uint32_t)(key[1] >> 32) >= floor_;
-                            const int kept = __syncthreads_count(keep0) + __syncthreads_count(keep1);   // the first so many
-                            if (how == WIDE) {
-                                // each of them adds to its warp's sum
-                                for (int round = 0; round < 2; ++round)
-                                    if (round ? keep1 : keep0)
-                                        atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)key[round]) / A.seg], w[round]);
-                                __syncthreads();
-                                if (kept) {
-                                    const u64 end = sm.sorted[kept - 1];
-                                    border = (uint32_t)(end >> 32);
-                                    last = (int)(0xFFFFFFFFu - (uint32_t)end);
-                                } else {
-                                    border = hi + 1;   // (none: those above alone)
-                                }
-                                S.finish(border, last);
-                            } else if (S.rank == 0) {
-                                // in the order of the indices: the index's complement first, downwards
-                                const int size = Sampler::rounded_up(kept);
-                                __syncthreads();
-                                for (int round = 0; round < 2; ++round) {
-                                    const int i = 2 * threadIdx.x + round;
-                                    if (i < size) sm.sorted[i] = i < kept ? key[round] << 32 | key[round] >> 32 : 0;
-                                }
-                                __syncthreads();
-                                S.sort(size);
-                                for (int round = 0; round < 2; ++round) {
-                                    const int i = 2 * threadIdx.x + round;
-                                    key[round] = i < kept ? sm.sorted[i] : 0;
-                                    w[round] = i < kept ? S.weight((uint32_t)key[round]) : 0;
-                                }
-                                u64 up = w[0] + w[1];
-                                const u64 both = up;
-                                S.block_scan(up, none);
-                                if (threadIdx.x == S.nt - 1) sm.found_sum = up + both;
-                                __syncthreads();
-                                const u64 all = sm.found_sum, at = S.target_of(all);
-                                for (int round = 0; round < 2; ++round) {
-                                    if (at >= up && at < up + w[round])
-                                        S.put((int)(0xFFFFFFFFu - (uint32_t)(key[round] >> 32)), (float)((double)w[round] / (double)all));
-                                    up += w[round];
-                                }
+                            // each of them adds to its warp's sum
+                            if (keep0) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[0]) / A.seg], w[0]);
+                            if (keep1) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[1]) / A.seg], w[1]);
+                            __syncthreads();
+                            border = hi + 1;               // none of them: those above alone
+                            if (kept) {
+                                const u64 end = sm.sorted[kept - 1];
+                                border = (uint32_t)(end >> 32);
+                                last = (int)(0xFFFFFFFFu - (uint32_t)end);
+                            }
+                            S.finish(logit_of(border), last);
+                        } else if (S.rank == 0) {
+                            // in the order of the indices: the index's complement first, downwards
+                            e[0] = keep0 ? e[0] << 32 | e[0] >> 32 : 0;
+                            e[1] = keep1 ? e[1] << 32 | e[1] >> 32 : 0;
+                            const uint32_t step = (uint32_t)(A.p.n - 1) / BUCKETS + 1;
+                            S.order(kept, e, [&](u64 v) { return (int)((0xFFFFFFFFu - (uint32_t)(v >> 32)) / step); });
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int i = 2 * threadIdx.x + j;
+                                e[j] = i < kept ? sm.sorted[i] : 0;
+                                w[j] = i < kept ? S.weight(logit_of((uint32_t)e[j])) : 0;
+                            }
+                            u64 all, up = S.block_scan(w[0] + w[1], all);
+                            const u64 at = S.target_of(all);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                if (at >= up && at < up + w[j]) S.put((int)(0xFFFFFFFFu - (uint32_t)(e[j] >> 32)), quotient(w[j], all));
+                                up += w[j];
                             }
                         }
                     }
                 }
             }
             if (how == AGAIN) {
-                const uint32_t live = S.edge(BINS - 1, LOWEST + 1, S.kmax, false);
-                Sampler::Border B = {live, 0, 0};
+                Sampler::Border B = {S.up_to(BINS) + 1, 0, 0};   // the lowest key with a weight
                 bool cut = false;
-                if (by_k && run_n > (u64)k) {
-                    B = S.select(false, k, live, 0);
+                if (by_k && live > (uint32_t)k) {
+                    B = S.select(false, k, B.key, 0);
                     cut = true;
                 }
                 if (by_p) {
-                    u64 all = S.total(B.key);
-                    if (cut) all -= (B.of - B.ties) * S.weight(B.key);
+                    u64 all = S.total(logit_of(B.key));
+                    if (cut) all -= (B.of - B.ties) * S.weight(logit_of(B.key));
                     u64 reach = share_of(all, fmaxf(p, 0.0f), true);
                     if (reach < 1) reach = 1;
                     B = S.select(true, reach, B.key, cut ? B.of - B.ties : 0);
@@ -821,18 +994,19 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
                 }
                 if (cut && B.key >= floor_) {
                     border = B.key;
-                    last = S.tie_at(border, B.ties - 1);
+                    last = S.tie_at(logit_of(border), B.ties - 1);
                 }
                 how = DONE;
             }
         }
         if (how == DONE) {
+            const float edge = logit_of(border);
             u64 v = 0;
-            S.each([&](uint32_t x, int i) {
-                if (x > border || (x == border && S.first + i <= last)) v += S.weight(x);
+            S.each([&](float x, int i) {
+                if (x > edge || (x == edge && i <= last)) v += S.weight(x);
             });
             S.tell(warp_sum64(v));
-            S.finish(border, last);
+            S.finish(edge, last);
         }
     }
     if (S.cs > 1) S.together();   // no CTA leaves while its shared memory is read
@@ -850,9 +1024,9 @@ cudaError_t launch_sample(const plm_sample_problem& p, cudaStream_t stream) {
     // are spread further
     int cs = 1, nt = 512;
     const int half = 113 * 1024 - (int)sizeof(SampleSmem);
-    while (cs < 8 && p.n * 4 > (long long)cs * half) cs *= 2;
-    while (cs < 8 && p.n > 4096LL * cs && p.m * cs * 2 <= sms) cs *= 2;
-    if (p.m * cs <= sms) nt = 1024;
+    while (cs < MOST_CS && p.n * 4 > (long long)cs * half) cs *= 2;
+    while (cs < MOST_CS && p.n > 4096LL * cs && p.m * cs * 2 <= sms) cs *= 2;
+    if (p.m * cs <= sms && p.n > 2048) nt = 1024;
     const int warps = cs * nt / 32;
     A.seg = (int)((p.n + 128LL * warps - 1) / (128LL * warps)) * 128;
     const int most = (nt == 512 && 4LL * A.seg * (nt / 32) <= half ? half : room) / 4 / (nt / 32) / 128 * 128;
