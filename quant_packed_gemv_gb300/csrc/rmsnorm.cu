@@ -25,7 +25,37 @@ struct NormArgs {
     plm_rmsnorm_problem p;
     int warps;                    // per row
     bool x4, r4, s4, y4, w4;      // four values in one access
+    bool whole;                   // all of them, and k whole chunks
 };
+
+// Four values as they lie in memory, and in f32: the loads of a warp's chunks are
+// issued one after the other, with nothing between them that waits or branches.
+template <int N> __device__ __forceinline__ void load_raw(const void* p, int type, const int (&at)[N], float4 (&v)[N]) {
+    if (type == PLM_F32) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at[j]);
+            v[j].x = __uint_as_float(u.x);
+            v[j].y = __uint_as_float(u.y);
+        }
+    }
+}
+template <int N> __device__ __forceinline__ void as_f32(int type, float4 (&v)[N]) {
+    if (type == PLM_F32) return;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint32_t a = __float_as_uint(v[j].x), b = __float_as_uint(v[j].y);
+        if (type == PLM_F16) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+            v[j] = make_float4(x.x, x.y, y.x, y.y);
+        } else {
+            v[j] = make_float4(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+        }
+    }
+}
 
 // (fused by hand: left to the compiler, the kernels round differently)
 __device__ __forceinline__ float sum8(const float4& a, const float4& b) {
@@ -140,26 +170,56 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) rmsnorm_kernel(const __grid_c
     const long long r = (long long)blockIdx.x * rows + mine;
     const bool in = r < A.p.m;
     const Row row(A, in ? r : 0, lane);
-    float4 a[NCH], b[NCH];
+    float4 h[2 * NCH];   // the halves of the chunks
     float* own = sums + mine * A.warps * NCH;
-    if (in) {
+    // (past the row's last chunk: the last again, not used)
+    auto places = [&](int (&at)[2 * NCH]) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            const int c = part + j * A.warps, i = c * QK + 4 * lane;
-            a[j] = b[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (c < chunks) {
-                a[j] = row.h(i);
-                b[j] = row.h(i + 128);
+            at[2 * j] = min(part + j * A.warps, chunks - 1) * QK + 4 * lane;
+            at[2 * j + 1] = at[2 * j] + 128;
+        }
+    };
+    if (in) {
+        if (A.whole) {
+            int at[2 * NCH];
+            places(at);
+            load_raw(static_cast<const uint8_t*>(A.p.x) + row.xo * type_bytes(A.p.x_type), A.p.x_type, at, h);
+            if (A.p.residual) {
+                float4 r4[2 * NCH];
+                load_raw(static_cast<const uint8_t*>(A.p.residual) + row.ro * type_bytes(A.p.r_type), A.p.r_type, at, r4);
+                as_f32(A.p.x_type, h);
+                as_f32(A.p.r_type, r4);
+#pragma unroll
+                for (int j = 0; j < 2 * NCH; ++j)
+                    h[j] = make_float4(h[j].x + r4[j].x, h[j].y + r4[j].y, h[j].z + r4[j].z, h[j].w + r4[j].w);
+                if (A.p.r_type != PLM_F32)
+#pragma unroll
+                    for (int j = 0; j < 2 * NCH; ++j)
+                        h[j] = make_float4(value_rounded(h[j].x, A.p.r_type), value_rounded(h[j].y, A.p.r_type), value_rounded(h[j].z, A.p.r_type),
+                                           value_rounded(h[j].w, A.p.r_type));
+            } else {
+                as_f32(A.p.x_type, h);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NCH; ++j) {
+                const int c = part + j * A.warps, i = c * QK + 4 * lane;
+                h[2 * j] = h[2 * j + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c < chunks) {
+                    h[2 * j] = row.h(i);
+                    h[2 * j + 1] = row.h(i + 128);
+                }
             }
         }
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             const int c = part + j * A.warps, i = c * QK + 4 * lane;
-            const float s = warp_sum(sum8(a[j], b[j]));
-            if (lane == 0) own[c] = s;   // (0 past the row)
+            const float s = warp_sum(sum8(h[2 * j], h[2 * j + 1]));
+            if (lane == 0) own[c] = s;
             if (c < chunks) {
-                row.keep(i, a[j]);
-                row.keep(i + 128, b[j]);
+                row.keep(i, h[2 * j]);
+                row.keep(i + 128, h[2 * j + 1]);
             }
         }
     }
@@ -168,10 +228,23 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) rmsnorm_kernel(const __grid_c
     float s = lane < chunks ? own[lane] : 0.0f;
     if (lane + 32 < chunks) s += own[lane + 32];
     const float inv = row.inverse(warp_sum(s));
+    float4 w[2 * NCH];
+    if (A.p.weight && A.whole) {
+        int at[2 * NCH];
+        places(at);
+        load_raw(A.p.weight, A.p.w_type, at, w);
+        as_f32(A.p.w_type, w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2 * NCH; ++j) {
+            const int i = (part + (j >> 1) * A.warps) * QK + 128 * (j & 1) + 4 * lane;
+            w[j] = i < A.p.k ? row.w(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-        const int c = part + j * A.warps, i = c * QK + 4 * lane;
-        if (c < chunks) row.put(c, a[j], b[j], row.w(i), row.w(i + 128), inv);
+        const int c = part + j * A.warps;
+        if (c < chunks) row.put(c, h[2 * j], h[2 * j + 1], w[2 * j], w[2 * j + 1], inv);
     }
 }
 
@@ -221,6 +294,7 @@ cudaError_t launch_rmsnorm(const plm_rmsnorm_problem& p, cudaStream_t stream) {
     A.s4 = four(p.sum, p.sum_stride, p.r_type);
     A.y4 = four(p.y, p.y_stride, p.y_type);
     A.w4 = four(p.weight, 0, p.w_type);
+    A.whole = p.k % QK == 0 && A.x4 && (A.r4 || !p.residual) && (A.w4 || !p.weight);
     const long long chunks = (p.k + QK - 1) / QK;
     if (chunks > NORM_WARPS * HELD) {
         A.warps = NORM_WARPS;
