@@ -64,52 +64,61 @@ __device__ __forceinline__ float sum8(const float4& a, const float4& b) {
     return __fadd_rn(s, t);
 }
 
-// The q8_K block of a warp's chunk v (values 4 lane .. and 128 + 4 lane ..): the
-// arithmetic of q8K_quantize_warp, with the reductions as single instructions.
-__device__ __forceinline__ void put_q8K(uint8_t* blk, const float (&v)[8], int lane) {
-    uint32_t top = 0;
+// The q8_K blocks of a warp's N chunks v (values 4 lane .. and 128 + 4 lane ..), the
+// first n of which are there: the arithmetic of q8K_quantize_warp, with the reductions
+// as single instructions and the chunks side by side.
+template <int N> __device__ __forceinline__ void put_q8K(uint8_t* const (&blk)[N], int n, const float (&v)[N][8], int lane) {
+    uint32_t amax[N], idx[N];
+    float mine[N], mx[N], d[N], iscale[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, top);
-    uint32_t idx = 0x7FFFFFFFu;
-    float mine = 0.0f;
+    for (int j = 0; j < N; ++j) {
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 7; i >= 0; --i)
-        if ((__float_as_uint(v[i]) & 0x7FFFFFFFu) == amax) {
-            idx = 4 * lane + (i & 3) + (i < 4 ? 0 : 128);
-            mine = v[i];
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+        amax[j] = __reduce_max_sync(0xFFFFFFFFu, top);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        idx[j] = 0x7FFFFFFFu;
+        mine[j] = 0.0f;
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+            if ((__float_as_uint(v[j][i]) & 0x7FFFFFFFu) == amax[j]) {
+                idx[j] = 4 * lane + (i & 3) + (i < 4 ? 0 : 128);
+                mine[j] = v[j][i];
+            }
+        idx[j] = __reduce_min_sync(0xFFFFFFFFu, idx[j]);   // the first occurrence
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) mx[j] = __shfl_sync(0xFFFFFFFFu, mine[j], (idx[j] & 127) >> 2);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        iscale[j] = __fdiv_rn(-128.0f, amax[j] ? mx[j] : 1.0f);   // (zeros: codes 0)
+        d[j] = amax[j] ? __fdiv_rn(1.0f, iscale[j]) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        int q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = min(127, __float2int_rn(__fmul_rn(iscale[j], v[j][i])));
+        const uint32_t w0 = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+        const uint32_t w1 = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+        // sums of 16 codes: four lanes each, in both halves
+        int both = q[0] + q[1] + q[2] + q[3] + (q[4] + q[5] + q[6] + q[7]) * 65536;   // both sums in one word
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
+        const int next = __shfl_down_sync(0xFFFFFFFFu, both, 4);
+        if (j >= n) continue;
+        uint32_t* words = reinterpret_cast<uint32_t*>(blk[j]);
+        words[1 + lane] = w0;
+        words[33 + lane] = w1;
+        if ((lane & 7) == 0) {   // sums 2h, 2h + 1 of each half
+            const int s0 = (short)(both & 0xFFFF), s1 = (both - s0) >> 16, n0 = (short)(next & 0xFFFF), n1 = (next - n0) >> 16;
+            words[65 + (lane >> 3)] = ((uint32_t)s0 & 0xFFFFu) | ((uint32_t)n0 << 16);
+            words[69 + (lane >> 3)] = ((uint32_t)s1 & 0xFFFFu) | ((uint32_t)n1 << 16);
         }
-    idx = __reduce_min_sync(0xFFFFFFFFu, idx);   // the first occurrence
-    const float mx = __shfl_sync(0xFFFFFFFFu, mine, (idx & 127) >> 2);
-    int q[8];
-    float d = 0.0f;
-    if (amax != 0) {
-        const float iscale = __fdiv_rn(-128.0f, mx);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = min(127, __float2int_rn(__fmul_rn(iscale, v[i])));
-        d = __fdiv_rn(1.0f, iscale);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = 0;
+        if (lane == 0) words[0] = __float_as_uint(d[j]);
     }
-    uint32_t w0, w1;
-    pack_codes8(q, w0, w1);
-    uint32_t* words = reinterpret_cast<uint32_t*>(blk);
-    words[1 + lane] = w0;
-    words[33 + lane] = w1;
-    // sums of 16 codes: four lanes each, in both halves
-    int s0 = q[0] + q[1] + q[2] + q[3], s1 = q[4] + q[5] + q[6] + q[7];
-    int both = s0 + s1 * 65536;   // both sums in one word
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
-    s0 = (int)(short)(both & 0xFFFF);
-    s1 = (both - s0) >> 16;
-    const int n0 = __shfl_down_sync(0xFFFFFFFFu, s0, 4), n1 = __shfl_down_sync(0xFFFFFFFFu, s1, 4);
-    if ((lane & 7) == 0) {   // sums 2h, 2h + 1 of each half
-        words[65 + (lane >> 3)] = ((uint32_t)s0 & 0xFFFFu) | ((uint32_t)n0 << 16);
-        words[69 + (lane >> 3)] = ((uint32_t)s1 & 0xFFFFu) | ((uint32_t)n1 << 16);
-    }
-    if (lane == 0) words[0] = __float_as_uint(d);
 }
 
 struct Row {
@@ -143,16 +152,23 @@ struct Row {
         if (!A.p.weight) return make_float4(1.0f, 1.0f, 1.0f, 1.0f);
         return load_four(A.p.weight, A.p.w_type, i, left(i), A.w4);
     }
-    // The outputs of chunk c
-    __device__ __forceinline__ void put(long long c, const float4& a, const float4& b, const float4& wa, const float4& wb, float inv) const {
-        const float v[8] = {a.x * inv * wa.x, a.y * inv * wa.y, a.z * inv * wa.z, a.w * inv * wa.w,
-                            b.x * inv * wb.x, b.y * inv * wb.y, b.z * inv * wb.z, b.w * inv * wb.w};
-        const int i = (int)(c * QK) + 4 * lane;
-        if (A.p.y) {
-            store_four(A.p.y, A.p.y_type, yo + i, left(i), A.y4, make_float4(v[0], v[1], v[2], v[3]));
-            store_four(A.p.y, A.p.y_type, yo + i + 128, left(i + 128), A.y4, make_float4(v[4], v[5], v[6], v[7]));
+    // The outputs of chunks c, c + step, .., the first n of N; halves h and their weights w
+    template <int N> __device__ __forceinline__ void put(long long c, int step, int n, const float4 (&h)[2 * N], const float4 (&w)[2 * N], float inv) const {
+        float v[N][8];
+        uint8_t* blk[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float4 a = h[2 * j], b = h[2 * j + 1], wa = w[2 * j], wb = w[2 * j + 1];
+            v[j][0] = a.x * inv * wa.x; v[j][1] = a.y * inv * wa.y; v[j][2] = a.z * inv * wa.z; v[j][3] = a.w * inv * wa.w;
+            v[j][4] = b.x * inv * wb.x; v[j][5] = b.y * inv * wb.y; v[j][6] = b.z * inv * wb.z; v[j][7] = b.w * inv * wb.w;
+            blk[j] = static_cast<uint8_t*>(A.p.xq) + (r * (A.p.k / QK) + c + j * step) * Q8K_BYTES;
+            if (A.p.y && j < n) {
+                const int i = (int)((c + j * step) * QK) + 4 * lane;
+                store_four(A.p.y, A.p.y_type, yo + i, left(i), A.y4, make_float4(v[j][0], v[j][1], v[j][2], v[j][3]));
+                store_four(A.p.y, A.p.y_type, yo + i + 128, left(i + 128), A.y4, make_float4(v[j][4], v[j][5], v[j][6], v[j][7]));
+            }
         }
-        if (A.p.xq) put_q8K(static_cast<uint8_t*>(A.p.xq) + (r * (A.p.k / QK) + c) * Q8K_BYTES, v, lane);
+        if (A.p.xq) put_q8K<N>(blk, n, v, lane);
     }
     __device__ __forceinline__ float inverse(float sum) const {
         return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)A.p.k) + A.p.eps));
@@ -241,11 +257,8 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) rmsnorm_kernel(const __grid_c
             w[j] = i < A.p.k ? row.w(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
     }
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-        const int c = part + j * A.warps;
-        if (c < chunks) row.put(c, h[2 * j], h[2 * j + 1], w[2 * j], w[2 * j + 1], inv);
-    }
+    const int n = (chunks - part + A.warps - 1) / A.warps;
+    row.put<NCH>(part, A.warps, n, h, w, inv);
 }
 
 // Rows too long for the registers: read twice.
@@ -278,7 +291,8 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) rmsnorm_long_kernel(const __g
         const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const bool two = i + 128 < A.p.k;
         const float4 a = again(i), b = two ? again(i + 128) : z;
-        row.put(c, a, b, row.w(i), two ? row.w(i + 128) : z, inv);
+        const float4 h[2] = {a, b}, w[2] = {row.w(i), two ? row.w(i + 128) : z};
+        row.put<1>(c, 0, 1, h, w, inv);
     }
 }
 
@@ -302,7 +316,7 @@ cudaError_t launch_rmsnorm(const plm_rmsnorm_problem& p, cudaStream_t stream) {
     }
     // chunks a warp: few rows are spread over warps, many keep more loads of a warp in flight
     int held = 1;
-    while (held < HELD && (chunks > NORM_WARPS * held || (chunks > held && p.m * chunks >= 16LL * num_sms() * held))) held *= 2;
+    while (held < HELD && (chunks > NORM_WARPS * held || (held < 2 && chunks > held && p.m * chunks >= 16LL * num_sms() * held))) held *= 2;
     A.warps = (int)((chunks + held - 1) / held);
     const int rows = A.warps >= 4 ? 1 : 8 / A.warps;   // of a CTA
     const dim3 grid((unsigned)((p.m + rows - 1) / rows)), block((unsigned)(32 * A.warps * rows));
