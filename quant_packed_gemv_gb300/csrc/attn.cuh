@@ -104,6 +104,11 @@ template <> __device__ __forceinline__ uint32_t mul_pairs<__nv_bfloat16>(uint32_
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t fma_pairs(uint32_t a, uint32_t b, uint32_t c) {   // f16
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 // The powers of two of two exponents, in the cache's type (f16: 0 below 2^-24, 2^15 at most).
 template <class E> __device__ __forceinline__ uint32_t exps_to_pair(uint32_t e0, uint32_t e1);
 template <> __device__ __forceinline__ uint32_t exps_to_pair<__half>(uint32_t e0, uint32_t e1) {

@@ -159,7 +159,7 @@ struct Choice8 {
 Choice8 choose8(const AttnArgs& A, int d, long long bound, void* ws) {
     const long long mine = (long long)A.nq * A.group;
     Choice8 c = {};
-    c.rows = mine <= 96;
+    c.rows = mine <= 64 || (mine <= 96 && bound <= 512);
     if (c.rows) {
         const double bytes = (A.batch - 1.0) * A.prefix * A.kv_heads * 2 * d * ((mine + 31) / 32);
         const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7);

@@ -11,9 +11,9 @@ namespace plm {
 // out as others end, so that sequences of unequal lengths even out (20 of up to
 // 16000 keys, 8 heads of 128: 132 us in one wave, 115 so; 64 of up to 4000: 97 and
 // 90; half the keys: 91; 4 tokens each, 3000: 85 and 78; 7 tokens: 73 and 75).
-int rows_cluster(const AttnArgs& A, int d, int chunks, int keys) {
-    const int rows = A.nq * A.group, cut = rows <= 16 ? 2048 : 0x7FFFFFFF;
-    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = attn_rows_room(d, rows);
+int rows_cluster(const AttnArgs& A, int d, int chunks, int keys, bool kv8) {
+    const int rows = A.nq * A.group, cut = rows <= 16 ? (kv8 ? 3000 : 2048) : 0x7FFFFFFF;
+    const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = attn_rows_room(d, rows, kv8);
     int cs = 1;
     while (cs < 8 && keys > 2 * 16 * DW * cs && (pairs * cs * 2 <= room || keys / cs > cut)) cs *= 2;
     return cs;
@@ -25,8 +25,8 @@ int rows_cluster(const AttnArgs& A, int d, int chunks, int keys) {
 // 192 39; 8 x 8 as 128 31, as 256 41; 18 x 8 as 144 50, as 288 57; 4 x 8 over 8000 as
 // 128 41, as 256 70; 7 heads on 2, over 2000: 40 x 4 as 80 39, as 160 29; 60 x 4 as
 // 120 40, as 240 46.
-long long attn_rows_room(int d, int rows) {
-    const int chunks = (rows + 31) / 32, ctas = rows_ctas(d, ((rows + chunks - 1) / chunks + 7) / 8), sms = num_sms();
+long long attn_rows_room(int d, int rows, bool kv8) {
+    const int chunks = (rows + 31) / 32, ctas = rows_ctas(d, ((rows + chunks - 1) / chunks + 7) / 8, kv8), sms = num_sms();
     return ctas == 1 ? sms + sms / 3 : (long long)ctas * sms;
 }
 

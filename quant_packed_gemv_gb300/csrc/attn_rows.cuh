@@ -27,6 +27,7 @@
 // 176 us (6.0 TB/s), 182 with a cold L2; 4 of 1100, 9.3 us, which is latency.
 #pragma once
 
+#include <cstddef>
 #include <type_traits>
 
 #include "attn_tile.cuh"
@@ -67,7 +68,7 @@ __device__ __forceinline__ uint32_t words(const uint4& u, int i) { return i == 0
 // O [rows][D + 4] (padded against conflicts).
 template <int D, int NB, bool KV8> struct RowsSmem {
     static constexpr int ROWS = 8 * NB, PITCH = D + 4;
-    static constexpr int STAGES = (KV8 ? 2 : 1) * (D == 64 ? 2 : 1) * (NB == 1 ? 2 : 3);
+    static constexpr int STAGES = KV8 && NB == 1 ? (D == 64 ? 6 : 3) : (KV8 ? 2 : 1) * (D == 64 ? 2 : 1) * (NB == 1 ? 2 : 3);
     static constexpr int STAGE = 16 * D * (KV8 ? 1 : 2);   // bytes of 16 keys' K, or V
     static constexpr int EXPS = KV8 ? 16 * (D / 32) : 0;   // of their exponents
     static constexpr int SLOT = 2 * (STAGE + EXPS);
@@ -78,14 +79,15 @@ template <int D, int NB, bool KV8> struct RowsSmem {
     };
     uint4 q[NB > 2 ? NB * (D / 32) * 32 : 1];
     union {
-        uint8_t ring[DW][STAGES][SLOT];
+        alignas(128) uint8_t ring[DW][STAGES][SLOT];   // (a copied row begins with the banks)
         Parts part;
     };
+    float q_size[KV8 ? ROWS : 1];   // powers of two that the rows of Q were divided by
 };
 
 // CTAs of 8 nb rows that an SM holds at once: registers bound the first, shared
 // memory the others (228 KB, of which a CTA takes 1 KB for itself).
-__host__ __device__ constexpr int rows_ctas(int d, int nb) { return nb == 1 ? 3 : nb == 4 && d == 128 ? 1 : 2; }
+__host__ __device__ constexpr int rows_ctas(int d, int nb, bool kv8) { return nb == 1 ? (kv8 ? 4 : 3) : nb == 4 && d == 128 ? 1 : 2; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -109,13 +111,14 @@ template <int D, bool KV8> __device__ __forceinline__ int v_chunk(int r, int c) 
 }
 
 template <class E, int D, int NB, class Args>
-__global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(const __grid_constant__ Args A, const __grid_constant__ TilePlan P) {
+__global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, AttnArgs8>::value)) attn_rows_kernel(const __grid_constant__ Args A, const __grid_constant__ TilePlan P) {
     constexpr bool KV8 = std::is_same<Args, AttnArgs8>::value;
     using Element = typename std::conditional<KV8, int8_t, E>::type;   // of the pages
+    using M = typename std::conditional<KV8, __half, E>::type;         // of the products
     using Sm = RowsSmem<D, NB, KV8>;
     constexpr int KC = D / 32, VC = D / 64;   // 16-byte chunks per lane of a K row, of a V row
     constexpr bool QS = NB > 2;
-    extern __shared__ __align__(16) uint8_t rows_raw[];
+    extern __shared__ __align__(128) uint8_t rows_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(rows_raw);
     grid_launch_dependents();
     // after the tile kernel there is nothing to wait for yet: it starts this
@@ -190,7 +193,48 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
         return __ldcg(reinterpret_cast<const uint4*>(static_cast<const E*>(A.q) + ((long long)b * A.nq + tr) * A.q_ts +
                                                      (long long)(h * A.group + r0 + r - tr * A.group) * A.q_hs + 8 * t + 32 * c));
     };
-    if constexpr (QS) {
+    if constexpr (KV8) {
+        // as f16, a row divided by a power of two so that its largest value lies in 2^12 .. 2^13
+        auto q_row = [&](int nb, uint4 (&f)[KC]) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                f[c] = q_part(nb, c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = pair_to_f32<E>(words(f[c], i));
+                    top = max(top, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu));
+                }
+            }
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const int e = max(min((int)(top >> 23), 253), 14);   // 2^(e - 127 - 12) is taken out
+            const float part = __uint_as_float((uint32_t)(254 - e) << 23) * 4096.0f;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = pair_to_f32<E>(words(f[c], i));
+                    h[i] = pack_pair<__half>(v.x * part, v.y * part);
+                }
+                f[c] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            if (t == 0) sm.q_size[8 * nb + g] = __uint_as_float((uint32_t)(e - 12) << 23);
+        };
+        if constexpr (QS) {
+            for (int nb = warp; nb < NB; nb += DW) {
+                uint4 f[KC];
+                q_row(nb, f);
+#pragma unroll
+                for (int c = 0; c < KC; ++c) sm.q[(nb * KC + c) * 32 + lane] = f[c];
+            }
+        } else {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) q_row(nb, qf[nb]);   // (each warp the same)
+        }
+        __syncthreads();
+    } else if constexpr (QS) {
         for (int i = warp; i < NB * KC; i += DW) sm.q[i * 32 + lane] = q_part(i / KC, i % KC);
         __syncthreads();
     } else {
@@ -199,6 +243,16 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
 #pragma unroll
             for (int c = 0; c < KC; ++c) qf[nb][c] = q_part(nb, c);
     }
+    float size[KV8 ? NB : 1][2];   // of rows 8 nb + 2t, + 1, with the scale
+    if constexpr (KV8) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) size[nb][i] = sm.q_size[8 * nb + 2 * t + i] * sl2;
+    }
+    // p is 2^AHEAD times what the reference says, so that f16 holds smaller ones too
+    constexpr float AHEAD = KV8 ? 7.0f : 0.0f;
+    int v_size = 0;   // KV8: O is in steps of 2^(v_size - 127), the largest exponent of the lane's block so far
     int seen[NB][2];   // keys that rows 8 nb + 2t, + 1 see
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -251,17 +305,17 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
                 const uint8_t* at = ks + k_chunk<D, true>(g, 2 * c + (t >> 1)) + 8 * (t & 1);
                 const uint2 k0 = *reinterpret_cast<const uint2*>(at), k1 = *reinterpret_cast<const uint2*>(at + 8 * D);
                 uint32_t a[2][4];   // of two products: rows g, g + 8, then both again
-                codes_to_pairs<E>(k0.x, a[0][0], a[0][2]);
-                codes_to_pairs<E>(k1.x, a[0][1], a[0][3]);
-                codes_to_pairs<E>(k0.y, a[1][0], a[1][2]);
-                codes_to_pairs<E>(k1.y, a[1][1], a[1][3]);
+                codes_to_pairs<M>(k0.x, a[0][0], a[0][2]);
+                codes_to_pairs<M>(k1.x, a[0][1], a[0][3]);
+                codes_to_pairs<M>(k0.y, a[1][0], a[1][2]);
+                codes_to_pairs<M>(k1.y, a[1][1], a[1][3]);
                 const float f0 = __uint_as_float((e[0] >> (8 * c) & 0xFFu) << 23), f1 = __uint_as_float((e[1] >> (8 * c) & 0xFFu) << 23);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
                     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816<E>(x, a[0][0], a[0][1], a[0][2], a[0][3], qv.x, qv.y);
-                    mma16816<E>(x, a[1][0], a[1][1], a[1][2], a[1][3], qv.z, qv.w);
+                    mma16816<M>(x, a[0][0], a[0][1], a[0][2], a[0][3], qv.x, qv.y);
+                    mma16816<M>(x, a[1][0], a[1][1], a[1][2], a[1][3], qv.z, qv.w);
                     s[nb][0] = fmaf(x[0], f0, s[nb][0]);
                     s[nb][1] = fmaf(x[1], f0, s[nb][1]);
                     s[nb][2] = fmaf(x[2], f1, s[nb][2]);
@@ -287,7 +341,7 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[nb][i] *= sl2;
+                s[nb][i] *= KV8 ? size[KV8 ? nb : 0][i & 1] : sl2;
                 if (part && j + g + 8 * (i >> 1) >= seen[nb][i & 1]) s[nb][i] = -INFINITY;
                 raise |= s[nb][i] > m[nb][i & 1] + RAISE;
             }
@@ -315,13 +369,13 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
             float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float base = m[nb][i & 1] == -INFINITY ? 0.0f : m[nb][i & 1];   // a row without keys so far
+                const float base = m[nb][i & 1] == -INFINITY ? 0.0f : m[nb][i & 1] - AHEAD;   // a row without keys so far
                 p[i] = ex2(s[nb][i] - base);
                 l[nb][i & 1] += p[i];
             }
             // rounded to the cache's type (attn.cuh); l has the whole p
-            pb[nb][0] = transpose8x8(pack_pair<E>(p[0], p[1]));
-            pb[nb][1] = transpose8x8(pack_pair<E>(p[2], p[3]));
+            pb[nb][0] = transpose8x8(pack_pair<M>(p[0], p[1]));
+            pb[nb][1] = transpose8x8(pack_pair<M>(p[2], p[3]));
         }
         if constexpr (KV8) {
             // dims (D / 8) g .. of V rows 2t, 2t + 1, 2t + 8, 2t + 9, all in one block
@@ -339,20 +393,36 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
                 }
                 e[i] = vs[Sm::STAGE + Sm::EXPS + r * (D / 32) + (D == 128 ? g >> 1 : g >> 2)];
             }
-            const uint32_t f01 = exps_to_pair<E>(e[0], e[1]), f89 = exps_to_pair<E>(e[2], e[3]);
+            int most = max(max(e[0], e[1]), max(e[2], e[3]));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            if (__any_sync(0xFFFFFFFFu, most > v_size)) {
+                const float keep = most > v_size ? ex2((float)(v_size - most)) : 1.0f;
+                v_size = max(most, v_size);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[nb][k][i] *= keep;
+            }
+            // 2^(e - v_size) in f16: exact from 2^-24 on, 0 below and for e = 0
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = e[i] ? __uint_as_float((uint32_t)max((int)e[i] - v_size + 127, 0) << 23) : 0.0f;
+            const uint32_t f01 = pack_pair<__half>(f[0], f[1]), f89 = pack_pair<__half>(f[2], f[3]);
+            const uint32_t n01 = mul_pairs<__half>(f01, 0xE480E480u), n89 = mul_pairs<__half>(f89, 0xE480E480u);   // times -1152
 #pragma unroll
             for (int w = 0; w < WORDS; ++w)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {   // dims 4 w + 2 i, + 1 of the lane's
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_pairs<E>(__byte_perm(v[0][w], v[1][w], i ? 0x7362 : 0x5140), a0, a1);
-                    codes_to_pairs<E>(__byte_perm(v[2][w], v[3][w], i ? 0x7362 : 0x5140), a2, a3);
-                    a0 = mul_pairs<E>(a0, f01);
-                    a1 = mul_pairs<E>(a1, f01);
-                    a2 = mul_pairs<E>(a2, f89);
-                    a3 = mul_pairs<E>(a3, f89);
+                    // c 2^.. as (1024 + (c + 128)) 2^.. less 1152 2^..: exact, one rounding that does nothing
+                    const uint32_t u0 = __byte_perm(v[0][w], v[1][w], i ? 0x7362 : 0x5140) ^ 0x80808080u;
+                    const uint32_t u8 = __byte_perm(v[2][w], v[3][w], i ? 0x7362 : 0x5140) ^ 0x80808080u;
+                    const uint32_t a0 = fma_pairs(__byte_perm(u0, 0x64646464u, 0x4140), f01, n01), a1 = fma_pairs(__byte_perm(u0, 0x64646464u, 0x4342), f01, n01);
+                    const uint32_t a2 = fma_pairs(__byte_perm(u8, 0x64646464u, 0x4140), f89, n89), a3 = fma_pairs(__byte_perm(u8, 0x64646464u, 0x4342), f89, n89);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma16816<E>(o[nb][2 * w + i], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                    for (int nb = 0; nb < NB; ++nb) mma16816<M>(o[nb][2 * w + i], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
                 }
         } else {
 #pragma unroll
@@ -376,6 +446,7 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
     __syncthreads();   // the rings make room for the parts
 
     // this warp's part
+    const float o_step = KV8 ? __uint_as_float((uint32_t)v_size << 23) : 1.0f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -383,13 +454,13 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
 #pragma unroll
             for (int of = 4; of < 32; of <<= 1) l[nb][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][i], of);
             if (g == 0) {
-                sm.part.m[warp][8 * nb + 2 * t + i] = m[nb][i];
+                sm.part.m[warp][8 * nb + 2 * t + i] = m[nb][i] - AHEAD;
                 sm.part.l[warp][8 * nb + 2 * t + i] = l[nb][i];
             }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
                 *reinterpret_cast<float2*>(&sm.part.o[warp][8 * nb + 2 * t + i][KV8 ? (D / 8) * g + 2 * k : 64 * (k >> 2) + 8 * g + 2 * (k & 3)]) =
-                    make_float2(o[nb][k][i], o[nb][k][i + 2]);
+                    make_float2(o[nb][k][i] * o_step, o[nb][k][i + 2] * o_step);
         }
     }
     const int cs = gridDim.z;   // the cluster: the CTAs of this pair
@@ -469,8 +540,10 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB)) attn_rows_kernel(co
 template <class E, int D, int NB, class Args>
 cudaError_t rows_launch(const Args& A, const TilePlan& P, int chunks, int cs, cudaStream_t stream) {
     const dim3 grid((unsigned)(A.batch * A.kv_heads), (unsigned)chunks, (unsigned)cs);
-    constexpr int bytes = sizeof(RowsSmem<D, NB, std::is_same<Args, AttnArgs8>::value>);
-    static_assert(rows_ctas(D, NB) * (bytes + 1024) <= 228 * 1024, "the CTAs of an SM");
+    using Sm = RowsSmem<D, NB, std::is_same<Args, AttnArgs8>::value>;
+    constexpr int bytes = sizeof(Sm);
+    static_assert(offsetof(Sm, ring) % 128 == 0 && Sm::SLOT % 16 == 0, "the rings' alignment");
+    static_assert(rows_ctas(D, NB, std::is_same<Args, AttnArgs8>::value) * (bytes + 1024) <= 228 * 1024, "the CTAs of an SM");
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<E, D, NB, Args>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
@@ -490,12 +563,12 @@ cudaError_t rows_nb(const Args& A, const TilePlan& P, int chunks, int cs, cudaSt
 }  // namespace
 
 // CTAs of a pair for a launch (attn_rows.cu).
-int rows_cluster(const AttnArgs& A, int d, int chunks, int keys);
+int rows_cluster(const AttnArgs& A, int d, int chunks, int keys, bool kv8);
 
 template <class Args>
 cudaError_t rows_any(const Args& A, const TilePlan* plan, int type, int d, cudaStream_t stream) {
     const TilePlan P = plan ? *plan : TilePlan{};
-    const int chunks = (A.nq * A.group + 31) / 32, cs = rows_cluster(A, d, chunks, plan ? A.cap - A.prefix : A.cap);
+    const int chunks = (A.nq * A.group + 31) / 32, cs = rows_cluster(A, d, chunks, plan ? A.cap - A.prefix : A.cap, std::is_same<Args, AttnArgs8>::value);
     if (type == PLM_F16) return d == 64 ? rows_nb<__half, 64>(A, P, chunks, cs, stream) : rows_nb<__half, 128>(A, P, chunks, cs, stream);
     return d == 64 ? rows_nb<__nv_bfloat16, 64>(A, P, chunks, cs, stream) : rows_nb<__nv_bfloat16, 128>(A, P, chunks, cs, stream);
 }

@@ -219,6 +219,6 @@ cudaError_t launch_attn_rows8(const AttnArgs8& A, const TilePlan* P, int type, i
 
 // CTAs of that kernel that the GPU takes well at once, for so many rows a sequence
 // and head.
-long long attn_rows_room(int d, int rows);
+long long attn_rows_room(int d, int rows, bool kv8 = false);
 
 }  // namespace plm

@@ -1,8 +1,13 @@
 """Attention over 8-bit pages on the GPU against the definition in f64, on the values that the pages stand for.
 
-The cases, their poisoned pages and the tolerance are those of the 16-bit pages (test_gpu_attn): a code times its power of
-two is exact in bf16 and here in f16 (steps of 2^-14 and more), so both operands of the first product are exact and the
-bound's terms are the same.  Where nothing may be read the codes are arbitrary and the exponents 255, which would give
+The cases, their poisoned pages and the terms of the tolerance are those of the 16-bit pages (test_gpu_attn): a code times
+its power of two is exact in bf16 and here in f16 (steps of 2^-14 and more), so both operands of the first product are
+exact.  Few rows have their second product in f16 whatever the type.  There
+  p is held as 2^7 .. 2^15 times what it is relative to the row's largest, so what f16 loses below its steps of 2^-24 is
+    2^-25 / 2^7 = 2^-32 of the largest p at most, n of them: n 2^-32 max|v|;
+  a value is held relative to the largest power of two 2^j of its 32 dims so far, to 2^-24 of it: a block of steps of 2^(j - 25)
+    or less may be lost, 127 2^(j - 25) a value, where a code of 2^j is 64 at least: 2^-24 max|v|, as sum p = 1.
+Both are added to the bound.  Where nothing may be read the codes are arbitrary and the exponents 255, which would give
 infinite values."""
 import math
 import random
@@ -63,6 +68,39 @@ class Case8(test_gpu_attn.Case):
             codes.copy_(c)
             exps.copy_(e)
             x.copy_(values.masked_fill(unused[..., None], float("nan")))
+
+    def check(self, o, lse):
+        g, u = self.hq // self.hkv, test_gpu_attn.U[self.q.dtype]
+        for b, n in enumerate(self.lens):
+            pages = [p for p in self.rows[b] if p >= 0]
+            k, v = (x[pages].transpose(1, 2).reshape(-1, self.hkv, self.d)[:n].double() for x in (self.k, self.v))
+            rows = slice(b * self.nq, (b + 1) * self.nq)
+            x = self.q[rows].double().view(self.nq, self.hkv, g, self.d)
+            pos = torch.arange(n - self.nq, n, device="cuda")
+            hidden = (torch.arange(n, device="cuda")[None] > pos[:, None])[:, None, None]
+            s = (torch.einsum("thgd,nhd->thgn", x, k) * self.scale).masked_fill(hidden, -math.inf)
+            size = (torch.einsum("thgd,nhd->thgn", x.abs(), k.abs()) * abs(self.scale)).masked_fill(hidden, 0.0)
+            size = size.amax(-1) if n else torch.zeros(self.nq, self.hkv, g, dtype=torch.float64, device="cuda")
+            empty = pos < 0
+            p = torch.softmax(s, -1).nan_to_num(0.0) if n else s
+            want, A = torch.einsum("thgn,nhd->thgd", p, v), torch.einsum("thgn,nhd->thgd", p, v.abs())
+            top = float(v.abs().amax()) if n else 0.0
+            e = 2 * ((self.d + 4) * 2.0 ** -24 + 2.0 ** -22) * (1 + size)
+            tol = (u + e[..., None] + 2 * n * 2.0 ** -24) * A + 1e-30 + (n * 2.0 ** -32 + 2.0 ** -24) * top
+            if self.q.dtype == torch.float16:
+                tol = tol + n * 2.0 ** -25 * top
+            tol = tol + test_gpu_attn.U[o.dtype] * (want.abs() + tol) + (2.0 ** -25 if o.dtype == torch.float16 else 0)
+            got = o[rows].double().view(want.shape)
+            assert not got.isnan().any()
+            err = (got - want).abs()
+            assert bool((err <= tol).all()), (b, n, float((err / tol).max()))
+            assert bool((got[empty] == 0).all())
+            ref = torch.logsumexp(s, -1) if n else s.sum(-1) - math.inf
+            got = lse[rows].double().view(ref.shape)
+            assert bool((got[empty] == -math.inf).all())
+            err = (got - ref).abs()[~empty]
+            bound = (e + n * 2.0 ** -24 + 2.0 ** -22 * (1 + ref.abs()))[~empty]
+            assert bool((err <= bound).all()), (b, n, float(err.max()))
 
     def size(self, prefix, most):
         return q.plm_attn_kv8_workspace_size(len(self.lens), self.nq, self.hq, self.hkv, self.d, prefix, most)
