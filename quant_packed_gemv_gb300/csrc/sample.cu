@@ -413,6 +413,7 @@ struct Sampler {
             uint32_t c = 0;
 #pragma unroll
             for (int z = 0; z < MOST_CS; ++z) c += z < cs ? sm.near[z][lane] : 0;
+            sm.near[0][lane] = c;   // (of the row now)
             const bool inside = lane >= 1 && lane <= COARSE;
             const u64 w = inside && c ? (sum ? c * middle(group * COARSE + lane - 1) : c) : 0, down = warp_scan(w, lane);
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, inside && c && at + down - w < target && at + down >= target);
@@ -426,6 +427,23 @@ struct Sampler {
             }
         }
         return P;
+    }
+
+    // The sum, by the middles, of the bins before `first_bin` (of a window around P; warp 0)
+    __device__ u64 estimate(const Place& P, int first_bin) const {
+        const int g = first_bin / COARSE, mine = P.b / COARSE;
+        u64 v = 0;
+        for (int i = lane; i < GROUPS; i += 32) v += i < g ? sm.group_sum[i] : 0;
+        if (first_bin % COARSE) {
+            // bins of its group: the border's group, or the last but one bin of the one above
+            if (g == mine) {
+                const int b = g * COARSE + lane - 1;
+                if (lane >= 1 && lane <= COARSE && b < first_bin) v += sm.near[0][lane] * middle(b);
+            } else if (lane == 0) {
+                v += sm.group_sum[g] - sm.near[0][0] * middle(mine * COARSE - 1);
+            }
+        }
+        return warp_sum64(v);
     }
 
     // Puts the logits of lo .. hi on this CTA's list, and the w's of those above
@@ -871,111 +889,137 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
             const u64 sum = S.exchange<false>(mine);
             u64 target = by_k ? k : share_of(sum, fmaxf(p, 0.0f), true);
             if (target < 1) target = 1;
-            const Sampler::Place P = S.locate(!by_k, target);
-            if (S.warp == 0) {
-                // The list: down to the border's bin for top_k, with what is around for top_p
-                uint32_t lo = LOWEST + 1, hi = key_of(S.top);
-                int first_bin = 0, last_bin = P.b;
-                bool wide = false, far = P.b >= BINS || (by_k && P.down_to > (uint32_t)LIST);
-                if (!far && !by_k) far = !S.window(P, first_bin, last_bin, wide);
-                if (!far) {
-                    lo = S.up_to(last_bin + 1) + 1;
-                    if (wide) hi = S.up_to(first_bin);
+            u64 aim = target;   // the target in what the middles say
+            uint32_t live = 0;
+            // By the middles the border may seem to lie where it does not.  Then the sum of what lies above the window,
+            // which is exact, says how far off they are.
+            for (int attempt = 0;; ++attempt) {
+                const Sampler::Place P = S.locate(!by_k, aim);
+                if (S.warp == 0) {
+                    // The list: down to the border's bin for top_k, with what is around for top_p
+                    uint32_t lo = LOWEST + 1, hi = key_of(S.top);
+                    int first_bin = 0, last_bin = P.b;
+                    bool wide = false, far = P.b >= BINS || (by_k && P.down_to > (uint32_t)LIST);
+                    if (!far && !by_k) far = !S.window(P, first_bin, last_bin, wide);
+                    u64 before = 0;
+                    if (!far) {
+                        lo = S.up_to(last_bin + 1) + 1;
+                        if (wide) {
+                            hi = S.up_to(first_bin);
+                            before = S.estimate(P, first_bin);
+                        }
+                    }
+                    if (S.lane == 0) {
+                        sm.found[0] = lo;
+                        sm.found[1] = hi;
+                        sm.found[2] = wide;
+                        sm.found[3] = far;
+                        sm.found[4] = P.live;
+                        sm.found[5] = last_bin;
+                        sm.found_sum = before;
+                    }
                 }
-                if (S.lane == 0) {
-                    sm.found[0] = lo;
-                    sm.found[1] = hi;
-                    sm.found[2] = wide;
-                    sm.found[3] = far;
-                    sm.found[4] = P.live;
-                    sm.found[5] = last_bin;
+                __syncthreads();
+                uint32_t lo = sm.found[0];
+                const uint32_t hi = sm.found[1], bins = sm.found[5] + 1;
+                const u64 before = sm.found_sum;
+                live = sm.found[4];
+                how = sm.found[3] ? AGAIN : sm.found[2] ? WIDE : LISTED;
+                __syncthreads();
+                if (by_k && live <= (uint32_t)k) {
+                    how = by_p ? AGAIN : DONE;                 // top_k leaves all that have a weight
+                    break;
                 }
-            }
-            __syncthreads();
-            uint32_t lo = sm.found[0];
-            const uint32_t hi = sm.found[1], live = sm.found[4], bins = sm.found[5] + 1;
-            how = sm.found[3] ? AGAIN : sm.found[2] ? WIDE : LISTED;
-            __syncthreads();
-            if (by_k && live <= (uint32_t)k) {
-                how = by_p ? AGAIN : DONE;                 // top_k leaves all that have a weight
-            } else if (how != AGAIN) {
+                if (how == AGAIN) break;
                 // what min_p leaves out need not be looked at, but counts in what top_p is of
                 if (!(by_k && by_p) && floor_ > lo) lo = floor_;
-                int n = 0, parts;
-                if (lo > hi) {                             // min_p seems to leave less than top_p
+                if (lo > hi) {                                 // min_p seems to leave less than top_p
                     how = S.total(logit_of(floor_)) <= target ? DONE : AGAIN;
-                } else {
-                    n = S.collect(logit_of(lo), logit_of(hi), parts);
-                    if (n > LIST || n == 0) how = AGAIN;
+                    break;
                 }
-                if (how == LISTED || how == WIDE) {
-                    u64 e[2], w[2], above = 0;
-                    S.bring(n, parts, e);
+                int parts;
+                const int n = S.collect(logit_of(lo), logit_of(hi), parts);
+                if (n > LIST || n == 0) {
+                    how = AGAIN;
+                    break;
+                }
+                u64 e[2], w[2], above = 0, listed;
+                S.bring(n, parts, e);
+                if (!by_k) {
                     if (how == WIDE) {
                         S.gather();
                         for (int i = S.lane; i < S.cs * S.nw; i += 32) above += sm.sums[i];
                         above = warp_sum64(above);
-                        const uint32_t step = (hi - lo) / BUCKETS + 1;
-                        S.order(n, e, [&](u64 v) { return (int)((hi - (uint32_t)(v >> 32)) / step); });
-                    } else {
-                        const uint32_t step = (bins + BUCKETS - 1) / BUCKETS;
-                        S.order(n, e, [&](u64 v) { return min(S.bin(logit_of((uint32_t)(v >> 32))) / (int)step, BUCKETS - 1); });
                     }
-                    // a thread's two values of the list, in descending order
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) w[j] = e[j] ? S.weight(logit_of((uint32_t)(e[j] >> 32))) : 0;
+                    S.block_scan(w[0] + w[1], listed);
+                    // (a list that min_p has cut short need not reach the target)
+                    if (above >= target || (above + listed < target && lo > floor_)) {
+                        how = AGAIN;
+                        aim = target + before - above;         // (below 0: the estimate was worth nothing)
+                        if (attempt == 2 || (long long)aim < 1) break;
+                        S.together();                          // every CTA has read the lists
+                        if (threadIdx.x == 0) sm.listed = 0;
+                        __syncthreads();
+                        continue;
+                    }
+                }
+                if (how == WIDE) {
+                    const uint32_t step = (hi - lo) / BUCKETS + 1;
+                    S.order(n, e, [&](u64 v) { return (int)((hi - (uint32_t)(v >> 32)) / step); });
+                } else {
+                    const uint32_t step = (bins + BUCKETS - 1) / BUCKETS;
+                    S.order(n, e, [&](u64 v) { return min(S.bin(logit_of((uint32_t)(v >> 32))) / (int)step, BUCKETS - 1); });
+                }
+                // a thread's two values of the list, in descending order
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int i = 2 * threadIdx.x + j;
+                    e[j] = i < n ? sm.sorted[i] : 0;
+                    w[j] = i < n && (!by_k || i < k) ? S.weight(logit_of((uint32_t)(e[j] >> 32))) : 0;
+                }
+                const u64 pre = S.block_scan(w[0] + w[1], listed);
+                if (by_k) {
+                    target = by_p ? share_of(listed, fmaxf(p, 0.0f), true) : listed;
+                    if (target < 1) target = 1;
+                }
+                const bool keep0 = w[0] && above + pre < target && (uint32_t)(e[0] >> 32) >= floor_;
+                const bool keep1 = w[1] && above + pre + w[0] < target && (uint32_t)(e[1] >> 32) >= floor_;
+                const int kept = __syncthreads_count(keep0) + __syncthreads_count(keep1);   // the first so many
+                if (how == WIDE) {
+                    // each of them adds to its warp's sum
+                    if (keep0) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[0]) / A.seg], w[0]);
+                    if (keep1) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[1]) / A.seg], w[1]);
+                    __syncthreads();
+                    border = hi + 1;                           // none of them: those above alone
+                    if (kept) {
+                        const u64 end = sm.sorted[kept - 1];
+                        border = (uint32_t)(end >> 32);
+                        last = (int)(0xFFFFFFFFu - (uint32_t)end);
+                    }
+                    S.finish(logit_of(border), last);
+                } else if (S.rank == 0) {
+                    // in the order of the indices: the index's complement first, downwards
+                    e[0] = keep0 ? e[0] << 32 | e[0] >> 32 : 0;
+                    e[1] = keep1 ? e[1] << 32 | e[1] >> 32 : 0;
+                    const uint32_t step = (uint32_t)(A.p.n - 1) / BUCKETS + 1;
+                    S.order(kept, e, [&](u64 v) { return (int)((0xFFFFFFFFu - (uint32_t)(v >> 32)) / step); });
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int i = 2 * threadIdx.x + j;
-                        e[j] = i < n ? sm.sorted[i] : 0;
-                        w[j] = i < n && (!by_k || i < k) ? S.weight(logit_of((uint32_t)(e[j] >> 32))) : 0;
+                        e[j] = i < kept ? sm.sorted[i] : 0;
+                        w[j] = i < kept ? S.weight(logit_of((uint32_t)e[j])) : 0;
                     }
-                    u64 listed;
-                    const u64 pre = S.block_scan(w[0] + w[1], listed);
-                    if (by_k) {
-                        target = by_p ? share_of(listed, fmaxf(p, 0.0f), true) : listed;
-                        if (target < 1) target = 1;
-                    }
-                    // (by the middles of the bins the border may seem to lie where it does not; a list that min_p has
-                    // cut short need not reach it)
-                    if (!by_k && (above >= target || (above + listed < target && lo > floor_))) {
-                        how = AGAIN;
-                    } else {
-                        const bool keep0 = w[0] && above + pre < target && (uint32_t)(e[0] >> 32) >= floor_;
-                        const bool keep1 = w[1] && above + pre + w[0] < target && (uint32_t)(e[1] >> 32) >= floor_;
-                        const int kept = __syncthreads_count(keep0) + __syncthreads_count(keep1);   // the first so many
-                        if (how == WIDE) {
-                            // each of them adds to its warp's sum
-                            if (keep0) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[0]) / A.seg], w[0]);
-                            if (keep1) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[1]) / A.seg], w[1]);
-                            __syncthreads();
-                            border = hi + 1;               // none of them: those above alone
-                            if (kept) {
-                                const u64 end = sm.sorted[kept - 1];
-                                border = (uint32_t)(end >> 32);
-                                last = (int)(0xFFFFFFFFu - (uint32_t)end);
-                            }
-                            S.finish(logit_of(border), last);
-                        } else if (S.rank == 0) {
-                            // in the order of the indices: the index's complement first, downwards
-                            e[0] = keep0 ? e[0] << 32 | e[0] >> 32 : 0;
-                            e[1] = keep1 ? e[1] << 32 | e[1] >> 32 : 0;
-                            const uint32_t step = (uint32_t)(A.p.n - 1) / BUCKETS + 1;
-                            S.order(kept, e, [&](u64 v) { return (int)((0xFFFFFFFFu - (uint32_t)(v >> 32)) / step); });
+                    u64 all, up = S.block_scan(w[0] + w[1], all);
+                    const u64 at = S.target_of(all);
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int i = 2 * threadIdx.x + j;
-                                e[j] = i < kept ? sm.sorted[i] : 0;
-                                w[j] = i < kept ? S.weight(logit_of((uint32_t)e[j])) : 0;
-                            }
-                            u64 all, up = S.block_scan(w[0] + w[1], all);
-                            const u64 at = S.target_of(all);
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                if (at >= up && at < up + w[j]) S.put((int)(0xFFFFFFFFu - (uint32_t)(e[j] >> 32)), quotient(w[j], all));
-                                up += w[j];
-                            }
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        if (at >= up && at < up + w[j]) S.put((int)(0xFFFFFFFFu - (uint32_t)(e[j] >> 32)), quotient(w[j], all));
+                        up += w[j];
                     }
                 }
+                break;
             }
             if (how == AGAIN) {
                 Sampler::Border B = {S.up_to(BINS) + 1, 0, 0};   // the lowest key with a weight

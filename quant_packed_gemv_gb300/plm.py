@@ -758,24 +758,27 @@ def plm_kv8_views(pool, kv_heads, page_tokens, head_dim):
     exponents of both, so that the page calls (plm_kv_state over the same pool) move them together."""
     import torch
     n, size = kv_heads * page_tokens * head_dim, plm_kv8_page_bytes(kv_heads, page_tokens, head_dim)
-    if head_dim % 32 or pool.dim() != 2 or pool.shape[1] < size or pool.dtype != torch.uint8 or pool.stride(1) != 1:
+    pages, width = pool.shape
+    if head_dim % 32 or width < size or pool.dtype != torch.uint8 or (width > 1 and pool.stride(1) != 1):
         raise ValueError("pool: expected uint8 [.][%d or more], and heads of a multiple of 32" % size)
-    e, pitch, at = n // 32, pool.stride(0), pool.storage_offset()
-    cs, es = (pitch, page_tokens * head_dim, head_dim, 1), (pitch, page_tokens * (head_dim // 32), head_dim // 32, 1)
-    pages, codes = pool.shape[0], pool.view(torch.int8)
-    code = lambda o: codes.as_strided((pages, kv_heads, page_tokens, head_dim), cs, at + o)  # noqa: E731
-    exps = lambda o: pool.as_strided((pages, kv_heads, page_tokens, head_dim // 32), es, at + o)  # noqa: E731
-    return code(0), code(n), exps(2 * n), exps(2 * n + e)
+    blocks, pitch, at, codes = head_dim // 32, pool.stride(0), pool.storage_offset(), pool.view(torch.int8)
+    shape, st = (pages, kv_heads, page_tokens, head_dim), (pitch, page_tokens * head_dim, head_dim, 1)
+    eshape, est, e = (pages, kv_heads, page_tokens, blocks), (pitch, page_tokens * blocks, blocks, 1), at + 2 * n
+    return (codes.as_strided(shape, st, at), codes.as_strided(shape, st, at + n), pool.as_strided(eshape, est, e),
+            pool.as_strided(eshape, est, e + n // 32))
 
 
 def _kv8_pages(codes, exps, name):
-    """Strides of 8-bit pages: of the codes, and the exponents' first two."""
+    """Strides of 8-bit pages: of the codes, and of the exponents."""
     import torch
+    cs, es, shape, eshape = codes.stride(), exps.stride(), codes.shape, exps.shape
     if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
         raise ValueError("%s: expected int8 codes and uint8 exponents" % name)
-    cs, es = _rows(codes, name, 4), _rows(exps, name + " exponents", 4)
-    blocks = codes.shape[3] // 32
-    if codes.shape[3] % 32 or exps.shape != codes.shape[:3] + (blocks,) or (es[2] != blocks and codes.shape[2] > 1):
+    if len(cs) != 4 or len(es) != 4 or cs[3] != 1 or es[3] != 1 or not (codes.is_cuda and exps.is_cuda):
+        _rows(codes, name, 4)   # an error, or a dimension of one: look closer
+        _rows(exps, name + " exponents", 4)
+    blocks = shape[3] // 32
+    if shape[3] % 32 or eshape[:3] != shape[:3] or eshape[3] != blocks or (es[2] != blocks and shape[2] > 1):
         raise ValueError("%s: expected exponents [pages][heads][page_tokens][head_dim / 32], a head's tokens dense" % name)
     return cs, es
 
@@ -784,13 +787,13 @@ def plm_kv8_tensor(rows, codes, exps, slots, rotate=True):
     """One tensor of a plm_kv8_write or plm_kv8_read call; it holds the tensors.  rows [tokens][heads][head_dim], codes and
     exps as plm_kv8_views gives them (any strided views), slots int64 [tokens]."""
     rt, rh, _ = _rows(rows, "rows", 3)
-    cs, es = _kv8_pages(codes, exps, "codes")
+    (cp, ch, ct, _), (ep, eh, _, _) = _kv8_pages(codes, exps, "codes")
     tokens, heads, d = rows.shape
     pages, cheads, page_tokens, cd = codes.shape
     if cheads != heads or cd != d:
         raise ValueError("codes: expected pages [.][%d][.][%d], got %s" % (heads, d, tuple(codes.shape)))
     return (_KV8_TENSOR.pack(rows.data_ptr(), codes.data_ptr(), exps.data_ptr(), _ints(slots, 64, "slots", (tokens,)), heads, rt, rh,
-                             page_tokens, pages, cs[0], cs[1], cs[2], es[0], es[1], _type(rows), 1 if rotate else 0),
+                             page_tokens, pages, cp, ch, ct, ep, eh, _type(rows), 1 if rotate else 0),
             tokens, d, (rows, codes, exps, slots), rotate)
 
 
@@ -808,7 +811,10 @@ def plm_kv8_write(tensors, positions=None, freqs=None, rotary_dim=0, layout="hal
     """Writes the tensors' rows (plm_kv8_tensor) to their slots in 8 bits, those with rotate turned by their positions
     (int32 [tokens]) first; see include/plm.h."""
     packed, tokens, d = _kv8_join(tensors)
-    if any(t[4] for t in tensors) and (positions is None or freqs is None or freqs.numel() != rotary_dim // 2):
+    turned = False
+    for t in tensors:
+        turned = turned or t[4]
+    if turned and (positions is None or freqs is None or freqs.numel() != rotary_dim // 2):
         raise ValueError("a tensor that rotates needs positions, and %d frequencies" % (rotary_dim // 2))
     if tokens == 0:
         return
@@ -863,11 +869,11 @@ def plm_attn_kv8(q, o, k, v, k_exps, v_exps, table, lens, tokens, prefix_len, ma
     _call(_ATTN_KV8, _ATTN_CALL.pack(ws, size, _stream(stream)) + p)
 
 
-def _per_row(t, name, m, code):
-    """Address of one value a row on the device, or 0."""
+def _per_row(t, name, m):
+    """Address of a float32 value a row on the device, or 0."""
     if t is None:
         return 0
-    if t.shape != (m,) or (_type(t) if code == PLM_F32 else code) != code:
+    if t.shape != (m,) or _type(t) != PLM_F32:
         raise ValueError("%s: expected float32 (%d,), got %s %s" % (name, m, t.dtype, tuple(t.shape)))
     return _addr(t)
 
@@ -878,7 +884,8 @@ def plm_sample(logits, tokens, u=None, temperature=None, top_k=None, top_p=None,
     probability with which it was met (see include/plm.h)."""
     stride, code = _matrix(logits, "logits")
     m, n = logits.shape
-    f = [_per_row(t, name, m, PLM_F32) for t, name in ((u, "u"), (temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (prob, "prob"))]
+    f = (_per_row(u, "u", m), _per_row(temperature, "temperature", m), _per_row(top_p, "top_p", m), _per_row(min_p, "min_p", m),
+         _per_row(prob, "prob", m))
     k, out = _ints(top_k, 32, "top_k", (m,)) or 0, _ints(tokens, 32, "tokens", (m,))
     if m == 0:
         return
