@@ -546,23 +546,23 @@ struct Sampler {
         }
         __syncthreads();
     }
-    // The first index at which the sum of f over the row exceeds `target`, which is
-    // less than the whole; in all lanes of one warp, -1 in the others.  The warps' sums
-    // are in sm.sums.  f: logit, index.
-    template <class F> __device__ int find(F f, u64 target) {
-        // the warp that has it
-        u64 pre = 0;
+    // The first index at which the sum of f over the row exceeds target_of(the whole),
+    // which is less than that; in all lanes of one warp, -1 in the others.  The warps'
+    // sums are in sm.sums.  f: logit, index.
+    template <class F, class G> __device__ int find(F f, G target_of) {
+        // the warp that has it: a lane adds up neighbouring ones
+        const int per = (cs * nw + 31) / 32;
+        u64 v = 0, pre;
+        for (int i = lane * per; i < min((lane + 1) * per, cs * nw); ++i) v += sm.sums[i];
+        const u64 in = warp_scan(v, lane);
+        const u64 target = target_of(__shfl_sync(0xFFFFFFFFu, in, 31));
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, in > target);
         int who = -1;
-        for (int i0 = 0; i0 < cs * nw && who < 0; i0 += 32) {
-            const u64 v = i0 + lane < cs * nw ? sm.sums[i0 + lane] : 0, all = warp_sum64(v);
-            if (pre + all > target) {
-                const u64 in = warp_scan(v, lane);
-                const int l = __ffs(__ballot_sync(0xFFFFFFFFu, pre + in > target)) - 1;
-                who = i0 + l;
-                pre += __shfl_sync(0xFFFFFFFFu, in - v, l);
-            } else {
-                pre += all;
-            }
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            who = l * per;
+            pre = __shfl_sync(0xFFFFFFFFu, in - v, l);
+            while (pre + sm.sums[who] <= target) pre += sm.sums[who++];
         }
         if (who < 0 || who / nw != rank) return -1;
         // its logits: 128 a warp of this CTA, in rounds
@@ -576,16 +576,16 @@ struct Sampler {
             __syncthreads();   // (what was there has been read)
             if (lane == 0) sm.scan[0][warp] = mine;
             __syncthreads();
-            const u64 v = lane < nw ? sm.scan[0][lane] : 0, here = pre + warp_sum64(lane < warp ? v : 0);
+            const u64 part = lane < nw ? sm.scan[0][lane] : 0, here = pre + warp_sum64(lane < warp ? part : 0);
             if (here <= target && target < here + mine) {
                 const u64 in = warp_scan(a + b + c + d, lane), before = here + in - (a + b + c + d);
                 const int l = __ffs(__ballot_sync(0xFFFFFFFFu, here + in > target)) - 1;
                 const int k = before + a > target ? 0 : before + a + b > target ? 1 : before + a + b + c > target ? 2 : 3;
                 return __shfl_sync(0xFFFFFFFFu, j + k, l);
             }
-            const u64 all = warp_sum64(v);
-            if (pre + all > target) return -1;   // (in another warp)
-            pre += all;
+            const u64 round = warp_sum64(part);
+            if (pre + round > target) return -1;   // (in another warp)
+            pre += round;
         }
         return -1;
     }
@@ -599,9 +599,8 @@ struct Sampler {
     // `last`; the warps' sums of their w's are in sm.sums.
     __device__ void finish(float border, int last) {
         u64 all = 0;
-        for (int i = lane; i < cs * nw; i += 32) all += sm.sums[i];
-        all = warp_sum64(all);
-        const int at = find([&](float x, int i) -> u64 { return x > border || (x == border && i <= last) ? weight(x) : 0; }, target_of(all));
+        const int at = find([&](float x, int i) -> u64 { return x > border || (x == border && i <= last) ? weight(x) : 0; },
+                            [&](u64 sum) { all = sum; return target_of(sum); });
         if (at >= 0 && lane == 0) {
             float x = value_at(A.p.logits, A.p.type, row * A.p.stride + at) + 0.0f;
             if (infinite) x = finite(x);
@@ -623,7 +622,7 @@ struct Sampler {
         u64 mine = 0;
         each([&](float x, int) { mine += x == border; });
         tell(warp_sum64(mine));
-        const int at = find([&](float x, int) -> u64 { return x == border; }, before);
+        const int at = find([&](float x, int) -> u64 { return x == border; }, [&](u64) { return before; });
         return (int)(0xFFFFFFFFu - (uint32_t)exchange<true>(at < 0 ? 0 : 0xFFFFFFFFu - (uint32_t)at));
     }
     // Empties the histogram, once every CTA has read it.
@@ -836,9 +835,10 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
         if (leader) S.put(-1, 0.0f);
     } else if (!(T > 0.0f) || !A.p.u) {
         uint32_t at = 0;   // the first index, as its complement
-        S.each([&](float x, int i) {
-            if (x == S.top) at = max(at, 0xFFFFFFFFu - (uint32_t)i);
-        });
+        if (__any_sync(0xFFFFFFFFu, best == S.top))   // (few warps)
+            S.each([&](float x, int i) {
+                if (x == S.top) at = max(at, 0xFFFFFFFFu - (uint32_t)i);
+            });
         at = (uint32_t)S.exchange<true>(at);
         if (leader) S.put((int)(0xFFFFFFFFu - at), 1.0f);
     } else {
