@@ -158,7 +158,7 @@ __device__ __forceinline__ u64 share_of(u64 v, float a, bool up) {
     }
     return q + (up && rest);
 }
-// w / all, w <= all: the f32 quotient, corrected once.
+// w / all, w below 2^63: the f32 quotient, corrected once.
 __device__ __forceinline__ float quotient(u64 w, u64 all) {
     const float w1 = __ull2float_rn(w), w2 = __ll2float_rn((long long)(w - (u64)w1));
     const float a1 = __ull2float_rn(all), a2 = __ll2float_rn((long long)(all - (u64)a1));
@@ -225,24 +225,31 @@ struct Sampler {
         const float s = steps((x - base) * c_hi);
         return weighs(s) ? bin_of(s) : BINS;
     }
-    // 2^(40 - f/64 - r)
-    __device__ __forceinline__ u64 power(uint32_t f, float r) const {
-        const float e = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);   // 2^-r - 1, below 2^-7
+    // 2^(60 - (f mod 64)/64 - r), and 2^(40 - f/64 - r).  2^-r - 1 (below 2^-7) in steps of 2^-29 is the rounding that
+    // counts: 2^-30; the series before it is good to 2^-31, the 28 bits of the table that it is multiplied by to 2^-34
+    __device__ __forceinline__ u64 power_of_rest(uint32_t f, float r) const {
+        constexpr float S = 536870912.0f;   // 2^29
+        const float s = fmaf(r, fmaf(r, fmaf(r, -0.0555041087f * S, 0.240226507f * S), -0.693147181f * S), MAGIC);
         const u64 v = sm.table[f & 63][lane & 15];
-        // v e in steps of 2^11, with v's 24 leading bits: v / 2^11 as f32
-        const float lead = __uint_as_float(((uint32_t)(v >> 16) & 0x7FFFFFu) | (uint32_t)(127 + 28) << 23);
-        const int more = bin_of(fmaf(lead, e, MAGIC));
-        return (v + (u64)((long long)more * 2048)) >> (f >> 6);
+        return v + (u64)((long long)(int)(v >> 32) * (8 * bin_of(s)));
     }
-    __device__ __forceinline__ u64 middle(int f) const { return sm.table[f & 63][lane & 15] >> (f >> 6); }
-    __device__ __forceinline__ u64 weight(float x, float p, float s) const {
+    __device__ __forceinline__ u64 power(uint32_t f, float r) const { return power_of_rest(f, r) >> (20 + (f >> 6)); }
+    __device__ __forceinline__ u64 middle(int f) const { return sm.table[f & 63][lane & 15] >> (20 + (f >> 6)); }
+    __device__ __forceinline__ float rest(float x, float p, float s) const {
         const float y = fmaf(s - MAGIC, -0.015625f, ref);       // ref - f/64, exact
-        const float r = fmaf(x, -c_lo, (y - p) - fmaf(x, c_hi, -p));
-        return power(bin_of(s), r);
+        return fmaf(x, -c_lo, (y - p) - fmaf(x, c_hi, -p));
     }
+    __device__ __forceinline__ u64 weight(float x, float p, float s) const { return power(bin_of(s), rest(x, p, s)); }
     __device__ __forceinline__ u64 weight(float logit) const {   // 0 where there is none
         const float x = logit - base, p = x * c_hi, s = steps(p);
         return weighs(s) ? weight(x, p, s) : 0;
+    }
+    // The share of a logit that has a weight in `all`.  Of a small w the bits below 1,
+    // which the sums leave out, count here.
+    __device__ __forceinline__ float chance(float logit, u64 all) const {
+        const float x = logit - base, p = x * c_hi, s = steps(p);
+        const int f = bin_of(s);
+        return quotient(power_of_rest(f, rest(x, p, s)), all) * __uint_as_float((uint32_t)(127 - 20 - (f >> 6)) << 23);
     }
 
     // Sum, or maximum (of 32 bits), of the threads' v over the row.
@@ -604,7 +611,7 @@ struct Sampler {
         if (at >= 0 && lane == 0) {
             float x = value_at(A.p.logits, A.p.type, row * A.p.stride + at) + 0.0f;
             if (infinite) x = finite(x);
-            put(at, quotient(weight(x), all));
+            put(at, chance(x, all));
         }
     }
 
@@ -703,7 +710,7 @@ struct Sampler {
                             const uint32_t k1 = hi - ((uint32_t)b << shift), left = k1 - lo, k0 = left >> shift ? k1 - (1u << shift) + 1 : lo;
                             w1 = weight(logit_of(k1));
                             w0 = k0 == k1 ? w1 : weight(logit_of(k0));
-                            if (k0 != k1) {   // w is right to 2^-28, and may fall by that where it should rise
+                            if (k0 != k1) {   // w is right to 2^-29, and may fall by that where it should rise
                                 w1 += (w1 >> 26) + 1;
                                 w0 -= w0 >> 26;
                             }
@@ -792,7 +799,7 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
     S.turn = S.owned = 0;
     S.infinite = false;
     S.held = reinterpret_cast<float*>(sample_raw + sizeof(SampleSmem)) + S.warp * A.held;
-    for (int i = threadIdx.x; i < 64 * 16; i += S.nt) sm.table[i / 16][i % 16] = EXP_TABLE[i / 16];
+    for (int i = threadIdx.x; i < 64 * 16; i += S.nt) sm.table[i / 16][i % 16] = EXP_TABLE[i / 16] << 20;
     for (int i = threadIdx.x; i < GROUPS; i += S.nt) sm.group[i] = sm.group_sum[i] = 0;
     if (threadIdx.x == 0) sm.listed = 0;
     for (int i = threadIdx.x; i < BINS / 4; i += S.nt) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
@@ -1015,7 +1022,7 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
                     const u64 at = S.target_of(all);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        if (at >= up && at < up + w[j]) S.put((int)(0xFFFFFFFFu - (uint32_t)(e[j] >> 32)), quotient(w[j], all));
+                        if (at >= up && at < up + w[j]) S.put((int)(0xFFFFFFFFu - (uint32_t)(e[j] >> 32)), S.chance(logit_of((uint32_t)e[j]), all));
                         up += w[j];
                     }
                 }

@@ -1,9 +1,10 @@
 """The sampler on the GPU against its definition in f64, row by row.
 
-Tokens have to be equal.  A weight is off by 2^-30 of itself, or 2^-40 of the largest, at most, a sum of n by n 2^-40 of the
+Tokens have to be equal.  A weight is off by 2^-29 of itself, or 2^-40 of the largest, at most, a sum of n by n 2^-40 of the
 largest besides.  So a token may differ only where u, top_p or min_p lies within that of a border: 1e-8 of the sum for the
 rows here.  For such a row (none is expected among the seeds used, and the reference says if one is) the neighbour is right too.
-prob is a quotient of two such sums, rounded once: 2^-28 + 2^-24 of itself, and n 2^-40 where it is small."""
+prob is a quotient of a weight and such a sum, rounded once: 2^-28 + 2^-24 of itself, and n 2^-40 where it is small.  A small
+weight's own bits below 2^-40 are not lost in it."""
 import math
 
 import numpy as np
@@ -117,6 +118,17 @@ def test_flat_and_peaked_rows(spread, params):
 @pytest.mark.parametrize("params", [dict(), dict(top_k=50), dict(top_p=0.9), dict(top_k=300, top_p=0.8, min_p=0.01), dict(temperature=0.0)])
 def test_16_bit_logits_have_many_ties(dtype, params):
     Rows(normal(2, 30, 9000, 1.0), dtype=T[dtype], **params).check()
+
+
+def test_probability_of_a_small_weight_keeps_its_bits():
+    # One token of weight 1 and one of 2^-32 or so, which u = 1 takes.  The weight is off by 2^-29 of itself, the sum, 1 + 2^-32,
+    # by 2^-29 too (the large one is exact but for 2^-40), and the quotient is rounded once: 2^-24 + 2^-28
+    for z in (-10.0, -17.3, -22.1803, -25.0, -27.5):
+        r = Rows(np.array([[0.0, z, -math.inf]] * 2, np.float32), u=1.0)
+        tokens, prob = r.run()
+        want = math.exp(float(np.float32(z))) / (1 + math.exp(float(np.float32(z))))
+        assert tokens.tolist() == [1, 1]
+        assert abs(float(prob[0]) - want) <= (2.0 ** -24 + 2.0 ** -28) * want, (z, prob[0], want)
 
 
 def test_ties_go_to_the_lowest_index():
