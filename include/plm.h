@@ -784,7 +784,7 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
  * sum may be x or residual, and y x or residual (an output that is also an
  * input has the input's type and stride); nothing else may overlap.  m = 0
  * does nothing.  PLM_ERR_INVALID_ARG: null x, neither xq nor y, sum without
- * residual, m < 0, k < 1, m or k past int32, eps negative or NaN, unknown types, a
+ * residual, m < 0 or past int32, k < 1 or past 2^30, eps negative or NaN, unknown types, a
  * row stride below k with m > 1, xq with k % 256 != 0, an output in place of an input of
  * another type or stride, sum = y.
  */

@@ -703,7 +703,8 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
 
 plm_status plm_rmsnorm(const plm_rmsnorm_problem* p, cudaStream_t stream) {
     if (!p || !p->x || (!p->xq && !p->y) || (p->sum && !p->residual)) return PLM_ERR_INVALID_ARG;
-    if (!in_range(p->m, 0, kMaxIndex) || !in_range(p->k, 1, kMaxIndex) || !(p->eps >= 0.0f)) return PLM_ERR_INVALID_ARG;
+    // (k: indices of a row stay in 32 bits, a chunk beyond its end too)
+    if (!in_range(p->m, 0, kMaxIndex) || !in_range(p->k, 1, 1 << 30) || !(p->eps >= 0.0f)) return PLM_ERR_INVALID_ARG;
     struct Part { const void* p; int64_t stride; int type; };
     const Part x = {p->x, p->x_stride, p->x_type}, r = {p->residual, p->residual_stride, p->r_type}, w = {p->weight, p->k, p->w_type},
                s = {p->sum, p->sum_stride, p->r_type}, y = {p->y, p->y_stride, p->y_type};

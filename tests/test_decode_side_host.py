@@ -33,6 +33,8 @@ def test_norm_refusals():
         assert st(**bad) == BAD, bad
     for bad in (dict(x=A + 2), dict(residual=A + 1), dict(weight=A + 2), dict(sum=A + 3), dict(xq=A + 2), dict(y=A + 4097, y_type=1)):
         assert st(**bad) == MIS, bad
+    wide = dict(x_stride=1 << 31, residual_stride=1 << 31, sum_stride=1 << 31)
+    assert st(m=0, k=1 << 30, **wide) == OK and st(m=0, k=(1 << 30) + 256, **wide) == BAD and st(m=1, k=(1 << 31) - 256, **wide) == BAD
     assert st(m=0) == OK
     assert st(m=0, sum=A) == OK and st(m=0, sum=A + (1 << 16)) == OK and st(m=0, y=A) == OK   # in place
     assert st(m=0, weight=None, w_type=9, residual=None, sum=None, r_type=9) == OK             # types of what is not there
