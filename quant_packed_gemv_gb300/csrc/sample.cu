@@ -6,7 +6,7 @@
 // whole f: f from the f32 product p of x and c = log2(e) / T, r from what is left,
 // which f32 subtraction gives exactly, and p's own rounding error.  2^-t is a
 // table's 2^(-i/64), a shift, and the series of 2^-r (a table-driven exponential as
-// in P. T. P. Tang, ACM TOMS 15, 1989), to 2^-28 of itself.  Sums of whole numbers
+// in P. T. P. Tang, ACM TOMS 15, 1989), to 2^-29 of itself.  Sums of whole numbers
 // do not depend on their order, so which token is met does not depend on the launch.
 //   A border (the k-th largest logit; the one at which the sum of the w's in
 // descending order reaches p of all) is found without sorting the row: f is the
@@ -18,7 +18,15 @@
 //
 // Layout.  A cluster of CTAs takes a row, each a piece of it in shared memory, so
 // the row is read once.  What does not fit is read again from L2.  A warp has
-// consecutive logits, so the sums of the warps say in which of them the token is.
+// consecutive logits, so the sums of the warps, which every CTA gets, say in which of
+// them the token is.
+//   What bounds it.  A row takes 3 (greedy) to 10 barriers of its cluster and 40
+// instructions a logit for each time its weights are formed (once without top-k and
+// top-p, up to three times with a top-p of many tokens); the read of the row hides behind
+// that.  One GB300, f32 logits, spread 2.5, us: 256 rows of 151936 (23 for the read alone)
+// greedy 48, no limits 117, min-p 77, top-k 40 147, with top-p 158, top-p 0.9 alone 196 to
+// 252; one row of them greedy 4.5, 13, 11, 17, 18, 26; 64 rows of 32000 4.6, 11, 10, 17, 18,
+// 25 to 50 (rows whose border the bins do not settle).
 #include "plm_device.cuh"
 #include "plm_internal.h"
 #include "values.cuh"
@@ -29,7 +37,7 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int MOST_THREADS = 1024, MOST_WARPS = MOST_THREADS / 32;   // of a CTA; 512 at least
+constexpr int NT = 512, NW = NT / 32;         // threads and warps of a CTA
 constexpr int BINS = 2560;                   // f of a logit with a weight: t below 40
 constexpr int COARSE = 16, GROUPS = BINS / COARSE;   // bins that are first looked at together
 constexpr int LIST = 1024;                   // logits that are put in order at most
@@ -59,7 +67,7 @@ __device__ const u64 EXP_TABLE[64] = {
     0x85AAC367CCull, 0x843A28C3ACull, 0x82CD8698ABull, 0x8164D1F3BBull,
 };
 
-// Logits as integers in their order, and back.
+// Logits as integers in their order (-0 is added to 0 before), and back.
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = __float_as_uint(x);
     return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
@@ -71,12 +79,10 @@ __device__ __forceinline__ float nothing() { return __uint_as_float(0x7FFFFFFFu)
 
 struct alignas(16) SampleSmem {
     u64 table[64][16];                           // a copy for every pair of banks
-    u64 part[2][MOST_WARPS], slot[2][MOST_CS];   // of an exchange, in turn
-    u64 own[2][MOST_WARPS];                      // the warps' sums, in turn
-    u64 scan[2][MOST_WARPS];
-    u64 sums[MOST_CS * MOST_WARPS];              // the same of all warps of the row
+    u64 part[2][NW], slot[2][MOST_CS];   // of an exchange, in turn
+    u64 scan[2][NW];
     u64 group_sum[GROUPS];                       // of the row's logits, by the bins' middles
-    u64 found_sum;
+    u64 found_sum, run[2];
     uint32_t group[GROUPS];                      // the row's logits
     uint32_t near[MOST_CS][32];                  // of a group's bins and those beside it, by CTA
     uint32_t found[8];
@@ -89,7 +95,9 @@ struct alignas(16) SampleSmem {
         };
     };
     u64 list[LIST];
+    // behind it: the sums of the row's warps, in turn; the row
 };
+__host__ __device__ constexpr size_t fixed_bytes(int warps) { return sizeof(SampleSmem) + 2 * sizeof(u64) * warps; }   // warps: of the row
 
 // (in parts whose sums fit 32 bits: an instruction each)
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -138,6 +146,11 @@ __device__ __forceinline__ void add_at_peer(uint32_t* p, int z, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" :: "r"(at_peer(p, z)), "r"(v) : "memory");
 }
 
+// Sixteen bytes from global memory, on their way
+__device__ __forceinline__ void cp_async16(float* to, const float* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(to)), "l"(from) : "memory");
+}
+
 // Floor and ceiling of v a for 0 <= a < 1, v below 2^63.
 __device__ __forceinline__ u64 share_of(u64 v, float a, bool up) {
     const uint32_t b = __float_as_uint(a);
@@ -172,20 +185,20 @@ struct Sampler {
     SampleSmem& sm;
     float* held;                // this warp's logits, the first A.held
     long long row;
-    int lane, warp, nw, nt, cs, rank, first;         // first: index of the warp's first logit
+    int lane, warp, cs, rank, first;                 // first: index of the warp's first logit
     int turn, owned;
     float top, u;
     float base, c_hi, c_lo, ref, ref64;              // t = ref - (x - base) (c_hi + c_lo)
     bool infinite;                                   // the largest logits are +inf: they are 0, the others nothing
 
-    // Four logits from index i on; -0 becomes 0
+    // Four logits from index i on
     __device__ __forceinline__ float4 load(int i) const {
         const long long n = A.p.n - i;
         float4 v = load_four(A.p.logits, A.p.type, row * A.p.stride + i, n < 4 ? (int)n : 4, A.four && n >= 4);
-        v.x = n > 0 ? v.x + 0.0f : nothing();
-        v.y = n > 1 ? v.y + 0.0f : nothing();
-        v.z = n > 2 ? v.z + 0.0f : nothing();
-        v.w = n > 3 ? v.w + 0.0f : nothing();
+        v.x = n > 0 ? v.x : nothing();
+        v.y = n > 1 ? v.y : nothing();
+        v.z = n > 2 ? v.z : nothing();
+        v.w = n > 3 ? v.w : nothing();
         return v;
     }
     __device__ __forceinline__ float finite(float x) const { return x == INFINITY ? 0.0f : nothing(); }
@@ -239,10 +252,44 @@ struct Sampler {
         const float y = fmaf(s - MAGIC, -0.015625f, ref);       // ref - f/64, exact
         return fmaf(x, -c_lo, (y - p) - fmaf(x, c_hi, -p));
     }
-    __device__ __forceinline__ u64 weight(float x, float p, float s) const { return power(bin_of(s), rest(x, p, s)); }
+    // w of any logit, to be used where `there`: without a branch, so that those of
+    // several logits are worked out side by side
+    __device__ __forceinline__ u64 weight(float logit, bool& there, int& b) const {
+        const float x = logit - base, p = x * c_hi, s = steps(p), in = fminf(s, MAGIC + (float)BINS);   // (NaN: BINS)
+        there = weighs(s);
+        b = bin_of(in);
+        return power(b, rest(x, p, in));
+    }
+    __device__ __forceinline__ u64 weight(float logit, bool& there) const {
+        int b;
+        return weight(logit, there, b);
+    }
     __device__ __forceinline__ u64 weight(float logit) const {   // 0 where there is none
-        const float x = logit - base, p = x * c_hi, s = steps(p);
-        return weighs(s) ? weight(x, p, s) : 0;
+        bool there;
+        const u64 w = weight(logit, there);
+        return there ? w : 0;
+    }
+    // The sum of the w's of this warp's logits that keep(logit, index) takes, a lane's part of it
+    template <class F> __device__ __forceinline__ u64 weights(F keep) const {
+        const int end = length(first);
+        u64 sum = 0;
+#pragma unroll 2
+        for (int i = 0; i < end; i += 128) {
+            const float4 v = four(held, first, i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            const int at = first + i + 4 * lane;
+            bool in[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) in[j] = keep(x[j], at + j);
+            if (!__any_sync(0xFFFFFFFFu, in[0] || in[1] || in[2] || in[3])) continue;   // (min_p leaves few)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bool there;
+                const u64 w = weight(x[j], there);
+                if (there && in[j]) sum += w;
+            }
+        }
+        return sum;
     }
     // The share of a logit that has a weight in `all`.  Of a small w the bits below 1,
     // which the sums leave out, count here.
@@ -260,7 +307,7 @@ struct Sampler {
         v = warps(v);
         if (lane == 0) sm.part[b][warp] = v;
         __syncthreads();
-        if (cs == 1 || warp == 0) v = warps(lane < nw ? sm.part[b][lane] : 0);
+        if (cs == 1 || warp == 0) v = warps(lane < NW ? sm.part[b][lane] : 0);
         if (cs == 1) return v;
         if (warp == 0 && lane < cs) to_peer64(&sm.slot[b][rank], lane, v);
         together();
@@ -272,7 +319,7 @@ struct Sampler {
         __syncthreads();   // (what was there has been read)
         if (lane == 31) sm.scan[0][warp] = in;
         __syncthreads();
-        const u64 x = lane < nw ? sm.scan[0][lane] : 0;
+        const u64 x = lane < NW ? sm.scan[0][lane] : 0;
         all = warp_sum64(x);
         return in - v + warp_sum64(lane < warp ? x : 0);
     }
@@ -305,7 +352,7 @@ struct Sampler {
     // Adds the histogram's bins up in groups, at every CTA (complete after a barrier).
     __device__ __forceinline__ void add_groups(bool sum) {
         __syncthreads();
-        for (int at = 0; at < BINS; at += 4 * nt) {   // four bins a thread, a group in four lanes
+        for (int at = 0; at < BINS; at += 4 * NT) {   // four bins a thread, a group in four lanes
             const int b = at + 4 * (int)threadIdx.x;
             if (b >= BINS) break;                     // (whole warps)
             const uint4 c = *reinterpret_cast<const uint4*>(sm.hist + b);
@@ -472,7 +519,7 @@ struct Sampler {
                 int at = 0;
                 if (lane == 0) at = atomicAdd(&sm.listed, __popc(who));
                 at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1));
-                if (in && at < LIST) sm.list[at] = (u64)key_of(x[j]) << 32 | (0xFFFFFFFFu - (uint32_t)(first + i + 4 * lane + j));
+                if (in && at < LIST) sm.list[at] = (u64)key_of(x[j] + 0.0f) << 32 | (0xFFFFFFFFu - (uint32_t)(first + i + 4 * lane + j));
             }
         }
         put_own(warp_sum64(above));
@@ -481,14 +528,14 @@ struct Sampler {
         parts = min(n, LIST + 1);
         return __reduce_add_sync(0xFFFFFFFFu, parts);
     }
-    // Values threadIdx.x and threadIdx.x + nt of all lists (0 past the n)
+    // Values threadIdx.x and threadIdx.x + NT of all lists (0 past the n)
     __device__ void bring(int n, int parts, u64 (&e)[2]) const {
         int end[MOST_CS];   // of the lists, one after the other
 #pragma unroll
         for (int z = 0; z < MOST_CS; ++z) end[z] = __shfl_sync(0xFFFFFFFFu, parts, z) + (z ? end[z ? z - 1 : 0] : 0);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int i = threadIdx.x + k * nt;
+            const int i = threadIdx.x + k * NT;
             int z = 0, from = 0;
 #pragma unroll
             for (int j = 0; j < MOST_CS - 1; ++j)
@@ -536,31 +583,27 @@ struct Sampler {
         __syncthreads();
     }
 
-    // The warps' sums of the whole row into sm.sums.
+    // The warps' sums into every CTA's sums() (complete once all are together; what was
+    // there a turn ago may still be read).
+    __device__ void put_own(u64 mine) {
+        ++owned;
+        u64* at = &sums()[rank * NW + warp];
+        if (cs == 1 && lane == 0) *at = mine;
+        if (cs > 1 && lane < cs) to_peer64(at, lane, mine);
+    }
+    __device__ __forceinline__ u64* sums() const { return reinterpret_cast<u64*>(&sm + 1) + (owned & 1 ? cs * NW : 0); }
     __device__ void tell(u64 mine) {
         put_own(mine);
         together();
-        gather();
-    }
-    __device__ void put_own(u64 mine) {   // (what a turn ago was written may still be read)
-        ++owned;
-        if (lane == 0) sm.own[owned & 1][warp] = mine;
-    }
-    __device__ void gather() {
-        for (int i = threadIdx.x; i < cs * nw; i += nt) {
-            const int z = i / nw;
-            sm.sums[i] = cs > 1 ? peer64(&sm.own[owned & 1][i - z * nw], z) : sm.own[owned & 1][i];
-        }
-        __syncthreads();
     }
     // The first index at which the sum of f over the row exceeds target_of(the whole),
     // which is less than that; in all lanes of one warp, -1 in the others.  The warps'
-    // sums are in sm.sums.  f: logit, index.
+    // sums are in sums().  f: logit, index.
     template <class F, class G> __device__ int find(F f, G target_of) {
         // the warp that has it: a lane adds up neighbouring ones
-        const int per = (cs * nw + 31) / 32;
+        const int per = (cs * NW + 31) / 32;
         u64 v = 0, pre;
-        for (int i = lane * per; i < min((lane + 1) * per, cs * nw); ++i) v += sm.sums[i];
+        for (int i = lane * per; i < min((lane + 1) * per, cs * NW); ++i) v += sums()[i];
         const u64 in = warp_scan(v, lane);
         const u64 target = target_of(__shfl_sync(0xFFFFFFFFu, in, 31));
         const unsigned hit = __ballot_sync(0xFFFFFFFFu, in > target);
@@ -569,13 +612,13 @@ struct Sampler {
             const int l = __ffs(hit) - 1;
             who = l * per;
             pre = __shfl_sync(0xFFFFFFFFu, in - v, l);
-            while (pre + sm.sums[who] <= target) pre += sm.sums[who++];
+            while (pre + sums()[who] <= target) pre += sums()[who++];
         }
-        if (who < 0 || who / nw != rank) return -1;
+        if (who < 0 || who / NW != rank) return -1;
         // its logits: 128 a warp of this CTA, in rounds
-        const int w = who - rank * nw, at = who * A.seg, end = length(at);
+        const int w = who - rank * NW, at = who * A.seg, end = length(at);
         const float* const theirs = held + (w - warp) * A.held;
-        for (int i0 = 0; i0 < end; i0 += 128 * nw) {
+        for (int i0 = 0; i0 < end; i0 += 128 * NW) {
             const int i = i0 + 128 * warp, j = at + i + 4 * lane;
             float4 x = make_float4(nothing(), nothing(), nothing(), nothing());
             if (i < end) x = four(theirs, at, i);
@@ -583,7 +626,7 @@ struct Sampler {
             __syncthreads();   // (what was there has been read)
             if (lane == 0) sm.scan[0][warp] = mine;
             __syncthreads();
-            const u64 part = lane < nw ? sm.scan[0][lane] : 0, here = pre + warp_sum64(lane < warp ? part : 0);
+            const u64 part = lane < NW ? sm.scan[0][lane] : 0, here = pre + warp_sum64(lane < warp ? part : 0);
             if (here <= target && target < here + mine) {
                 const u64 in = warp_scan(a + b + c + d, lane), before = here + in - (a + b + c + d);
                 const int l = __ffs(__ballot_sync(0xFFFFFFFFu, here + in > target)) - 1;
@@ -603,7 +646,7 @@ struct Sampler {
         if (A.p.prob) A.p.prob[row] = prob;
     }
     // The token, of the logits above `border` and those equal to it up to index
-    // `last`; the warps' sums of their w's are in sm.sums.
+    // `last`; the warps' sums of their w's are in sums().
     __device__ void finish(float border, int last) {
         u64 all = 0;
         const int at = find([&](float x, int i) -> u64 { return x > border || (x == border && i <= last) ? weight(x) : 0; },
@@ -618,11 +661,7 @@ struct Sampler {
     // ------------------------------------------------ rows that the histogram does not settle
     // The w's sum of the logits from `from` on.
     __device__ u64 total(float from) {
-        u64 v = 0;
-        each([&](float x, int) {
-            if (x >= from) v += weight(x);
-        });
-        return exchange<false>(v);
+        return exchange<false>(weights([&](float x, int) { return x >= from; }));
     }
     // The index of the logit equal to `border` that `before` equal ones precede.
     __device__ int tie_at(float border, u64 before) {
@@ -635,7 +674,7 @@ struct Sampler {
     // Empties the histogram, once every CTA has read it.
     __device__ __forceinline__ void empty() const {
         together();
-        for (int i = threadIdx.x; i < BINS / 4; i += nt) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < BINS / 4; i += NT) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
     // Four bins of the row's histogram (after a barrier)
@@ -682,13 +721,13 @@ struct Sampler {
             const float hi_x = logit_of(hi), lo_x = logit_of(lo);
             each([&](float x, int) {
                 if (x > hi_x) mine += mass ? weight(x) : 1;
-                else if (x >= lo_x) atomicAdd(&sm.hist[place(key_of(x))], 1u);
+                else if (x >= lo_x) atomicAdd(&sm.hist[place(key_of(x + 0.0f))], 1u);
             });
             const u64 above = exchange<false>(mine);
             // a thread's bins, four at a time: how many, and the bounds of their sums
             u64 up_run = above, down_run = above;
             if (threadIdx.x == 0) { sm.found[0] = BINS; sm.found[1] = BINS; sm.found[4] = 0; }
-            for (int at = 0; at < BINS; at += 4 * nt) {
+            for (int at = 0; at < BINS; at += 4 * NT) {
                 const int b0 = at + 4 * (int)threadIdx.x;
                 uint32_t n[4] = {0, 0, 0, 0};
                 u64 most[4], least[4], up = 0, down = 0;
@@ -723,7 +762,7 @@ struct Sampler {
                 }
                 u64 up_at = up, down_at = down;
                 block_scan_two(up_at, down_at);
-                if (threadIdx.x == nt - 1) { sm.sums[0] = up_at + up; sm.sums[1] = down_at + down; }
+                if (threadIdx.x == NT - 1) { sm.run[0] = up_at + up; sm.run[1] = down_at + down; }
                 up_at += up_run;
                 down_at += down_run;
                 // the first bin whose upper bound reaches the target, the first whose lower bound does
@@ -742,8 +781,8 @@ struct Sampler {
                     down_at += least[j];
                 }
                 __syncthreads();
-                up_run += sm.sums[0];
-                down_run += sm.sums[1];
+                up_run += sm.run[0];
+                down_run += sm.run[1];
             }
             const int last = (int)sm.found[4], b1 = min((int)sm.found[0], last), b2 = min((int)sm.found[1], last);
             const uint32_t count = sm.found[2];
@@ -783,27 +822,35 @@ struct Sampler {
 };
 
 // CTA (row, , rank in the row's cluster).
-__global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_constant__ SampleArgs A) {
+__global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ SampleArgs A) {
     extern __shared__ __align__(16) uint8_t sample_raw[];
     SampleSmem& sm = *reinterpret_cast<SampleSmem*>(sample_raw);
     grid_launch_dependents();
+    if (gridDim.z > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // waited for before peers are written to
     Sampler S{A, sm};
     S.row = blockIdx.x;
     S.lane = threadIdx.x & 31;
     S.warp = threadIdx.x >> 5;
-    S.nt = blockDim.x;
-    S.nw = S.nt >> 5;
     S.cs = gridDim.z;
     S.rank = blockIdx.z;
-    S.first = (int)min((long long)(S.rank * S.nw + S.warp) * A.seg, (long long)A.p.n);
+    S.first = (int)min((long long)(S.rank * NW + S.warp) * A.seg, (long long)A.p.n);
     S.turn = S.owned = 0;
     S.infinite = false;
-    S.held = reinterpret_cast<float*>(sample_raw + sizeof(SampleSmem)) + S.warp * A.held;
-    for (int i = threadIdx.x; i < 64 * 16; i += S.nt) sm.table[i / 16][i % 16] = EXP_TABLE[i / 16] << 20;
-    for (int i = threadIdx.x; i < GROUPS; i += S.nt) sm.group[i] = sm.group_sum[i] = 0;
-    if (threadIdx.x == 0) sm.listed = 0;
-    for (int i = threadIdx.x; i < BINS / 4; i += S.nt) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+    S.held = reinterpret_cast<float*>(sample_raw + fixed_bytes(S.cs * NW)) + S.warp * A.held;
+    // The row's copy into shared memory, under way while the rest of it is made ready
+    const int end = S.length(S.first), copied = A.four && A.p.type == PLM_F32 ? min(end, A.held) : 0;
     grid_wait_prior();
+    {
+        const float* const from = static_cast<const float*>(A.p.logits) + S.row * A.p.stride + S.first;
+        for (int i = 4 * S.lane; i < ((copied + 127) & ~127); i += 128)
+            if (i + 4 <= copied) cp_async16(S.held + i, from + i);
+            else
+                for (int j = i; j < i + 4; ++j) S.held[j] = j < copied ? from[j] : nothing();
+    }
+    for (int i = threadIdx.x; i < 64 * 16; i += NT) sm.table[i / 16][i % 16] = EXP_TABLE[i / 16] << 20;
+    for (int i = threadIdx.x; i < GROUPS; i += NT) sm.group[i] = sm.group_sum[i] = 0;
+    if (threadIdx.x == 0) sm.listed = 0;
+    for (int i = threadIdx.x; i < BINS / 4; i += NT) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
     const float T = A.p.temperature ? A.p.temperature[S.row] : 1.0f;
     const int k = A.p.top_k ? A.p.top_k[S.row] : 0;
     const float p = A.p.top_p ? A.p.top_p[S.row] : 1.0f, low = A.p.min_p ? A.p.min_p[S.row] : 0.0f;
@@ -811,22 +858,13 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
     // the row, and its largest logit
     float best = -INFINITY;
     {
-        const int end = S.length(S.first);
         constexpr int AHEAD = 5;   // loads in flight
 #pragma unroll 1
-        for (int i0 = 0; i0 < end; i0 += 128 * AHEAD) {
+        for (int i0 = (copied + 127) & ~127; i0 < end; i0 += 128 * AHEAD) {
             float4 v[AHEAD];
-            if (A.four && A.p.type == PLM_F32 && i0 + 128 * AHEAD <= end) {   // whole: nothing between the loads
-                const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(A.p.logits) + S.row * A.p.stride + S.first + i0) + S.lane;
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) v[j] = at[32 * j];
-#pragma unroll
-                for (int j = 0; j < AHEAD; ++j) v[j] = make_float4(v[j].x + 0.0f, v[j].y + 0.0f, v[j].z + 0.0f, v[j].w + 0.0f);
-            } else {
-#pragma unroll
-                for (int j = 0; j < AHEAD; ++j)
-                    v[j] = i0 + 128 * j < end ? S.load(S.first + i0 + 128 * j + 4 * S.lane) : make_float4(nothing(), nothing(), nothing(), nothing());
-            }
+            for (int j = 0; j < AHEAD; ++j)
+                v[j] = i0 + 128 * j < end ? S.load(S.first + i0 + 128 * j + 4 * S.lane) : make_float4(nothing(), nothing(), nothing(), nothing());
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int i = i0 + 128 * j;
@@ -834,8 +872,16 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
                 best = fmaxf(fmaxf(best, fmaxf(v[j].x, v[j].y)), fmaxf(v[j].z, v[j].w));   // (NaN counts for nothing)
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < copied; i += 128) {
+            const float4 v = *reinterpret_cast<const float4*>(S.held + i + 4 * S.lane);
+            best = fmaxf(fmaxf(best, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+        }
     }
-    const uint32_t most = (uint32_t)S.exchange<true>(key_of(best));
+    if (S.cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // all CTAs of the row have begun
+    const uint32_t most = (uint32_t)S.exchange<true>(key_of(best + 0.0f));
     S.top = logit_of(most);
     const bool leader = S.rank == 0 && threadIdx.x == 0;
     if (most <= LOWEST) {
@@ -885,13 +931,22 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
         if (by_k || by_p) {
             // The histogram; for top_p alone also the sum of all w's
             u64 mine = 0;
-            S.each([&](float logit, int) {
-                const float x = logit - S.base, v = x * S.c_hi, s = S.steps(v);
-                if (S.weighs(s)) {
-                    atomicAdd(&sm.hist[S.bin_of(s)], 1u);
-                    if (!by_k) mine += S.weight(x, v, s);
-                }
-            });
+            if (by_k) {
+                S.each([&](float x, int) {
+                    const float s = S.steps((x - S.base) * S.c_hi);
+                    if (S.weighs(s)) atomicAdd(&sm.hist[S.bin_of(s)], 1u);
+                });
+            } else {
+                S.each([&](float x, int) {
+                    bool there;
+                    int b;
+                    const u64 w = S.weight(x, there, b);
+                    if (there) {
+                        atomicAdd(&sm.hist[b], 1u);
+                        mine += w;
+                    }
+                });
+            }
             S.add_groups(!by_k);
             const u64 sum = S.exchange<false>(mine);
             u64 target = by_k ? k : share_of(sum, fmaxf(p, 0.0f), true);
@@ -954,8 +1009,7 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
                 S.bring(n, parts, e);
                 if (!by_k) {
                     if (how == WIDE) {
-                        S.gather();
-                        for (int i = S.lane; i < S.cs * S.nw; i += 32) above += sm.sums[i];
+                        for (int i = S.lane; i < S.cs * NW; i += 32) above += S.sums()[i];
                         above = warp_sum64(above);
                     }
 #pragma unroll
@@ -996,8 +1050,8 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
                 const int kept = __syncthreads_count(keep0) + __syncthreads_count(keep1);   // the first so many
                 if (how == WIDE) {
                     // each of them adds to its warp's sum
-                    if (keep0) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[0]) / A.seg], w[0]);
-                    if (keep1) atomicAdd(&sm.sums[(0xFFFFFFFFu - (uint32_t)e[1]) / A.seg], w[1]);
+                    if (keep0) atomicAdd(&S.sums()[(0xFFFFFFFFu - (uint32_t)e[0]) / A.seg], w[0]);
+                    if (keep1) atomicAdd(&S.sums()[(0xFFFFFFFFu - (uint32_t)e[1]) / A.seg], w[1]);
                     __syncthreads();
                     border = hi + 1;                           // none of them: those above alone
                     if (kept) {
@@ -1052,15 +1106,13 @@ __global__ void __launch_bounds__(MOST_THREADS) sample_kernel(const __grid_const
         }
         if (how == DONE) {
             const float edge = logit_of(border);
-            u64 v = 0;
-            S.each([&](float x, int i) {
-                if (x > edge || (x == edge && i <= last)) v += S.weight(x);
-            });
+            const u64 v = last == 0x7FFFFFFF ? S.weights([&](float x, int) { return x >= edge; })
+                                             : S.weights([&](float x, int i) { return x > edge || (x == edge && i <= last); });
             S.tell(warp_sum64(v));
             S.finish(edge, last);
         }
+        if (S.cs > 1 && (by_k || by_p)) S.together();   // no CTA leaves while its list is read
     }
-    if (S.cs > 1) S.together();   // no CTA leaves while its shared memory is read
 }
 
 }  // namespace
@@ -1069,25 +1121,24 @@ cudaError_t launch_sample(const plm_sample_problem& p, cudaStream_t stream) {
     SampleArgs A = {};
     A.p = p;
     A.four = four_aligned(p.logits, p.m > 1 ? p.stride : 0, p.type);
-    constexpr int room = 227 * 1024 - (int)sizeof(SampleSmem);
     const int sms = num_sms();
-    // CTAs of a row: two of 16 warps an SM, with all the row in shared memory; few rows
-    // are spread further
-    int cs = 1, nt = 512;
-    const int half = 113 * 1024 - (int)sizeof(SampleSmem);
-    while (cs < MOST_CS && p.n * 4 > (long long)cs * half) cs *= 2;
+    // Two CTAs an SM, 8 a row at most: what of a row does not fit half the SM's shared
+    // memory is left in L2.  256 rows of 200064 take 152 us so, top-k 182, and 241 and 322
+    // with all of the row in one CTA of 32 warps an SM.  Few rows are spread further.
+    int cs = 1;
+    constexpr int HALF = 113 * 1024, WHOLE = 227 * 1024;   // bytes of a CTA
+    const auto room = [&](int bytes) { return bytes - (int)fixed_bytes(cs * NW); };   // for its part of the row
+    while (cs < MOST_CS && p.n * 4 > (long long)cs * room(HALF)) cs *= 2;
     while (cs < MOST_CS && p.n > 4096LL * cs && p.m * cs * 2 <= sms) cs *= 2;
-    if (p.m * cs <= sms && p.n > 2048) nt = 1024;
-    const int warps = cs * nt / 32;
-    A.seg = (int)((p.n + 128LL * warps - 1) / (128LL * warps)) * 128;
-    const int most = (nt == 512 && 4LL * A.seg * (nt / 32) <= half ? half : room) / 4 / (nt / 32) / 128 * 128;
+    A.seg = (int)((p.n + 128LL * cs * NW - 1) / (128LL * cs * NW)) * 128;
+    const int most = room(p.m * cs <= sms ? WHOLE : HALF) / (4 * NW) / 128 * 128;
     A.held = A.seg < most ? A.seg : most;
-    const size_t bytes = sizeof(SampleSmem) + 4 * (size_t)A.held * (nt / 32);
+    const size_t bytes = fixed_bytes(cs * NW) + 4 * (size_t)A.held * NW;
     const cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)p.m, 1, (unsigned)cs);
-    if (cs == 1) return launch_kernel(sample_kernel, grid, dim3(nt), bytes, stream, A);
-    return launch_kernel_cluster(sample_kernel, grid, dim3(nt), bytes, stream, (unsigned)cs, A);
+    if (cs == 1) return launch_kernel(sample_kernel, grid, dim3(NT), bytes, stream, A);
+    return launch_kernel_cluster(sample_kernel, grid, dim3(NT), bytes, stream, (unsigned)cs, A);
 }
 
 }  // namespace plm
