@@ -483,19 +483,18 @@ struct Sampler {
         return P;
     }
 
-    // The sum, by the middles, of the bins before `first_bin` (of a window around P; warp 0)
-    __device__ u64 estimate(const Place& P, int first_bin) const {
-        const int g = first_bin / COARSE, mine = P.b / COARSE;
+    // The sum, by the middles, of the bins before bin b; P: what was located last (warp 0)
+    __device__ u64 estimate(const Place& P, int b) const {
+        const int g = b / COARSE;
         u64 v = 0;
-        for (int i = lane; i < GROUPS; i += 32) v += i < g ? sm.group_sum[i] : 0;
-        if (first_bin % COARSE) {
-            // bins of its group: the border's group, or the last but one bin of the one above
-            if (g == mine) {
-                const int b = g * COARSE + lane - 1;
-                if (lane >= 1 && lane <= COARSE && b < first_bin) v += sm.near[0][lane] * middle(b);
-            } else if (lane == 0) {
-                v += sm.group_sum[g] - sm.near[0][0] * middle(mine * COARSE - 1);
-            }
+        for (int i = lane; i < g; i += 32) v += sm.group_sum[i];
+        const int at = g * COARSE + lane;
+        if (at < b) {   // bins of its own group
+            uint32_t c = 0;
+            if (g == P.b / COARSE) c = sm.near[0][lane + 1];
+            else
+                for (int z = 0; z < cs; ++z) c += cs > 1 ? peer32(&sm.hist[at], z) : sm.hist[at];
+            v += c * middle(at);
         }
         return warp_sum64(v);
     }
@@ -1018,9 +1017,19 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
                     // (a list that min_p has cut short need not reach the target)
                     if (above >= target || (above + listed < target && lo > floor_)) {
                         how = AGAIN;
-                        aim = target + before - above;         // (below 0: the estimate was worth nothing)
-                        if (attempt == 2 || (long long)aim < 1) break;
-                        S.together();                          // every CTA has read the lists
+                        if (attempt == 2) break;
+                        if (above >= target) {
+                            aim = target + before - above;
+                        } else {                               // what the list reaches, by the middles
+                            if (S.warp == 0) {
+                                const u64 end = S.estimate(P, (int)bins);
+                                if (S.lane == 0) sm.found_sum = end;
+                            }
+                            __syncthreads();
+                            aim = target + sm.found_sum - (above + listed);
+                        }
+                        if ((long long)aim < 1) break;         // (the estimate was worth nothing)
+                        S.together();                          // every CTA has read the lists and histograms
                         if (threadIdx.x == 0) sm.listed = 0;
                         __syncthreads();
                         continue;
