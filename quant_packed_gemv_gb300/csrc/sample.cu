@@ -20,13 +20,13 @@
 // the row is read once.  What does not fit is read again from L2.  A warp has
 // consecutive logits, so the sums of the warps, which every CTA gets, say in which of
 // them the token is.
-//   What bounds it.  A row takes 3 (greedy) to 10 barriers of its cluster and 40
+//   What bounds it.  A row takes 2 (greedy) to 10 barriers of its cluster and 40
 // instructions a logit for each time its weights are formed (once without top-k and
 // top-p, up to three times with a top-p of many tokens); the read of the row hides behind
 // that.  One GB300, f32 logits, spread 2.5, us: 256 rows of 151936 (23 for the read alone)
-// greedy 48, no limits 117, min-p 77, top-k 40 147, with top-p 158, top-p 0.9 alone 196 to
-// 252; one row of them greedy 4.5, 13, 11, 17, 18, 26; 64 rows of 32000 4.6, 11, 10, 17, 18,
-// 25 to 50 (rows whose border the bins do not settle).
+// greedy 46, no limits 115, min-p 75, top-k 144, with top-p and min-p 155, top-p 0.9 alone
+// 250 (spread 4: 193); one row of them 4.3, 10, 9, 15, 17, 25; 64 rows of 32000 greedy 4.7,
+// top-k 17, top-p 26.
 #include "plm_device.cuh"
 #include "plm_internal.h"
 #include "values.cuh"
@@ -1133,12 +1133,15 @@ cudaError_t launch_sample(const plm_sample_problem& p, cudaStream_t stream) {
     const int sms = num_sms();
     // Two CTAs an SM, 8 a row at most: what of a row does not fit half the SM's shared
     // memory is left in L2.  256 rows of 200064 take 152 us so, top-k 182, and 241 and 322
-    // with all of the row in one CTA of 32 warps an SM.  Few rows are spread further.
+    // with all of the row in one CTA of 32 warps an SM.  Few rows are spread further, over
+    // CTAs with 4096 logits: 64 of 32000 with top-p 26 us, and 33 while only half as many
+    // CTAs were made; with 2048 or 8192 logits a CTA one row of 32000 takes 6.7 and 7.1
+    // (4096: 6.7), 16 of them 8.4 and 7.9 (8.3).
     int cs = 1;
     constexpr int HALF = 113 * 1024, WHOLE = 227 * 1024;   // bytes of a CTA
     const auto room = [&](int bytes) { return bytes - (int)fixed_bytes(cs * NW); };   // for its part of the row
     while (cs < MOST_CS && p.n * 4 > (long long)cs * room(HALF)) cs *= 2;
-    while (cs < MOST_CS && p.n > 4096LL * cs && p.m * cs * 2 <= sms) cs *= 2;
+    while (cs < MOST_CS && p.n > 4096LL * cs && p.m * cs <= sms) cs *= 2;
     A.seg = (int)((p.n + 128LL * cs * NW - 1) / (128LL * cs * NW)) * 128;
     const int most = room(p.m * cs <= sms ? WHOLE : HALF) / (4 * NW) / 128 * 128;
     A.held = A.seg < most ? A.seg : most;
