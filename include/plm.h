@@ -864,9 +864,17 @@ plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t to
  * values beyond f16 are undefined).
  *   k, v codes, k_exps, v_exps their exponents, both with the strides given (in bytes).
  * PLM_ERR_MISALIGNED: as there, and codes, exponents or one of their strides
- * not a multiple of 16 bytes.  More than 96 rows a sequence and head, and a
- * prefix that is done apart, are read back into the workspace as 16-bit pages
- * first (2 * 2 * head_dim bytes a key and key/value head), as that is faster.
+ * not a multiple of 16 bytes.  PLM_ERR_UNSUPPORTED also where the workspace's
+ * pages cannot be counted.
+ * More than 64 rows (tokens * heads / kv_heads) a sequence and head (96 where
+ * max_len <= 512), and a prefix that is done apart, are read back into the
+ * workspace as 16-bit pages first (2 * 2 * head_dim bytes a key and key/value
+ * head, whole pages of 128 tokens, max_len tokens a sequence), as that is faster.
+ * Their roundings are those of plm_attn_shared_prefix.  Fewer rows have their
+ * products in f16, summed in f32, with powers of two taken out: of q, what is
+ * below 2^-26 of its row's largest loses bits, p is rounded to f16, 2^-32 of
+ * the row's largest at least, and of v, a block of steps below 2^-24 of the largest of the
+ * same 32 dims so far counts as zeros.
  */
 typedef struct {
     const void* q;
@@ -909,8 +917,10 @@ plm_status plm_attn_kv8(const plm_attn_kv8_problem* p, void* workspace, size_t w
  * +inf are equal and the others nothing.  A row without a token has tokens = -1, prob = 0.
  * temperature, top_k, top_p, min_p: [m] on the device, or null: 1, off, off,
  * off.  A NaN top_p or min_p is off, min_p above 1 counts as 1.
- * The w's are held in fixed point, 2^-40 of the largest (relative error 2^-30): their
+ * The w's are held in fixed point, 2^-40 of the largest (relative error 2^-29): their
  * sums do not depend on an order, and tokens below 2^-40 of the largest have no weight.
+ * So a token may differ from the one that exact sums give only where u, top_p or min_p lies
+ * that near to a border, and the same row gives the same token in any batch.
  * logits [m][n] of `type`, `stride` elements from row to row, aligned to their
  * elements; tokens int32 [m], prob f32 [m] or null.  PLM_ERR_INVALID_ARG: null
  * logits or tokens, m < 0 or past 2^24, n < 1 or past 2^22, an unknown type, a stride below n

@@ -17,14 +17,26 @@
 // beyond, the warps share it in shared memory, so that O (32 registers per 8
 // rows at D = 128) has room.
 //
-// Bound: HBM (4 D bytes per key and head pair, ~2 operations per byte and
-// row).  Each warp brings its blocks (8 KB of K and V at D = 128) into a ring of
-// its own by cp.async, 16-byte chunks XORed so that the fragment loads are free
-// of bank conflicts; keys past the end are filled with zeros and not read.  The
-// warps of a CTA and the CTAs of a cluster take the blocks in turn and add
-// their parts through shared memory, in a fixed order.  One GB300, 8 heads of 128
-// in bf16: 64 sequences of up to 4000 keys, 95 us (5.5 TB/s); 256 of up to 2000,
-// 176 us (6.0 TB/s), 182 with a cold L2; 4 of 1100, 9.3 us, which is latency.
+// 8-bit pages (plm_attn_kv8).  Codes become f16 pairs by two byte permutes and a
+// subtraction, exactly, whatever the cache's type.  A block's power of two comes in
+// after the first product, whose sums over 32 dims it scales in f32; so Q has to fit
+// f16, and its rows are divided by powers of two.  The values' powers of two go into
+// the codes before the second product, relative to the largest of the same 32 dims
+// so far (an f16 FMA, exact above 2^-24 of it), and p is held 2^7 times as large, so
+// that f16 keeps what is above 2^-32 of the row's largest.  bf16 operands would be
+// exact without any of this, but a code costs two instructions more in bf16, and
+// instructions are what the 8-bit form is bound by: 64 sequences of up to 4000 keys took
+// 72 us so, and take 63 with f16 operands, four CTAs an SM and the ring's place below.
+//
+// Bound: HBM (4 D bytes per key and head pair, ~2 operations per byte and row; 8-bit
+// pages 2 D + D / 16, where issue comes first).  Each warp brings its blocks (8 KB of K
+// and V at D = 128) into a ring of its own by cp.async, 16-byte chunks XORed so that the
+// fragment loads are free of bank conflicts, rows beginning with the banks (rings 16 bytes
+// off: 90 us instead of 82); keys past the end are filled with zeros and not read.  The warps
+// of a CTA and the CTAs of a cluster take the blocks in turn and add their parts through
+// shared memory, in a fixed order.  One GB300, 8 heads of 128, 4 query heads each, bf16, us
+// for 16-bit pages and 8-bit ones: 64 sequences of up to 4000 keys 82 (6.4 TB/s) and 63
+// (4.3), 256 of 2000 162 (6.5) and 111 (4.9), 4 of 1100 9 and 9, which is latency.
 #pragma once
 
 #include <cstddef>
