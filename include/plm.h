@@ -866,8 +866,8 @@ plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t to
  * PLM_ERR_MISALIGNED: as there, and codes, exponents or one of their strides
  * not a multiple of 16 bytes.  PLM_ERR_UNSUPPORTED also where the workspace's
  * pages cannot be counted.
- * More than 64 rows (tokens * heads / kv_heads) a sequence and head (96 where
- * max_len <= 512), and a prefix that is done apart, are read back into the
+ * More than 48 rows (tokens * heads / kv_heads) a sequence and head (64 where
+ * max_len <= 5120, 96 where it is <= 2048), and a prefix that is done apart, are read back into the
  * workspace as 16-bit pages first (2 * 2 * head_dim bytes a key and key/value
  * head, whole pages of 128 tokens, max_len tokens a sequence), as that is faster.
  * Their roundings are those of plm_attn_shared_prefix.  Fewer rows have their

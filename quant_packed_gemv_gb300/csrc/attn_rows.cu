@@ -9,8 +9,10 @@ namespace plm {
 // takes 17), while every warp still gets two blocks of 16 keys.  Long rows up to 16
 // are cut into CTAs of 1024 keys and more whatever their number: the GPU hands them
 // out as others end, so that sequences of unequal lengths even out (20 of up to
-// 16000 keys, 8 heads of 128: 132 us in one wave, 115 so; 64 of up to 4000: 97 and
-// 90; half the keys: 91; 4 tokens each, 3000: 85 and 78; 7 tokens: 73 and 75).
+// 16000 keys, 8 heads of 128: 116 us in one wave, 104 so; 128 of up to 6000: 254 and
+// 241; 64 of up to 4000: 83 and 82; 4 tokens each, 3000: 76 and 72).  8-bit pages are
+// cut at 3000 keys: 20 of up to 16000 112 and 78 (cut at 4096: 88, at 2048: 79), 128 of
+// up to 6000 184 and 162 (163, 171), 64 of up to 4000 86 and 62 (85, 63).
 int rows_cluster(const AttnArgs& A, int d, int chunks, int keys, bool kv8) {
     const int rows = A.nq * A.group, cut = rows <= 16 ? (kv8 ? 3000 : 2048) : 0x7FFFFFFF;
     const long long pairs = (long long)A.batch * A.kv_heads * chunks, room = attn_rows_room(d, rows, kv8);

@@ -12,6 +12,11 @@
 // lane.  The rows of a lane differ by the head alone, so their places are one
 // addition apart, and their loads are issued together.  The values that a lane's are
 // paired with come from another lane.
+//
+// Bound: HBM (a value's bytes and 33 / 32 of a byte), for writing after the issue of ~10
+// instructions a value.  One GB300, 8 heads of 128, keys and values: 8191 tokens from f32,
+// half of each head turned, 20 us (4.2 TB/s); 48000 tokens of scattered slots into bf16
+// 51 us (5.7 TB/s); 61 tokens written in 3.2 us and read in 2.1, which is latency.
 #include <type_traits>
 
 #include "plm_device.cuh"
@@ -23,9 +28,11 @@ namespace plm {
 namespace {
 
 constexpr int WT = 256;          // threads per CTA
-constexpr int KV8_TB = 8;        // tokens of a CTA at most
-constexpr int READ_ROWS = 2;      // rows that a lane has in flight
-constexpr int WRITE_ROWS = 2;
+constexpr int KV8_TB = 8;        // tokens of a CTA at most (4: 72 us for the 48000, 25 for the 8191; 16: 50 and 21)
+// Rows that a lane has in flight.  8 heads of 128, 48000 tokens read: 51 us with one, 61
+// with two, 68 with four (registers, and longer runs of a CTA); 8191 written: 22 with one,
+// 23 with two, 20 with four, 27 with eight.
+constexpr int READ_ROWS = 1, WRITE_ROWS = 4;
 constexpr float LARGEST = 0x1p120f;
 
 struct Kv8Args {

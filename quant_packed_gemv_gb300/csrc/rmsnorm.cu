@@ -10,6 +10,10 @@
 // half of a chunk: whole 512-byte lines per access.  Chunk sums go through
 // shared memory and every warp adds them in the same order, which depends on k
 // alone: a row's bits do not depend on m or on the launch.
+//
+// Bound: HBM (x, r and h once, 292 bytes of blocks per 256 values), ~25 instructions a value
+// of a lane next to it.  One GB300: 8191 rows of 4096 in f32 with residual, sum and blocks
+// 69 us, 6.4 TB/s; one row of 1024 2.2 us, which is the launch and two trips to memory.
 #include "plm_device.cuh"
 #include "plm_internal.h"
 #include "values.cuh"
@@ -314,7 +318,8 @@ cudaError_t launch_rmsnorm(const plm_rmsnorm_problem& p, cudaStream_t stream) {
         A.warps = NORM_WARPS;
         return launch_kernel(rmsnorm_long_kernel, dim3((unsigned)p.m), dim3(NORM_WARPS * 32), 0, stream, A);
     }
-    // chunks a warp: few rows are spread over warps, many keep more loads of a warp in flight
+    // chunks a warp: few rows are spread over warps, many keep more loads of a warp in flight (8191 rows of 4096:
+    // one chunk 78 us, two 69, four 78)
     int held = 1;
     while (held < HELD && (chunks > NORM_WARPS * held || (held < 2 && chunks > held && p.m * chunks >= 16LL * num_sms() * held))) held *= 2;
     A.warps = (int)((chunks + held - 1) / held);

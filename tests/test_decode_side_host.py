@@ -104,6 +104,11 @@ def test_attention_refusals():
     for bad in ((0, 1, 16, 8, 128, 64, 100), (4, 0, 16, 8, 128, 64, 100), (4, 1, 12, 8, 128, 64, 100),
                 (4, 1, 16, 8, 96, 64, 100), (4, 1, 16, 8, 128, 101, 100), (4, 1, 16, 8, 128, 64, 0)):
         assert size(*bad) == 0
+    # which calls read back: by rows and keys, and a prefix that enough others would read
+    assert [size(24, n, 32, 8, 128, 0, most) > 0 for n, most in ((12, 1 << 20), (13, 5120), (16, 5120), (16, 5121), (17, 2048), (24, 2048), (24, 2049),
+                                                                 (25, 100))] == [False, False, False, True, False, False, True, True]
+    assert [size(b, n, 32, 8, 128, p, p + 300) > 0 for b, n, p in ((1, 1, 32768), (2, 1, 16384), (16, 1, 1024), (64, 1, 512), (128, 1, 1024), (24, 1, 4096),
+                                                                   (2, 7, 8192))] == [False, False, False, False, True, True, True]
     need = size(4, 100, 16, 8, 128, 64, 200)   # 200 rows a head: read back, 2 bytes a value
     assert need > 4 * 200 * 8 * 128 * 2 * 2
     assert st(tokens=100, max_len=200, b=need - 1) == BAD and st(tokens=100, max_len=200, w=None) == BAD

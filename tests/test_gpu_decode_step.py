@@ -89,3 +89,79 @@ def test_the_example_runs():
     assert bool((probs > 0).all()) and bool((probs <= 1).all())
     again, _, _, _ = E.run(prompt=40, steps=6, samples=6)    # the same seed, the same tokens
     assert torch.equal(found, again)
+
+
+class Step:
+    """The calls of a step on tensors of its own, captured into a graph on a stream of its own."""
+
+    def __init__(self, seed, tokens):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+        b, heads, kv_heads, d, page, prefix, most = 40, 8, 2, 128, 16, 8192, 8192 + 128
+        m, pages, own = b * tokens, 40 * 8 + prefix // page, (most - prefix) // page
+        self.x, self.r, w = rand(m, 2048), rand(m, 2048), rand(2048)
+        self.h, self.xq = torch.empty_like(self.x), torch.zeros(m * 8 * q.Q8K_BYTES, dtype=torch.uint8, device="cuda")
+        pool = torch.zeros(pages, q.plm_kv8_page_bytes(kv_heads, page, d), dtype=torch.uint8, device="cuda")
+        pool[:, :2 * kv_heads * page * d] = torch.randint(0, 256, (pages, 2 * kv_heads * page * d), generator=g, device="cuda", dtype=torch.uint8)
+        pool[:, 2 * kv_heads * page * d:] = 121   # steps of 2^-6
+        self.parts = q.plm_kv8_views(pool, kv_heads, page, d)
+        shared = torch.arange(prefix // page, dtype=torch.int32, device="cuda")
+        table = torch.cat((shared.expand(b, -1), len(shared) + torch.arange(b * own, dtype=torch.int32, device="cuda").view(b, own)), 1).contiguous()
+        lens = torch.full((b,), prefix + 90, dtype=torch.int32, device="cuda")
+        positions = (prefix + 90 - tokens + torch.arange(tokens, dtype=torch.int32, device="cuda")).repeat(b)
+        slots = (table.long().gather(1, (positions // page).long().view(b, tokens)) * page + (positions % page).view(b, tokens)).reshape(-1)
+        k, v, qx = rand(m, kv_heads, d), rand(m, kv_heads, d), rand(m, heads, d).bfloat16()
+        self.back, self.o = torch.empty(m, kv_heads, d, device="cuda"), torch.empty(m, heads, d, device="cuda")
+        freqs, _ = q.plm_rope_freqs(d, 1e6, device="cuda")
+        need = q.plm_attn_kv8_workspace_size(b, tokens, heads, kv_heads, d, prefix, most)
+        assert need > 0
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        logits, u, p = rand(b, 32000), torch.rand(b, generator=g, device="cuda"), torch.full((b,), 0.9, device="cuda")
+        self.token, self.prob = torch.empty(b, dtype=torch.int32, device="cuda"), torch.empty(b, device="cuda")
+
+        def call():
+            q.plm_rmsnorm(self.x, w, 1e-6, residual=self.r, sum=self.h, xq=self.xq)
+            q.plm_kv8_write([q.plm_kv8_tensor(k, self.parts[0], self.parts[2], slots), q.plm_kv8_tensor(v, self.parts[1], self.parts[3], slots, rotate=False)],
+                            positions, freqs, d)
+            q.plm_kv8_read([q.plm_kv8_tensor(self.back, self.parts[0], self.parts[2], slots)])
+            q.plm_attn_kv8(qx, self.o, *self.parts, table, lens, tokens, prefix, most, d ** -0.5, ws)
+            q.plm_sample(logits, self.token, u=u, top_p=p, prob=self.prob)
+
+        self.keep = (pool, w, table, lens, positions, slots, k, v, qx, freqs, ws, logits, u, p)
+        self.stream = torch.cuda.Stream()
+        self.stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(self.stream):
+            call()
+            self.stream.synchronize()
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph, stream=self.stream):
+                call()
+
+    def results(self):
+        return [t.clone() for t in (self.h, self.xq, self.back, self.o, self.token, self.prob)]
+
+    def run(self, times):
+        with torch.cuda.stream(self.stream):
+            for _ in range(times):
+                self.graph.replay()
+
+
+def test_two_captured_steps_replayed_at_once():
+    # with workspaces of their own, neither sees anything of the other
+    steps = [Step(1, 4), Step(2, 20)]
+    want = []
+    for s in steps:
+        s.run(1)
+        torch.cuda.synchronize()
+        want.append(s.results())
+    for t in (t for s in steps for t in (s.h, s.back, s.o, s.token, s.prob)):
+        t.fill_(-3)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s in steps:
+            s.run(2)
+    torch.cuda.synchronize()
+    assert q.plm_device_fault() == 0
+    for s, w in zip(steps, want):
+        for a, b in zip(s.results(), w):
+            assert not a.float().isnan().any() and torch.equal(a, b)
