@@ -52,6 +52,7 @@ Choice choose(const AttnArgs& A, int d, long long bound, void* ws) {
         // cluster goes through.  One GB300, us unshared and shared: 4 streams behind 1024
         // tokens 9.8 and 11.1, 149 behind 64 16 and 25; 16 behind 1024 15.9 and 11.6, 2
         // behind 8192 22 and 19, 12 x 28 rows behind 3072 59 and 32.
+        // (The rows kernel's ring begins with the banks since then: 5 to 12 % less, here and below.)
         const double bytes = (A.batch - 1.0) * A.prefix * A.kv_heads * 4 * d * ((mine + 31) / 32);
         const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7);
         c.share = common && (bytes / 6e6 > chain ? bytes / 6e6 : chain) > 7.0;

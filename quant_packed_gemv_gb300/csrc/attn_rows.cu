@@ -26,7 +26,8 @@ int rows_cluster(const AttnArgs& A, int d, int chunks, int keys, bool kv8) {
 // tokens, 4 query heads each on 8 heads, up to 3000 keys: 12 x 8 as 96 CTAs 50 us, as
 // 192 39; 8 x 8 as 128 31, as 256 41; 18 x 8 as 144 50, as 288 57; 4 x 8 over 8000 as
 // 128 41, as 256 70; 7 heads on 2, over 2000: 40 x 4 as 80 39, as 160 29; 60 x 4 as
-// 120 40, as 240 46.
+// 120 40, as 240 46.  (With rings 16 bytes off the banks; the ones kept now take 35, 26,
+// 46, 37, 26 and 36.)
 long long attn_rows_room(int d, int rows, bool kv8) {
     const int chunks = (rows + 31) / 32, ctas = rows_ctas(d, ((rows + chunks - 1) / chunks + 7) / 8, kv8), sms = num_sms();
     return ctas == 1 ? sms + sms / 3 : (long long)ctas * sms;
