@@ -211,6 +211,15 @@ def test_rows_too_long_for_shared_memory(n):
         Rows(x, **params).check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows_that_fit_shared_memory_in_part(dtype):
+    # more CTAs than SMs: two share one, and a row's rest stays in L2
+    m, n = 24, 200063
+    x = normal(12, m, n, 2.5)
+    Rows(x, dtype=T[dtype], top_p=np.repeat([0.9, 1.0, 0.5], 8), top_k=np.tile([0, 0, 50, 1000], 6), min_p=np.tile([0.0, 0.1], 12),
+         temperature=np.linspace(0.0, 1.5, m)).check()
+
+
 def test_each_row_has_its_own_parameters():
     m, n = 240, 6007
     g = np.random.RandomState(4)
