@@ -29,6 +29,7 @@
 // top-k 17, top-p 26.
 #include "plm_device.cuh"
 #include "plm_internal.h"
+#include "sample_keys.cuh"
 #include "values.cuh"
 
 namespace plm {
@@ -38,12 +39,11 @@ namespace {
 using u64 = unsigned long long;
 
 constexpr int NT = 512, NW = NT / 32;         // threads and warps of a CTA
-constexpr int BINS = 2560;                   // f of a logit with a weight: t below 40
+static_assert(BINS == 64 * 40);               // f of a logit with a weight: t below 40
 constexpr int COARSE = 16, GROUPS = BINS / COARSE;   // bins that are first looked at together
 constexpr int LIST = 1024;                   // logits that are put in order at most
 constexpr int BUCKETS = 512;
 constexpr int MOST_CS = 8;                   // CTAs of a row at most
-constexpr uint32_t LOWEST = 0x007FFFFFu;     // the key of -inf
 constexpr float MAGIC = 12582912.0f;         // 1.5 2^23: adding it rounds to a whole number
 
 struct SampleArgs {
@@ -67,14 +67,6 @@ __device__ const u64 EXP_TABLE[64] = {
     0x85AAC367CCull, 0x843A28C3ACull, 0x82CD8698ABull, 0x8164D1F3BBull,
 };
 
-// Logits as integers in their order (-0 is added to 0 before), and back.
-__device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x);
-    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float logit_of(uint32_t key) {
-    return __uint_as_float(key ^ ((uint32_t)((int)~key >> 31) | 0x80000000u));
-}
 __device__ __forceinline__ float nothing() { return __uint_as_float(0x7FFFFFFFu); }   // NaN: no logit
 
 struct alignas(16) SampleSmem {
@@ -712,9 +704,9 @@ struct Sampler {
         uint32_t hi = key_of(top), lo = floor_;
         bool by_t = true;
         for (;;) {
-            int shift = 0;
-            while (((hi - lo) >> shift) >= (uint32_t)BINS) ++shift;
-            auto place = [&](uint32_t k) { return by_t ? min(bin(logit_of(k)), BINS - 1) : (int)((hi - k) >> shift); };
+            hi = range_end(hi);
+            const KeyBins K(lo, hi);
+            auto place = [&](uint32_t k) { return by_t ? min(bin(logit_of(k)), BINS - 1) : K.bin(k); };
             empty();
             u64 mine = 0;
             const float hi_x = logit_of(hi), lo_x = logit_of(lo);
@@ -745,7 +737,7 @@ struct Sampler {
                             w1 = power(b, -0.0079f) + 1;
                             w0 = power(b, 0.0079f);
                         } else {
-                            const uint32_t k1 = hi - ((uint32_t)b << shift), left = k1 - lo, k0 = left >> shift ? k1 - (1u << shift) + 1 : lo;
+                            const uint32_t k1 = K.first(b), k0 = K.last(b);
                             w1 = weight(logit_of(k1));
                             w0 = k0 == k1 ? w1 : weight(logit_of(k0));
                             if (k0 != k1) {   // w is right to 2^-29, and may fall by that where it should rise
@@ -787,7 +779,7 @@ struct Sampler {
             const uint32_t count = sm.found[2];
             const u64 before = sm.found_sum;
             __syncthreads();
-            if (!by_t && shift == 0) {
+            if (!by_t && K.shift == 0) {
                 Border B;
                 B.key = hi - b1;
                 B.of = count;
@@ -803,11 +795,10 @@ struct Sampler {
                 by_t = false;
                 continue;
             }
-            const uint32_t k1 = hi - ((uint32_t)b1 << shift), k2 = hi - ((uint32_t)b2 << shift);
-            lo = (k2 - lo) >> shift ? k2 - (1u << shift) + 1 : lo;
-            hi = k1;
+            lo = K.last(b2);
+            hi = K.first(b1);
             if (hi - lo > wide / 4) {   // bounds that tell the bins apart badly: halve what is left
-                const uint32_t mid = lo + (hi - lo) / 2;
+                const uint32_t mid = range_end(lo + (hi - lo) / 2);
                 const float mid_x = logit_of(mid);
                 u64 v = 0;
                 each([&](float x, int) {
