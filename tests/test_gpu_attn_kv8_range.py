@@ -1,0 +1,52 @@
+"""Attention over 8-bit pages at the ends of its ranges (tests/test_gpu_attn_kv8.py has the definition, the cases and the
+terms of the tolerance)."""
+import math
+
+import pytest
+import torch
+
+import quant_packed_gemv_gb300 as q
+from tests import test_gpu_attn_kv8 as base
+
+pytestmark = pytest.mark.gpu
+
+
+def test_more_heads_than_a_grid_has_rows():
+    # 97 rows a head are read back; compared with the same call on a few of the heads
+    heads, n, d, page = 65600, 97, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pages = -(-n // page)
+    pool = torch.randint(0, 256, (pages, q.plm_kv8_page_bytes(heads, page, d)), generator=g, dtype=torch.uint8, device="cuda")
+    parts = q.plm_kv8_views(pool, heads, page, d)
+    for exps in parts[2:]:
+        exps.fill_(121)                         # steps of 2^-6
+    for codes in parts[:2]:
+        codes.clamp_(min=-127)
+    x = torch.randn(n, heads, d, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None], torch.tensor([n], **i32)
+
+    def run(h0, h1):
+        few = h1 - h0
+        o = torch.full((n, few, d), float("nan"), dtype=torch.float32, device="cuda")
+        size = q.plm_attn_kv8_workspace_size(1, n, few, few, d, 0, n)
+        assert size > 2 * 2 * 128 * few * d
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        q.plm_attn_kv8(x[:, h0:h1], o, *(p[:, h0:h1] for p in parts), table, lens, n, 0, n, 0.1, ws)
+        torch.cuda.synchronize()
+        assert q.plm_device_fault() == 0
+        return o
+
+    o = run(0, heads)
+    for h0 in (0, 65533, heads - 4):
+        few = run(h0, h0 + 4)
+        k, v = (base.decode(c[:, h0:h0 + 4], e[:, h0:h0 + 4])[table[0].long()].transpose(1, 2).reshape(-1, 4, d)[:n].double() for c, e in
+                ((parts[0], parts[2]), (parts[1], parts[3])))
+        s = torch.einsum("thd,nhd->thn", x[:, h0:h0 + 4].double(), k) * 0.1
+        hidden = torch.arange(n, device="cuda")[None] > torch.arange(n, device="cuda")[:, None]
+        p = torch.softmax(s.masked_fill(hidden[:, None], -math.inf), -1)
+        want, A = torch.einsum("thn,nhd->thd", p, v), torch.einsum("thn,nhd->thd", p, v.abs())
+        size = torch.einsum("thd,nhd->thn", x[:, h0:h0 + 4].double().abs(), k.abs()).amax(-1, keepdim=True) * 0.1
+        tol = (2.0 ** -8 + 2 * ((d + 4) * 2.0 ** -24 + 2.0 ** -22) * (1 + size) + 2 * n * 2.0 ** -24) * A   # (p is rounded to bf16)
+        for got in (o[:, h0:h0 + 4], few):
+            assert bool(((got.double() - want).abs() <= tol + 1e-30).all())
