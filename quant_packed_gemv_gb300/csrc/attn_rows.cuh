@@ -20,7 +20,9 @@
 // 8-bit pages (plm_attn_kv8).  Codes become f16 pairs by two byte permutes and a
 // subtraction, exactly, whatever the cache's type.  A block's power of two comes in
 // after the first product, whose sums over 32 dims it scales in f32; so Q has to fit
-// f16, and its rows are divided by powers of two.  The values' powers of two go into
+// f16, and its rows are divided by powers of two, to 2^13 at most.  A key's values reach
+// 2^120, so that a sum of 128 products would reach 2^140: the keys' codes are made 2^13
+// times smaller, which costs nothing, and that comes back with the row's power of two.  The values' powers of two go into
 // the codes before the second product, relative to the largest of the same 32 dims
 // so far (an f16 FMA, exact above 2^-24 of it), and p is held 2^7 times as large, so
 // that f16 keeps what is above 2^-32 of the row's largest.  bf16 operands would be
@@ -68,6 +70,16 @@ template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four codes as two pairs of f16, 2^13 times smaller, exact: c as 2^-3 + (c + 128)
+// 2^-13 less 2^-3 + 2^-6.
+constexpr int CODES_DOWN = 13;
+__device__ __forceinline__ void codes_down(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u, less = 0x30803080u;
+    const uint32_t a = __byte_perm(u, 0x30303030u, 0x4140), b = __byte_perm(u, 0x30303030u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(less));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(less));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -94,7 +106,7 @@ template <int D, int NB, bool KV8> struct RowsSmem {
         alignas(128) uint8_t ring[DW][STAGES][SLOT];   // (a copied row begins with the banks)
         Parts part;
     };
-    float q_size[KV8 ? ROWS : 1];   // powers of two that the rows of Q were divided by
+    float q_size[KV8 ? ROWS : 1];   // powers of two that the rows of Q, and the codes, were divided by
 };
 
 // CTAs of 8 nb rows that an SM holds at once: registers bound the first, shared
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
                 }
                 f[c] = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            if (t == 0) sm.q_size[8 * nb + g] = __uint_as_float((uint32_t)(e - 12) << 23);
+            if (t == 0) sm.q_size[8 * nb + g] = __uint_as_float((uint32_t)(e - 12 + CODES_DOWN) << 23);   // (2^127 at most)
         };
         if constexpr (QS) {
             for (int nb = warp; nb < NB; nb += DW) {
@@ -317,10 +329,10 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
                 const uint8_t* at = ks + k_chunk<D, true>(g, 2 * c + (t >> 1)) + 8 * (t & 1);
                 const uint2 k0 = *reinterpret_cast<const uint2*>(at), k1 = *reinterpret_cast<const uint2*>(at + 8 * D);
                 uint32_t a[2][4];   // of two products: rows g, g + 8, then both again
-                codes_to_pairs<M>(k0.x, a[0][0], a[0][2]);
-                codes_to_pairs<M>(k1.x, a[0][1], a[0][3]);
-                codes_to_pairs<M>(k0.y, a[1][0], a[1][2]);
-                codes_to_pairs<M>(k1.y, a[1][1], a[1][3]);
+                codes_down(k0.x, a[0][0], a[0][2]);
+                codes_down(k1.x, a[0][1], a[0][3]);
+                codes_down(k0.y, a[1][0], a[1][2]);
+                codes_down(k1.y, a[1][1], a[1][3]);
                 const float f0 = __uint_as_float((e[0] >> (8 * c) & 0xFFu) << 23), f1 = __uint_as_float((e[1] >> (8 * c) & 0xFFu) << 23);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {

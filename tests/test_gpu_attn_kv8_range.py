@@ -50,3 +50,38 @@ def test_more_heads_than_a_grid_has_rows():
         tol = (2.0 ** -8 + 2 * ((d + 4) * 2.0 ** -24 + 2.0 ** -22) * (1 + size) + 2 * n * 2.0 ** -24) * A   # (p is rounded to bf16)
         for got in (o[:, h0:h0 + 4], few):
             assert bool(((got.double() - want).abs() <= tol + 1e-30).all())
+
+
+def sized(c, k=0, v=0):
+    """The case with keys and values of up to 2^(k + 1), 2^(v + 1), and queries as much smaller as the keys are larger."""
+    c.k.copy_((c.k.float().clamp(-1.99, 1.99) * 2.0 ** k).to(c.k.dtype))
+    c.v.copy_((c.v.float().clamp(-1.99, 1.99) * 2.0 ** v).to(c.v.dtype))
+    c.q.mul_(2.0 ** -k)
+    c.q[c.q.abs() < 2.0 ** -126] = 0   # (that a product takes numbers below that is not promised)
+    c.encode()
+    return c
+
+
+# rows a sequence and head: up to 32 in four kernels, in chunks, and read back
+ROWS = [(1, 8, 4), (6, 2, 1), (9, 4, 2), (24, 2, 2), (30, 4, 4), (20, 4, 2), (60, 4, 2)]
+
+
+@pytest.mark.parametrize("nq,hq,hkv", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [119, 112, 105, 96, -90])
+def test_keys_of_any_size(nq, hq, hkv, d, power):
+    c = sized(base.Case8([40 + nq, 33 + nq, nq, 3], nq, hq, hkv, d, 0, 16, torch.bfloat16, seed=power + 200), k=power)
+    c.check(*c.run(o_type=torch.float32))
+    if power > 0 and c.size(0, max(c.lens)) == 0:   # queries of the usual size, in the rows that take any score: the largest has all of the sum
+        c.q.mul_(2.0 ** power)
+        c.check(*c.run())
+
+
+def test_keys_of_unlike_sizes():
+    # blocks of 2^119 and of 2^-90 beside ordinary ones in the same key: where the queries are zero they cost the others nothing
+    c = base.Case8([77, 50, 61], 4, 4, 2, 128, 0, 16, torch.bfloat16, seed=4)
+    c.k[..., :32] = (c.k[..., :32].float().clamp(-1.9, 1.9) * 2.0 ** 119).to(c.k.dtype)
+    c.k[..., 96:] *= 2.0 ** -90
+    c.q[..., :32] = 0
+    c.encode()
+    c.check(*c.run(o_type=torch.float32))
