@@ -870,8 +870,9 @@ plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t to
  * max_len <= 5120, 96 where it is <= 2048), and a prefix that is done apart, are read back into the
  * workspace as 16-bit pages first (2 * 2 * head_dim bytes a key and key/value
  * head, whole pages of 128 tokens, max_len tokens a sequence), as that is faster.
- * Their roundings are those of plm_attn_shared_prefix, and so are their ranges: scores below 2^30 in size
- * (from 2^31 on the rounding of their maximum passes an exponent, and the result may be NaN). Fewer rows have their
+ * Their roundings are those of plm_attn_shared_prefix, and so are their ranges: scores below 2^30 in
+ * size (from 2^31 on the rounding of their maximum passes an exponent and the result may be NaN), values below
+ * 2^119 / keys (as their sums are divided last, and a p counts up to 2^8).  Fewer rows have their
  * products in f16, summed in f32, with powers of two taken out: of q, what is
  * below 2^-26 of its row's largest loses bits, p is rounded to f16, 2^-32 of
  * the row's largest at least, and of v, a block of steps below 2^-24 of the largest of the

@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
     cp_wait<0>();
     __syncthreads();   // the rings make room for the parts
 
-    // this warp's part
+    // this warp's part.  8-bit pages: with a power of two taken out of l and O that leaves l
+    // between 1 and 2, so that O, in steps of the values again, is no larger than they are
     const float o_step = KV8 ? __uint_as_float((uint32_t)v_size << 23) : 1.0f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -477,14 +478,22 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int of = 4; of < 32; of <<= 1) l[nb][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][i], of);
+            float step = 1.0f;
+            if constexpr (KV8) {
+                const int e = l[nb][i] == 0.0f ? 127 : min((int)(__float_as_uint(l[nb][i]) >> 23), 253);
+                const float part = __uint_as_float((uint32_t)(254 - e) << 23);
+                m[nb][i] += (float)(e - 127) - AHEAD;
+                l[nb][i] *= part;
+                step = part * o_step;
+            }
             if (g == 0) {
-                sm.part.m[warp][8 * nb + 2 * t + i] = m[nb][i] - AHEAD;
+                sm.part.m[warp][8 * nb + 2 * t + i] = m[nb][i];
                 sm.part.l[warp][8 * nb + 2 * t + i] = l[nb][i];
             }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
                 *reinterpret_cast<float2*>(&sm.part.o[warp][8 * nb + 2 * t + i][KV8 ? (D / 8) * g + 2 * k : 64 * (k >> 2) + 8 * g + 2 * (k & 3)]) =
-                    make_float2(o[nb][k][i] * o_step, o[nb][k][i + 2] * o_step);
+                    make_float2(o[nb][k][i] * step, o[nb][k][i + 2] * step);
         }
     }
     const int cs = gridDim.z;   // the cluster: the CTAs of this pair

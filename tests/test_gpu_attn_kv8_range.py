@@ -85,3 +85,26 @@ def test_keys_of_unlike_sizes():
     c.q[..., :32] = 0
     c.encode()
     c.check(*c.run(o_type=torch.float32))
+
+
+@pytest.mark.parametrize("nq,hq,hkv", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k,v", [(0, 119), (119, 119), (-90, 112), (0, -90)])
+def test_values_of_any_size(nq, hq, hkv, d, k, v):
+    c = sized(base.Case8([40 + nq, 33 + nq, nq, 3], nq, hq, hkv, d, 0, 16, torch.bfloat16, seed=nq + v + 200), k, v)
+    c.check(*c.run(o_type=torch.float32))
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("nq", [1, 4, 10])
+def test_large_values_of_many_keys(nq):
+    # several CTAs a sequence, scores that rise so that the running reference lags: sums of 5000 p up to 2^8 before they are divided
+    c = base.Case8([5000 + nq, 5000, 4000], nq, 4, 2, 128, 0, 16, torch.bfloat16, seed=3)
+    assert c.size(0, max(c.lens)) == 0
+    for row, n in zip(c.rows, c.lens):
+        pages = [p for p in row if p >= 0]
+        c.k[pages] = (c.q[0, 0] * torch.linspace(0.0, 3.0, len(pages), device="cuda")[:, None, None, None] + 0.1 * c.k[pages].float().nan_to_num(0.0)).to(c.k.dtype)
+    sized(c, 0, 119)
+    c.check(*c.run(o_type=torch.float32))
+    c.q.zero_()          # the mean of all of them
+    c.check(*c.run())
