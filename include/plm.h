@@ -875,8 +875,8 @@ plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t to
  * 2^119 / keys (as their sums are divided last, and a p counts up to 2^8).  Fewer rows have their
  * products in f16, summed in f32, with powers of two taken out: of q, what is
  * below 2^-26 of its row's largest loses bits, p is rounded to f16, 2^-32 of
- * the row's largest at least, and of v, a block of steps below 2^-24 of the largest of the
- * same 32 dims so far counts as zeros.
+ * the row's largest at least, and of v, what is below 2^-126 of the largest step of the
+ * same 32 dims so far.  (Where steps differ by more than 2^24, keys are gone through twice.)
  */
 typedef struct {
     const void* q;

@@ -22,10 +22,15 @@
 // after the first product, whose sums over 32 dims it scales in f32; so Q has to fit
 // f16, and its rows are divided by powers of two, to 2^13 at most.  A key's values reach
 // 2^120, so that a sum of 128 products would reach 2^140: the keys' codes are made 2^13
-// times smaller, which costs nothing, and that comes back with the row's power of two.  The values' powers of two go into
-// the codes before the second product, relative to the largest of the same 32 dims
-// so far (an f16 FMA, exact above 2^-24 of it), and p is held 2^7 times as large, so
-// that f16 keeps what is above 2^-32 of the row's largest.  bf16 operands would be
+// times smaller, which costs nothing, and that comes back with the row's power of two.  The
+// values' powers of two go into the codes before the second product, relative to the
+// largest of the same 32 dims so far, and p is held 2^7 times as large, so that f16 keeps
+// what is above 2^-32 of the row's largest.  The relative powers are exponents of f16 down
+// to 2^-14 (two instructions a pair of keys), its smallest numbers down to 2^-24.  A warp
+// that meets a block below that starts over, and then takes such blocks by products of their
+// own, whose sums f32 holds down to 2^-126: no value is lost beside one that a row does not
+// see or gives no share to (64 sequences of up to 4000 keys, 63 us: 67 with one key in 50
+// 2^-16 of the others, 86 with 2^-30).  bf16 operands would be
 // exact without any of this, but a code costs two instructions more in bf16, and
 // instructions are what the 8-bit form is bound by: 64 sequences of up to 4000 keys took
 // 72 us so, and take 63 with f16 operands, four CTAs an SM and the ring's place below.
@@ -51,6 +56,8 @@ namespace plm {
 namespace {
 
 constexpr int DW = 4;               // warps per CTA
+constexpr int V_LEAST = 24;         // 2^-24 is the smallest number of f16
+constexpr int F16_ONE = 15;         // the exponent of 1 in f16
 constexpr float RAISE = 8.0f;       // log2 by which a score may exceed the reference
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -132,6 +139,39 @@ template <int D, bool KV8> __device__ __forceinline__ int v_chunk(int r, int c) 
     if (!KV8) return r * (2 * D) + ((c ^ (r & 6)) << 4);
     // (64 bytes a row: even rows would all begin in the same half of the banks)
     return D == 128 ? r * D + ((c ^ (r & 6)) << 4) : (r ^ ((r >> 1) & 1)) * D + ((c ^ ((r >> 1) & 2)) << 4);
+}
+
+// 8-bit pages: dims (D / 8) g .. of V rows 2t, 2t + 1, 2t + 8, 2t + 9, all in one block.
+template <int D> __device__ __forceinline__ void bring_codes(const uint8_t* vs, int t, int g, uint32_t (&x)[4][D / 32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+        if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vs + v_chunk<D, true>(r, g));
+            x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(vs + v_chunk<D, true>(r, g >> 1) + 8 * (g & 1));
+            x[i][0] = u.x; x[i][1] = u.y;
+        }
+    }
+}
+
+// 2^(e - of), e <= of; 0 for e = 0.
+__device__ __forceinline__ float power_below(int e, int of) { return e ? __uint_as_float((uint32_t)max(e - of + 127, 0) << 23) : 0.0f; }
+// Their values as operands: take(k, a0 .. a3) for dims 2 k, 2 k + 1 of the lane's.  f01, f89: the rows' powers of two in
+// f16, 1 at most, 2^-V_LEAST at least or 0.
+template <int D, class F> __device__ __forceinline__ void value_fragments(const uint32_t (&x)[4][D / 32], uint32_t f01, uint32_t f89, F take) {
+    const uint32_t n01 = mul_pairs<__half>(f01, 0xE480E480u), n89 = mul_pairs<__half>(f89, 0xE480E480u);   // times -1152
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // c 2^.. as (1024 + (c + 128)) 2^.. less 1152 2^..: exact, one rounding that does nothing
+            const uint32_t u0 = __byte_perm(x[0][w], x[1][w], i ? 0x7362 : 0x5140) ^ 0x80808080u;
+            const uint32_t u8 = __byte_perm(x[2][w], x[3][w], i ? 0x7362 : 0x5140) ^ 0x80808080u;
+            take(2 * w + i, fma_pairs(__byte_perm(u0, 0x64646464u, 0x4140), f01, n01), fma_pairs(__byte_perm(u0, 0x64646464u, 0x4342), f01, n01),
+                 fma_pairs(__byte_perm(u8, 0x64646464u, 0x4140), f89, n89), fma_pairs(__byte_perm(u8, 0x64646464u, 0x4342), f89, n89));
+        }
 }
 
 template <class E, int D, int NB, class Args>
@@ -277,6 +317,7 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
     // p is 2^AHEAD times what the reference says, so that f16 holds smaller ones too
     constexpr float AHEAD = KV8 ? 7.0f : 0.0f;
     int v_size = 0;   // KV8: O is in steps of 2^(v_size - 127), the largest exponent of the lane's block so far
+    uint32_t v_bias = (uint32_t)(-255 & 0xFFFF) * 0x00010001u;   // F16_ONE - v_size, twice (before the first block: no power at all)
     int seen[NB][2];   // keys that rows 8 nb + 2t, + 1 see
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -286,185 +327,222 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
             seen[nb][i] = rr < rows ? attn_seen(A, len, small_row(A, r0 + rr)) : 0;
         }
 
-    int blk = first + stream, page = page_of(blk);
-#pragma unroll
-    for (int i = 0; i < Sm::STAGES - 1; ++i) {
-        const int next = page_of(blk + (i + 1) * streams);
-        fetch(blk + i * streams, page, i);
-        page = next;
-    }
-
     float m[NB][2], l[NB][2], o[NB][2 * VC * 2][4];   // o: D / 16 tiles of 16 dims x 8 rows
+    // All blocks of this warp.  Without EXACT it gives up, and says so, where a block of values is
+    // too small for f16 beside others: taken there and then, such blocks cost the loop 5 % where there are none
+    auto all_blocks = [&](auto exact) -> bool {
+        constexpr bool EXACT = decltype(exact)::value;
+        int blk = first + stream, page = page_of(blk);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        m[nb][0] = m[nb][1] = -INFINITY;
-        l[nb][0] = l[nb][1] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[nb][i][j] = 0.0f;
-    }
-    for (int n = 0; blk < blocks; blk += streams, ++n) {
-        const int j = blk << 4, ahead = blk + (Sm::STAGES - 1) * streams;
-        const int next = page_of(ahead + streams);
-        cp_wait<Sm::STAGES - 2>();
-        __syncwarp();   // the block is there, and the slot of the one before has been read
-        fetch(ahead, page, (n + Sm::STAGES - 1) % Sm::STAGES);
-        page = next;
-        const uint8_t* ks = &sm.ring[warp][n % Sm::STAGES][0];
-        const uint8_t* vs = ks + Sm::STAGE;
-        float s[NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
-        if constexpr (KV8) {
-            // keys g and g + 8; a block of 32 dims has its own power of two
-            uint32_t e[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t* at = vs + Sm::STAGE + (g + 8 * i) * (D / 32);
-                e[i] = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-            }
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const uint8_t* at = ks + k_chunk<D, true>(g, 2 * c + (t >> 1)) + 8 * (t & 1);
-                const uint2 k0 = *reinterpret_cast<const uint2*>(at), k1 = *reinterpret_cast<const uint2*>(at + 8 * D);
-                uint32_t a[2][4];   // of two products: rows g, g + 8, then both again
-                codes_down(k0.x, a[0][0], a[0][2]);
-                codes_down(k1.x, a[0][1], a[0][3]);
-                codes_down(k0.y, a[1][0], a[1][2]);
-                codes_down(k1.y, a[1][1], a[1][3]);
-                const float f0 = __uint_as_float((e[0] >> (8 * c) & 0xFFu) << 23), f1 = __uint_as_float((e[1] >> (8 * c) & 0xFFu) << 23);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
-                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816<M>(x, a[0][0], a[0][1], a[0][2], a[0][3], qv.x, qv.y);
-                    mma16816<M>(x, a[1][0], a[1][1], a[1][2], a[1][3], qv.z, qv.w);
-                    s[nb][0] = fmaf(x[0], f0, s[nb][0]);
-                    s[nb][1] = fmaf(x[1], f0, s[nb][1]);
-                    s[nb][2] = fmaf(x[2], f1, s[nb][2]);
-                    s[nb][3] = fmaf(x[3], f1, s[nb][3]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const int at = k_chunk<D, false>(g, 4 * c + t);
-                const uint4 k0 = *reinterpret_cast<const uint4*>(ks + at), k1 = *reinterpret_cast<const uint4*>(ks + at + 16 * D);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
-                    mma16816<E>(s[nb], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
-                    mma16816<E>(s[nb], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
-                }
-            }
+        for (int i = 0; i < Sm::STAGES - 1; ++i) {
+            const int next = page_of(blk + (i + 1) * streams);
+            fetch(blk + i * streams, page, i);
+            page = next;
         }
-        const bool part = j + 16 > all;
-        bool raise = false;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[nb][i] *= KV8 ? size[KV8 ? nb : 0][i & 1] : sl2;
-                if (part && j + g + 8 * (i >> 1) >= seen[nb][i & 1]) s[nb][i] = -INFINITY;
-                raise |= s[nb][i] > m[nb][i & 1] + RAISE;
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nb][i][j] = 0.0f;
+        }
+        for (int n = 0; blk < blocks; blk += streams, ++n) {
+            const int j = blk << 4, ahead = blk + (Sm::STAGES - 1) * streams;
+            const int next = page_of(ahead + streams);
+            cp_wait<Sm::STAGES - 2>();
+            __syncwarp();   // the block is there, and the slot of the one before has been read
+            fetch(ahead, page, (n + Sm::STAGES - 1) % Sm::STAGES);
+            page = next;
+            const uint8_t* ks = &sm.ring[warp][n % Sm::STAGES][0];
+            const uint8_t* vs = ks + Sm::STAGE;
+            float s[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
+            if constexpr (KV8) {
+                // keys g and g + 8; a block of 32 dims has its own power of two
+                uint32_t e[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t* at = vs + Sm::STAGE + (g + 8 * i) * (D / 32);
+                    e[i] = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+                }
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const uint8_t* at = ks + k_chunk<D, true>(g, 2 * c + (t >> 1)) + 8 * (t & 1);
+                    const uint2 k0 = *reinterpret_cast<const uint2*>(at), k1 = *reinterpret_cast<const uint2*>(at + 8 * D);
+                    uint32_t a[2][4];   // of two products: rows g, g + 8, then both again
+                    codes_down(k0.x, a[0][0], a[0][2]);
+                    codes_down(k1.x, a[0][1], a[0][3]);
+                    codes_down(k0.y, a[1][0], a[1][2]);
+                    codes_down(k1.y, a[1][1], a[1][3]);
+                    const float f0 = __uint_as_float((e[0] >> (8 * c) & 0xFFu) << 23), f1 = __uint_as_float((e[1] >> (8 * c) & 0xFFu) << 23);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
+                        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma16816<M>(x, a[0][0], a[0][1], a[0][2], a[0][3], qv.x, qv.y);
+                        mma16816<M>(x, a[1][0], a[1][1], a[1][2], a[1][3], qv.z, qv.w);
+                        s[nb][0] = fmaf(x[0], f0, s[nb][0]);
+                        s[nb][1] = fmaf(x[1], f0, s[nb][1]);
+                        s[nb][2] = fmaf(x[2], f1, s[nb][2]);
+                        s[nb][3] = fmaf(x[3], f1, s[nb][3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const int at = k_chunk<D, false>(g, 4 * c + t);
+                    const uint4 k0 = *reinterpret_cast<const uint4*>(ks + at), k1 = *reinterpret_cast<const uint4*>(ks + at + 16 * D);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const uint4 qv = QS ? sm.q[(nb * KC + c) * 32 + lane] : qf[QS ? 0 : nb][QS ? 0 : c];
+                        mma16816<E>(s[nb], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
+                        mma16816<E>(s[nb], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
+                    }
+                }
             }
-        if (__any_sync(0xFFFFFFFFu, raise)) {
+            const bool part = j + 16 > all;
+            bool raise = false;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = fmaxf(s[nb][i], s[nb][i + 2]);
-#pragma unroll
-                    for (int of = 4; of < 32; of <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, of));
-                    const float mn = fmaxf(m[nb][i], x), keep = mn == -INFINITY ? 1.0f : ex2(m[nb][i] - mn);
-                    m[nb][i] = mn;
-                    l[nb][i] *= keep;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        o[nb][k][i] *= keep;
-                        o[nb][k][i + 2] *= keep;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    s[nb][i] *= KV8 ? size[KV8 ? nb : 0][i & 1] : sl2;
+                    if (part && j + g + 8 * (i >> 1) >= seen[nb][i & 1]) s[nb][i] = -INFINITY;
+                    raise |= s[nb][i] > m[nb][i & 1] + RAISE;
                 }
-        }
-        uint32_t pb[NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float base = m[nb][i & 1] == -INFINITY ? 0.0f : m[nb][i & 1] - AHEAD;   // a row without keys so far
-                p[i] = ex2(s[nb][i] - base);
-                l[nb][i & 1] += p[i];
-            }
-            // rounded to the cache's type (attn.cuh); l has the whole p
-            pb[nb][0] = transpose8x8(pack_pair<M>(p[0], p[1]));
-            pb[nb][1] = transpose8x8(pack_pair<M>(p[2], p[3]));
-        }
-        if constexpr (KV8) {
-            // dims (D / 8) g .. of V rows 2t, 2t + 1, 2t + 8, 2t + 9, all in one block
-            constexpr int WORDS = D / 32;
-            uint32_t v[4][WORDS], e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-                if constexpr (D == 128) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(vs + v_chunk<D, true>(r, g));
-                    v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(vs + v_chunk<D, true>(r, g >> 1) + 8 * (g & 1));
-                    v[i][0] = u.x; v[i][1] = u.y;
-                }
-                e[i] = vs[Sm::STAGE + Sm::EXPS + r * (D / 32) + (D == 128 ? g >> 1 : g >> 2)];
-            }
-            int most = max(max(e[0], e[1]), max(e[2], e[3]));
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-            if (__any_sync(0xFFFFFFFFu, most > v_size)) {
-                const float keep = most > v_size ? ex2((float)(v_size - most)) : 1.0f;
-                v_size = max(most, v_size);
+            if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
+                    for (int i = 0; i < 2; ++i) {
+                        float x = fmaxf(s[nb][i], s[nb][i + 2]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[nb][k][i] *= keep;
+                        for (int of = 4; of < 32; of <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, of));
+                        const float mn = fmaxf(m[nb][i], x), keep = mn == -INFINITY ? 1.0f : ex2(m[nb][i] - mn);
+                        m[nb][i] = mn;
+                        l[nb][i] *= keep;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            o[nb][k][i] *= keep;
+                            o[nb][k][i + 2] *= keep;
+                        }
+                    }
             }
-            // 2^(e - v_size) in f16: exact from 2^-24 on, 0 below and for e = 0
-            float f[4];
+            uint32_t pb[NB][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = e[i] ? __uint_as_float((uint32_t)max((int)e[i] - v_size + 127, 0) << 23) : 0.0f;
-            const uint32_t f01 = pack_pair<__half>(f[0], f[1]), f89 = pack_pair<__half>(f[2], f[3]);
-            const uint32_t n01 = mul_pairs<__half>(f01, 0xE480E480u), n89 = mul_pairs<__half>(f89, 0xE480E480u);   // times -1152
+            for (int nb = 0; nb < NB; ++nb) {
+                float p[4];
 #pragma unroll
-            for (int w = 0; w < WORDS; ++w)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {   // dims 4 w + 2 i, + 1 of the lane's
-                    // c 2^.. as (1024 + (c + 128)) 2^.. less 1152 2^..: exact, one rounding that does nothing
-                    const uint32_t u0 = __byte_perm(v[0][w], v[1][w], i ? 0x7362 : 0x5140) ^ 0x80808080u;
-                    const uint32_t u8 = __byte_perm(v[2][w], v[3][w], i ? 0x7362 : 0x5140) ^ 0x80808080u;
-                    const uint32_t a0 = fma_pairs(__byte_perm(u0, 0x64646464u, 0x4140), f01, n01), a1 = fma_pairs(__byte_perm(u0, 0x64646464u, 0x4342), f01, n01);
-                    const uint32_t a2 = fma_pairs(__byte_perm(u8, 0x64646464u, 0x4140), f89, n89), a3 = fma_pairs(__byte_perm(u8, 0x64646464u, 0x4342), f89, n89);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma16816<M>(o[nb][2 * w + i], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                for (int i = 0; i < 4; ++i) {
+                    const float base = m[nb][i & 1] == -INFINITY ? 0.0f : m[nb][i & 1] - AHEAD;   // a row without keys so far
+                    p[i] = ex2(s[nb][i] - base);
+                    l[nb][i & 1] += p[i];
                 }
-        } else {
-#pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                uint4 vf[4];   // rows 2t, 2t + 1, 2t + 8, 2t + 9
+                // rounded to the cache's type (attn.cuh); l has the whole p
+                pb[nb][0] = transpose8x8(pack_pair<M>(p[0], p[1]));
+                pb[nb][1] = transpose8x8(pack_pair<M>(p[2], p[3]));
+            }
+            if constexpr (KV8) {
+                constexpr int WORDS = D / 32;
+                uint32_t v[4][WORDS], e[4];
+                bring_codes<D>(vs, t, g, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    vf[i] = *reinterpret_cast<const uint4*>(vs + v_chunk<D, false>(2 * t, 8 * c + g) + ((i & 1) + 8 * (i >> 1)) * (2 * D));
+                    e[i] = vs[Sm::STAGE + Sm::EXPS + (2 * t + (i & 1) + 8 * (i >> 1)) * (D / 32) + (D == 128 ? g >> 1 : g >> 2)];
+                // f: the rows' powers of two in f16, 2^(e - v_size), as exponents of f16 where they are normal there
+                const uint32_t e01 = __byte_perm(e[0], e[1], 0x5410), e89 = __byte_perm(e[2], e[3], 0x5410);
+                const uint32_t x01 = __viaddmax_s16x2_relu(e01, v_bias, 0), x89 = __viaddmax_s16x2_relu(e89, v_bias, 0);
+                uint32_t f01 = x01 << 10, f89 = x89 << 10;
+                bool small = false;
+                if (__any_sync(0xFFFFFFFFu, ((x01 | x89) & 0xFFF0FFF0u) | (((x01 - 0x00010001u) | (x89 - 0x00010001u)) & 0x80008000u))) {
+                    // a larger block than before, one that is no exponent of f16, or zeros (rare)
+                    int most = max(max(e[0], e[1]), max(e[2], e[3]));
+                    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                    if (__any_sync(0xFFFFFFFFu, most > v_size)) {
+                        const float keep = most > v_size ? ex2((float)(v_size - most)) : 1.0f;
+                        v_size = max(most, v_size);
+                        v_bias = (uint32_t)((F16_ONE - v_size) & 0xFFFF) * 0x00010001u;
+                        f01 = __viaddmax_s16x2_relu(e01, v_bias, 0) << 10;
+                        f89 = __viaddmax_s16x2_relu(e89, v_bias, 0) << 10;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {   // dims 64 c + 8 g + 2 i, + 1
-                    const uint32_t w0 = words(vf[0], i), w1 = words(vf[1], i), w2 = words(vf[2], i), w3 = words(vf[3], i);
-                    const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-                    const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+                        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma16816<E>(o[nb][4 * c + i], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[nb][k][i] *= keep;
+                    }
+                    int least = 255;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) least = min(least, e[i] ? (int)e[i] : 255);
+                    if (__builtin_expect(__any_sync(0xFFFFFFFFu, least < v_size - F16_ONE + 1), 0)) {
+                        small = __any_sync(0xFFFFFFFFu, least < v_size - V_LEAST);
+                        if (!EXACT && small) return false;
+                        f01 = pack_pair<__half>(power_below(e[0], v_size), power_below(e[1], v_size));
+                        f89 = pack_pair<__half>(power_below(e[2], v_size), power_below(e[3], v_size));
+                    }
+                }
+                value_fragments<D>(v, f01, f89, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma16816<M>(o[nb][k], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                });
+                if (EXACT && small) {
+                    // blocks too small for that: by themselves, relative to the largest of them, then of those still left
+                    int left = v_size - V_LEAST;   // exponents below
+#pragma unroll 1
+                    for (;;) {
+                        asm volatile("" ::: "memory");   // (the codes once more, from shared memory: kept in registers they cost every block)
+                        uint32_t again[4][WORDS];
+                        bring_codes<D>(vs, t, g, again);
+                        int top = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = max(top, (int)e[i] < left ? (int)e[i] : 0);
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                        if (!__any_sync(0xFFFFFFFFu, top > 0)) break;
+                        const float back = ex2((float)(top - v_size));
+                        float f[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] = (int)e[i] < left ? power_below(e[i], top) : 0.0f;
+                        value_fragments<D>(again, pack_pair<__half>(f[0], f[1]), pack_pair<__half>(f[2], f[3]), [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma16816<M>(y, a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[nb][k][i] = fmaf(y[i], back, o[nb][k][i]);
+                            }
+                        });
+                        left = top - V_LEAST;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < VC; ++c) {
+                    uint4 vf[4];   // rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vf[i] = *reinterpret_cast<const uint4*>(vs + v_chunk<D, false>(2 * t, 8 * c + g) + ((i & 1) + 8 * (i >> 1)) * (2 * D));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // dims 64 c + 8 g + 2 i, + 1
+                        const uint32_t w0 = words(vf[0], i), w1 = words(vf[1], i), w2 = words(vf[2], i), w3 = words(vf[3], i);
+                        const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+                        const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma16816<E>(o[nb][4 * c + i], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                    }
                 }
             }
         }
+        return true;
+    };
+    if (__builtin_expect(!all_blocks(std::false_type()) && KV8, 0)) {
+        cp_wait<0>();
+        __syncwarp();   // all that was brought has been read
+        if constexpr (KV8) all_blocks(std::true_type());
     }
     cp_wait<0>();
     __syncthreads();   // the rings make room for the parts

@@ -108,3 +108,70 @@ def test_large_values_of_many_keys(nq):
     c.check(*c.run(o_type=torch.float32))
     c.q.zero_()          # the mean of all of them
     c.check(*c.run())
+
+
+def check_beside(c, o):
+    """The output where values differ by far more than an f16 holds.  As in Case8.check, but that what is lost of p is relative to
+    the values that have a share in the row (a key below 2^-100 of the row's largest has none: its p is 0), and what is
+    lost of small values below 2^-126 of the largest step: 2^-149 of it in each sum, which is divided by 2^7 at least."""
+    g = c.hq // c.hkv
+    for b, n in enumerate(c.lens):
+        pages = [p for p in c.rows[b] if p >= 0]
+        k, v = (x[pages].transpose(1, 2).reshape(-1, c.hkv, c.d)[:n].double() for x in (c.k, c.v))
+        rows = slice(b * c.nq, (b + 1) * c.nq)
+        x = c.q[rows].double().view(c.nq, c.hkv, g, c.d)
+        hidden = (torch.arange(n, device="cuda")[None] > torch.arange(n - c.nq, n, device="cuda")[:, None])[:, None, None]
+        s = (torch.einsum("thgd,nhd->thgn", x, k) * c.scale).masked_fill(hidden, -math.inf)
+        size = (torch.einsum("thgd,nhd->thgn", x.abs(), k.abs()) * c.scale).masked_fill(s < s.amax(-1, keepdim=True) - 70, 0.0).amax(-1)
+        p = torch.softmax(s, -1)
+        p = p.masked_fill(p < 2.0 ** -100 * p.amax(-1, keepdim=True), 0.0)
+        want, A = torch.einsum("thgn,nhd->thgd", p, v), torch.einsum("thgn,nhd->thgd", p, v.abs())
+        # (of each key/value head and dim: the largest value with a share)
+        top = ((p > 0).permute(1, 3, 0, 2)[..., None] * v.abs().transpose(0, 1)[:, :, None, None]).amax(1).permute(1, 0, 2, 3)
+        e = 2 * ((c.d + 4) * 2.0 ** -24 + 2.0 ** -22) * (1 + size)
+        tol = (2.0 ** -11 + e[..., None] + 3 * n * 2.0 ** -24) * A + n * 2.0 ** -32 * top + n * 2.0 ** -149 * float(v.abs().amax())
+        tol = tol + half_step(o.dtype) * (want.abs() + tol)
+        got = o[rows].double().view(want.shape)
+        assert not got.isnan().any()
+        err = (got - want).abs()
+        assert bool((err <= tol).all()), (b, n, float((err / tol).max()))
+
+
+def half_step(dtype):
+    return {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}[dtype]
+
+
+@pytest.mark.parametrize("nq,hq,hkv", [(2, 8, 4), (6, 2, 1), (9, 4, 2), (20, 2, 2), (24, 2, 2), (30, 4, 4), (20, 4, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [119, 40, 25])
+@pytest.mark.parametrize("lens", [[40, 33, 97], [3000, 1711]])
+def test_values_beside_others_that_a_row_does_not_see(nq, hq, hkv, d, power, lens):
+    # drafted tokens: the last one's value is huge, as after an overflow; the queries before it do not see it
+    c = base.Case8([n + nq for n in lens], nq, hq, hkv, d, 0, 16, torch.bfloat16, seed=nq + power)
+    assert c.size(0, max(c.lens)) == 0
+    for row, n in zip(c.rows, c.lens):
+        c.v[row[(n - 1) // 16], :, (n - 1) % 16] = 1.5 * 2.0 ** power
+    c.encode()
+    o, _ = c.run(o_type=torch.float32)
+    check_beside(c, o)
+
+
+@pytest.mark.parametrize("nq,hq,hkv", [(1, 8, 4), (6, 4, 2), (9, 4, 2), (24, 2, 2), (20, 4, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("first", [True, False])
+def test_values_beside_others_without_probability(nq, hq, hkv, d, first):
+    # keys whose score leaves them no share, with values of 2^100, 2^60 and 2^30 beside those of the others, of 1 and 2^-30
+    c = base.Case8([48 + nq, 2000 + nq], nq, hq, hkv, d, 0, 16, torch.bfloat16, seed=nq)
+    c.q[..., 0] = 8.0
+    c.k[..., 0] = 0.0
+    for row, n in zip(c.rows, c.lens):
+        for i, power in enumerate((100, 60, 30)):
+            j = i if first else n - nq - 1 - 17 * i
+            at = (row[j // 16], slice(None), j % 16)
+            c.k[at] = 0.0
+            c.k[at + (slice(0, 1),)] = -2000.0
+            c.v[at] = c.v[at] * 2.0 ** power
+        c.v[[p for p in row if p >= 0], :, 5] *= 2.0 ** -30
+    c.encode()
+    o, _ = c.run(o_type=torch.float32)
+    check_beside(c, o)
