@@ -158,6 +158,7 @@ plm_status plm_probe_tcgen05_rate(double* cycles_per_mma, double* cycles_per_mma
  * magnitude (first occurrence on ties), iscale = -128/max, code =
  * min(127, round-half-even(iscale*x)), d = 1/iscale, bsums[g] = sum of codes
  * 16g..16g+15; an all-zero chunk gives d = 0 and zero codes and sums.
+ * A NaN has no magnitude and code 0, so a chunk of nothing else counts as zeros.
  * Bit-exact with that scalar rule.
  *   x  : f32 [m][k], 16-byte aligned.       xq : q8_K [m][k/256], 4-byte aligned.
  */
@@ -776,7 +777,8 @@ plm_status plm_attn_shared_prefix(const plm_attn_problem* p, void* workspace, si
  * Wanted outputs (at least one of xq and y, others null):
  *   sum [m][k] of r_type: h, the next residual;
  *   xq  q8_K [m][k/256]: what plm_quantize_q8K makes of y in f32, bit for bit
- *       (k a multiple of 256);
+ *       (k a multiple of 256): a NaN, which y shows, is 0 in the blocks, and a NaN in h
+ *       makes all of its row NaN;
  *   y   [m][k] of y_type, rounded once from f32.
  * weight [k] of w_type, or null (1).  Strides are in elements from row to row,
  * rows are dense.  Every pointer is aligned to its elements (xq: 4 bytes);

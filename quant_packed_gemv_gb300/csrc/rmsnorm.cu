@@ -76,10 +76,10 @@ template <int N> __device__ __forceinline__ void put_q8K(uint8_t* const (&blk)[N
     float mine[N], mx[N], d[N], iscale[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        uint32_t top = 0;
+        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
-        amax[j] = __reduce_max_sync(0xFFFFFFFFu, top);
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[j][i]));   // (of numbers: NaN has no size)
+        amax[j] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -97,7 +97,7 @@ template <int N> __device__ __forceinline__ void put_q8K(uint8_t* const (&blk)[N
     for (int j = 0; j < N; ++j) mx[j] = __shfl_sync(0xFFFFFFFFu, mine[j], (idx[j] & 127) >> 2);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        iscale[j] = __fdiv_rn(-128.0f, amax[j] ? mx[j] : 1.0f);   // (zeros: codes 0)
+        iscale[j] = __fdiv_rn(-128.0f, amax[j] ? mx[j] : 1.0f);   // (zeros and NaN: codes 0)
         d[j] = amax[j] ? __fdiv_rn(1.0f, iscale[j]) : 0.0f;
     }
 #pragma unroll
