@@ -108,7 +108,8 @@ template <int N> __device__ __forceinline__ void put_q8K(uint8_t* const (&blk)[N
         const uint32_t w0 = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
         const uint32_t w1 = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
         // sums of 16 codes: four lanes each, in both halves
-        int both = q[0] + q[1] + q[2] + q[3] + (q[4] + q[5] + q[6] + q[7]) * 65536;   // both sums in one word
+        // both sums in one word, to 16 bits each (codes of the smallest values, whose scale is infinite, pass them)
+        int both = (short)(q[0] + q[1] + q[2] + q[3]) + (q[4] + q[5] + q[6] + q[7]) * 65536;
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
         const int next = __shfl_down_sync(0xFFFFFFFFu, both, 4);

@@ -58,3 +58,13 @@ def test_values_of_one_block_alone():
     assert not bool(y[:, 511].isnan().any()) and bool(y[:, 256:511].isnan().all())
     d = blocks[:, 1, :4].contiguous().view(torch.float32)[:, 0]
     assert torch.equal(d, 1.0 / (-128.0 / y[:, 511])) and bool((blocks[:, 1, 4 + 255] == 128).all()) and bool((blocks[:, 1, 4:4 + 255] == 0).all())
+
+
+@pytest.mark.parametrize("m,k", [(3, 256), (700, 1024), (5, 4096), (2, 16640)])
+@pytest.mark.parametrize("size", [1e-36, 3e-38, 1e-40, 1.5e-45])
+def test_blocks_of_the_smallest_values(m, k, size):
+    # -128 / max is infinite from 128 / 2^128 downwards: codes are 127, 0 or what is left of -2^31 in a byte
+    x, w = rand(m, m, k), torch.full((k,), size, device="cuda")
+    x[:, 7] = 0.0
+    y, blocks = run(x, w)
+    assert size > 1e-37 or bool((blocks[:, :, 4:260] == 127).any())
