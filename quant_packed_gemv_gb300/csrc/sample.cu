@@ -221,13 +221,17 @@ struct Sampler {
         else __syncthreads();
     }
 
+    // p is the rounded product wherever it is formed, and what is taken from it is taken from the rounded
+    // one: left to the compiler, some of these may be fused, and a weight be off by p's own rounding
+    __device__ __forceinline__ float less_base(float logit) const { return __fsub_rn(logit, base); }
+    __device__ __forceinline__ float times_c(float x) const { return __fmul_rn(x, c_hi); }
     // 64 t rounded, MAGIC added: its bits count in steps of 1.  No less for a smaller
     // logit; NaN for none.  (x: less base; p: times c_hi)
     __device__ __forceinline__ float steps(float p) const { return fmaf(p, -64.0f, ref64); }
     __device__ __forceinline__ bool weighs(float s) const { return s < MAGIC + (float)BINS; }   // (false for NaN)
     __device__ __forceinline__ int bin_of(float s) const { return (int)(__float_as_uint(s) - __float_as_uint(MAGIC)); }
     __device__ __forceinline__ int bin(float x) const {   // BINS where there is no weight
-        const float s = steps((x - base) * c_hi);
+        const float s = steps(times_c(less_base(x)));
         return weighs(s) ? bin_of(s) : BINS;
     }
     // 2^(60 - (f mod 64)/64 - r), and 2^(40 - f/64 - r).  2^-r - 1 (below 2^-7) in steps of 2^-29 is the rounding that
@@ -242,12 +246,12 @@ struct Sampler {
     __device__ __forceinline__ u64 middle(int f) const { return sm.table[f & 63][lane & 15] >> (20 + (f >> 6)); }
     __device__ __forceinline__ float rest(float x, float p, float s) const {
         const float y = fmaf(s - MAGIC, -0.015625f, ref);       // ref - f/64, exact
-        return fmaf(x, -c_lo, (y - p) - fmaf(x, c_hi, -p));
+        return fmaf(x, -c_lo, __fsub_rn(__fsub_rn(y, p), fmaf(x, c_hi, -p)));
     }
     // w of any logit, to be used where `there`: without a branch, so that those of
     // several logits are worked out side by side
     __device__ __forceinline__ u64 weight(float logit, bool& there, int& b) const {
-        const float x = logit - base, p = x * c_hi, s = steps(p), in = fminf(s, MAGIC + (float)BINS);   // (NaN: BINS)
+        const float x = less_base(logit), p = times_c(x), s = steps(p), in = fminf(s, MAGIC + (float)BINS);   // (NaN: BINS)
         there = weighs(s);
         b = bin_of(in);
         return power(b, rest(x, p, in));
@@ -286,7 +290,7 @@ struct Sampler {
     // The share of a logit that has a weight in `all`.  Of a small w the bits below 1,
     // which the sums leave out, count here.
     __device__ __forceinline__ float chance(float logit, u64 all) const {
-        const float x = logit - base, p = x * c_hi, s = steps(p);
+        const float x = less_base(logit), p = times_c(x), s = steps(p);
         const int f = bin_of(s);
         return quotient(power_of_rest(f, rest(x, p, s)), all) * __uint_as_float((uint32_t)(127 - 20 - (f >> 6)) << 23);
     }
@@ -923,7 +927,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
             u64 mine = 0;
             if (by_k) {
                 S.each([&](float x, int) {
-                    const float s = S.steps((x - S.base) * S.c_hi);
+                    const float s = S.steps(S.times_c(S.less_base(x)));
                     if (S.weighs(s)) atomicAdd(&sm.hist[S.bin_of(s)], 1u);
                 });
             } else {
