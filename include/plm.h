@@ -862,8 +862,8 @@ plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t to
 /*
  * plm_attn_shared_prefix over 8-bit pages: the same sums, lengths, tables,
  * prefix and refusals, with k and v the pages' values in `type` (that of q:
- * exact in bf16; in f16 a block counts as zeros below 2^(e - 127) = 2^-24, and
- * values beyond f16 are undefined).
+ * exact in bf16; in f16, where pages are read back, a block counts as zeros below
+ * 2^(e - 127) = 2^-24, and values beyond f16 are undefined).
  *   k, v codes, k_exps, v_exps their exponents, both with the strides given (in bytes).
  * PLM_ERR_MISALIGNED: as there, and codes, exponents or one of their strides
  * not a multiple of 16 bytes.  PLM_ERR_UNSUPPORTED also where the workspace's
@@ -954,8 +954,8 @@ plm_status plm_sample(const plm_sample_problem* p, cudaStream_t stream);
  * which follow the fields in the block itself.  entry: 0 plm_rope, 1
  * plm_kv_reserve, 2 plm_kv_fork, 3 plm_kv_free, 4 plm_kv_compact, 5
  * plm_kv_copy_pages, 6 plm_attn_shared_prefix, 8 plm_rmsnorm, 9 plm_kv8_write, 10
- * plm_kv8_read, 11 plm_attn_kv8, 12 plm_sample; PLM_ERR_INVALID_ARG otherwise
- * and for a null block.  args is 8-byte aligned HOST memory, read during the
+ * plm_kv8_read, 11 plm_attn_kv8, 12 plm_sample; PLM_ERR_INVALID_ARG otherwise (7 is
+ * not in use) and for a null block.  args is 8-byte aligned HOST memory, read during the
  * call only.
  */
 plm_status plm_call(int entry, const void* args);
