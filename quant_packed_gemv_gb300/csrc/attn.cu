@@ -50,21 +50,21 @@ Choice choose(const AttnArgs& A, int d, long long bound, void* ws) {
         // The prefix apart costs a launch and longer sums, ~7 us.  Read by every sequence
         // it takes its bytes at ~6 TB/s, or the 16-key blocks that a warp of a full
         // cluster goes through.  One GB300, us unshared and shared: 4 streams behind 1024
-        // tokens 9.8 and 11.1, 149 behind 64 16 and 25; 16 behind 1024 15.9 and 11.6, 2
-        // behind 8192 22 and 19, 12 x 28 rows behind 3072 59 and 32.
-        // (The rows kernel's ring begins with the banks since then: 5 to 12 % less, here and below.)
+        // tokens and up to 300 of their own 8.5 and 11.7, 149 behind 64 22 and 36; 16 behind 1024
+        // 12.7 and 11.7, 2 behind 8192 16.1 and 16.7, 12 x 28 rows behind 3072 59 and 38; but 64
+        // behind 512, which the rule takes apart, 21.0 and 24.2.
         const double bytes = (A.batch - 1.0) * A.prefix * A.kv_heads * 4 * d * ((mine + 31) / 32);
         const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7);
         c.share = common && (bytes / 6e6 > chain ? bytes / 6e6 : chain) > 7.0;
         // Beyond 32 rows the rows kernel goes over the keys again for each chunk of 32, which
         // pays as long as they are few, and for longer where its CTAs leave room on the GPU;
         // the prefix apart, and its sums, count as 512 keys.  One GB300, 8 heads of 128, us
-        // here and in the tile kernel: 24 x 40 rows over 4000 keys 74 and 97, over 16000 254 and
-        // 178; 24 x 64 over 2000 74 and 81, over 3000 101 and 81; 60 x 72 over 2000 136 and 137,
-        // over 3000 184 and 152; 2 x 64 over 4000 23 and 27, 5 x 72 over 3000 24 and 28; 60 x 80
-        // over 1000 154 and 114, 8 x 80 27 and 30, over 3000 56 and 39; 8 x 96 behind 4096 51
-        // and 41.  Heads of 64: 24 x 64 over 4000 57 and 71, 24 x 80 over 1000 31 and 40, over
-        // 4000 82 and 68, 3 x 80 19 and 22.
+        // here and in the tile kernel: 24 x 40 rows over 4000 keys 70 and 93, over 16000 240 and
+        // 173; 24 x 64 over 2000 68 and 76, over 3000 96 and 79; 60 x 72 over 2000 133 and 168,
+        // over 3000 181 and 158; 2 x 64 over 4000 21 and 25, 5 x 72 over 3000 22 and 28; 60 x 80
+        // over 1000 148 and 119, 8 x 80 25 and 27, over 3000 53 and 35; 8 x 96 behind 4096 49
+        // and 39.  Heads of 64: 24 x 64 over 4000 54 and 68, 24 x 80 over 1000 28 and 38, over
+        // 4000 78 and 64, 3 x 80 19 and 21.
         c.rows = true;
         if (mine > 32) {
             const long long keys = c.share ? bound - A.prefix + 512 : bound, pairs = (long long)A.batch * A.kv_heads;

@@ -163,19 +163,19 @@ Choice8 choose8(const AttnArgs& A, int d, long long bound, void* ws) {
     Choice8 c = {};
     // Beyond 32 rows the rows kernel goes over the keys again for each chunk of 32; the tile
     // kernel needs them read back first.  One GB300, 24 sequences, 8 heads of 128, us here and
-    // there: 40 rows over 500 keys 20 and 62, over 4000 80 and 155; 64 over 500 33 and 63, 3000
-    // 110 and 129, 12000 377 and 317 (2 sequences, 4000: 24 and 37); 96 over 400 43 and 55, 1000
-    // 66 and 81, 3000 151 and 138.
+    // there: 40 rows over 500 keys 21 and 59, over 4000 79 and 152; 64 over 500 34 and 60, 3000
+    // 111 and 128, 12000 378 and 312 (2 sequences, 4000: 24 and 38); 96 over 400 44 and 53, 1000
+    // 67 and 77, 3000 153 and 137.
     c.rows = mine <= 48 || (mine <= 64 && bound <= 5120) || (mine <= 96 && bound <= 2048);
     if (c.rows) {
         // The prefix apart costs two launches, a trip of every row's O through memory, and
         // reading it back.  It saves what every other sequence would read of it (~35 keys and
         // heads a ns; more than 16 rows take twice as long), or the blocks that a warp of a full
         // cluster goes through.  One GB300, us unshared and shared, a token each on 8 heads of
-        // 128: 16 behind 1024 14 and 25, 64 behind 512 23 and 28, behind 1024 35 and 33, 128 58
-        // and 47, behind 2048 99 and 50, 24 behind 4096 56 and 32, 2 behind 16384 35 and 48; 61
-        // on 2 heads of 64 behind 8176 39 and 30; 2 x 28 rows behind 8192 56 and 48, 4 behind
-        // 16384 79 and 59, 12 behind 2048 51 and 49, 48 x 20 behind 8192 255 and 85.
+        // 128: 16 behind 1024 14 and 26, 64 behind 512 23 and 29, behind 1024 34 and 34, 128 58
+        // and 47, behind 2048 96 and 51, 24 behind 4096 54 and 33, 2 behind 16384 34 and 51; 61
+        // on 2 heads of 64 behind 8176 39 and 30; 2 x 28 rows behind 8192 57 and 47, 4 behind
+        // 16384 80 and 60, 12 behind 2048 (not taken apart) 52 and 48, 48 x 20 behind 8192 255 and 84.
         const double others = (A.batch - 1.0) * A.prefix * A.kv_heads * ((mine + 31) / 32) * (mine > 16 ? 2.2 : 1.0) / 35e3;
         const double chain = A.prefix / 512.0 * (mine > 16 ? 1.4 : 0.7), back = 6.0 * A.prefix * A.kv_heads * d / 5.5e6;
         c.share = A.prefix > 0 && A.batch > 1 && (others > chain ? others : chain) > 13.0 + back;

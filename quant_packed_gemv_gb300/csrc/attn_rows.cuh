@@ -42,8 +42,12 @@
 // off: 90 us instead of 82); keys past the end are filled with zeros and not read.  The warps
 // of a CTA and the CTAs of a cluster take the blocks in turn and add their parts through
 // shared memory, in a fixed order.  One GB300, 8 heads of 128, 4 query heads each, bf16, us
-// for 16-bit pages and 8-bit ones: 64 sequences of up to 4000 keys 82 (6.4 TB/s) and 63
-// (4.3), 256 of 2000 162 (6.5) and 111 (4.9), 4 of 1100 9 and 9, which is latency.
+// for 16-bit pages and 8-bit ones: 64 sequences of up to 4000 keys 83 (6.4 TB/s) and 63
+// (4.4), 256 of 2000 162 (6.5) and 109 (5.0), 4 of 1100 7.2 and 8.4, which is latency.  From 16
+// rows on, 8-bit pages are the slower ones: 64 x 8 rows over up to 3000 keys 66 and 64, 16 rows 72
+// and 75, 32 rows 124 and 142, 48 x 20 behind 8192 63 and 83.  With more than 8 rows an SM holds 8 warps
+// (4 for 25 to 32 rows of 128), which issue the conversions.  Spills at the registers of those CTAs, bytes
+// stored: 8-bit pages of 128 dims up to 8 rows 16, 25 to 32 rows 36 (16-bit pages 32).
 #pragma once
 
 #include <cstddef>
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(DW * 32, rows_ctas(D, NB, std::is_same<Args, A
     // All blocks of this warp.  Without EXACT it gives up, and says so, where a block of values is
     // too small for f16 beside others: taken there and then, such blocks cost the loop 5 % where there are none
     auto all_blocks = [&](auto exact) -> bool {
-        constexpr bool EXACT = decltype(exact)::value;
+        [[maybe_unused]] constexpr bool EXACT = decltype(exact)::value;
         int blk = first + stream, page = page_of(blk);
 #pragma unroll
         for (int i = 0; i < Sm::STAGES - 1; ++i) {

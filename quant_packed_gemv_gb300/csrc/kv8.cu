@@ -15,8 +15,9 @@
 //
 // Bound: HBM (a value's bytes and 33 / 32 of a byte), for writing after the issue of ~10
 // instructions a value.  One GB300, 8 heads of 128, keys and values: 8191 tokens from f32,
-// half of each head turned, 20 us (4.2 TB/s); 48000 tokens of scattered slots into bf16
-// 51 us (5.7 TB/s); 61 tokens written in 3.2 us and read in 2.1, which is latency.
+// interleaved pairs, half of each head turned, 18.5 us (4.5 TB/s), all of it 18.9; halves 20.6
+// and 21.1, whose kernels spill 28 to 36 bytes at their 80 registers; 48000 tokens of scattered
+// slots into bf16 52 us (5.6 TB/s); 61 tokens written in 3.8 us and read in 2.2, which is latency.
 #include <type_traits>
 
 #include "plm_device.cuh"
@@ -28,10 +29,12 @@ namespace plm {
 namespace {
 
 constexpr int WT = 256;          // threads per CTA
-constexpr int KV8_TB = 8;        // tokens of a CTA at most (4: 72 us for the 48000, 25 for the 8191; 16: 50 and 21)
-// Rows that a lane has in flight.  8 heads of 128, 48000 tokens read: 51 us with one, 61
-// with two, 68 with four (registers, and longer runs of a CTA); 8191 written: 22 with one,
-// 23 with two, 20 with four, 27 with eight.
+// Tokens of a CTA at most (4: 59 us for the 48000 instead of 52, 24.9 for the 8191 instead of 18.5;
+// 16: 50 and 20.0).
+constexpr int KV8_TB = 8;
+// Rows that a lane has in flight.  8 heads of 128, 48000 tokens read: 52 us with one, 61
+// with two, 69 with four (registers, and longer runs of a CTA); 8191 written, interleaved and in
+// halves: 21 and 29 with one, 22 and 23 with two, 18.5 and 20.6 with four, 27 and 42 with eight.
 constexpr int READ_ROWS = 1, WRITE_ROWS = 4;
 constexpr float LARGEST = 0x1p120f;
 

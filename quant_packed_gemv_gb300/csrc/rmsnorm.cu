@@ -14,6 +14,8 @@
 // Bound: HBM (x, r and h once, 292 bytes of blocks per 256 values), ~25 instructions a value
 // of a lane next to it.  One GB300: 8191 rows of 4096 in f32 with residual, sum and blocks
 // 69 us, 6.4 TB/s; one row of 1024 2.2 us, which is the launch and two trips to memory.
+// Rows that are no whole chunks take their values by four with a look at each place, and half
+// of the lanes of a row of 128 hold nothing: 131056 such rows (a head each) 51 us, 2.6 TB/s.
 #include "plm_device.cuh"
 #include "plm_internal.h"
 #include "values.cuh"

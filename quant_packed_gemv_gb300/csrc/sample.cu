@@ -23,10 +23,11 @@
 //   What bounds it.  A row takes 2 (greedy) to 10 barriers of its cluster and 40
 // instructions a logit for each time its weights are formed (once without top-k and
 // top-p, up to three times with a top-p of many tokens); the read of the row hides behind
-// that.  One GB300, f32 logits, spread 2.5, us: 256 rows of 151936 (23 for the read alone)
-// greedy 46, no limits 115, min-p 75, top-k 144, with top-p and min-p 155, top-p 0.9 alone
-// 250 (spread 4: 193); one row of them 4.3, 10, 9, 15, 17, 25; 64 rows of 32000 greedy 4.7,
-// top-k 17, top-p 26.
+// that.  One row is held by 8 SMs, 19000 logits each: a pass that forms weights is 3 us of
+// issue there.  One GB300, f32 logits, spread 2.5, us: 256 rows of 151936 (23 for the read alone)
+// greedy 47, no limits 114, min-p 75, top-k 146, with top-p and min-p 156, top-p 0.9 alone
+// 250 (spread 4: 193); one row of them 4.3, 10, 9, 15, 17, 25; 64 rows of 32000 greedy 4.3,
+// top-k 15, top-p 26.  At the 64 registers that two CTAs leave, 100 bytes are spilled.
 #include "plm_device.cuh"
 #include "plm_internal.h"
 #include "sample_keys.cuh"
