@@ -863,7 +863,7 @@ plm_status plm_kv8_read(const plm_kv8_tensor* tensors, int64_t count, int64_t to
  * plm_attn_shared_prefix over 8-bit pages: the same sums, lengths, tables,
  * prefix and refusals, with k and v the pages' values in `type` (that of q:
  * exact in bf16; in f16, where pages are read back, a block counts as zeros below
- * 2^(e - 127) = 2^-24, and values beyond f16 are undefined).
+ * 2^(e - 127) = 2^-24, and values beyond f16 as its largest, 65504).
  *   k, v codes, k_exps, v_exps their exponents, both with the strides given (in bytes).
  * PLM_ERR_MISALIGNED: as there, and codes, exponents or one of their strides
  * not a multiple of 16 bytes.  PLM_ERR_UNSUPPORTED also where the workspace's

@@ -109,6 +109,15 @@ __device__ __forceinline__ uint32_t fma_pairs(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
+// Two values cut to the largest of the cache's type: an infinite one behind the last key that a row
+// sees would make it NaN.
+template <class E> __device__ __forceinline__ uint32_t finite_pair(uint32_t v) { return v; }   // (bf16 holds the cache's 2^120)
+template <> __device__ __forceinline__ uint32_t finite_pair<__half>(uint32_t v) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7BFF7BFFu));
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0xFBFFFBFFu));
+    return r;
+}
 // The powers of two of two exponents, in the cache's type (f16: 0 below 2^-24, 2^15 at most).
 template <class E> __device__ __forceinline__ uint32_t exps_to_pair(uint32_t e0, uint32_t e1);
 template <> __device__ __forceinline__ uint32_t exps_to_pair<__half>(uint32_t e0, uint32_t e1) {

@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256) kv8_pages_kernel(const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 codes_to_pairs<E>(w[k], r[2 * k], r[2 * k + 1]);
-                r[2 * k] = mul_pairs<E>(r[2 * k], f);
-                r[2 * k + 1] = mul_pairs<E>(r[2 * k + 1], f);
+                r[2 * k] = finite_pair<E>(mul_pairs<E>(r[2 * k], f));
+                r[2 * k + 1] = finite_pair<E>(mul_pairs<E>(r[2 * k + 1], f));
             }
             uint4* out = reinterpret_cast<uint4*>((value ? W.v : W.k) + to + (long long)t * D + 16 * c);
             out[0] = make_uint4(r[0], r[1], r[2], r[3]);

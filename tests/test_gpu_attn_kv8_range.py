@@ -175,3 +175,34 @@ def test_values_beside_others_without_probability(nq, hq, hkv, d, first):
     c.encode()
     o, _ = c.run(o_type=torch.float32)
     check_beside(c, o)
+
+
+@pytest.mark.parametrize("nq,hq,hkv,prefix,lens", [(60, 4, 2, 0, [100, 61, 300]), (130, 2, 2, 0, [140, 700]), (1, 8, 2, 4096, [4096 + 17 + i for i in range(128)])])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [16, 40, 119])
+def test_f16_beside_values_that_it_does_not_hold(nq, hq, hkv, prefix, lens, d, power):
+    # pages that are read back; keys and values of 2^16 and more count as 65504, and nothing where a row does not see them:
+    # the last token of each sequence for all queries but its own (of the prefix: behind its end)
+    c = base.Case8(lens, nq, hq, hkv, d, prefix, 16, torch.float16, seed=power)
+    assert c.size(prefix, max(lens)) > 0
+    if nq == 1:
+        # a query each: one more token behind the one that asks, which the page holds and nobody sees
+        c.lens = [n - 1 for n in lens]
+        for b, n in enumerate(c.lens):
+            c.row_lens[c.seq[b]] = n
+    last = [(row[(n - 1) // 16], slice(None), (n - 1) % 16) for row, n in zip(c.rows, lens)]
+    for codes, exps in (c.parts[::2], c.parts[1::2]):
+        for at in last:
+            codes[at] = 127 - 254 * (torch.arange(d, device="cuda") % 2).to(torch.int8)
+            exps[at] = 127 + power - 6
+    o, lse = c.run(o_type=torch.float32)
+    assert not o.isnan().any() and not o.isinf().any()
+    for at in last:   # what the rows that do not see it get, they get without it
+        c.parts[2][at] = 0
+        c.parts[3][at] = 0
+        c.k[at] = 0
+        c.v[at] = 0
+    want, _ = c.run(o_type=torch.float32)
+    c.check(want, _)
+    seeing = torch.arange(o.shape[0], device="cuda") % nq == nq - 1 if nq > 1 else torch.zeros(o.shape[0], dtype=torch.bool, device="cuda")
+    assert torch.equal(o[~seeing], want[~seeing])
