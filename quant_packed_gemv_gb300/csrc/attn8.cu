@@ -23,16 +23,17 @@ struct Back {
     size_t bytes;
 };
 
-// Reads pages back.  CTA (page of the workspace, head; of more heads than a grid has rows, every so manieth).
+// Reads pages back.  A CTA a page of the workspace and head.
 template <class E, int D>
 __global__ void __launch_bounds__(256) kv8_pages_kernel(const __grid_constant__ AttnArgs8 A, const __grid_constant__ Back W) {
     __shared__ int first;
     grid_launch_dependents();
     grid_wait_prior();
+    const int at_page = (int)(blockIdx.x / (unsigned)A.kv_heads), h = (int)(blockIdx.x - (unsigned)at_page * A.kv_heads);
     int b, j;                             // sequence, page of it
-    const bool common = (int)blockIdx.x < W.shared;
+    const bool common = at_page < W.shared;
     if (common) {   // of the first sequence that sees all of the prefix
-        j = blockIdx.x;
+        j = at_page;
         if (threadIdx.x == 0) first = A.batch;
         __syncthreads();
         for (int i = threadIdx.x; i < A.batch; i += 256)
@@ -42,17 +43,17 @@ __global__ void __launch_bounds__(256) kv8_pages_kernel(const __grid_constant__ 
             }
         __syncthreads();
         b = first;
-        if (threadIdx.x == 0 && blockIdx.y == 0 && !W.own) W.table[j] = j;
+        if (threadIdx.x == 0 && h == 0 && !W.own) W.table[j] = j;
         if (b == A.batch) return;         // nobody reads it
     } else {
-        b = ((int)blockIdx.x - W.shared) / W.each;
-        j = (int)blockIdx.x - W.shared - b * W.each;
+        b = (at_page - W.shared) / W.each;
+        j = at_page - W.shared - b * W.each;
     }
     const int row = attn_row(A, b), len = attn_len(A, row), end = common ? A.prefix : len;
     if (!common) {
         const bool shares = j < W.shared && len - A.nq + 1 >= A.prefix;
-        if (threadIdx.x == 0 && blockIdx.y == 0) {
-            W.table[(long long)b * W.each + j] = shares ? j : (int)blockIdx.x;
+        if (threadIdx.x == 0 && h == 0) {
+            W.table[(long long)b * W.each + j] = shares ? j : at_page;
             if (j == 0) W.lens[b] = len;
         }
         if (shares) return;
@@ -61,40 +62,37 @@ __global__ void __launch_bounds__(256) kv8_pages_kernel(const __grid_constant__ 
     const int* tab = A.table + (long long)row * A.table_stride;
     constexpr int CH = D / 16;            // 16 codes a thread
     const int mask = (1 << A.page_shift) - 1;
-    for (int h = blockIdx.y; h < A.kv_heads; h += gridDim.y) {
-        const long long to = ((long long)blockIdx.x * A.kv_heads + h) * PT * D;
+    const long long to = (long long)blockIdx.x * PT * D;
 #pragma unroll 2
-        for (int u = threadIdx.x; u < 2 * PT * CH; u += 256) {
-            const bool value = u >= PT * CH;
-            const int i = value ? u - PT * CH : u, t = i / CH, c = i - t * CH, tok = j * PT + t;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            uint32_t e = 0;
-            const int page = tok < end ? tab[tok >> A.page_shift] : -1;
-            if (page >= 0 && page < A.pages) {
-                const int at = tok & mask;
-                const int8_t* codes = static_cast<const int8_t*>(value ? A.v : A.k) + page * A.page_stride + h * A.kv_hs + at * A.kv_ts + 16 * c;
-                x = *reinterpret_cast<const uint4*>(codes);
-                e = (value ? A.v_exps : A.k_exps)[page * A.exp_page + h * A.exp_hs + at * (D / 32) + (c >> 1)];
-            }
-            const uint32_t f = exps_to_pair<E>(e, e), w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t r[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                codes_to_pairs<E>(w[k], r[2 * k], r[2 * k + 1]);
-                r[2 * k] = finite_pair<E>(mul_pairs<E>(r[2 * k], f));
-                r[2 * k + 1] = finite_pair<E>(mul_pairs<E>(r[2 * k + 1], f));
-            }
-            uint4* out = reinterpret_cast<uint4*>((value ? W.v : W.k) + to + (long long)t * D + 16 * c);
-            out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-            out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    for (int u = threadIdx.x; u < 2 * PT * CH; u += 256) {
+        const bool value = u >= PT * CH;
+        const int i = value ? u - PT * CH : u, t = i / CH, c = i - t * CH, tok = j * PT + t;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        uint32_t e = 0;
+        const int page = tok < end ? tab[tok >> A.page_shift] : -1;
+        if (page >= 0 && page < A.pages) {
+            const int at = tok & mask;
+            const int8_t* codes = static_cast<const int8_t*>(value ? A.v : A.k) + page * A.page_stride + h * A.kv_hs + at * A.kv_ts + 16 * c;
+            x = *reinterpret_cast<const uint4*>(codes);
+            e = (value ? A.v_exps : A.k_exps)[page * A.exp_page + h * A.exp_hs + at * (D / 32) + (c >> 1)];
         }
+        const uint32_t f = exps_to_pair<E>(e, e), w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t r[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            codes_to_pairs<E>(w[k], r[2 * k], r[2 * k + 1]);
+            r[2 * k] = finite_pair<E>(mul_pairs<E>(r[2 * k], f));
+            r[2 * k + 1] = finite_pair<E>(mul_pairs<E>(r[2 * k + 1], f));
+        }
+        uint4* out = reinterpret_cast<uint4*>((value ? W.v : W.k) + to + (long long)t * D + 16 * c);
+        out[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        out[1] = make_uint4(r[4], r[5], r[6], r[7]);
     }
 }
 
 template <class E, int D> cudaError_t pages_launch(const AttnArgs8& A, const Back& W, cudaStream_t stream) {
     const long long pages = W.shared + (W.own ? (long long)A.batch * W.each : 0);
-    const unsigned heads = A.kv_heads < 65535 ? A.kv_heads : 65535;   // (of a grid's y at most)
-    return launch_kernel(kv8_pages_kernel<E, D>, dim3((unsigned)pages, heads), dim3(256), 0, stream, A, W);
+    return launch_kernel(kv8_pages_kernel<E, D>, dim3((unsigned)(pages * A.kv_heads)), dim3(256), 0, stream, A, W);
 }
 cudaError_t launch_pages(const AttnArgs8& A, const Back& W, int type, int d, cudaStream_t stream) {
     if (type == PLM_F16) return d == 64 ? pages_launch<__half, 64>(A, W, stream) : pages_launch<__half, 128>(A, W, stream);
@@ -111,7 +109,7 @@ Back back_plan(const AttnArgs& A, int d, bool own, long long bound, uint8_t* ws)
     W.shared = own ? (A.batch > 1 ? A.prefix / PT : 0) : (A.prefix + PT - 1) / PT;
     W.each = (int)((bound + PT - 1) / PT);
     const long long pages = W.shared + (own ? (long long)A.batch * W.each : 0);
-    if (pages > 0x7FFFFFFFLL || pages > (long long)(SIZE_MAX / 8) / ((long long)A.kv_heads * PT * d)) {
+    if (pages > 0x7FFFFFFFLL / A.kv_heads) {   // (a CTA each)
         W.bytes = SIZE_MAX;
         return W;
     }
